@@ -437,6 +437,161 @@ sag_status lightning_indexer_grad(const sli_desc *desc, const sli_io *io, void *
                                   void *stream);
 
 /*
+ * Rotary positions of queries and keys: the step before an attention, and its
+ * gradient.  A head has d columns; d_rot of them, from column `offset` on, are
+ * rotated in pairs (a_i, b_i), i < d_rot / 2, by the angle p * inv_freq[i] of
+ * the row's position p, the other columns pass unchanged:
+ *     a' = magnitude * (a cos - b sin),   b' = magnitude * (a sin + b cos)
+ *   style SRT_HALF:        a_i = column i, b_i = column i + d_rot / 2
+ *   style SRT_INTERLEAVED: a_i = column 2i, b_i = column 2i + 1
+ * The gradient is the same map with the angle negated.
+ *
+ *   batch, layout, cu_seqlens, s_max: as in sag_desc, for one kind of rows that
+ *                 query and key share (batch <= 65536; sequences of any length,
+ *                 empty ones too)
+ *   n1, n2        heads of query and of key; n2 = 0: no key
+ *   d             head dim, 1..512
+ *   d_rot, offset even, >= 2; offset + d_rot <= d; d_rot <= 256
+ *   dtype         SAG_BF16 / SAG_FP16
+ *   inv_freq      host double[d_rot / 2], radians per position, finite
+ *   magnitude     factor on sine and cosine (1 unless the frequencies' scaling asks for more)
+ *   q_stride ...  elements from one row (token) to the next of query, key, query_out, key_out;
+ *                 0: dense (n * d).  Columns and heads of a row are dense.
+ * Angles are computed in 64-bit fixed-point turns (positions of any int32
+ * value lose nothing), the rotation in fp32, with one rounding to the dtype.
+ */
+typedef enum srt_style { SRT_HALF = 0, SRT_INTERLEAVED = 1 } srt_style;
+
+typedef struct srt_desc {
+    int32_t batch;
+    int32_t n1, n2;
+    int32_t d, d_rot, offset;
+    int32_t style;
+    int32_t dtype;
+    int32_t layout;
+    int32_t s_max;
+    const int32_t *cu_seqlens;
+    const double *inv_freq;
+    double magnitude;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+} srt_desc;
+
+/*
+ * Tensors (device pointers; query, key and the outputs 16-byte aligned and of
+ * R rows, positions 4-byte aligned):
+ *   query      [R, n1, d], key [R, n2, d]   dtype, read (key NULL when n2 = 0)
+ *   positions  [R] int32, or NULL: a row's position is then its place in its sequence
+ *   query_out, key_out                      dtype, written; each may be the input itself
+ *                                           (same pointer and stride), but must not overlap it otherwise
+ * BSND: padding rows are not read and get zeros.  TND: rows behind the last sequence are left as they were.
+ */
+typedef struct srt_io {
+    const void *query, *key;
+    const int32_t *positions;
+    void *query_out, *key_out;
+} srt_io;
+
+/*
+ * Frequencies and magnitude of the usual rotary positions (host only):
+ * inv_freq[i] = base^(-2i / d_rot), then, for a context longer by `factor` than
+ * the `original_length` positions seen in training (turns_i = original_length *
+ * inv_freq[i] / 2 pi):
+ *   SRT_SCALE_NONE    as they are
+ *   SRT_SCALE_LINEAR  all divided by factor
+ *   SRT_SCALE_BASE    base replaced by base * factor^(d_rot / (d_rot - 2))  (d_rot >= 4)
+ *   SRT_SCALE_RAMP    divided by factor from the pair that makes beta_slow turns on, kept up to the one that makes
+ *                     beta_fast, linear in i between; magnitude = 0.1 ln(factor) + 1
+ *   SRT_SCALE_BANDS   divided by factor where turns_i <= low, kept where turns_i >= high, linear in turns between
+ * SAG_ERR_SHAPE for d_rot odd or outside 2..256, base <= 1, factor < 1, or (ramp, bands) original_length < 1,
+ * beta_fast <= beta_slow, beta_slow <= 0, high <= low, low < 0; or an unknown scaling.
+ */
+typedef enum srt_scaling {
+    SRT_SCALE_NONE = 0,
+    SRT_SCALE_LINEAR = 1,
+    SRT_SCALE_BASE = 2,
+    SRT_SCALE_RAMP = 3,
+    SRT_SCALE_BANDS = 4
+} srt_scaling;
+
+sag_status rotary_frequencies(int32_t d_rot, double base, int32_t scaling, double factor, double original_length,
+                              double beta_fast, double beta_slow, double low, double high, double *inv_freq,
+                              double *magnitude);
+
+/* Phase 1 (host only): validation and workspace size (0 for batches of up to 64 sequences). */
+sag_status rotary_workspace_size(const srt_desc *desc, size_t *workspace_bytes);
+
+/* Phase 2: the rotation and its gradient, enqueued on `stream`.  The workspace may be NULL where phase 1 said 0. */
+sag_status rotary_fwd(const srt_desc *desc, const srt_io *io, void *workspace, size_t workspace_bytes, void *stream);
+sag_status rotary_grad(const srt_desc *desc, const srt_io *io, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Cross attention: a batch's query tokens attend to all of an encoder's states
+ * (key and value rows) of their sequence, whose number is another one, with G =
+ * n1 / n2 query heads sharing a key / value head.  Over the states that are there:
+ *     S = scale Q K^T,  lse = ln sum exp(S),  O = exp(S - lse) V
+ * and, with P = exp(S - lse) and Delta = rowsum(dY * O), the gradient
+ *     dV = P^T dY,  dS = P * (dY V^T - Delta),  dQ = scale dS K,  dK = scale dS^T Q.
+ * A query row with no state to attend to (an encoder sequence of length 0, or
+ * all masked) has O = 0 and lse = -inf and gives and takes no gradient.
+ *
+ *   batch, layout, cu_seqlens_q / cu_seqlens_kv, s1_max / s2_max: as in sag_desc, but key lengths are free, 0 included
+ *                 (batch <= 65536; up to 2M rows in all on each side)
+ *   n1, n2        as in sag_desc (up to 128 heads, G <= 32)
+ *   d             head dim of query, key and value: 64 or 128
+ *   dtype         SAG_BF16 / SAG_FP16
+ *   scale         finite, > 0
+ *   q_stride ...  elements from one row (token) to the next of query, key and value, a multiple of 8; 0: dense (n * d).
+ *                 Columns and heads of a row are dense, and so are all other tensors.
+ */
+typedef struct sca_desc {
+    int32_t batch;
+    int32_t n1, n2;
+    int32_t d;
+    int32_t dtype;
+    int32_t layout;
+    double scale;
+    const int32_t *cu_seqlens_q;
+    const int32_t *cu_seqlens_kv;
+    int32_t s1_max, s2_max;
+    int64_t q_stride, k_stride, v_stride;
+} sca_desc;
+
+/*
+ * Tensors (device pointers, 16-byte aligned but for key_mask; R1 / R2 rows as in sag_io):
+ *   query               [R1, n1, d]  dtype
+ *   key, value          [R2, n2, d]  dtype (may be NULL when there are no key rows at all)
+ *   attention_out       [R1, n1, d]  dtype; the forward writes it, the gradient reads it
+ *   attention_out_grad  [R1, n1, d]  dtype (gradient)
+ *   softmax_lse         [R1, n1]     fp32; the forward writes it, the gradient reads it
+ *   key_mask            [R2] bytes, or NULL: a key row of byte 0 is not there (its contents, and those of padding rows,
+ *                       may be anything, NaN included)
+ *   dq, dk, dv          like query, key, value but dense: written (masked key rows get zeros)
+ * BSND: padding rows get zeros in every output, softmax_lse too.  TND: rows behind the last sequence are left as they were.
+ */
+typedef struct sca_io {
+    const void *query, *key, *value;
+    void *attention_out;
+    const void *attention_out_grad;
+    float *softmax_lse;
+    const uint8_t *key_mask;
+    void *dq, *dk, *dv;
+} sca_io;
+
+/* Phase 1 (host only): validation and workspace size.  SAG_ERR_UNSUPPORTED for d other than 64 or 128, or a batch of more
+ * than 65536 sequences. */
+sag_status cross_attn_fwd_workspace_size(const sca_desc *desc, size_t *workspace_bytes);
+sag_status cross_attn_grad_workspace_size(const sca_desc *desc, size_t *workspace_bytes);
+
+/* Phase 2: enqueue on `stream`; ownership and host-side errors as for sel_attn_grad.  Every output is bit-identical run to
+ * run (sums are taken in a fixed order). */
+sag_status cross_attn_fwd(const sca_desc *desc, const sca_io *io, void *workspace, size_t workspace_bytes, void *stream);
+sag_status cross_attn_grad(const sca_desc *desc, const sca_io *io, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Waits for `stream` and returns the status the device recorded in `workspace` during the last cross_attn_fwd or
+ * cross_attn_grad on it: SAG_OK, SAG_ERR_TIMEOUT, or SAG_ERR_CUDA. */
+sag_status cross_attn_query_error(const void *workspace, void *stream);
+
+/*
  * Self-test of the device failure path (not part of the operator; the pages
  * have no counterpart).  Enqueues one small kernel that runs the library's
  * bounded mbarrier wait on a barrier nothing ever arrives on: after limit_ns

@@ -422,3 +422,403 @@ def indexer_backward(q, k, weights, dy, indices, cu_seqlens_q, cu_seqlens_kv, de
         if st != SAG_OK:
             raise SagError(st, "device")
     return out
+
+
+# ------------------------------------------- rotary positions, cross attention
+EXPORTED_NEIGHBOURS = ("rotary_frequencies", "rotary_workspace_size", "rotary_fwd", "rotary_grad",
+                       "cross_attn_fwd_workspace_size", "cross_attn_fwd", "cross_attn_grad_workspace_size",
+                       "cross_attn_grad", "cross_attn_query_error")
+SRT_HALF, SRT_INTERLEAVED = 0, 1
+_ROTARY_STYLES = {"half": SRT_HALF, "interleaved": SRT_INTERLEAVED}
+_ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
+
+
+class SrtDesc(ctypes.Structure):
+    """Mirror of ``srt_desc`` in include/selattn.h."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("n1", ctypes.c_int32), ("n2", ctypes.c_int32), ("d", ctypes.c_int32),
+        ("d_rot", ctypes.c_int32), ("offset", ctypes.c_int32), ("style", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("layout", ctypes.c_int32), ("s_max", ctypes.c_int32),
+        ("cu_seqlens", ctypes.POINTER(ctypes.c_int32)), ("inv_freq", ctypes.POINTER(ctypes.c_double)),
+        ("magnitude", ctypes.c_double),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+        ("k_out_stride", ctypes.c_int64),
+    ]
+
+
+class SrtIo(ctypes.Structure):
+    """Mirror of ``srt_io`` in include/selattn.h (device pointers as ints)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("query", "key", "positions", "query_out", "key_out")]
+
+
+class ScaDesc(ctypes.Structure):
+    """Mirror of ``sca_desc`` in include/selattn.h."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("n1", ctypes.c_int32), ("n2", ctypes.c_int32), ("d", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32), ("scale", ctypes.c_double),
+        ("cu_seqlens_q", ctypes.POINTER(ctypes.c_int32)), ("cu_seqlens_kv", ctypes.POINTER(ctypes.c_int32)),
+        ("s1_max", ctypes.c_int32), ("s2_max", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+    ]
+
+
+class ScaIo(ctypes.Structure):
+    """Mirror of ``sca_io`` in include/selattn.h (device pointers as ints)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "query", "key", "value", "attention_out", "attention_out_grad", "softmax_lse", "key_mask", "dq", "dk", "dv")]
+
+
+def _lib_neighbours():
+    lib = load()
+    if not getattr(lib, "_neighbours_ready", False):
+        vp, sz = ctypes.c_void_p, ctypes.c_size_t
+        dbl, psz = ctypes.c_double, ctypes.POINTER(ctypes.c_size_t)
+        lib.rotary_frequencies.argtypes = [ctypes.c_int32, dbl, ctypes.c_int32] + [dbl] * 6 + [ctypes.POINTER(dbl)] * 2
+        lib.cross_attn_query_error.argtypes = [vp, vp]
+        for prefix, desc, io, names in (("rotary", SrtDesc, SrtIo, ("fwd", "grad")),
+                                        ("cross_attn", ScaDesc, ScaIo, ("fwd", "grad"))):
+            for n in names:
+                getattr(lib, f"{prefix}_{n}").argtypes = [ctypes.POINTER(desc), ctypes.POINTER(io), vp, sz, vp]
+        lib.rotary_workspace_size.argtypes = [ctypes.POINTER(SrtDesc), psz]
+        lib.cross_attn_fwd_workspace_size.argtypes = [ctypes.POINTER(ScaDesc), psz]
+        lib.cross_attn_grad_workspace_size.argtypes = [ctypes.POINTER(ScaDesc), psz]
+        for n in EXPORTED_NEIGHBOURS:
+            getattr(lib, n).restype = ctypes.c_int
+        lib._neighbours_ready = True
+    return lib
+
+
+def _phase1(name: str, desc) -> int:
+    n = ctypes.c_size_t(0)
+    st = getattr(_lib_neighbours(), name)(ctypes.byref(desc), ctypes.byref(n))
+    if st != SAG_OK:
+        raise SagError(st, name)
+    return n.value
+
+
+def _i32(xs):
+    return (ctypes.c_int32 * len(xs))(*[int(x) for x in xs])
+
+
+def _sag_dtype(t):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return SAG_BF16
+    if t.dtype == torch.float16:
+        return SAG_FP16
+    raise SagError(SAG_ERR_DTYPE, f"tensor of {t.dtype}")
+
+
+def _row_stride(name, t, heads, d):
+    """Elements from one row (token) to the next of a TND or BSND tensor whose
+    rows are dense; 0 for a dense tensor."""
+    if t.is_contiguous():
+        return 0
+    if (d > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != d):
+        raise ValueError(f"{name}: the heads and columns of a row must be dense")
+    if t.dim() == 3:
+        step = t.stride(0) if t.shape[0] > 1 else heads * d
+    else:
+        b, s = t.shape[0], t.shape[1]
+        step = t.stride(1) if s > 1 else (t.stride(0) if b > 1 else heads * d)
+        if b > 1 and t.stride(0) != s * step:
+            raise ValueError(f"{name}: the batches of a padded tensor must follow one another in memory")
+    if step < heads * d:
+        raise ValueError(f"{name}: rows overlap")
+    return step
+
+
+def _check(name, t, like, shape, dtype=None):
+    if t.device != like.device:
+        raise ValueError(f"{name}: on {t.device}, not on {like.device}")
+    if t.dtype != (like.dtype if dtype is None else dtype):
+        raise SagError(SAG_ERR_DTYPE, f"{name}: tensor of {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+class _on_device:
+    """The tensors' device and the call's stream: allocations of the call come
+    from that stream's pool, and the library launches on that device."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.torch, self.device, self.given = torch, device, stream
+        self.ctx = []
+
+    def __enter__(self):
+        cuda = self.torch.cuda
+        if self.given is not None:
+            self.ctx.append(cuda.stream(self.given))
+        elif cuda.current_device() != self.device.index:
+            self.ctx.append(cuda.device(self.device))
+        for c in self.ctx:
+            c.__enter__()
+        return (self.given if self.given is not None else cuda.current_stream(self.device)).cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+class Rotary:
+    """Frequencies, column range and style of rotary positions (see
+    ``rotary_frequencies`` and ``srt_desc`` in include/selattn.h).
+
+    ``d_rot`` columns from ``offset`` on are rotated; ``style`` is "half" or
+    "interleaved", ``scaling`` "none", "linear", "base", "ramp" or "bands".
+    ``inv_freq`` (radians per position, d_rot / 2 floats) and ``magnitude``
+    replace the computed ones.
+    """
+
+    def __init__(self, d_rot, base=10000.0, style="half", offset=0, scaling="none", factor=1.0, original_length=0,
+                 beta_fast=32.0, beta_slow=1.0, low=1.0, high=4.0, inv_freq=None, magnitude=None):
+        if style not in _ROTARY_STYLES:
+            raise ValueError(f"style {style!r} is none of {sorted(_ROTARY_STYLES)}")
+        if scaling not in _ROTARY_SCALINGS:
+            raise ValueError(f"scaling {scaling!r} is none of {sorted(_ROTARY_SCALINGS)}")
+        self.d_rot, self.offset, self.style = int(d_rot), int(offset), _ROTARY_STYLES[style]
+        self._freq = (ctypes.c_double * max(1, self.d_rot // 2))()
+        mag = ctypes.c_double(1.0)
+        if inv_freq is None:
+            st = _lib_neighbours().rotary_frequencies(self.d_rot, base, _ROTARY_SCALINGS[scaling], factor,
+                                                      original_length, beta_fast, beta_slow, low, high, self._freq,
+                                                      ctypes.byref(mag))
+            if st != SAG_OK:
+                raise SagError(st, "rotary_frequencies")
+        else:
+            if len(inv_freq) != self.d_rot // 2:
+                raise ValueError(f"{len(inv_freq)} frequencies for {self.d_rot} columns")
+            self._freq[:] = [float(f) for f in inv_freq]
+        self.magnitude = mag.value if magnitude is None else float(magnitude)
+
+    @property
+    def inv_freq(self):
+        return list(self._freq)
+
+
+def make_rotary_desc(rotary: Rotary, cu_seqlens, n1, n2, d, dtype=SAG_BF16, layout=SAG_LAYOUT_TND, s_max=0) -> SrtDesc:
+    """Descriptor of a rotation (n2 = 0: no key); keeps the host arrays alive."""
+    cu = _i32(cu_seqlens)
+    desc = SrtDesc(batch=len(cu) - 1, n1=n1, n2=n2, d=d, d_rot=rotary.d_rot, offset=rotary.offset, style=rotary.style,
+                   dtype=dtype, layout=int(layout), s_max=int(s_max),
+                   cu_seqlens=ctypes.cast(cu, ctypes.POINTER(ctypes.c_int32)),
+                   inv_freq=ctypes.cast(rotary._freq, ctypes.POINTER(ctypes.c_double)), magnitude=rotary.magnitude)
+    desc._keep = (cu, rotary._freq)
+    desc._rows = cu[len(cu) - 1] if layout == SAG_LAYOUT_TND else desc.batch * int(s_max)
+    return desc
+
+
+def rotary_workspace_size(desc: SrtDesc) -> int:
+    """Phase 1: validate and return the workspace size in bytes (0 for small batches)."""
+    return _phase1("rotary_workspace_size", desc)
+
+
+def _with(desc, **fields):
+    """The descriptor, or a copy where a field differs (a kept one is never changed)."""
+    if all(getattr(desc, k) == v for k, v in fields.items()):
+        return desc
+    new = type(desc).from_buffer_copy(desc)
+    for k in desc.__dict__:
+        setattr(new, k, desc.__dict__[k])
+    for k, v in fields.items():
+        setattr(new, k, v)
+    return new
+
+
+def _check_rows(name, t, rows, s_max):
+    """The tensor holds the descriptor's rows (a packed one, s_max None, may hold more behind them)."""
+    if s_max is not None:
+        if t.dim() != 4 or t.shape[0] * t.shape[1] != rows or t.shape[1] != s_max:
+            raise ValueError(f"{name}: shape {tuple(t.shape)} is not that of the padded batch")
+    elif t.dim() != 3 or t.shape[0] < rows:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} does not hold {rows} packed rows")
+
+
+def _rotary(entry, q, k, rotary, cu_seqlens, positions, out, workspace, stream, desc):
+    import torch
+    if not q.is_cuda:
+        raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
+    n1, d = q.shape[-2], q.shape[-1]
+    n2 = k.shape[-2] if k is not None else 0
+    if desc is None:
+        bsnd = q.dim() == 4
+        desc = make_rotary_desc(rotary, cu_seqlens, n1, n2, d, _sag_dtype(q), SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND,
+                                q.shape[1] if bsnd else 0)
+    elif (desc.n1, desc.n2, desc.d, desc.dtype) != (n1, n2, d, _sag_dtype(q)):
+        raise ValueError("the descriptor is of other heads, columns or type")
+    _check_rows("q", q, desc._rows, desc.s_max if desc.layout == SAG_LAYOUT_BSND else None)
+    lead = tuple(q.shape[:-2])
+    if k is not None:
+        _check("k", k, q, lead + (n2, d))
+    if positions is not None:
+        _check("positions", positions, q, lead, torch.int32)
+        if not positions.is_contiguous():
+            raise ValueError("positions must be contiguous")
+    with _on_device(q.device, stream) as handle:
+        if out is None:
+            qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            ko = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k is not None else None
+        else:
+            qo, ko = (out, None) if k is None and not isinstance(out, (tuple, list)) else out
+            _check("out", qo, q, q.shape)
+            if k is not None:
+                _check("out", ko, q, k.shape)
+        strides = dict(q_stride=_row_stride("q", q, n1, d), q_out_stride=_row_stride("out", qo, n1, d))
+        io = SrtIo(query=q.data_ptr(), query_out=qo.data_ptr())
+        if k is not None:
+            strides.update(k_stride=_row_stride("k", k, n2, d), k_out_stride=_row_stride("out", ko, n2, d))
+            io.key, io.key_out = k.data_ptr(), ko.data_ptr()
+        if positions is not None:
+            io.positions = positions.data_ptr()
+        desc = _with(desc, **strides)
+        ws = None
+        if desc.batch > 64:
+            need = rotary_workspace_size(desc)
+            if need and (workspace is None or workspace.numel() < need):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr() if need else None
+        else:
+            need = 0
+        st = getattr(_lib_neighbours(), entry)(ctypes.byref(desc), ctypes.byref(io), ws, need, handle)
+    if st != SAG_OK:
+        raise SagError(st, entry)
+    return (qo, ko) if k is not None else qo
+
+
+def rotary_forward(q, k, rotary, cu_seqlens=None, positions=None, out=None, workspace=None, stream=None, desc=None):
+    """Rotary positions of q [.., n1, d] and k [.., n2, d] (or None), TND or 4-D
+    BSND tensors of the same rows: returns (q, k) rotated, or q alone.
+
+    A row's position is its place in its sequence (``cu_seqlens``), or
+    ``positions[row]`` (int32, the shape of q without heads and columns).
+    ``out=(q, k)`` rotates in place; rows may be strided (slices of a fused
+    projection).  ``desc`` (make_rotary_desc) replaces rotary and cu_seqlens.
+    """
+    return _rotary("rotary_fwd", q, k, rotary, cu_seqlens, positions, out, workspace, stream, desc)
+
+
+def rotary_backward(dq, dk, rotary, cu_seqlens=None, positions=None, out=None, workspace=None, stream=None, desc=None):
+    """Gradient of ``rotary_forward``: the gradients of its outputs to those of
+    its inputs; arguments alike."""
+    return _rotary("rotary_grad", dq, dk, rotary, cu_seqlens, positions, out, workspace, stream, desc)
+
+
+def make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, dtype=SAG_BF16, layout=SAG_LAYOUT_TND, s1_max=0,
+                    s2_max=0) -> ScaDesc:
+    """Descriptor of a cross attention; keeps the host arrays alive."""
+    cq, ck = _i32(cu_seqlens_q), _i32(cu_seqlens_kv)
+    if len(cq) != len(ck):
+        raise ValueError("cu_seqlens_q and cu_seqlens_kv are of different batches")
+    desc = ScaDesc(batch=len(cq) - 1, n1=n1, n2=n2, d=d, dtype=dtype, layout=int(layout), scale=float(scale),
+                   cu_seqlens_q=ctypes.cast(cq, ctypes.POINTER(ctypes.c_int32)),
+                   cu_seqlens_kv=ctypes.cast(ck, ctypes.POINTER(ctypes.c_int32)), s1_max=int(s1_max), s2_max=int(s2_max))
+    desc._keep = (cq, ck)
+    bsnd = layout == SAG_LAYOUT_BSND
+    desc._rows = (desc.batch * int(s1_max) if bsnd else cq[len(cq) - 1], desc.batch * int(s2_max) if bsnd else ck[len(ck) - 1])
+    return desc
+
+
+def cross_fwd_workspace_size(desc: ScaDesc) -> int:
+    """Phase 1 of the forward: validate and return the workspace size in bytes."""
+    return _phase1("cross_attn_fwd_workspace_size", desc)
+
+
+def cross_grad_workspace_size(desc: ScaDesc) -> int:
+    """Phase 1 of the gradient: validate and return the workspace size in bytes."""
+    return _phase1("cross_attn_grad_workspace_size", desc)
+
+
+def cross_query_error(workspace, stream) -> int:
+    """Wait for the stream; return the status the device recorded."""
+    return _lib_neighbours().cross_attn_query_error(workspace, stream)
+
+
+def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, workspace, stream, check, desc, tensors):
+    """Shared by the two directions: ``tensors(lead1, lead2, n1, n2, d)`` gives
+    the remaining sca_io pointers and the outputs."""
+    import torch
+    if not q.is_cuda:
+        raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
+    n1, d, n2 = q.shape[-2], q.shape[-1], k.shape[-2]
+    if desc is None:
+        bsnd = q.dim() == 4
+        if bsnd and k.dim() != 4:
+            raise ValueError("BSND needs 4-D query and key tensors")
+        desc = make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, _sag_dtype(q),
+                               SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND, q.shape[1] if bsnd else 0,
+                               k.shape[1] if bsnd else 0)
+    elif (desc.n1, desc.n2, desc.d, desc.dtype) != (n1, n2, d, _sag_dtype(q)):
+        raise ValueError("the descriptor is of other heads, columns or type")
+    bsnd = desc.layout == SAG_LAYOUT_BSND
+    _check_rows("q", q, desc._rows[0], desc.s1_max if bsnd else None)
+    _check_rows("k", k, desc._rows[1], desc.s2_max if bsnd else None)
+    lead1, lead2 = tuple(q.shape[:-2]), tuple(k.shape[:-2])
+    _check("k", k, q, lead2 + (n2, d))
+    _check("v", v, q, lead2 + (n2, d))
+    desc = _with(desc, q_stride=_row_stride("q", q, n1, d), k_stride=_row_stride("k", k, n2, d),
+                 v_stride=_row_stride("v", v, n2, d))
+    io = ScaIo(query=q.data_ptr(), key=k.data_ptr(), value=v.data_ptr())
+    if key_mask is not None:
+        if key_mask.dtype not in (torch.bool, torch.uint8) or not key_mask.is_contiguous():
+            raise ValueError("key_mask must be a contiguous bool or uint8 tensor")
+        _check("key_mask", key_mask, q, lead2, key_mask.dtype)
+        io.key_mask = key_mask.data_ptr()
+    with _on_device(q.device, stream) as handle:
+        outs = tensors(io, lead1 + (n1, d), lead2 + (n2, d))
+        need = size(desc)
+        if workspace is None or workspace.numel() < need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        st = getattr(_lib_neighbours(), entry)(ctypes.byref(desc), ctypes.byref(io), workspace.data_ptr(), need, handle)
+        if st == SAG_OK and check:
+            st = cross_query_error(workspace.data_ptr(), handle)
+    if st != SAG_OK:
+        raise SagError(st, entry)
+    return outs
+
+
+def _dense(name, t, like, shape, dtype=None):
+    _check(name, t, like, shape, dtype)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def cross_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, key_mask=None, out=None, workspace=None,
+                  stream=None, check=False, desc=None):
+    """Cross attention of q [.., n1, d] to the encoder states k, v [.., n2, d] of
+    the same sequences, TND or 4-D BSND: returns (attention_out [.., n1, d],
+    softmax_lse [.., n1] in fp32).
+
+    ``key_mask`` (bool or uint8, the shape of k without heads and columns):
+    states where it is 0 are not there.  q, k and v may be strided by rows.
+    ``desc`` (make_cross_desc) replaces cu_seqlens_* and scale; ``check`` reads
+    the device status back (this synchronizes the stream).
+    """
+    def tensors(io, s1, s2):
+        import torch
+        o, lse = out if out is not None else (torch.empty(s1, dtype=q.dtype, device=q.device),
+                                              torch.empty(s1[:-1], dtype=torch.float32, device=q.device))
+        io.attention_out = _dense("attention_out", o, q, s1)
+        io.softmax_lse = _dense("softmax_lse", lse, q, s1[:-1], torch.float32)
+        return o, lse
+
+    return _cross("cross_attn_fwd", cross_fwd_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,
+                  workspace, stream, check, desc, tensors)
+
+
+def cross_backward(q, k, v, o, dy, lse, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, key_mask=None, out=None,
+                   workspace=None, stream=None, check=False, desc=None):
+    """Gradient of ``cross_forward``: returns (dq, dk, dv), from the forward's o
+    and lse and the gradient dy of o; the other arguments as there."""
+    def tensors(io, s1, s2):
+        import torch
+        io.attention_out = _dense("o", o, q, s1)
+        io.attention_out_grad = _dense("dy", dy, q, s1)
+        io.softmax_lse = _dense("lse", lse, q, s1[:-1], torch.float32)
+        outs = out if out is not None else tuple(torch.empty(s, dtype=q.dtype, device=q.device) for s in (s1, s2, s2))
+        io.dq, io.dk, io.dv = (_dense(n, t, q, s) for n, t, s in zip(("dq", "dk", "dv"), outs, (s1, s2, s2)))
+        return outs
+
+    return _cross("cross_attn_grad", cross_grad_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,
+                  workspace, stream, check, desc, tensors)

@@ -323,6 +323,17 @@ bool DeviceGuard::bind(cudaStream_t s) {
     if (s == nullptr) return true;
     int dev = 0;
     if (cudaStreamGetDevice(s, &dev) != cudaSuccess) return false;
+    return make_current(dev);
+}
+
+bool DeviceGuard::bind_memory(const void *ptr) {
+    cudaPointerAttributes at{};
+    if (cudaPointerGetAttributes(&at, ptr) != cudaSuccess) return false;
+    if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) return false;
+    return make_current(at.device);
+}
+
+bool DeviceGuard::make_current(int dev) {
     int cur = -1;
     if (cudaGetDevice(&cur) != cudaSuccess) return false;
     if (cur == dev) return true;

@@ -1,0 +1,267 @@
+// Pieces shared by the cross-attention kernels: arguments, tile geometry, the
+// TMEM and cluster instructions they add, and the masks of a key tile.
+//
+// A tile has 128 rows.  A query tile packs 128 / G tokens with the G heads that
+// share a key/value head (row = token * G + head), so keys are read once for the
+// whole group and the key gradients sum over it inside the matrix product.
+#pragma once
+
+#include "common.cuh"
+#include "seqtab.cuh"
+#include "tc.cuh"
+
+namespace sag {
+
+constexpr int kXRows = 128;             // rows of a query tile, keys of a key tile
+constexpr int kXThreads = 320;          // warps 0-7 softmax and epilogue, 8 TMA, 9 MMA
+constexpr uint64_t kXWaitNs = 2000000000ull;
+// A half keeps 11 bits down to 2^-14 only, and a probability of a long sequence lies below that.  Both passes shift
+// fp16 probabilities up by a power of two that cannot overflow 65504, and undo it in fp32.
+constexpr float kFwdShiftF16 = 7.f;     // forward: exp2(x - max) <= 2^8 (lazy maximum), so <= 2^15
+constexpr float kGradShiftF16 = 15.f;   // gradient: P <= 1 (up to rounding), so <= 2^15
+
+struct XArgs {
+    SeqTab seq;
+    int32_t n1, n2, group;
+    int32_t tpt;                        // tokens per query tile
+    int32_t s1_pad, s2_pad;             // BSND: padded lengths, else 0
+    int32_t nsplit;                     // CTAs (one cluster) that share a unit
+    float scale, scale_log2;
+    const uint8_t *mask;
+    const uint16_t *o_in, *dy, *v_in;   // preprocess
+    int64_t v_stride;
+    uint16_t *o, *dq, *dk, *dv;
+    float *lse;                         // forward: written, gradient: read
+    float *stats;                       // [query tile][n2][256]: lse * log2(e), then Delta, of the tile's 128 rows
+    float *norms;                       // fp16: largest row norm of dY of each [query tile][n2], then of V of each [key tile][n2]
+    int32_t q_tiles, k_tiles;
+    int32_t *count, *status;            // device status: number of words, one word for each CTA
+    int32_t n_status;                   // value for *count
+};
+
+cudaError_t launch_xfwd(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s);
+cudaError_t launch_xpre(const XArgs &a, bool fp16, int d, cudaStream_t s);
+cudaError_t launch_xdq(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s);
+cudaError_t launch_xdkv(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s);
+
+namespace {
+
+// ---------------------------------------------------------------- PTX
+// A from TMEM (K-major: lane = row, two elements a column), B from shared memory; one elected lane issues.
+__device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// global -> shared copy of `bytes` (a multiple of 16, both ends 16-byte aligned)
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     tc::smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// address of the same shared-memory variable in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, int rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float2 peer_ld2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float xex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// two fp32 operations an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+template <bool kFp16>
+__device__ __forceinline__ uint32_t xpack(float a, float b) {
+    if constexpr (kFp16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+// ---------------------------------------------------------------- geometry
+// Unit -> sequence, key/value head, tile within the sequence.  Units of a
+// sequence are consecutive, and within it those of a head, so that CTAs that
+// run at the same time read the same keys (or queries) from L2.
+struct XUnit {
+    SeqRow seq;
+    int head, tile;
+    int64_t tile_id;                    // (tiles of the sequences before + tile) * n2 + head
+};
+template <int32_t SeqRow::*field>
+__device__ __forceinline__ XUnit x_decode(const XArgs &A, int unit) {
+    const SeqRow *tab = A.seq.rows();
+    const int b = seq_find<field>(tab, A.seq.batch, unit / A.n2);
+    XUnit x;
+    x.seq = tab[b];
+    const int first = tab[b].*field, nt = tab[b + 1].*field - first;
+    const int local = unit - first * A.n2;
+    x.head = local / nt;
+    x.tile = local % nt;
+    x.tile_id = (int64_t)(first + x.tile) * A.n2 + x.head;
+    return x;
+}
+
+// Which of the 128 keys from key `first` of a sequence are there, as four
+// words.  Collective over a warp when there is a mask.
+struct KeyBits {
+    uint32_t w[4];
+    __device__ __forceinline__ bool all() const { return (w[0] & w[1] & w[2] & w[3]) == 0xffffffffu; }
+};
+__device__ __forceinline__ KeyBits key_bits(const uint8_t *mask, const SeqRow &seq, int first, int lane) {
+    KeyBits k;
+    const int left = seq.klen - first;
+    if (!mask) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = left - 32 * j;
+            k.w[j] = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+        }
+        return k;
+    }
+    const uint8_t *m = mask + (int64_t)seq.k0 + first;
+    bool on[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) on[j] = 32 * j + lane < left && m[32 * j + lane] != 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k.w[j] = __ballot_sync(0xffffffffu, on[j]);
+    return k;
+}
+
+// Zeros the rows of a [128 x 64 * kChunks] shared tile whose bit is not set, before the matrix product reads it: a
+// probability of 0 does not cancel a NaN.  Collective over the MMA warp.
+template <int kChunks>
+__device__ __forceinline__ void zero_rows(uint8_t *tile, const KeyBits &k, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t dead = ~k.w[j];
+        while (dead) {
+            // up to four dead rows at a time, eight lanes a row
+            int row = -1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (!dead) break;
+                const int r = __ffs(dead) - 1;
+                dead &= dead - 1;
+                if ((lane >> 3) == i) row = 32 * j + r;
+            }
+            if (row >= 0)
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+                    *reinterpret_cast<uint4 *>(tile + c * 16384 + row * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+    }
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// Products over a tile pair, each with K = 16 steps; the operands' 64-column chunks are 16 KB apart.
+// A [128 x D] K-major, B [128 x D] K-major: D columns 0..127 of the accumulator.
+template <int D>
+__device__ __forceinline__ void mma_abt(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc) {
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+        tc::mma_f16_ss_warp(acc, tc::sw128_desc(a + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
+                            tc::sw128_desc(b + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024), idesc, kk > 0);
+}
+// A [128 x 128] in TMEM (16-bit pairs; the second half of K starts `gap` columns after the first), B [128 x D] MN-major.
+template <int kGap>
+__device__ __forceinline__ void mma_ab(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+        mma_f16_ts_warp(acc, a + (kk >> 2) * kGap + (kk & 3) * 8, tc::sw128_desc(b + kk * 2048, 16384, 1024), idesc,
+                        accumulate || kk > 0);
+}
+
+// 16-bit row piece of `n` (a multiple of 8) fp32 values
+template <bool kFp16, int n>
+__device__ __forceinline__ void store_row(uint16_t *dst, const float *x) {
+#pragma unroll
+    for (int j = 0; j < n; j += 8) {
+        uint4 v;
+        v.x = xpack<kFp16>(x[j], x[j + 1]);
+        v.y = xpack<kFp16>(x[j + 2], x[j + 3]);
+        v.z = xpack<kFp16>(x[j + 4], x[j + 5]);
+        v.w = xpack<kFp16>(x[j + 6], x[j + 7]);
+        *reinterpret_cast<uint4 *>(dst + j) = v;
+    }
+}
+
+}  // namespace
+}  // namespace sag

@@ -1,0 +1,240 @@
+// C ABI of the cross attention: validation and workspace sizes (phase 1),
+// sequence tables and launches (phase 2).
+#include <math.h>
+
+#include "cross.cuh"
+#include "kernels.cuh"
+
+namespace sag {
+
+namespace {
+
+constexpr size_t kAlign = 256;
+constexpr size_t kStatusAt = 256;           // status words, behind the workspace's header
+size_t up256(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+// CTAs that splitting may add to a launch (it stops at one CTA per SM), for the status words
+constexpr int64_t kSplitCtas = 1024;
+
+struct XPlan {
+    bool fp16, bsnd;
+    int tpt;
+    int64_t fwd_units, q_tiles, k_tiles;    // query tile pairs, query tiles, key tiles (of all sequences, padding included)
+    int max_q, max_k;                       // most query / key tiles of one sequence that have work
+    size_t o_seq, o_stats, o_norms, total;
+};
+
+sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {
+    if (!d || !d->cu_seqlens_q || !d->cu_seqlens_kv) return SAG_ERR_NULL;
+    if (d->dtype != SAG_BF16 && d->dtype != SAG_FP16) return SAG_ERR_DTYPE;
+    if (d->n1 < 1 || d->n1 > 128 || d->n2 < 1 || d->n2 > 128 || d->n1 % d->n2 != 0 || d->n1 / d->n2 > 32)
+        return SAG_ERR_SHAPE;
+    if (d->d < 1 || !(d->scale > 0.0) || d->scale > 1e30) return SAG_ERR_SHAPE;
+    sag_status st = check_seqs(d->batch, d->layout, d->cu_seqlens_q, d->s1_max);
+    const sag_status st2 = check_seqs(d->batch, d->layout, d->cu_seqlens_kv, d->s2_max);
+    if (st == SAG_OK || (st == SAG_ERR_UNSUPPORTED && st2 != SAG_OK)) st = st2;
+    if (st != SAG_OK) return st;
+    const int64_t strides[] = {d->q_stride, d->k_stride, d->v_stride};
+    for (int i = 0; i < 3; ++i)
+        if (strides[i] != 0 && (strides[i] % 8 != 0 || strides[i] < (int64_t)(i ? d->n2 : d->n1) * d->d ||
+                                strides[i] > (1LL << 36)))
+            return SAG_ERR_SHAPE;
+    if (d->d != 64 && d->d != 128) return SAG_ERR_UNSUPPORTED;
+    p->fp16 = d->dtype == SAG_FP16;
+    p->bsnd = d->layout == SAG_LAYOUT_BSND;
+    p->tpt = kXRows / (d->n1 / d->n2);
+    p->fwd_units = p->q_tiles = p->k_tiles = 0;
+    p->max_q = p->max_k = 0;
+    for (int b = 0; b < d->batch; ++b) {
+        const int ql = d->cu_seqlens_q[b + 1] - d->cu_seqlens_q[b], kl = d->cu_seqlens_kv[b + 1] - d->cu_seqlens_kv[b];
+        const int qt = ((p->bsnd ? d->s1_max : ql) + p->tpt - 1) / p->tpt;
+        const int kt = ((p->bsnd ? d->s2_max : kl) + kXRows - 1) / kXRows;
+        p->fwd_units += (qt + 1) / 2;
+        p->q_tiles += qt;
+        p->k_tiles += kt;
+        const int qw = (ql + p->tpt - 1) / p->tpt, kw = (kl + kXRows - 1) / kXRows;
+        if (qw > p->max_q) p->max_q = qw;
+        if (kw > p->max_k) p->max_k = kw;
+    }
+    p->fwd_units *= d->n2;
+    size_t o = 0;
+    auto take = [&](size_t bytes) { const size_t at = o; o = up256(o + bytes); return at; };
+    take(kStatusAt);                        // header: number of status words
+    const int64_t ctas = grad ? (p->q_tiles + p->k_tiles) * d->n2 + 2 * kSplitCtas : p->fwd_units + kSplitCtas;
+    take(sizeof(int32_t) * ctas);           // status words, one a CTA
+    p->o_seq = take(seq_ws_bytes(d->batch));
+    p->o_stats = take(grad ? sizeof(float) * 256 * p->q_tiles * d->n2 : 0);
+    p->o_norms = take(grad && p->fp16 ? sizeof(float) * (p->q_tiles + p->k_tiles) * d->n2 : 0);
+    p->total = o;
+    return SAG_OK;
+}
+
+// CTAs that share a unit: while SMs are idle, as long as each still has two tiles of the loop
+int split_of(int64_t units, int tiles, int sms) {
+    if (sms > kSplitCtas) sms = kSplitCtas;
+    int ns = 1;
+    while (ns < 8 && units * ns * 2 <= sms && tiles >= 4 * ns) ns *= 2;
+    return ns;
+}
+
+XArgs x_args(const sca_desc *d, const sca_io *io, const XPlan &p, char *ws) {
+    XArgs a{};
+    a.n1 = d->n1;
+    a.n2 = d->n2;
+    a.group = d->n1 / d->n2;
+    a.tpt = p.tpt;
+    a.s1_pad = p.bsnd ? d->s1_max : 0;
+    a.s2_pad = p.bsnd ? d->s2_max : 0;
+    a.nsplit = 1;
+    a.scale = (float)d->scale;
+    a.scale_log2 = (float)(d->scale * 1.4426950408889634);
+    a.mask = io->key_mask;
+    a.o_in = static_cast<const uint16_t *>(io->attention_out);
+    a.dy = static_cast<const uint16_t *>(io->attention_out_grad);
+    a.v_in = static_cast<const uint16_t *>(io->value);
+    a.v_stride = d->v_stride ? d->v_stride : (int64_t)d->n2 * d->d;
+    a.o = static_cast<uint16_t *>(io->attention_out);
+    a.dq = static_cast<uint16_t *>(io->dq);
+    a.dk = static_cast<uint16_t *>(io->dk);
+    a.dv = static_cast<uint16_t *>(io->dv);
+    a.lse = io->softmax_lse;
+    a.stats = reinterpret_cast<float *>(ws + p.o_stats);
+    a.norms = reinterpret_cast<float *>(ws + p.o_norms);
+    a.q_tiles = (int)p.q_tiles;
+    a.k_tiles = (int)p.k_tiles;
+    a.count = reinterpret_cast<int32_t *>(ws);
+    a.status = reinterpret_cast<int32_t *>(ws + kStatusAt);
+    return a;
+}
+
+// rows of the table; `pairs`: query tiles counted in pairs (the forward's units)
+cudaError_t x_table(XArgs *a, const sca_desc *d, const XPlan &p, char *ws, bool pairs, cudaStream_t s) {
+    int qt = 0, kt = 0;
+    return fill_seq_tab(&a->seq, d->batch, reinterpret_cast<SeqRow *>(ws + p.o_seq), s, [&](int b) {
+        SeqRow r{};
+        r.qtile0 = qt;
+        r.ktile0 = kt;
+        r.q0 = p.bsnd ? b * d->s1_max : d->cu_seqlens_q[b];
+        r.k0 = p.bsnd ? b * d->s2_max : d->cu_seqlens_kv[b];
+        if (b < d->batch) {
+            r.qlen = d->cu_seqlens_q[b + 1] - d->cu_seqlens_q[b];
+            r.klen = d->cu_seqlens_kv[b + 1] - d->cu_seqlens_kv[b];
+            const int t = ((p.bsnd ? d->s1_max : r.qlen) + p.tpt - 1) / p.tpt;
+            qt += pairs ? (t + 1) / 2 : t;
+            kt += ((p.bsnd ? d->s2_max : r.klen) + kXRows - 1) / kXRows;
+        }
+        return r;
+    });
+}
+
+// required pointers and alignment; those of a side without rows may be NULL
+sag_status x_check(const sca_desc *d, const sca_io *io, const XPlan &p, bool grad, const void *ws, size_t ws_bytes) {
+    if (!io) return SAG_ERR_NULL;
+    const bool has_q = p.q_tiles > 0, has_k = p.k_tiles > 0;
+    const void *qs[] = {io->query, io->attention_out, io->softmax_lse, grad ? io->attention_out_grad : io->query,
+                        grad ? io->dq : io->query};
+    const void *ks[] = {io->key, io->value, grad ? io->dk : io->key, grad ? io->dv : io->key};
+    for (const void *x : qs)
+        if (has_q && !x) return SAG_ERR_NULL;
+    for (const void *x : ks)
+        if (has_k && !x) return SAG_ERR_NULL;
+    if (!ws || ws_bytes < p.total) return SAG_ERR_WORKSPACE;
+    auto off = [](const void *x) { return (reinterpret_cast<uintptr_t>(x) & 15) != 0; };
+    for (const void *x : qs)
+        if (has_q && off(x)) return SAG_ERR_ALIGN;
+    for (const void *x : ks)
+        if (has_k && off(x)) return SAG_ERR_ALIGN;
+    if (off(ws)) return SAG_ERR_ALIGN;
+    return SAG_OK;
+}
+
+}  // namespace
+}  // namespace sag
+
+using namespace sag;
+
+extern "C" sag_status cross_attn_fwd_workspace_size(const sca_desc *desc, size_t *workspace_bytes) {
+    if (!workspace_bytes) return SAG_ERR_NULL;
+    XPlan p;
+    const sag_status st = x_plan(desc, false, &p);
+    if (st == SAG_OK) *workspace_bytes = p.total;
+    return st;
+}
+
+extern "C" sag_status cross_attn_grad_workspace_size(const sca_desc *desc, size_t *workspace_bytes) {
+    if (!workspace_bytes) return SAG_ERR_NULL;
+    XPlan p;
+    const sag_status st = x_plan(desc, true, &p);
+    if (st == SAG_OK) *workspace_bytes = p.total;
+    return st;
+}
+
+extern "C" sag_status cross_attn_fwd(const sca_desc *desc, const sca_io *io, void *workspace, size_t workspace_bytes,
+                                     void *stream) {
+    XPlan p;
+    sag_status st = x_plan(desc, false, &p);
+    if (st != SAG_OK) return st;
+    st = x_check(desc, io, p, false, workspace, workspace_bytes);
+    if (st != SAG_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    DeviceGuard dg;
+    if (!dg.bind_memory(workspace)) return SAG_ERR_CUDA;
+    char *ws = static_cast<char *>(workspace);
+    if (p.fwd_units == 0)                   // no query rows: nothing to write, no device status
+        return cudaMemsetAsync(ws, 0, sizeof(int32_t), s) == cudaSuccess ? SAG_OK : SAG_ERR_CUDA;
+    XArgs a = x_args(desc, io, p, ws);
+    if (x_table(&a, desc, p, ws, true, s) != cudaSuccess) return SAG_ERR_CUDA;
+    a.nsplit = split_of(p.fwd_units, p.max_k, current_device_sms());
+    a.n_status = (int32_t)(p.fwd_units * a.nsplit);
+    return launch_xfwd(a, *io, *desc, (int)p.fwd_units, s) == cudaSuccess ? SAG_OK : SAG_ERR_CUDA;
+}
+
+extern "C" sag_status cross_attn_grad(const sca_desc *desc, const sca_io *io, void *workspace, size_t workspace_bytes,
+                                      void *stream) {
+    XPlan p;
+    sag_status st = x_plan(desc, true, &p);
+    if (st != SAG_OK) return st;
+    st = x_check(desc, io, p, true, workspace, workspace_bytes);
+    if (st != SAG_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    DeviceGuard dg;
+    if (!dg.bind_memory(workspace)) return SAG_ERR_CUDA;
+    char *ws = static_cast<char *>(workspace);
+    const int q_units = (int)(p.q_tiles * desc->n2), k_units = (int)(p.k_tiles * desc->n2);
+    if (k_units == 0 && cudaMemsetAsync(ws, 0, sizeof(int32_t), s) != cudaSuccess) return SAG_ERR_CUDA;
+    XArgs a = x_args(desc, io, p, ws);
+    if (x_table(&a, desc, p, ws, false, s) != cudaSuccess) return SAG_ERR_CUDA;
+    const int sms = current_device_sms();
+    if (launch_xpre(a, p.fp16, desc->d, s) != cudaSuccess) return SAG_ERR_CUDA;
+    if (q_units) {
+        a.nsplit = split_of(q_units, p.max_k, sms);
+        if (launch_xdq(a, *io, *desc, q_units, s) != cudaSuccess) return SAG_ERR_CUDA;
+        a.status += (int64_t)q_units * a.nsplit;
+    }
+    if (k_units) {
+        const int64_t before = q_units ? (int64_t)q_units * a.nsplit : 0;
+        a.nsplit = split_of(k_units, p.max_q, sms);
+        a.n_status = (int32_t)(before + (int64_t)k_units * a.nsplit);
+        if (launch_xdkv(a, *io, *desc, k_units, s) != cudaSuccess) return SAG_ERR_CUDA;
+    }
+    return SAG_OK;
+}
+
+extern "C" sag_status cross_attn_query_error(const void *workspace, void *stream) {
+    if (!workspace) return SAG_ERR_NULL;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    DeviceGuard dg;
+    if (!dg.bind_memory(workspace)) return SAG_ERR_CUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return SAG_ERR_CUDA;
+    const char *ws = static_cast<const char *>(workspace);
+    int32_t count = 0, words[1024];
+    if (cudaMemcpy(&count, ws, sizeof(count), cudaMemcpyDeviceToHost) != cudaSuccess) return SAG_ERR_CUDA;
+    for (int32_t at = 0; at < count; at += 1024) {
+        const int n = count - at < 1024 ? count - at : 1024;
+        if (cudaMemcpy(words, ws + kStatusAt + sizeof(int32_t) * (size_t)at, sizeof(int32_t) * n, cudaMemcpyDeviceToHost) !=
+            cudaSuccess)
+            return SAG_ERR_CUDA;
+        for (int i = 0; i < n; ++i)
+            if (words[i] != SAG_OK) return static_cast<sag_status>(words[i]);
+    }
+    return SAG_OK;
+}

@@ -14,9 +14,14 @@ public:
     DeviceGuard(const DeviceGuard &) = delete;
     DeviceGuard &operator=(const DeviceGuard &) = delete;
     bool bind(cudaStream_t s);
+    // The device that `ptr` lives on instead: a stream cannot be asked for its
+    // device while it is being captured, and the legacy default stream has
+    // none of its own.  False for memory that no device owns.
+    bool bind_memory(const void *ptr);
     ~DeviceGuard();
 
 private:
+    bool make_current(int dev);
     int saved_ = -1;
 };
 
