@@ -509,6 +509,11 @@ def _sag_dtype(t):
     raise SagError(SAG_ERR_DTYPE, f"tensor of {t.dtype}")
 
 
+def _torch_dtype(desc):
+    import torch
+    return torch.float16 if desc.dtype == SAG_FP16 else torch.bfloat16
+
+
 def _row_stride(name, t, heads, d):
     """Elements from one row (token) to the next of a TND or BSND tensor whose
     rows are dense; 0 for a dense tensor."""
@@ -528,37 +533,53 @@ def _row_stride(name, t, heads, d):
     return step
 
 
-def _check(name, t, like, shape, dtype=None):
-    if t.device != like.device:
-        raise ValueError(f"{name}: on {t.device}, not on {like.device}")
-    if t.dtype != (like.dtype if dtype is None else dtype):
-        raise SagError(SAG_ERR_DTYPE, f"{name}: tensor of {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+def _check_rows(name, t, shape):
+    """A tensor of the descriptor's rows: a padded batch of just its shape, or
+    packed rows, possibly with more behind them."""
+    if tuple(t.shape) == shape:
+        return
+    if len(shape) == 4 or t.dim() != 3 or tuple(t.shape[1:]) != shape[1:] or t.shape[0] < shape[0]:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} does not hold the descriptor's {shape}")
+
+
+def _check(name, t, like, shape, dtype):
+    if t.dtype != dtype:
+        raise SagError(SAG_ERR_DTYPE, f"{name}: tensor of {t.dtype}, expected {dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name}: on {t.device}, not on {like.device}")
 
 
-class _on_device:
-    """The tensors' device and the call's stream: allocations of the call come
-    from that stream's pool, and the library launches on that device."""
+def _dense(name, t, like, shape, dtype):
+    _check(name, t, like, shape, dtype)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
-    def __init__(self, device, stream):
-        import torch
-        self.torch, self.device, self.given = torch, device, stream
-        self.ctx = []
 
-    def __enter__(self):
-        cuda = self.torch.cuda
-        if self.given is not None:
-            self.ctx.append(cuda.stream(self.given))
-        elif cuda.current_device() != self.device.index:
-            self.ctx.append(cuda.device(self.device))
-        for c in self.ctx:
-            c.__enter__()
-        return (self.given if self.given is not None else cuda.current_stream(self.device)).cuda_stream
+def _with(desc, **fields):
+    """The descriptor, or a copy where a field differs (a kept one is never changed)."""
+    if all(getattr(desc, k) == v for k, v in fields.items()):
+        return desc
+    new = type(desc).from_buffer_copy(desc)
+    new.__dict__.update(desc.__dict__)
+    for k, v in fields.items():
+        setattr(new, k, v)
+    return new
 
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
+
+def _launch(device, stream, call):
+    """call(raw stream) with the tensors' device current; what the call
+    allocates comes from the pool of the stream that it runs on."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return call(torch.cuda.current_stream().cuda_stream)
+    return call(torch._C._cuda_getCurrentRawStream(device))   # a stream object costs several microseconds
 
 
 class Rotary:
@@ -598,14 +619,17 @@ class Rotary:
 
 
 def make_rotary_desc(rotary: Rotary, cu_seqlens, n1, n2, d, dtype=SAG_BF16, layout=SAG_LAYOUT_TND, s_max=0) -> SrtDesc:
-    """Descriptor of a rotation (n2 = 0: no key); keeps the host arrays alive."""
+    """Descriptor of a rotation (n2 = 0: no key); keeps the host arrays alive.
+    Its fields stay as they are once it is in use."""
     cu = _i32(cu_seqlens)
     desc = SrtDesc(batch=len(cu) - 1, n1=n1, n2=n2, d=d, d_rot=rotary.d_rot, offset=rotary.offset, style=rotary.style,
                    dtype=dtype, layout=int(layout), s_max=int(s_max),
                    cu_seqlens=ctypes.cast(cu, ctypes.POINTER(ctypes.c_int32)),
                    inv_freq=ctypes.cast(rotary._freq, ctypes.POINTER(ctypes.c_double)), magnitude=rotary.magnitude)
     desc._keep = (cu, rotary._freq)
-    desc._rows = cu[len(cu) - 1] if layout == SAG_LAYOUT_TND else desc.batch * int(s_max)
+    lead = (desc.batch, int(s_max)) if layout == SAG_LAYOUT_BSND else (cu[len(cu) - 1],)
+    desc._shapes = (lead + (n1, d), lead + (n2, d))
+    desc._dtype = _torch_dtype(desc)
     return desc
 
 
@@ -614,76 +638,50 @@ def rotary_workspace_size(desc: SrtDesc) -> int:
     return _phase1("rotary_workspace_size", desc)
 
 
-def _with(desc, **fields):
-    """The descriptor, or a copy where a field differs (a kept one is never changed)."""
-    if all(getattr(desc, k) == v for k, v in fields.items()):
-        return desc
-    new = type(desc).from_buffer_copy(desc)
-    for k in desc.__dict__:
-        setattr(new, k, desc.__dict__[k])
-    for k, v in fields.items():
-        setattr(new, k, v)
-    return new
-
-
-def _check_rows(name, t, rows, s_max):
-    """The tensor holds the descriptor's rows (a packed one, s_max None, may hold more behind them)."""
-    if s_max is not None:
-        if t.dim() != 4 or t.shape[0] * t.shape[1] != rows or t.shape[1] != s_max:
-            raise ValueError(f"{name}: shape {tuple(t.shape)} is not that of the padded batch")
-    elif t.dim() != 3 or t.shape[0] < rows:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} does not hold {rows} packed rows")
-
-
 def _rotary(entry, q, k, rotary, cu_seqlens, positions, out, workspace, stream, desc):
     import torch
     if not q.is_cuda:
         raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
-    n1, d = q.shape[-2], q.shape[-1]
+    n1, d = q.shape[-2:]
     n2 = k.shape[-2] if k is not None else 0
     if desc is None:
         bsnd = q.dim() == 4
         desc = make_rotary_desc(rotary, cu_seqlens, n1, n2, d, _sag_dtype(q), SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND,
                                 q.shape[1] if bsnd else 0)
-    elif (desc.n1, desc.n2, desc.d, desc.dtype) != (n1, n2, d, _sag_dtype(q)):
-        raise ValueError("the descriptor is of other heads, columns or type")
-    _check_rows("q", q, desc._rows, desc.s_max if desc.layout == SAG_LAYOUT_BSND else None)
-    lead = tuple(q.shape[:-2])
+    qs, ks = desc._shapes
+    dtype = desc._dtype
+    _check_rows("q", q, qs)
+    _check("q", q, q, q.shape, dtype)
     if k is not None:
-        _check("k", k, q, lead + (n2, d))
-    if positions is not None:
-        _check("positions", positions, q, lead, torch.int32)
-        if not positions.is_contiguous():
-            raise ValueError("positions must be contiguous")
-    with _on_device(q.device, stream) as handle:
+        _check("k", k, q, q.shape[:-2] + ks[-2:], dtype)
+    elif ks[-2]:
+        raise ValueError("the descriptor has a key")
+    pos = _dense("positions", positions, q, q.shape[:-2], torch.int32) if positions is not None else None
+
+    def call(handle):
         if out is None:
-            qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            ko = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k is not None else None
+            qo = torch.empty(q.shape, dtype=dtype, device=q.device)
+            ko = torch.empty(k.shape, dtype=dtype, device=q.device) if k is not None else None
         else:
             qo, ko = (out, None) if k is None and not isinstance(out, (tuple, list)) else out
-            _check("out", qo, q, q.shape)
+            _check("out", qo, q, q.shape, dtype)
             if k is not None:
-                _check("out", ko, q, k.shape)
-        strides = dict(q_stride=_row_stride("q", q, n1, d), q_out_stride=_row_stride("out", qo, n1, d))
-        io = SrtIo(query=q.data_ptr(), query_out=qo.data_ptr())
-        if k is not None:
-            strides.update(k_stride=_row_stride("k", k, n2, d), k_out_stride=_row_stride("out", ko, n2, d))
-            io.key, io.key_out = k.data_ptr(), ko.data_ptr()
-        if positions is not None:
-            io.positions = positions.data_ptr()
-        desc = _with(desc, **strides)
-        ws = None
-        if desc.batch > 64:
-            need = rotary_workspace_size(desc)
-            if need and (workspace is None or workspace.numel() < need):
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            ws = workspace.data_ptr() if need else None
-        else:
-            need = 0
-        st = getattr(_lib_neighbours(), entry)(ctypes.byref(desc), ctypes.byref(io), ws, need, handle)
-    if st != SAG_OK:
-        raise SagError(st, entry)
-    return (qo, ko) if k is not None else qo
+                _check("out", ko, q, k.shape, dtype)
+        use = _with(desc, q_stride=_row_stride("q", q, n1, d), q_out_stride=_row_stride("out", qo, n1, d),
+                    k_stride=_row_stride("k", k, n2, d) if n2 else 0,
+                    k_out_stride=_row_stride("out", ko, n2, d) if n2 else 0)
+        io = SrtIo(q.data_ptr(), k.data_ptr() if n2 else None, pos, qo.data_ptr(), ko.data_ptr() if n2 else None)
+        ws, need = workspace, 0
+        if use.batch > 64:          # smaller tables travel with the launch
+            need = rotary_workspace_size(use)
+            if ws is None or ws.numel() < need:
+                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        st = getattr(_lib_neighbours(), entry)(use, io, ws.data_ptr() if need else None, need, handle)
+        if st != SAG_OK:
+            raise SagError(st, entry)
+        return (qo, ko) if k is not None else qo
+
+    return _launch(q.get_device(), stream, call)
 
 
 def rotary_forward(q, k, rotary, cu_seqlens=None, positions=None, out=None, workspace=None, stream=None, desc=None):
@@ -706,7 +704,8 @@ def rotary_backward(dq, dk, rotary, cu_seqlens=None, positions=None, out=None, w
 
 def make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, dtype=SAG_BF16, layout=SAG_LAYOUT_TND, s1_max=0,
                     s2_max=0) -> ScaDesc:
-    """Descriptor of a cross attention; keeps the host arrays alive."""
+    """Descriptor of a cross attention; keeps the host arrays alive.  Its fields
+    stay as they are once it is in use."""
     cq, ck = _i32(cu_seqlens_q), _i32(cu_seqlens_kv)
     if len(cq) != len(ck):
         raise ValueError("cu_seqlens_q and cu_seqlens_kv are of different batches")
@@ -715,7 +714,9 @@ def make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, dtype=SAG_BF1
                    cu_seqlens_kv=ctypes.cast(ck, ctypes.POINTER(ctypes.c_int32)), s1_max=int(s1_max), s2_max=int(s2_max))
     desc._keep = (cq, ck)
     bsnd = layout == SAG_LAYOUT_BSND
-    desc._rows = (desc.batch * int(s1_max) if bsnd else cq[len(cq) - 1], desc.batch * int(s2_max) if bsnd else ck[len(ck) - 1])
+    desc._shapes = (((desc.batch, int(s1_max)) if bsnd else (cq[len(cq) - 1],)) + (n1, d),
+                    ((desc.batch, int(s2_max)) if bsnd else (ck[len(ck) - 1],)) + (n2, d))
+    desc._dtype = _torch_dtype(desc)
     return desc
 
 
@@ -735,12 +736,13 @@ def cross_query_error(workspace, stream) -> int:
 
 
 def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, workspace, stream, check, desc, tensors):
-    """Shared by the two directions: ``tensors(lead1, lead2, n1, n2, d)`` gives
-    the remaining sca_io pointers and the outputs."""
+    """Shared by the two directions: ``tensors(io, dtype)`` fills in the
+    remaining sca_io pointers and gives the outputs."""
     import torch
     if not q.is_cuda:
         raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
-    n1, d, n2 = q.shape[-2], q.shape[-1], k.shape[-2]
+    n1, d = q.shape[-2:]
+    n2 = k.shape[-2]
     if desc is None:
         bsnd = q.dim() == 4
         if bsnd and k.dim() != 4:
@@ -748,40 +750,36 @@ def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, w
         desc = make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, _sag_dtype(q),
                                SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND, q.shape[1] if bsnd else 0,
                                k.shape[1] if bsnd else 0)
-    elif (desc.n1, desc.n2, desc.d, desc.dtype) != (n1, n2, d, _sag_dtype(q)):
-        raise ValueError("the descriptor is of other heads, columns or type")
-    bsnd = desc.layout == SAG_LAYOUT_BSND
-    _check_rows("q", q, desc._rows[0], desc.s1_max if bsnd else None)
-    _check_rows("k", k, desc._rows[1], desc.s2_max if bsnd else None)
-    lead1, lead2 = tuple(q.shape[:-2]), tuple(k.shape[:-2])
-    _check("k", k, q, lead2 + (n2, d))
-    _check("v", v, q, lead2 + (n2, d))
-    desc = _with(desc, q_stride=_row_stride("q", q, n1, d), k_stride=_row_stride("k", k, n2, d),
-                 v_stride=_row_stride("v", v, n2, d))
-    io = ScaIo(query=q.data_ptr(), key=k.data_ptr(), value=v.data_ptr())
+    dtype = desc._dtype
+    _check_rows("q", q, desc._shapes[0])
+    _check_rows("k", k, desc._shapes[1])
+    _check("q", q, q, q.shape, dtype)
+    _check("k", k, q, k.shape, dtype)
+    _check("v", v, q, k.shape, dtype)
+    use = _with(desc, q_stride=_row_stride("q", q, n1, d), k_stride=_row_stride("k", k, n2, d),
+                v_stride=_row_stride("v", v, n2, d))
+    io = ScaIo(q.data_ptr(), k.data_ptr(), v.data_ptr())
     if key_mask is not None:
-        if key_mask.dtype not in (torch.bool, torch.uint8) or not key_mask.is_contiguous():
-            raise ValueError("key_mask must be a contiguous bool or uint8 tensor")
-        _check("key_mask", key_mask, q, lead2, key_mask.dtype)
-        io.key_mask = key_mask.data_ptr()
-    with _on_device(q.device, stream) as handle:
-        outs = tensors(io, lead1 + (n1, d), lead2 + (n2, d))
-        need = size(desc)
-        if workspace is None or workspace.numel() < need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        st = getattr(_lib_neighbours(), entry)(ctypes.byref(desc), ctypes.byref(io), workspace.data_ptr(), need, handle)
+        if key_mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("key_mask must be a bool or uint8 tensor")
+        io.key_mask = _dense("key_mask", key_mask, q, k.shape[:-2], key_mask.dtype)
+
+    def call(handle):
+        outs = tensors(io, dtype)
+        need = desc.__dict__.get(entry)
+        if need is None:
+            need = desc.__dict__[entry] = size(desc)
+        ws = workspace
+        if ws is None or ws.numel() < need:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        st = getattr(_lib_neighbours(), entry)(use, io, ws.data_ptr(), need, handle)
         if st == SAG_OK and check:
-            st = cross_query_error(workspace.data_ptr(), handle)
-    if st != SAG_OK:
-        raise SagError(st, entry)
-    return outs
+            st = cross_query_error(ws.data_ptr(), handle)
+        if st != SAG_OK:
+            raise SagError(st, entry)
+        return outs
 
-
-def _dense(name, t, like, shape, dtype=None):
-    _check(name, t, like, shape, dtype)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    return _launch(q.get_device(), stream, call)
 
 
 def cross_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, key_mask=None, out=None, workspace=None,
@@ -795,12 +793,12 @@ def cross_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, ke
     ``desc`` (make_cross_desc) replaces cu_seqlens_* and scale; ``check`` reads
     the device status back (this synchronizes the stream).
     """
-    def tensors(io, s1, s2):
+    def tensors(io, dtype):
         import torch
-        o, lse = out if out is not None else (torch.empty(s1, dtype=q.dtype, device=q.device),
-                                              torch.empty(s1[:-1], dtype=torch.float32, device=q.device))
-        io.attention_out = _dense("attention_out", o, q, s1)
-        io.softmax_lse = _dense("softmax_lse", lse, q, s1[:-1], torch.float32)
+        o, lse = out if out is not None else (torch.empty(q.shape, dtype=dtype, device=q.device),
+                                              torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device))
+        io.attention_out = _dense("attention_out", o, q, q.shape, dtype)
+        io.softmax_lse = _dense("softmax_lse", lse, q, q.shape[:-1], torch.float32)
         return o, lse
 
     return _cross("cross_attn_fwd", cross_fwd_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,
@@ -811,13 +809,14 @@ def cross_backward(q, k, v, o, dy, lse, cu_seqlens_q=None, cu_seqlens_kv=None, s
                    workspace=None, stream=None, check=False, desc=None):
     """Gradient of ``cross_forward``: returns (dq, dk, dv), from the forward's o
     and lse and the gradient dy of o; the other arguments as there."""
-    def tensors(io, s1, s2):
+    def tensors(io, dtype):
         import torch
-        io.attention_out = _dense("o", o, q, s1)
-        io.attention_out_grad = _dense("dy", dy, q, s1)
-        io.softmax_lse = _dense("lse", lse, q, s1[:-1], torch.float32)
-        outs = out if out is not None else tuple(torch.empty(s, dtype=q.dtype, device=q.device) for s in (s1, s2, s2))
-        io.dq, io.dk, io.dv = (_dense(n, t, q, s) for n, t, s in zip(("dq", "dk", "dv"), outs, (s1, s2, s2)))
+        io.attention_out = _dense("o", o, q, q.shape, dtype)
+        io.attention_out_grad = _dense("dy", dy, q, q.shape, dtype)
+        io.softmax_lse = _dense("lse", lse, q, q.shape[:-1], torch.float32)
+        shapes = (q.shape, k.shape, k.shape)
+        outs = out if out is not None else tuple(torch.empty(s, dtype=dtype, device=q.device) for s in shapes)
+        io.dq, io.dk, io.dv = (_dense(n, t, q, s, dtype) for n, t, s in zip(("dq", "dk", "dv"), outs, shapes))
         return outs
 
     return _cross("cross_attn_grad", cross_grad_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,

@@ -13,6 +13,7 @@
 namespace sag {
 
 constexpr int kXRows = 128;             // rows of a query tile, keys of a key tile
+constexpr int kMaxSplit = 8;             // CTAs of a cluster
 constexpr int kXThreads = 320;          // warps 0-7 softmax and epilogue, 8 TMA, 9 MMA
 constexpr uint64_t kXWaitNs = 2000000000ull;
 // A half keeps 11 bits down to 2^-14 only, and a probability of a long sequence lies below that.  Both passes shift
@@ -98,18 +99,23 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  : "memory");
 }
 
+// Registers of the calling warpgroup; the shares of a block stay within what it was launched with.
+template <int n> __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n)); }
+template <int n> __device__ __forceinline__ void regs_fewer() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n)); }
+
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // address of the same shared-memory variable in CTA `rank` of the cluster
 __device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, int rank) {
     uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
     return a;
 }
+// (no memory clobber: the reads of several ranks overlap; cluster_sync has one)
 __device__ __forceinline__ float2 peer_ld2(uint32_t a) {
     float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
     return v;
 }
 
@@ -161,16 +167,15 @@ __device__ __forceinline__ uint32_t xpack(float a, float b) {
 // run at the same time read the same keys (or queries) from L2.
 struct XUnit {
     SeqRow seq;
-    int head, tile;
+    int b, head, tile;
     int64_t tile_id;                    // (tiles of the sequences before + tile) * n2 + head
 };
 template <int32_t SeqRow::*field>
 __device__ __forceinline__ XUnit x_decode(const XArgs &A, int unit) {
-    const SeqRow *tab = A.seq.rows();
-    const int b = seq_find<field>(tab, A.seq.batch, unit / A.n2);
     XUnit x;
-    x.seq = tab[b];
-    const int first = tab[b].*field, nt = tab[b + 1].*field - first;
+    x.b = seq_find<field>(A.seq, unit / A.n2);
+    x.seq = seq_row(A.seq, x.b);
+    const int first = x.seq.*field, nt = seq_get<field>(A.seq, x.b + 1) - first;
     const int local = unit - first * A.n2;
     x.head = local / nt;
     x.tile = local % nt;
@@ -208,24 +213,17 @@ __device__ __forceinline__ KeyBits key_bits(const uint8_t *mask, const SeqRow &s
 // probability of 0 does not cancel a NaN.  Collective over the MMA warp.
 template <int kChunks>
 __device__ __forceinline__ void zero_rows(uint8_t *tile, const KeyBits &k, int lane) {
+    // eight lanes a row, four rows a step, every step independent of the others
+    uint8_t *at = tile + (lane >> 3) * 128 + (lane & 7) * 16;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        uint32_t dead = ~k.w[j];
-        while (dead) {
-            // up to four dead rows at a time, eight lanes a row
-            int row = -1;
+        if (k.w[j] == 0xffffffffu) continue;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (!dead) break;
-                const int r = __ffs(dead) - 1;
-                dead &= dead - 1;
-                if ((lane >> 3) == i) row = 32 * j + r;
-            }
-            if (row >= 0)
+        for (int i = 0; i < 8; ++i)
+            if (!((k.w[j] >> (4 * i + (lane >> 3))) & 1u))
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c)
-                    *reinterpret_cast<uint4 *>(tile + c * 16384 + row * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
+                    *reinterpret_cast<uint4 *>(at + c * 16384 + (32 * j + 4 * i) * 128) = make_uint4(0, 0, 0, 0);
     }
     tc::fence_proxy_async_smem();
     __syncwarp();
@@ -241,10 +239,10 @@ __device__ __forceinline__ void mma_abt(uint32_t acc, uint32_t a, uint32_t b, ui
                             tc::sw128_desc(b + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024), idesc, kk > 0);
 }
 // A [128 x 128] in TMEM (16-bit pairs; the second half of K starts `gap` columns after the first), B [128 x D] MN-major.
-template <int kGap>
+template <int kGap, int kFrom = 0, int kTo = 8>
 __device__ __forceinline__ void mma_ab(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
+    for (int kk = kFrom; kk < kTo; ++kk)
         mma_f16_ts_warp(acc, a + (kk >> 2) * kGap + (kk & 3) * 8, tc::sw128_desc(b + kk * 2048, 16384, 1024), idesc,
                         accumulate || kk > 0);
 }

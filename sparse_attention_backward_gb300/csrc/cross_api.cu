@@ -68,11 +68,11 @@ sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {
     return SAG_OK;
 }
 
-// CTAs that share a unit: while SMs are idle, as long as each still has two tiles of the loop
+// CTAs that share a unit: while SMs are idle, as long as each has a tile of the loop
 int split_of(int64_t units, int tiles, int sms) {
     if (sms > kSplitCtas) sms = kSplitCtas;
     int ns = 1;
-    while (ns < 8 && units * ns * 2 <= sms && tiles >= 4 * ns) ns *= 2;
+    while (ns < kMaxSplit && units * ns * 2 <= sms && tiles >= 2 * ns) ns *= 2;
     return ns;
 }
 

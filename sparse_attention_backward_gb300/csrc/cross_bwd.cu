@@ -179,16 +179,19 @@ __device__ __forceinline__ void join_rows(float *xo, int rows, int ns, int rank,
     for (int k = rank + ns * warp; k < rows; k += ns * 8) {
         uint16_t *dst = out(k);
         if (!dst) continue;
-        float2 acc[E] = {};
-        for (int p = 0; p < ns; ++p) {
-            const uint32_t a = peer_addr(tc::smem_u32(xo + k * (D + 4) + lane * 2), p);
+        float2 y[kMaxSplit][E], acc[E] = {};
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float2 y = peer_ld2(a + e * 256);
-                acc[e].x += y.x;
-                acc[e].y += y.y;
+        for (int p = 0; p < kMaxSplit; ++p)
+            if (p < ns) {
+                const uint32_t a = peer_addr(tc::smem_u32(xo + k * (D + 4) + lane * 2), p);
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[p][e] = peer_ld2(a + e * 256);
             }
-        }
+#pragma unroll
+        for (int p = 0; p < kMaxSplit; ++p)
+            if (p < ns)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = add2(acc[e], y[p][e]);
         const float f = mul(k);
 #pragma unroll
         for (int e = 0; e < E; ++e)
@@ -221,20 +224,25 @@ __global__ void __launch_bounds__(kXThreads, 1)
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
     }
+    if (threadIdx.x == 256) {
+        tc::prefetch_tmap(&map_q);
+        tc::prefetch_tmap(&map_dy);
+        tc::prefetch_tmap(&map_k);
+        tc::prefetch_tmap(&map_v);
+    }
+    const int ns = A.nsplit, rank = blockIdx.x % ns;
+    const XUnit u = x_decode<&SeqRow::qtile0>(A, blockIdx.x / ns);
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot, sbase = tc::smem_u32(smem);
-    const int ns = A.nsplit, rank = blockIdx.x % ns;
-    const XUnit u = x_decode<&SeqRow::qtile0>(A, blockIdx.x / ns);
     const int G = A.group, tok0 = u.tile * A.tpt;
     const int cover = A.s1_pad ? A.s1_pad : u.seq.qlen;
     const int nkt = tok0 < u.seq.qlen ? (u.seq.klen + kXRows - 1) / kXRows : 0;
     const int t0 = (int)((int64_t)nkt * rank / ns), n = (int)((int64_t)nkt * (rank + 1) / ns) - t0;
     float up = 0.f;                                      // exponent that dS is scaled by
     if constexpr (kFp16) {
-        const SeqRow *next = A.seq.rows() + (seq_find<&SeqRow::qtile0>(A.seq.rows(), A.seq.batch, blockIdx.x / ns / A.n2) + 1);
-        up = ds_exponent(A, u.seq, *next, u.head, reinterpret_cast<float *>(smem + L::OFF_STAT));
+        up = ds_exponent(A, u.seq, seq_row(A.seq, u.b + 1), u.head, reinterpret_cast<float *>(smem + L::OFF_STAT));
     }
     auto fail = [&]() { *abort_flag = 1; };
 
@@ -454,21 +462,25 @@ __global__ void __launch_bounds__(kXThreads, 1)
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
     }
+    if (threadIdx.x == 256) {
+        tc::prefetch_tmap(&map_q);
+        tc::prefetch_tmap(&map_dy);
+        tc::prefetch_tmap(&map_k);
+        tc::prefetch_tmap(&map_v);
+    }
+    const int ns = A.nsplit, rank = blockIdx.x % ns;
+    const XUnit u = x_decode<&SeqRow::ktile0>(A, blockIdx.x / ns);
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot, sbase = tc::smem_u32(smem);
-    const int ns = A.nsplit, rank = blockIdx.x % ns;
-    const XUnit u = x_decode<&SeqRow::ktile0>(A, blockIdx.x / ns);
-    const SeqRow *tab = A.seq.rows();
     const int G = A.group, key0 = u.tile * kXRows;
     const int cover = A.s2_pad ? A.s2_pad : u.seq.klen;
     const int nqt = key0 < u.seq.klen ? (u.seq.qlen + A.tpt - 1) / A.tpt : 0;
     const int t0 = (int)((int64_t)nqt * rank / ns), n = (int)((int64_t)nqt * (rank + 1) / ns) - t0;
     float up = 0.f;
     if constexpr (kFp16) {
-        const int b = seq_find<&SeqRow::ktile0>(tab, A.seq.batch, blockIdx.x / ns / A.n2);
-        up = ds_exponent(A, u.seq, tab[b + 1], u.head, reinterpret_cast<float *>(smem + L::OFF_STAT));
+        up = ds_exponent(A, u.seq, seq_row(A.seq, u.b + 1), u.head, reinterpret_cast<float *>(smem + L::OFF_STAT));
         __syncthreads();                                 // the scratch becomes the ring of statistics
     }
     auto fail = [&]() { *abort_flag = 1; };
@@ -719,7 +731,7 @@ template <bool kFp16, int D>
 cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, bool dkv, int units, cudaStream_t s) {
     BwdMaps m;
     if (!maps(&m, a, io, d)) return cudaErrorInvalidValue;
-    return x_launch(dkv ? k_xdkv<kFp16, D> : k_xdq<kFp16, D>, units * a.nsplit, a.nsplit, BwdSmem<D>::TOTAL, s, m.q, m.dy,
+    return x_launch(dkv ? k_xdkv<kFp16, D> : k_xdq<kFp16, D>, units * a.nsplit, kXThreads, a.nsplit, BwdSmem<D>::TOTAL, s, m.q, m.dy,
                     m.k, m.v, a);
 }
 

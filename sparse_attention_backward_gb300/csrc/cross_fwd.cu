@@ -29,6 +29,10 @@ namespace sag {
 
 namespace {
 
+// warps 0-3 and 4-7: softmax and epilogue of the two tiles, 8: TMA, 9: MMA, 10-11: none (a warpgroup's registers are
+// handed over as a whole: 2 * 208 + 88 = 3 * 168, what the block is launched with)
+constexpr int kFwdThreads = 384;
+
 template <int D>
 struct FwdSmem {
     static constexpr int KC = D / 64;
@@ -41,10 +45,11 @@ struct FwdSmem {
     static constexpr int XROW = D + 4;                            // exchange rows, padded against bank conflicts
     static_assert(2 * kXRows * XROW * 4 <= OFF_ML, "the exchange overlays Q and the ring");
 };
-enum { XF_Q = 0, XF_S = 1, XF_P = 3, XF_DRAIN = 5, XF_FULL = 6 };
+// XF_P: per tile, one barrier for each half of its probabilities
+enum { XF_Q = 0, XF_S = 1, XF_P = 3, XF_DRAIN = 7, XF_FULL = 8 };
 
 template <bool kFp16, int D>
-__global__ void __launch_bounds__(kXThreads, 1)
+__global__ void __launch_bounds__(kFwdThreads, 1)
     k_xfwd(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
            const __grid_constant__ CUtensorMap map_v, const __grid_constant__ XArgs A) {
     using L = FwdSmem<D>;
@@ -61,7 +66,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
         tc::mbar_init(&bars[XF_Q], 1);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars[XF_S + i], 1);
-            tc::mbar_init(&bars[XF_P + i], 128);
+            tc::mbar_init(&bars[XF_P + 2 * i], 128);
+            tc::mbar_init(&bars[XF_P + 2 * i + 1], 128);
         }
         tc::mbar_init(&bars[XF_DRAIN], 1);
         for (int i = 0; i < ST; ++i) {
@@ -74,13 +80,18 @@ __global__ void __launch_bounds__(kXThreads, 1)
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
     }
+    if (threadIdx.x == 256) {
+        tc::prefetch_tmap(&map_q);
+        tc::prefetch_tmap(&map_k);
+        tc::prefetch_tmap(&map_v);
+    }
+    const int ns = A.nsplit, rank = blockIdx.x % ns;
+    const XUnit u = x_decode<&SeqRow::qtile0>(A, blockIdx.x / ns);
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t sbase = tc::smem_u32(smem);
-    const int ns = A.nsplit, rank = blockIdx.x % ns;
-    const XUnit u = x_decode<&SeqRow::qtile0>(A, blockIdx.x / ns);
     const int G = A.group;
     const int cover = A.s1_pad ? A.s1_pad : u.seq.qlen;
     const int tok0[2] = {u.tile * 2 * A.tpt, (u.tile * 2 + 1) * A.tpt};
@@ -89,6 +100,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const int t0 = (int)((int64_t)nkt * rank / ns), n = (int)((int64_t)nkt * (rank + 1) / ns) - t0;
     auto fail = [&]() { *abort_flag = 1; };
 
+    // The softmax warps take registers from the others.  The two sides share no code up to the end of the kernel: what
+    // both run must fit the smaller number.
+    if (warp >= 8) {
+    regs_fewer<88>();
     if (warp == 8) {
         // ------------------------------------------------------ TMA producer
         if (lane == 0 && n > 0) {
@@ -130,6 +145,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             return __all_sync(0xffffffffu, tc::mbar_wait(b, parity, abort_flag, kXWaitNs));
         };
         const uint32_t ring = sbase + L::OFF_RING;
+        KeyBits next = key_bits(A.mask, u.seq, t0 * kXRows, lane);
         bool ok = n == 0 || wait(&bars[XF_Q], 0);
         if (ok && n > 0) ok = wait(&full[0], 0);
         if (ok && n > 0) {
@@ -144,15 +160,20 @@ __global__ void __launch_bounds__(kXThreads, 1)
         for (int i = 0; i < n && ok; ++i) {
             const int sv = (2 * i + 1) % ST, uv = (2 * i + 1) / ST;
             const int sk = (2 * i + 2) % ST, uk = (2 * i + 2) / ST;
-            const KeyBits kb = key_bits(A.mask, u.seq, (t0 + i) * kXRows, lane);
             if (!wait(&full[sv], uv & 1)) { ok = false; break; }
+            const KeyBits kb = next;
+            if (i + 1 < n) next = key_bits(A.mask, u.seq, (t0 + i + 1) * kXRows, lane);
             if (!kb.all()) zero_rows<L::KC>(smem + L::OFF_RING + sv * L::TILE, kb, lane);
             const bool more = i + 1 < n;
             for (int sl = 0; sl < 2; ++sl) {
                 if (!active[sl]) continue;
-                if (!wait(&bars[XF_P + sl], i & 1)) { ok = false; break; }
+                // the first half of the keys while the softmax forms the second half's probabilities
+                if (!wait(&bars[XF_P + 2 * sl], i & 1)) { ok = false; break; }
                 tc::tc_fence_after();
-                mma_ab<32>(tmem + 256 + sl * 128, tmem + sl * 128, ring + sv * L::TILE, id_o, i > 0);
+                mma_ab<32, 0, 4>(tmem + 256 + sl * 128, tmem + sl * 128, ring + sv * L::TILE, id_o, i > 0);
+                if (!wait(&bars[XF_P + 2 * sl + 1], i & 1)) { ok = false; break; }
+                tc::tc_fence_after();
+                mma_ab<32, 4, 8>(tmem + 256 + sl * 128, tmem + sl * 128, ring + sv * L::TILE, id_o, true);
                 if (more) {
                     if (sl == 0 && !wait(&full[sk], uk & 1)) { ok = false; break; }
                     tc::tc_fence_after();
@@ -170,11 +191,18 @@ __global__ void __launch_bounds__(kXThreads, 1)
         if (!__all_sync(0xffffffffu, tc::mbar_wait_drain(&bars[XF_DRAIN], 0, kXWaitNs)) && lane == 0) fail();
     }
 
+    if (ns > 1) {                                        // as below
+        __syncthreads();
+        cluster_sync();
+        cluster_sync();
+    }
+    } else {
+    regs_more<208>();
     const int sl = warp >> 2;                            // softmax warps: their tile
     const int r = (warp & 3) * 32 + lane;                // query row = TMEM lane
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     float m = -INFINITY, l = 0.f;                        // reference maximum (log2 units), sum
-    if (warp < 8 && active[sl] && n > 0) {
+    if (active[sl] && n > 0) {
         // ------------------------------------------------------ softmax
         const float c = A.scale_log2;
         const uint32_t ts = trow + sl * 128, to = trow + 256 + sl * 128;
@@ -194,7 +222,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
             }
             float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int j = 4; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+            for (int j = 4; j < 124; j += 8) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], x[j + e]), x[j + 4 + e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[124 + e]);
             const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
             const bool grow = mt > m + 8.f;
             if (__any_sync(0xffffffffu, grow)) {
@@ -216,25 +249,25 @@ __global__ void __launch_bounds__(kXThreads, 1)
             }
             const float base = m == -INFINITY ? 0.f : m - kShift;
             const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
-            float2 s4[2] = {};
+            float2 s4[4] = {};
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t p[16];
+            for (int h = 0; h < 2; ++h) {
+                uint32_t p[32];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float2 e = fma2(make_float2(x[h * 32 + 2 * j], x[h * 32 + 2 * j + 1]), c2, b2);
+                for (int j = 0; j < 32; ++j) {
+                    float2 e = fma2(make_float2(x[h * 64 + 2 * j], x[h * 64 + 2 * j + 1]), c2, b2);
                     e.x = xex2(e.x);
                     e.y = xex2(e.y);
-                    s4[j & 1] = add2(s4[j & 1], e);
+                    s4[j & 3] = add2(s4[j & 3], e);
                     p[j] = xpack<kFp16>(e.x, e.y);
                 }
-                tmem_st16(ts + h * 16, p);
+                tmem_st32(ts + h * 32, p);
+                tmem_wait_st();
+                tc::tc_fence_before();
+                tc::mbar_arrive(&bars[XF_P + 2 * sl + h]);
             }
-            const float2 s2 = add2(s4[0], s4[1]);
+            const float2 s2 = add2(add2(s4[0], s4[1]), add2(s4[2], s4[3]));
             l += s2.x + s2.y;
-            tmem_wait_st();
-            tc::tc_fence_before();
-            tc::mbar_arrive(&bars[XF_P + sl]);
         }
         if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[XF_S + sl], n & 1, abort_flag, kXWaitNs));
         if (!ok && lane == 0) fail();
@@ -244,7 +277,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     // ---------------------------------------------------------- epilogue
     const float kLn2 = 0.6931471805599453f;
     if (ns == 1) {
-        if (warp < 8) {
+        {
             const int tok = tok0[sl] + r / G;
             const bool mine = r < A.tpt * G && tok < cover;
             const bool pad = tok >= u.seq.qlen;
@@ -270,7 +303,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         float2 *ml = reinterpret_cast<float2 *>(smem + L::OFF_ML);
         float *xo = reinterpret_cast<float *>(smem);
         __syncthreads();                                 // all loads and products on this memory are complete
-        if (warp < 8 && active[sl]) {
+        if (active[sl]) {
             ml[sl * 128 + r] = make_float2(m, l);
             if (n > 0) {
 #pragma unroll
@@ -286,30 +319,39 @@ __global__ void __launch_bounds__(kXThreads, 1)
             }
         }
         cluster_sync();
-        if (warp < 8) {
+        {
             constexpr int E = D / 64;                    // float2 a lane and row
             for (int k = rank + ns * warp; k < 2 * kXRows; k += ns * 8) {
                 const int ks = k / kXRows, kr = k % kXRows, tok = tok0[ks] + kr / G;
                 if (kr >= A.tpt * G || tok >= cover) continue;
                 const int64_t row = (int64_t)(u.seq.q0 + tok) * A.n1 + u.head * G + kr % G;
                 const bool pad = tok >= u.seq.qlen;
-                float top = -INFINITY, sum = 0.f;
-                float2 acc[E] = {};
-                if (!pad) {
-                    for (int p = 0; p < ns; ++p)
-                        top = fmaxf(top, peer_ld2(peer_addr(tc::smem_u32(ml + k), p)).x);
-                    for (int p = 0; p < ns; ++p) {
-                        const float2 v = peer_ld2(peer_addr(tc::smem_u32(ml + k), p));
-                        if (v.y == 0.f) continue;        // nothing seen by this rank
-                        const float w = xex2(v.x - top);
-                        sum += v.y * w;
+                // lane p holds rank p's maximum and sum; a rank that saw nothing has (-inf, 0) and no O
+                float2 v = make_float2(-INFINITY, 0.f);
+                if (!pad && lane < ns) v = peer_ld2(peer_addr(tc::smem_u32(ml + k), lane));
+                float2 y[kMaxSplit][E], acc[E] = {};
+#pragma unroll
+                for (int p = 0; p < kMaxSplit; ++p)
+                    if (p < ns) {
                         const uint32_t a = peer_addr(tc::smem_u32(xo + k * L::XROW + lane * 2), p);
 #pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            const float2 y = peer_ld2(a + e * 256);
-                            acc[e].x += y.x * w;
-                            acc[e].y += y.y * w;
-                        }
+                        for (int e = 0; e < E; ++e) y[p][e] = peer_ld2(a + e * 256);
+                    }
+                float top = v.x;
+#pragma unroll
+                for (int o = kMaxSplit / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                top = __shfl_sync(0xffffffffu, top, 0);
+                const float w = v.y == 0.f ? 0.f : xex2(v.x - top);
+                float sum = 0.f;
+#pragma unroll
+                for (int p = 0; p < kMaxSplit; ++p) {
+                    const float wp = __shfl_sync(0xffffffffu, w, p), lp = __shfl_sync(0xffffffffu, v.y, p);
+                    if (wp == 0.f) continue;
+                    sum += lp * wp;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        acc[e].x += y[p][e].x * wp;
+                        acc[e].y += y[p][e].y * wp;
                     }
                 }
                 const bool some = sum > 0.f || sum != sum;
@@ -322,6 +364,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             }
         }
         cluster_sync();                                  // peers are done with this CTA's shared memory
+    }
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -341,7 +384,7 @@ cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, int unit
     if (!x_map_q(&mq, io.query, d, a, d.q_stride) || !x_map_k(&mk, io.key, io.query, d, a, d.k_stride) ||
         !x_map_k(&mv, io.value, io.query, d, a, d.v_stride))
         return cudaErrorInvalidValue;
-    return x_launch(k_xfwd<kFp16, D>, units * a.nsplit, a.nsplit, FwdSmem<D>::TOTAL, s, mq, mk, mv, a);
+    return x_launch(k_xfwd<kFp16, D>, units * a.nsplit, kFwdThreads, a.nsplit, FwdSmem<D>::TOTAL, s, mq, mk, mv, a);
 }
 
 }  // namespace

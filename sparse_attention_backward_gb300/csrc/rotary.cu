@@ -65,15 +65,14 @@ __global__ void __launch_bounds__(kRotThreads) k_rotary(const __grid_constant__ 
     const int row = (int)row64;
 
     // the row's sequence, and whether it is padding
-    const SeqRow *tab = A.seq.rows();
     int place = 0;
     bool live = true;
     if (A.s_max) {
         const int b = row / A.s_max;
         place = row - b * A.s_max;
-        live = place < tab[b].qlen;
+        live = place < seq_get<&SeqRow::qlen>(A.seq, b);
     } else if (!A.positions) {
-        place = row - tab[seq_find<&SeqRow::q0>(tab, A.seq.batch, row)].q0;
+        place = row - seq_get<&SeqRow::q0>(A.seq, seq_find<&SeqRow::q0>(A.seq, row));
     }
     const bool rot = u < A.rot_units;
     int col;                            // first column of the vector

@@ -24,17 +24,29 @@ struct SeqTab {
     int32_t batch;
     const SeqRow *ext;                  // in the workspace, or nullptr: row[]
     SeqRow row[kInlineSeqs + 1];
-    __host__ __device__ __forceinline__ const SeqRow *rows() const { return ext ? ext : row; }
 };
+
+// Row b of the table.  Two plain accesses, not one pointer: row[] is then read
+// through the constant bank (about 40 cycles), which a generic pointer into the
+// parameters is not (it cost over a thousand cycles at the start of each block).
+__device__ __forceinline__ SeqRow seq_row(const SeqTab &t, int b) {
+    if (t.ext) return t.ext[b];
+    return t.row[b];
+}
+template <int32_t SeqRow::*field>
+__device__ __forceinline__ int seq_get(const SeqTab &t, int b) {
+    if (t.ext) return t.ext[b].*field;
+    return t.row[b].*field;
+}
 
 // Last sequence whose `field` is <= x (empty sequences share their successor's
 // value, so the last one is the one that holds x).
 template <int32_t SeqRow::*field>
-__device__ __forceinline__ int seq_find(const SeqRow *t, int batch, int x) {
-    int lo = 0, hi = batch - 1;
+__device__ __forceinline__ int seq_find(const SeqTab &t, int x) {
+    int lo = 0, hi = t.batch - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (t[mid].*field <= x) lo = mid; else hi = mid - 1;
+        if (seq_get<field>(t, mid) <= x) lo = mid; else hi = mid - 1;
     }
     return lo;
 }

@@ -43,13 +43,13 @@ inline bool x_map_k(CUtensorMap *m, const void *base, const void *other, const s
 }
 
 template <class... P, class... Args>
-cudaError_t x_launch(void (*kernel)(P...), int ctas, int cluster, int smem, cudaStream_t s, const Args &...args) {
+cudaError_t x_launch(void (*kernel)(P...), int ctas, int threads, int cluster, int smem, cudaStream_t s, const Args &...args) {
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kXThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
