@@ -40,6 +40,7 @@ struct XArgs {
     int32_t n_status;                   // value for *count
 };
 
+// units: query (k_xdkv: key) tiles times key/value heads
 cudaError_t launch_xfwd(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s);
 cudaError_t launch_xpre(const XArgs &a, bool fp16, int d, cudaStream_t s);
 cudaError_t launch_xdq(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s);
@@ -48,15 +49,35 @@ cudaError_t launch_xdkv(const XArgs &a, const sca_io &io, const sca_desc &d, int
 namespace {
 
 // ---------------------------------------------------------------- PTX
-// A from TMEM (K-major: lane = row, two elements a column), B from shared memory; one elected lane issues.
-__device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                                uint32_t accumulate) {
+// Shared-memory descriptors (128-byte swizzle, 1024 bytes between groups of eight rows) as two words: the low one holds
+// the address, so a step along K is one 32-bit addition, and the high one is a constant.  Descriptors built anew for each
+// instruction were kept in registers by the compiler, and spilled: a thousand cycles a tile in the MMA warp.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+// (the mask drops the CTA's rank, which addresses carry from bit 24 on in a cluster)
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+    return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+
+// One elected lane of the (convergent) warp issues.  A and B from shared memory, or A from TMEM (K-major: lane = row, two
+// elements a column).
+__device__ __forceinline__ void xmma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void xmma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
@@ -90,6 +111,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// One arrival for a warp whose lanes have all done what the barrier stands for.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar);
+}
 
 // global -> shared copy of `bytes` (a multiple of 16, both ends 16-byte aligned)
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -233,18 +260,20 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, const KeyBits &k, int l
 // A [128 x D] K-major, B [128 x D] K-major: D columns 0..127 of the accumulator.
 template <int D>
 __device__ __forceinline__ void mma_abt(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc) {
+    const uint32_t al = desc_lo(a, 16), bl = desc_lo(b, 16);
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-        tc::mma_f16_ss_warp(acc, tc::sw128_desc(a + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
-                            tc::sw128_desc(b + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024), idesc, kk > 0);
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t step = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+        xmma_ss(acc, al + step, bl + step, idesc, kk > 0);
+    }
 }
 // A [128 x 128] in TMEM (16-bit pairs; the second half of K starts `gap` columns after the first), B [128 x D] MN-major.
 template <int kGap, int kFrom = 0, int kTo = 8>
 __device__ __forceinline__ void mma_ab(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    const uint32_t bl = desc_lo(b, 16384);
 #pragma unroll
     for (int kk = kFrom; kk < kTo; ++kk)
-        mma_f16_ts_warp(acc, a + (kk >> 2) * kGap + (kk & 3) * 8, tc::sw128_desc(b + kk * 2048, 16384, 1024), idesc,
-                        accumulate || kk > 0);
+        xmma_ts(acc, a + (kk >> 2) * kGap + (kk & 3) * 8, bl + (kk * 2048 >> 4), idesc, accumulate || kk > 0);
 }
 
 // 16-bit row piece of `n` (a multiple of 8) fp32 values

@@ -1,6 +1,7 @@
 // C ABI of the cross attention: validation and workspace sizes (phase 1),
 // sequence tables and launches (phase 2).
 #include <math.h>
+#include <stdlib.h>
 
 #include "cross.cuh"
 #include "kernels.cuh"
@@ -18,7 +19,7 @@ constexpr int64_t kSplitCtas = 1024;
 struct XPlan {
     bool fp16, bsnd;
     int tpt;
-    int64_t fwd_units, q_tiles, k_tiles;    // query tile pairs, query tiles, key tiles (of all sequences, padding included)
+    int64_t q_tiles, k_tiles;               // query and key tiles of all sequences, padding included
     int max_q, max_k;                       // most query / key tiles of one sequence that have work
     size_t o_seq, o_stats, o_norms, total;
 };
@@ -42,24 +43,22 @@ sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {
     p->fp16 = d->dtype == SAG_FP16;
     p->bsnd = d->layout == SAG_LAYOUT_BSND;
     p->tpt = kXRows / (d->n1 / d->n2);
-    p->fwd_units = p->q_tiles = p->k_tiles = 0;
+    p->q_tiles = p->k_tiles = 0;
     p->max_q = p->max_k = 0;
     for (int b = 0; b < d->batch; ++b) {
         const int ql = d->cu_seqlens_q[b + 1] - d->cu_seqlens_q[b], kl = d->cu_seqlens_kv[b + 1] - d->cu_seqlens_kv[b];
         const int qt = ((p->bsnd ? d->s1_max : ql) + p->tpt - 1) / p->tpt;
         const int kt = ((p->bsnd ? d->s2_max : kl) + kXRows - 1) / kXRows;
-        p->fwd_units += (qt + 1) / 2;
         p->q_tiles += qt;
         p->k_tiles += kt;
         const int qw = (ql + p->tpt - 1) / p->tpt, kw = (kl + kXRows - 1) / kXRows;
         if (qw > p->max_q) p->max_q = qw;
         if (kw > p->max_k) p->max_k = kw;
     }
-    p->fwd_units *= d->n2;
     size_t o = 0;
     auto take = [&](size_t bytes) { const size_t at = o; o = up256(o + bytes); return at; };
     take(kStatusAt);                        // header: number of status words
-    const int64_t ctas = grad ? (p->q_tiles + p->k_tiles) * d->n2 + 2 * kSplitCtas : p->fwd_units + kSplitCtas;
+    const int64_t ctas = grad ? (p->q_tiles + p->k_tiles) * d->n2 + 2 * kSplitCtas : p->q_tiles * d->n2 + kSplitCtas;
     take(sizeof(int32_t) * ctas);           // status words, one a CTA
     p->o_seq = take(seq_ws_bytes(d->batch));
     p->o_stats = take(grad ? sizeof(float) * 256 * p->q_tiles * d->n2 : 0);
@@ -69,10 +68,10 @@ sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {
 }
 
 // CTAs that share a unit: while SMs are idle, as long as each has a tile of the loop
-int split_of(int64_t units, int tiles, int sms) {
-    if (sms > kSplitCtas) sms = kSplitCtas;
+int split_of(int64_t units, int tiles, int room) {
+    if (room > kSplitCtas) room = kSplitCtas;
     int ns = 1;
-    while (ns < kMaxSplit && units * ns * 2 <= sms && tiles >= 2 * ns) ns *= 2;
+    while (ns < kMaxSplit && units * ns * 2 <= room && tiles >= 2 * ns) ns *= 2;
     return ns;
 }
 
@@ -106,8 +105,7 @@ XArgs x_args(const sca_desc *d, const sca_io *io, const XPlan &p, char *ws) {
     return a;
 }
 
-// rows of the table; `pairs`: query tiles counted in pairs (the forward's units)
-cudaError_t x_table(XArgs *a, const sca_desc *d, const XPlan &p, char *ws, bool pairs, cudaStream_t s) {
+cudaError_t x_table(XArgs *a, const sca_desc *d, const XPlan &p, char *ws, cudaStream_t s) {
     int qt = 0, kt = 0;
     return fill_seq_tab(&a->seq, d->batch, reinterpret_cast<SeqRow *>(ws + p.o_seq), s, [&](int b) {
         SeqRow r{};
@@ -118,8 +116,7 @@ cudaError_t x_table(XArgs *a, const sca_desc *d, const XPlan &p, char *ws, bool 
         if (b < d->batch) {
             r.qlen = d->cu_seqlens_q[b + 1] - d->cu_seqlens_q[b];
             r.klen = d->cu_seqlens_kv[b + 1] - d->cu_seqlens_kv[b];
-            const int t = ((p.bsnd ? d->s1_max : r.qlen) + p.tpt - 1) / p.tpt;
-            qt += pairs ? (t + 1) / 2 : t;
+            qt += ((p.bsnd ? d->s1_max : r.qlen) + p.tpt - 1) / p.tpt;
             kt += ((p.bsnd ? d->s2_max : r.klen) + kXRows - 1) / kXRows;
         }
         return r;
@@ -179,13 +176,15 @@ extern "C" sag_status cross_attn_fwd(const sca_desc *desc, const sca_io *io, voi
     DeviceGuard dg;
     if (!dg.bind_memory(workspace)) return SAG_ERR_CUDA;
     char *ws = static_cast<char *>(workspace);
-    if (p.fwd_units == 0)                   // no query rows: nothing to write, no device status
+    if (p.q_tiles == 0)                     // no query rows: nothing to write, no device status
         return cudaMemsetAsync(ws, 0, sizeof(int32_t), s) == cudaSuccess ? SAG_OK : SAG_ERR_CUDA;
     XArgs a = x_args(desc, io, p, ws);
-    if (x_table(&a, desc, p, ws, true, s) != cudaSuccess) return SAG_ERR_CUDA;
-    a.nsplit = split_of(p.fwd_units, p.max_k, current_device_sms());
-    a.n_status = (int32_t)(p.fwd_units * a.nsplit);
-    return launch_xfwd(a, *io, *desc, (int)p.fwd_units, s) == cudaSuccess ? SAG_OK : SAG_ERR_CUDA;
+    if (x_table(&a, desc, p, ws, s) != cudaSuccess) return SAG_ERR_CUDA;
+    const int units = (int)(p.q_tiles * desc->n2);
+    a.nsplit = split_of(units, p.max_k, 2 * current_device_sms());   // two CTAs an SM
+    const char *e = getenv("XSPLIT"); if (e) a.nsplit = atoi(e);
+    a.n_status = units * a.nsplit;
+    return launch_xfwd(a, *io, *desc, units, s) == cudaSuccess ? SAG_OK : SAG_ERR_CUDA;
 }
 
 extern "C" sag_status cross_attn_grad(const sca_desc *desc, const sca_io *io, void *workspace, size_t workspace_bytes,
@@ -202,7 +201,7 @@ extern "C" sag_status cross_attn_grad(const sca_desc *desc, const sca_io *io, vo
     const int q_units = (int)(p.q_tiles * desc->n2), k_units = (int)(p.k_tiles * desc->n2);
     if (k_units == 0 && cudaMemsetAsync(ws, 0, sizeof(int32_t), s) != cudaSuccess) return SAG_ERR_CUDA;
     XArgs a = x_args(desc, io, p, ws);
-    if (x_table(&a, desc, p, ws, false, s) != cudaSuccess) return SAG_ERR_CUDA;
+    if (x_table(&a, desc, p, ws, s) != cudaSuccess) return SAG_ERR_CUDA;
     const int sms = current_device_sms();
     if (launch_xpre(a, p.fp16, desc->d, s) != cudaSuccess) return SAG_ERR_CUDA;
     if (q_units) {

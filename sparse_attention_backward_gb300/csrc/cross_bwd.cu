@@ -22,6 +22,8 @@
 //
 // Few tiles: a cluster's CTAs split the loop and join their accumulators
 // through distributed shared memory, in rank order.
+#include <type_traits>
+
 #include "cross.cuh"
 #include "kernels.cuh"
 #include "xtmap.cuh"
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        for (int i = 0; i < XB_RING; ++i) tc::mbar_init(&bars[i], i == XB_DS || i == XB_PF ? 256 : 1);
+        for (int i = 0; i < XB_RING; ++i) tc::mbar_init(&bars[i], i == XB_DS || i == XB_PF ? 8 : 1);   // one arrival a warp
         for (int i = 0; i < 2 * (L::RA + L::RB); ++i) tc::mbar_init(&ra.full[i], 1);
         tc::fence_mbar_init();
     }
@@ -284,36 +286,51 @@ __global__ void __launch_bounds__(kXThreads, 1)
         auto wait = [&](uint64_t *b, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, tc::mbar_wait(b, parity, abort_flag, kXWaitNs));
         };
-        auto issue_s = [&](int i) -> bool {
-            const int s = i % L::RA;
-            if (!wait(&ra.full[s], (i / L::RA) & 1)) return false;
+        // a product is issued behind its tile's wait, which another product's queue hides (see the forward)
+        auto wait_k = [&](int i) { return wait(&ra.full[i % L::RA], (i / L::RA) & 1); };
+        auto wait_v = [&](int i) { return wait(&rb.full[i % L::RB], (i / L::RB) & 1); };
+        auto issue_s = [&](int i) {
             tc::tc_fence_after();
-            mma_abt<D>(tmem + (i & 1) * 128, sbase + L::OFF_X, sbase + L::OFF_A + s * L::TILE, id_s);
+            mma_abt<D>(tmem + (i & 1) * 128, sbase + L::OFF_X, sbase + L::OFF_A + i % L::RA * L::TILE, id_s);
             tc::mma_commit_warp(&bars[XB_S + (i & 1)]);
-            return true;
         };
-        auto issue_dp = [&](int i) -> bool {
-            const int s = i % L::RB;
-            if (!wait(&rb.full[s], (i / L::RB) & 1)) return false;
+        auto issue_dp = [&](int i) {
             tc::tc_fence_after();
-            mma_abt<D>(tmem + 256, sbase + L::OFF_Y, sbase + L::OFF_B + s * L::TILE, id_s);
+            mma_abt<D>(tmem + 256, sbase + L::OFF_Y, sbase + L::OFF_B + i % L::RB * L::TILE, id_s);
             tc::mma_commit_warp(&bars[XB_DP]);
-            tc::mma_commit_warp(&rb.empty[s]);
-            return true;
+            tc::mma_commit_warp(&rb.empty[i % L::RB]);
         };
-        bool ok = n == 0 || (wait(&bars[XB_XY], 0) && issue_s(0) && issue_dp(0) && (n == 1 || issue_s(1)));
+        KeyBits kb = key_bits(A.mask, u.seq, t0 * kXRows, lane);
+        bool ok = n == 0 || (wait(&bars[XB_XY], 0) && wait_k(0));
+        if (ok && n > 0) {
+            issue_s(0);
+            ok = wait_v(0);
+            if (ok) issue_dp(0);
+            if (ok && n > 1) {
+                ok = wait_k(1);
+                if (ok) issue_s(1);
+                ok = ok && wait_v(1);
+            }
+        }
         for (int i = 0; i < n && ok; ++i) {
-            const int s = i % L::RA;
             // the next dP once this one has been read, then this tile's dQ, then the scores two tiles on
-            if (i + 1 < n && !(wait(&bars[XB_PF], i & 1) && issue_dp(i + 1))) { ok = false; break; }
-            const KeyBits kb = key_bits(A.mask, u.seq, (t0 + i) * kXRows, lane);
+            if (i + 1 < n) {
+                if (!wait(&bars[XB_PF], i & 1)) { ok = false; break; }
+                issue_dp(i + 1);
+            }
             if (!wait(&bars[XB_DS], i & 1)) { ok = false; break; }
             tc::tc_fence_after();
+            const uint32_t kt = L::OFF_A + i % L::RA * L::TILE;
             // S(i) has read this tile already (dS(i) follows from it), so its dead rows may go
-            if (!kb.all()) zero_rows<L::KC>(smem + L::OFF_A + s * L::TILE, kb, lane);
-            mma_ab<64>(tmem + 384, tmem + (i & 1) * 128, sbase + L::OFF_A + s * L::TILE, id_q, i > 0);
-            tc::mma_commit_warp(&ra.empty[s]);
-            if (i + 2 < n && !issue_s(i + 2)) { ok = false; break; }
+            if (!kb.all()) zero_rows<L::KC>(smem + kt, kb, lane);
+            mma_ab<64>(tmem + 384, tmem + (i & 1) * 128, sbase + kt, id_q, i > 0);
+            tc::mma_commit_warp(&ra.empty[i % L::RA]);
+            if (i + 2 < n) {
+                if (!wait_k(i + 2)) { ok = false; break; }
+                issue_s(i + 2);
+                if (!wait_v(i + 2)) { ok = false; break; }
+            }
+            if (i + 1 < n) kb = key_bits(A.mask, u.seq, (t0 + i + 1) * kXRows, lane);
         }
         if (!ok && lane == 0) fail();
         tc::mma_commit_warp(&bars[XB_ACC]);
@@ -327,53 +344,50 @@ __global__ void __launch_bounds__(kXThreads, 1)
         // ------------------------------------------------------ softmax
         const float *st = A.stats + u.tile_id * 256;
         const float c = A.scale_log2, nl = st[r] + up, nd = st[128 + r];
-        const float2 c2 = make_float2(c, c), nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             const KeyBits kb = key_bits(A.mask, u.seq, (t0 + i) * kXRows, lane);
-            const bool all = kb.all();
             const uint32_t ts = trow + (i & 1) * 128 + h * 64;
             if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[XB_S + (i & 1)], (i >> 1) & 1, abort_flag, kXWaitNs))) {
                 ok = false;
                 break;
             }
             tc::tc_fence_after();
-            float p[64];
-            tmem_ld32(ts, reinterpret_cast<uint32_t *>(p));
-            tmem_ld32(ts + 32, reinterpret_cast<uint32_t *>(p) + 32);
-            tc::tmem_wait_ld();
+            // dS over the scores; a copy of its own for tiles with absent keys
+            auto tile = [&](auto masked) -> bool {
+                float p[64];
+                tmem_ld32(ts, reinterpret_cast<uint32_t *>(p));
+                tmem_ld32(ts + 32, reinterpret_cast<uint32_t *>(p) + 32);
+                tc::tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 64; j += 2) {
-                const float2 e = fma2(make_float2(p[j], p[j + 1]), c2, nl2);
-                p[j] = xex2(e.x);
-                p[j + 1] = xex2(e.y);
-            }
-            if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[XB_DP], i & 1, abort_flag, kXWaitNs))) {
-                ok = false;
-                break;
-            }
-            tc::tc_fence_after();
-            float y[64];
-            tmem_ld32(trow + 256 + h * 64, reinterpret_cast<uint32_t *>(y));
-            tmem_ld32(trow + 256 + h * 64 + 32, reinterpret_cast<uint32_t *>(y) + 32);
-            tc::tmem_wait_ld();
-            tc::tc_fence_before();
-            tc::mbar_arrive(&bars[XB_PF]);               // dP has been read
-            uint32_t q[32];
+                for (int j = 0; j < 64; ++j) p[j] = xex2(fmaf(p[j], c, nl));
+                if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[XB_DP], i & 1, abort_flag, kXWaitNs))) return false;
+                tc::tc_fence_after();
+                float y[64];
+                tmem_ld32(trow + 256 + h * 64, reinterpret_cast<uint32_t *>(y));
+                tmem_ld32(trow + 256 + h * 64 + 32, reinterpret_cast<uint32_t *>(y) + 32);
+                tc::tmem_wait_ld();
+                tc::tc_fence_before();
+                warp_arrive(&bars[XB_PF], lane);           // dP has been read
+                uint32_t q[32];
 #pragma unroll
-            for (int j = 0; j < 64; j += 2) {
-                float2 e = mul2(make_float2(p[j], p[j + 1]), add2(make_float2(y[j], y[j + 1]), nd2));
-                if (!all) {
-                    const uint32_t w = h ? kb.w[2 + (j >> 5)] : kb.w[j >> 5];
-                    if (!((w >> (j & 31)) & 1u)) e.x = 0.f;
-                    if (!((w >> ((j + 1) & 31)) & 1u)) e.y = 0.f;
+                for (int j = 0; j < 64; j += 2) {
+                    float a = p[j] * (y[j] + nd), b = p[j + 1] * (y[j + 1] + nd);
+                    if constexpr (decltype(masked)::value) {
+                        const uint32_t w = h ? kb.w[2 + (j >> 5)] : kb.w[j >> 5];
+                        if (!((w >> (j & 31)) & 1u)) a = 0.f;
+                        if (!((w >> ((j + 1) & 31)) & 1u)) b = 0.f;
+                    }
+                    q[j / 2] = xpack<kFp16>(a, b);
                 }
-                q[j / 2] = xpack<kFp16>(e.x, e.y);
-            }
-            tmem_st32(ts, q);
-            tmem_wait_st();
-            tc::tc_fence_before();
-            tc::mbar_arrive(&bars[XB_DS]);
+                tmem_st32(ts, q);
+                tmem_wait_st();
+                tc::tc_fence_before();
+                warp_arrive(&bars[XB_DS], lane);
+                return true;
+            };
+            ok = kb.all() ? tile(std::false_type{}) : tile(std::true_type{});
+            if (!ok) break;
         }
         if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[XB_ACC], 0, abort_flag, kXWaitNs));
         if (!ok && lane == 0) fail();
@@ -454,7 +468,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         for (int i = 0; i < XB_RING; ++i)
-            tc::mbar_init(&bars[i], i == XB_DS || i == XB_PF ? 256 : i == XB_STE || i == XB_STE + 1 ? 8 : 1);
+            tc::mbar_init(&bars[i], i == XB_DS || i == XB_PF || i == XB_STE || i == XB_STE + 1 ? 8 : 1);   // one arrival a warp
         for (int i = 0; i < 2 * (L::RA + L::RB); ++i) tc::mbar_init(&ra.full[i], 1);
         tc::fence_mbar_init();
     }
@@ -585,18 +599,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
     if (warp < 8 && n > 0) {
         // ------------------------------------------------------ softmax
         const float c = A.scale_log2;
-        const float2 c2 = make_float2(c, c);
         const bool live = key0 + r < u.seq.klen && (!A.mask || A.mask[(int64_t)u.seq.k0 + key0 + r]);
-        const bool all = __all_sync(0xffffffffu, live);
         const float k = kFp16 ? exp2f(up - kShift) : 1.f;
-        const float2 k2 = make_float2(k, k), sh2 = make_float2(kShift, kShift);
-        bool ok = true;
-        for (int i = 0; i < n; ++i) {
+        // One query tile; a copy of its own for key tiles with absent keys.
+        auto tile = [&](auto masked, int i) -> bool {
+            constexpr bool kMasked = decltype(masked)::value;
             const float4 *st = reinterpret_cast<const float4 *>(smem + L::OFF_STAT + (i & 1) * 1024) + h * 16;
-            bool got = tc::mbar_wait(&rs.full[i & 1], (i >> 1) & 1, abort_flag, kXWaitNs);
-            got = got && tc::mbar_wait(&bars[XB_S], i & 1, abort_flag, kXWaitNs);
-            if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-            tc::tc_fence_after();
             float p[64];
             tmem_ld32(trow + h * 64, reinterpret_cast<uint32_t *>(p));
             tmem_ld32(trow + h * 64 + 32, reinterpret_cast<uint32_t *>(p) + 32);
@@ -604,29 +612,23 @@ __global__ void __launch_bounds__(kXThreads, 1)
             uint32_t q[32];
 #pragma unroll
             for (int j = 0; j < 64; j += 4) {
-                const float4 nl = st[j / 4];
-                float2 a = fma2(make_float2(p[j], p[j + 1]), c2, make_float2(nl.x, nl.y));
-                float2 b = fma2(make_float2(p[j + 2], p[j + 3]), c2, make_float2(nl.z, nl.w));
-                if (kFp16) {
-                    a = add2(a, sh2);
-                    b = add2(b, sh2);
+                const float4 nl4 = st[j / 4];
+                const float nl[4] = {nl4.x, nl4.y, nl4.z, nl4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = fmaf(p[j + e], c, nl[e]);
+                    if (kFp16) x += kShift;
+                    p[j + e] = xex2(x);
+                    if (kMasked && !live) p[j + e] = 0.f;
                 }
-                p[j] = xex2(a.x);
-                p[j + 1] = xex2(a.y);
-                p[j + 2] = xex2(b.x);
-                p[j + 3] = xex2(b.y);
-                if (!all && !live) p[j] = p[j + 1] = p[j + 2] = p[j + 3] = 0.f;
                 q[j / 2] = xpack<kFp16>(p[j], p[j + 1]);
                 q[j / 2 + 1] = xpack<kFp16>(p[j + 2], p[j + 3]);
             }
             tmem_st32(trow + h * 64, q);
             tmem_wait_st();
             tc::tc_fence_before();
-            tc::mbar_arrive(&bars[XB_PF]);
-            if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[XB_DP], i & 1, abort_flag, kXWaitNs))) {
-                ok = false;
-                break;
-            }
+            warp_arrive(&bars[XB_PF], lane);
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[XB_DP], i & 1, abort_flag, kXWaitNs))) return false;
             tc::tc_fence_after();
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
@@ -635,27 +637,35 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 tc::tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
-                    const float4 nd = st[32 + (g * 32 + j) / 4];
-                    const float *pp = p + g * 32 + j;
-                    float2 a = add2(make_float2(y[j], y[j + 1]), make_float2(nd.x, nd.y));
-                    float2 b = add2(make_float2(y[j + 2], y[j + 3]), make_float2(nd.z, nd.w));
-                    if (kFp16) {
-                        a = mul2(a, k2);
-                        b = mul2(b, k2);
+                    const float4 nd4 = st[32 + (g * 32 + j) / 4];
+                    const float nd[4] = {nd4.x, nd4.y, nd4.z, nd4.w};
+                    float a[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        a[e] = y[j + e] + nd[e];
+                        if (kFp16) a[e] *= k;
+                        a[e] *= p[g * 32 + j + e];
+                        if (kMasked && !live) a[e] = 0.f;
                     }
-                    a = mul2(a, make_float2(pp[0], pp[1]));
-                    b = mul2(b, make_float2(pp[2], pp[3]));
-                    if (!all && !live) a.x = a.y = b.x = b.y = 0.f;
-                    q[(g * 32 + j) / 2] = xpack<kFp16>(a.x, a.y);
-                    q[(g * 32 + j) / 2 + 1] = xpack<kFp16>(b.x, b.y);
+                    q[(g * 32 + j) / 2] = xpack<kFp16>(a[0], a[1]);
+                    q[(g * 32 + j) / 2 + 1] = xpack<kFp16>(a[2], a[3]);
                 }
             }
             tmem_st32(trow + 128 + h * 64, q);
             tmem_wait_st();
             tc::tc_fence_before();
-            tc::mbar_arrive(&bars[XB_DS]);
-            __syncwarp();
+            warp_arrive(&bars[XB_DS], lane);
             if (lane == 0) tc::mbar_arrive(&rs.empty[i & 1]);
+            return true;
+        };
+        const bool all = __all_sync(0xffffffffu, live);
+        bool ok = true;
+        for (int i = 0; i < n && ok; ++i) {
+            ok = tc::mbar_wait(&rs.full[i & 1], (i >> 1) & 1, abort_flag, kXWaitNs);
+            ok = ok && tc::mbar_wait(&bars[XB_S], i & 1, abort_flag, kXWaitNs);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            tc::tc_fence_after();
+            ok = all ? tile(std::false_type{}, i) : tile(std::true_type{}, i);
         }
         if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[XB_ACC], 0, abort_flag, kXWaitNs));
         if (!ok && lane == 0) fail();

@@ -1,25 +1,28 @@
 // Cross attention, forward: O = softmax(scale Q K^T) V over the key rows of
 // each query row's sequence, one pass with a running maximum and sum.
 //
-// A CTA takes 256 query rows (two tiles) of one key/value head and walks over
+// A CTA takes a tile of 128 query rows of one key/value head and walks over
 // the key tiles: S = Q K^T and O += P V on the tensor cores (tcgen05), S, P and
-// O in TMEM, P written over S as the TMEM operand of the second product, so
-// that scores and probabilities never touch shared memory.  The two tiles
-// alternate: while one tile's softmax runs on its four warps (a thread a row,
-// no shuffles), the MMA warp does the other tile's products.
+// O in TMEM, P as the TMEM operand of the second product, so that scores and
+// probabilities never touch shared memory.  Softmax: four warps, a thread a
+// row, no shuffles.  Two CTAs share an SM (256 TMEM columns and about 100 KB
+// each), so one's softmax, start and end run beside the other's products.
+// One CTA of two tiles that read the keys together was built too: its softmax
+// warps wait for one MMA warp, and it measured slower at every size (largest
+// case 795 us against 778, 131072 keys 427 against 228).
 //
 // The running maximum is lazy: O and the sum are rescaled only when a row's
 // maximum grows by more than 2^8 over the reference in use, which any reference
 // allows (O / sum does not depend on it); P then stays <= 2^8, far from the
-// 16-bit types' limits.  The rescaling happens in the row's own thread, when
-// the score tile has arrived: the earlier P V is complete then, since both
-// were issued in order by one thread.  P is rounded to 16 bits as an operand;
-// the sum is taken of the unrounded fp32 values.
+// 16-bit types' limits.  P is rounded to 16 bits as an operand; the sum is
+// taken of the unrounded fp32 values.
 //
 // Few query rows and many keys: the key tiles of a unit are split over the
 // CTAs of a cluster, whose partial O, maximum and sum are joined through
 // distributed shared memory in rank order: one launch, no workspace, the same
 // bits on every run.
+#include <type_traits>
+
 #include "cross.cuh"
 #include "kernels.cuh"
 #include "tmap.cuh"
@@ -29,30 +32,39 @@ namespace sag {
 
 namespace {
 
-// warps 0-3 and 4-7: softmax and epilogue of the two tiles, 8: TMA, 9: MMA, 10-11: none (a warpgroup's registers are
-// handed over as a whole: 2 * 208 + 88 = 3 * 168, what the block is launched with)
-constexpr int kFwdThreads = 384;
+// Warps 0-3: softmax and epilogue, 4: TMA, 5: MMA, 6-7: none (a warpgroup's
+// registers are handed over as a whole: 184 + 72 = 2 * 128, what the block is
+// launched with).
+constexpr int kFwdThreads = 256, kFwdTma = 4, kFwdMma = 5;
+constexpr int kRegsSoftmax = 184, kRegsOther = 72;
 
+// TMEM columns: S 0, O 128.  64-wide heads leave room for P beside S (column
+// 192): the next S is then formed while this tile's exponentials are, and the
+// chain from tile to tile is the softmax alone.  128-wide heads put P over S.
 template <int D>
-struct FwdSmem {
+struct FwdShape {
+    static constexpr bool P_APART = D == 64;
+    static constexpr int COL_P = P_APART ? 192 : 0;
     static constexpr int KC = D / 64;
     static constexpr int TILE = KC * 16384;
-    static constexpr int STAGES = 131072 / TILE;
-    static constexpr int OFF_RING = 2 * TILE;
-    static constexpr int OFF_ML = OFF_RING + STAGES * TILE;       // float2 [2][128]
-    static constexpr int OFF_BAR = OFF_ML + 2048;
+    static constexpr int STAGES = D == 64 ? 5 : 2;                // K and V tiles in turn
+    static constexpr int OFF_RING = TILE;
+    static constexpr int OFF_ML = OFF_RING + STAGES * TILE;       // float2 [128]
+    static constexpr int OFF_BAR = OFF_ML + 1024;
     static constexpr int TOTAL = OFF_BAR + 256;
     static constexpr int XROW = D + 4;                            // exchange rows, padded against bank conflicts
-    static_assert(2 * kXRows * XROW * 4 <= OFF_ML, "the exchange overlays Q and the ring");
+    static_assert(kXRows * XROW * 4 <= OFF_ML, "the exchange overlays Q and the ring");
+    static_assert(2 * (TOTAL + 1024) <= 228 * 1024, "two CTAs an SM");
 };
-// XF_P: per tile, one barrier for each half of its probabilities
-enum { XF_Q = 0, XF_S = 1, XF_P = 3, XF_DRAIN = 7, XF_FULL = 8 };
+// XF_S: scores formed (and, with P over S, the product before them complete); XF_R: scores read; XF_P: halves of P written;
+// XF_O: P V complete (P apart)
+enum { XF_Q = 0, XF_S = 1, XF_R = 2, XF_P = 3, XF_O = 5, XF_DRAIN = 6, XF_FULL = 7 };
 
 template <bool kFp16, int D>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(kFwdThreads, 2)
     k_xfwd(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
            const __grid_constant__ CUtensorMap map_v, const __grid_constant__ XArgs A) {
-    using L = FwdSmem<D>;
+    using L = FwdShape<D>;
     constexpr int ST = L::STAGES;
     constexpr float kShift = kFp16 ? kFwdShiftF16 : 0.f;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -63,24 +75,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        tc::mbar_init(&bars[XF_Q], 1);
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&bars[XF_S + i], 1);
-            tc::mbar_init(&bars[XF_P + 2 * i], 128);
-            tc::mbar_init(&bars[XF_P + 2 * i + 1], 128);
-        }
-        tc::mbar_init(&bars[XF_DRAIN], 1);
-        for (int i = 0; i < ST; ++i) {
-            tc::mbar_init(&full[i], 1);
-            tc::mbar_init(&empty[i], 1);
-        }
+        // one arrival a softmax warp, one of everything else
+        for (int i = 0; i < XF_FULL + 2 * ST; ++i) tc::mbar_init(&bars[i], i >= XF_R && i < XF_O ? 4 : 1);
         tc::fence_mbar_init();
     }
-    if (warp == 9) {
-        tc::tmem_alloc(tmem_slot, 512);
+    if (warp == kFwdMma) {
+        tc::tmem_alloc(tmem_slot, 256);
         tc::tmem_relinquish();
     }
-    if (threadIdx.x == 256) {
+    if (threadIdx.x == kFwdTma * 32) {
         tc::prefetch_tmap(&map_q);
         tc::prefetch_tmap(&map_k);
         tc::prefetch_tmap(&map_v);
@@ -92,204 +95,227 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t sbase = tc::smem_u32(smem);
-    const int G = A.group;
+    const int G = A.group, tok0 = u.tile * A.tpt;
     const int cover = A.s1_pad ? A.s1_pad : u.seq.qlen;
-    const int tok0[2] = {u.tile * 2 * A.tpt, (u.tile * 2 + 1) * A.tpt};
-    const bool active[2] = {tok0[0] < u.seq.qlen, tok0[1] < u.seq.qlen};
-    const int nkt = active[0] ? (u.seq.klen + kXRows - 1) / kXRows : 0;
+    const int nkt = tok0 < u.seq.qlen ? (u.seq.klen + kXRows - 1) / kXRows : 0;
     const int t0 = (int)((int64_t)nkt * rank / ns), n = (int)((int64_t)nkt * (rank + 1) / ns) - t0;
     auto fail = [&]() { *abort_flag = 1; };
 
-    // The softmax warps take registers from the others.  The two sides share no code up to the end of the kernel: what
-    // both run must fit the smaller number.
-    if (warp >= 8) {
-    regs_fewer<88>();
-    if (warp == 8) {
-        // ------------------------------------------------------ TMA producer
-        if (lane == 0 && n > 0) {
-            bool ok = true;
-            const uint32_t qbytes = (uint32_t)L::KC * A.tpt * G * 128;
-            int loads = 0;
-            auto stage = [&](const CUtensorMap *map, int key) {
-                const int s = loads % ST, use = loads / ST;
-                if (use > 0 && !tc::mbar_wait(&empty[s], (use - 1) & 1, abort_flag, kXWaitNs)) return false;
-                tc::mbar_arrive_expect_tx(&full[s], L::TILE);
-                for (int c = 0; c < L::KC; ++c)
-                    tc::tma_load_3d(smem + L::OFF_RING + s * L::TILE + c * 16384, map, c * 64, u.head, u.seq.k0 + key,
-                                    &full[s]);
-                ++loads;
-                return true;
-            };
-            tc::mbar_arrive_expect_tx(&bars[XF_Q], qbytes * (active[1] ? 2 : 1));
-            for (int sl = 0; sl < 2; ++sl)
-                if (active[sl])
+    // The softmax warps take registers from the others.  The two sides share
+    // no code up to the end of the kernel: what both run must fit the smaller
+    // number.
+    if (warp >= kFwdTma) {
+        regs_fewer<kRegsOther>();
+        if (warp == kFwdTma) {
+            // -------------------------------------------------- TMA producer
+            if (lane == 0 && n > 0) {
+                bool ok = true;
+                int loads = 0;
+                auto stage = [&](const CUtensorMap *map, int key) {
+                    const int s = loads % ST, use = loads / ST;
+                    if (use > 0 && !tc::mbar_wait(&empty[s], (use - 1) & 1, abort_flag, kXWaitNs)) return false;
+                    tc::mbar_arrive_expect_tx(&full[s], L::TILE);
                     for (int c = 0; c < L::KC; ++c)
-                        tc::tma_load_3d(smem + sl * L::TILE + c * 16384, &map_q, c * 64, u.head * G, u.seq.q0 + tok0[sl],
-                                        &bars[XF_Q]);
+                        tc::tma_load_3d(smem + L::OFF_RING + s * L::TILE + c * 16384, map, c * 64, u.head,
+                                        u.seq.k0 + key, &full[s]);
+                    ++loads;
+                    return true;
+                };
+                tc::mbar_arrive_expect_tx(&bars[XF_Q], (uint32_t)L::KC * A.tpt * G * 128);
+                for (int c = 0; c < L::KC; ++c)
+                    tc::tma_load_3d(smem + c * 16384, &map_q, c * 64, u.head * G, u.seq.q0 + tok0, &bars[XF_Q]);
+                for (int i = 0; i < n && ok; ++i) {
+                    const int key = (t0 + i) * kXRows;
+                    ok = stage(&map_k, key) && stage(&map_v, key);
+                }
+                if (!ok) fail();
+                // every load issued must have landed before the CTA exits
+                bool drained = tc::drain_armed(&bars[XF_Q], 1, kXWaitNs);
+                for (int s = 0; s < ST; ++s)
+                    drained = tc::drain_armed(&full[s], loads > s ? (loads - s - 1) / ST + 1 : 0, kXWaitNs) && drained;
+                if (!drained) fail();
+            }
+        } else if (warp == kFwdMma) {
+            // -------------------------------------------------- MMA issuer
+            // The tensor pipe queues about four instructions (256 cycles),
+            // which hides a wait, a commit or some arithmetic between two
+            // products, but not all of a tile's together: they are spread.
+            constexpr uint32_t id_s = tc::idesc_f16(kXRows, kXRows, !kFp16, false, false);
+            constexpr uint32_t id_o = tc::idesc_f16(kXRows, D, !kFp16, false, true);
+            const uint32_t ring = sbase + L::OFF_RING;
+            auto wait = [&](uint64_t *b, uint32_t parity) -> bool {
+                return __all_sync(0xffffffffu, tc::mbar_wait(b, parity, abort_flag, kXWaitNs));
+            };
+            // load j of the ring (K of tile i: 2 i, V: 2 i + 1)
+            auto landed = [&](int j) { return wait(&full[j % ST], j / ST & 1); };
+            auto tile_at = [&](int j) { return (uint32_t)(j % ST * L::TILE); };
+            auto issue_s = [&](int i) {
+                tc::tc_fence_after();
+                mma_abt<D>(tmem, sbase, ring + tile_at(2 * i), id_s);
+            };
+            KeyBits kb = key_bits(A.mask, u.seq, t0 * kXRows, lane);
+            bool ok = n == 0 || (wait(&bars[XF_Q], 0) && landed(0));
+            if (ok && n > 0) {
+                issue_s(0);
+                tc::mma_commit_warp(&bars[XF_S]);
+                tc::mma_commit_warp(&empty[0]);
+                ok = landed(1);
+                if (ok && !kb.all()) zero_rows<L::KC>(smem + L::OFF_RING + tile_at(1), kb, lane);
+            }
             for (int i = 0; i < n && ok; ++i) {
-                const int key = (t0 + i) * kXRows;
-                ok = stage(&map_k, key) && stage(&map_v, key);
-            }
-            if (!ok) fail();
-            // every load issued must have landed before the CTA exits
-            bool drained = tc::drain_armed(&bars[XF_Q], 1, kXWaitNs);
-            for (int s = 0; s < ST; ++s)
-                drained = tc::drain_armed(&full[s], loads > s ? (loads - s - 1) / ST + 1 : 0, kXWaitNs) && drained;
-            if (!drained) fail();
-        }
-    } else if (warp == 9) {
-        // ------------------------------------------------------ MMA issuer
-        constexpr uint32_t id_s = tc::idesc_f16(kXRows, kXRows, !kFp16, false, false);
-        constexpr uint32_t id_o = tc::idesc_f16(kXRows, D, !kFp16, false, true);
-        auto wait = [&](uint64_t *b, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, tc::mbar_wait(b, parity, abort_flag, kXWaitNs));
-        };
-        const uint32_t ring = sbase + L::OFF_RING;
-        KeyBits next = key_bits(A.mask, u.seq, t0 * kXRows, lane);
-        bool ok = n == 0 || wait(&bars[XF_Q], 0);
-        if (ok && n > 0) ok = wait(&full[0], 0);
-        if (ok && n > 0) {
-            tc::tc_fence_after();
-            for (int sl = 0; sl < 2; ++sl)
-                if (active[sl]) {
-                    mma_abt<D>(tmem + sl * 128, sbase + sl * L::TILE, ring, id_s);
-                    tc::mma_commit_warp(&bars[XF_S + sl]);
+                const bool more = i + 1 < n;
+                if (L::P_APART && more) {
+                    if (!landed(2 * i + 2) || !wait(&bars[XF_R], i & 1)) { ok = false; break; }
+                    issue_s(i + 1);
+                    tc::mma_commit_warp(&bars[XF_S]);
+                    tc::mma_commit_warp(&empty[(2 * i + 2) % ST]);
                 }
-            tc::mma_commit_warp(&empty[0]);
-        }
-        for (int i = 0; i < n && ok; ++i) {
-            const int sv = (2 * i + 1) % ST, uv = (2 * i + 1) / ST;
-            const int sk = (2 * i + 2) % ST, uk = (2 * i + 2) / ST;
-            if (!wait(&full[sv], uv & 1)) { ok = false; break; }
-            const KeyBits kb = next;
-            if (i + 1 < n) next = key_bits(A.mask, u.seq, (t0 + i + 1) * kXRows, lane);
-            if (!kb.all()) zero_rows<L::KC>(smem + L::OFF_RING + sv * L::TILE, kb, lane);
-            const bool more = i + 1 < n;
-            for (int sl = 0; sl < 2; ++sl) {
-                if (!active[sl]) continue;
                 // the first half of the keys while the softmax forms the second half's probabilities
-                if (!wait(&bars[XF_P + 2 * sl], i & 1)) { ok = false; break; }
+                const uint32_t vt = ring + tile_at(2 * i + 1);
+                if (!wait(&bars[XF_P], i & 1)) { ok = false; break; }
                 tc::tc_fence_after();
-                mma_ab<32, 0, 4>(tmem + 256 + sl * 128, tmem + sl * 128, ring + sv * L::TILE, id_o, i > 0);
-                if (!wait(&bars[XF_P + 2 * sl + 1], i & 1)) { ok = false; break; }
+                mma_ab<32, 0, 4>(tmem + 128, tmem + L::COL_P, vt, id_o, i > 0);
+                if (!wait(&bars[XF_P + 1], i & 1)) { ok = false; break; }
                 tc::tc_fence_after();
-                mma_ab<32, 4, 8>(tmem + 256 + sl * 128, tmem + sl * 128, ring + sv * L::TILE, id_o, true);
-                if (more) {
-                    if (sl == 0 && !wait(&full[sk], uk & 1)) { ok = false; break; }
-                    tc::tc_fence_after();
-                    mma_abt<D>(tmem + sl * 128, sbase + sl * L::TILE, ring + sk * L::TILE, id_s);
+                mma_ab<32, 4, 8>(tmem + 128, tmem + L::COL_P, vt, id_o, true);
+                if (L::P_APART) tc::mma_commit_warp(&bars[XF_O]);
+                tc::mma_commit_warp(&empty[(2 * i + 1) % ST]);
+                if (!L::P_APART) {
+                    if (more) {
+                        if (!landed(2 * i + 2)) { ok = false; break; }
+                        issue_s(i + 1);
+                    }
+                    tc::mma_commit_warp(&bars[XF_S]);
+                    if (more) tc::mma_commit_warp(&empty[(2 * i + 2) % ST]);
                 }
-                tc::mma_commit_warp(&bars[XF_S + sl]);
+                if (more) {
+                    kb = key_bits(A.mask, u.seq, (t0 + i + 1) * kXRows, lane);
+                    if (!landed(2 * i + 3)) { ok = false; break; }
+                    if (!kb.all()) zero_rows<L::KC>(smem + L::OFF_RING + tile_at(2 * i + 3), kb, lane);
+                }
             }
-            if (!ok) break;
-            tc::mma_commit_warp(&empty[sv]);
-            if (more) tc::mma_commit_warp(&empty[sk]);
+            if (!ok && lane == 0) fail();
+            // every MMA issued must be complete before TMEM is freed
+            tc::mma_commit_warp(&bars[XF_DRAIN]);
+            if (!__all_sync(0xffffffffu, tc::mbar_wait_drain(&bars[XF_DRAIN], 0, kXWaitNs)) && lane == 0) fail();
         }
-        if (!ok && lane == 0) fail();
-        // every MMA issued must be complete before TMEM is freed
-        tc::mma_commit_warp(&bars[XF_DRAIN]);
-        if (!__all_sync(0xffffffffu, tc::mbar_wait_drain(&bars[XF_DRAIN], 0, kXWaitNs)) && lane == 0) fail();
-    }
-
-    if (ns > 1) {                                        // as below
-        __syncthreads();
-        cluster_sync();
-        cluster_sync();
-    }
+        if (ns > 1) {                                    // as below
+            __syncthreads();
+            cluster_sync();
+            cluster_sync();
+        }
     } else {
-    regs_more<208>();
-    const int sl = warp >> 2;                            // softmax warps: their tile
-    const int r = (warp & 3) * 32 + lane;                // query row = TMEM lane
-    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    float m = -INFINITY, l = 0.f;                        // reference maximum (log2 units), sum
-    if (active[sl] && n > 0) {
-        // ------------------------------------------------------ softmax
-        const float c = A.scale_log2;
-        const uint32_t ts = trow + sl * 128, to = trow + 256 + sl * 128;
-        bool ok = true;
-        for (int i = 0; i < n; ++i) {
-            const KeyBits kb = key_bits(A.mask, u.seq, (t0 + i) * kXRows, lane);
-            ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[XF_S + sl], i & 1, abort_flag, kXWaitNs));
-            if (!ok) break;
-            tc::tc_fence_after();
-            float x[128];
-            for (int j = 0; j < 4; ++j) tmem_ld32(ts + j * 32, reinterpret_cast<uint32_t *>(x) + j * 32);
-            tc::tmem_wait_ld();
-            if (!kb.all()) {
+        regs_more<kRegsSoftmax>();
+        const int r = warp * 32 + lane;                  // query row = TMEM lane
+        const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+        const uint32_t tp = trow + L::COL_P, to = trow + 128;
+        float m = -INFINITY, l = 0.f;                    // reference maximum (log2 units), sum
+        if (n > 0) {
+            // -------------------------------------------------- softmax
+            const float c = A.scale_log2;
+            auto wait = [&](int b, uint32_t parity) {
+                return __all_sync(0xffffffffu, tc::mbar_wait(&bars[b], parity, abort_flag, kXWaitNs));
+            };
+            // One tile; a copy of its own for tiles with absent keys, whose
+            // selects otherwise run for every tile.  Scalar fp32 operations:
+            // paired ones (fma.f32x2) have no more throughput here and
+            // measured 10 % slower.
+            auto tile = [&](auto masked, int i, const KeyBits &kb) -> bool {
+                float x[128];
 #pragma unroll
-                for (int j = 0; j < 128; ++j)
-                    if (!((kb.w[j >> 5] >> (j & 31)) & 1u)) x[j] = -INFINITY;
-            }
-            float mx[4] = {x[0], x[1], x[2], x[3]};
+                for (int j = 0; j < 4; ++j) tmem_ld32(trow + j * 32, reinterpret_cast<uint32_t *>(x) + j * 32);
+                tc::tmem_wait_ld();
+                if (L::P_APART) {
+                    tc::tc_fence_before();
+                    warp_arrive(&bars[XF_R], lane);
+                }
+                if constexpr (decltype(masked)::value) {
 #pragma unroll
-            for (int j = 4; j < 124; j += 8) {
+                    for (int j = 0; j < 128; ++j)
+                        if (!((kb.w[j >> 5] >> (j & 31)) & 1u)) x[j] = -INFINITY;
+                }
+                float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], x[j + e]), x[j + 4 + e]);
-            }
+                for (int j = 4; j < 124; j += 8) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[124 + e]);
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-            const bool grow = mt > m + 8.f;
-            if (__any_sync(0xffffffffu, grow)) {
-                const float mnew = grow ? mt : m;
-                const float f = grow ? xex2(m - mnew) : 1.f;
-                l *= f;
-                m = mnew;
-                if (i > 0) {
+                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], x[j + e]), x[j + 4 + e]);
+                }
 #pragma unroll
-                    for (int j = 0; j < D; j += 32) {
-                        float y[32];
-                        tmem_ld32(to + j, reinterpret_cast<uint32_t *>(y));
-                        tc::tmem_wait_ld();
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[124 + e]);
+                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                // O and P may be written once the product of the tile before is complete
+                if (L::P_APART && i > 0) {
+                    if (!wait(XF_O, (i - 1) & 1)) return false;
+                    tc::tc_fence_after();
+                }
+                const bool grow = mt > m + 8.f;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float mnew = grow ? mt : m;
+                    const float f = grow ? xex2(m - mnew) : 1.f;
+                    l *= f;
+                    m = mnew;
+                    if (i > 0) {
+#pragma unroll 1
+                        for (int j = 0; j < D; j += 16) {
+                            uint32_t y[16];
+                            tc::tmem_ld16(to + j, y);
+                            tc::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) y[e] *= f;
-                        tmem_st32(to + j, reinterpret_cast<const uint32_t *>(y));
+                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+                            tmem_st16(to + j, y);
+                        }
                     }
                 }
-            }
-            const float base = m == -INFINITY ? 0.f : m - kShift;
-            const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
-            float2 s4[4] = {};
+                const float base = m == -INFINITY ? 0.f : m - kShift;
+                float sum[4] = {};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t p[32];
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t p[16];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    float2 e = fma2(make_float2(x[h * 64 + 2 * j], x[h * 64 + 2 * j + 1]), c2, b2);
-                    e.x = xex2(e.x);
-                    e.y = xex2(e.y);
-                    s4[j & 3] = add2(s4[j & 3], e);
-                    p[j] = xpack<kFp16>(e.x, e.y);
+                    for (int j = 0; j < 16; ++j) {
+                        const float a = xex2(fmaf(x[h * 32 + 2 * j], c, -base));
+                        const float b = xex2(fmaf(x[h * 32 + 2 * j + 1], c, -base));
+                        sum[2 * (j & 1)] += a;
+                        sum[2 * (j & 1) + 1] += b;
+                        p[j] = xpack<kFp16>(a, b);
+                    }
+                    tmem_st16(tp + h * 16, p);
+                    if (h & 1) {
+                        tmem_wait_st();
+                        tc::tc_fence_before();
+                        warp_arrive(&bars[XF_P + h / 2], lane);
+                    }
                 }
-                tmem_st32(ts + h * 32, p);
-                tmem_wait_st();
-                tc::tc_fence_before();
-                tc::mbar_arrive(&bars[XF_P + 2 * sl + h]);
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                return true;
+            };
+            bool ok = true;
+            for (int i = 0; i < n && ok; ++i) {
+                const KeyBits kb = key_bits(A.mask, u.seq, (t0 + i) * kXRows, lane);
+                ok = wait(XF_S, i & 1);
+                if (!ok) break;
+                tc::tc_fence_after();
+                ok = kb.all() ? tile(std::false_type{}, i, kb) : tile(std::true_type{}, i, kb);
             }
-            const float2 s2 = add2(add2(s4[0], s4[1]), add2(s4[2], s4[3]));
-            l += s2.x + s2.y;
+            if (ok) ok = L::P_APART ? wait(XF_O, (n - 1) & 1) : wait(XF_S, n & 1);
+            if (!ok && lane == 0) fail();
+            tc::tc_fence_after();
         }
-        if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[XF_S + sl], n & 1, abort_flag, kXWaitNs));
-        if (!ok && lane == 0) fail();
-        tc::tc_fence_after();
-    }
 
-    // ---------------------------------------------------------- epilogue
-    const float kLn2 = 0.6931471805599453f;
-    if (ns == 1) {
-        {
-            const int tok = tok0[sl] + r / G;
+        // ------------------------------------------------------ epilogue
+        const float kLn2 = 0.6931471805599453f;
+        if (ns == 1) {
+            const int tok = tok0 + r / G;
             const bool mine = r < A.tpt * G && tok < cover;
             const bool pad = tok >= u.seq.qlen;
             const int64_t row = (int64_t)(u.seq.q0 + tok) * A.n1 + u.head * G + r % G;
             const bool some = l > 0.f || l != l;         // l is NaN when a score was
             const float inv = some ? 1.f / l : 0.f;
-            const bool have = active[sl] && n > 0;
 #pragma unroll
             for (int j = 0; j < D; j += 32) {
                 float y[32];
-                if (have) {
-                    tmem_ld32(trow + 256 + sl * 128 + j, reinterpret_cast<uint32_t *>(y));
+                if (n > 0) {
+                    tmem_ld32(to + j, reinterpret_cast<uint32_t *>(y));
                     tc::tmem_wait_ld();
                 }
 #pragma unroll
@@ -297,34 +323,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (mine) store_row<kFp16, 32>(A.o + row * D + j, y);
             }
             if (mine) A.lse[row] = pad ? 0.f : some ? (m - kShift) * kLn2 + logf(l) : -INFINITY;
-        }
-    } else {
-        // partial O, maximum and sum of every rank into its shared memory, then each rank joins its share of the rows
-        float2 *ml = reinterpret_cast<float2 *>(smem + L::OFF_ML);
-        float *xo = reinterpret_cast<float *>(smem);
-        __syncthreads();                                 // all loads and products on this memory are complete
-        if (active[sl]) {
-            ml[sl * 128 + r] = make_float2(m, l);
+        } else {
+            // partial O, maximum and sum of every rank into its shared memory, then each rank joins its share of the rows
+            float2 *ml = reinterpret_cast<float2 *>(smem + L::OFF_ML);
+            float *xo = reinterpret_cast<float *>(smem);
+            __syncthreads();                             // all loads and products on this memory are complete
+            ml[r] = make_float2(m, l);
             if (n > 0) {
 #pragma unroll
                 for (int j = 0; j < D; j += 32) {
                     float y[32];
-                    tmem_ld32(trow + 256 + sl * 128 + j, reinterpret_cast<uint32_t *>(y));
+                    tmem_ld32(to + j, reinterpret_cast<uint32_t *>(y));
                     tc::tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4 *>(xo + (sl * 128 + r) * L::XROW + j + e) =
+                        *reinterpret_cast<float4 *>(xo + r * L::XROW + j + e) =
                             make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
                 }
             }
-        }
-        cluster_sync();
-        {
+            cluster_sync();
             constexpr int E = D / 64;                    // float2 a lane and row
-            for (int k = rank + ns * warp; k < 2 * kXRows; k += ns * 8) {
-                const int ks = k / kXRows, kr = k % kXRows, tok = tok0[ks] + kr / G;
-                if (kr >= A.tpt * G || tok >= cover) continue;
-                const int64_t row = (int64_t)(u.seq.q0 + tok) * A.n1 + u.head * G + kr % G;
+            for (int k = rank + ns * warp; k < A.tpt * G; k += ns * 4) {
+                const int tok = tok0 + k / G;
+                if (tok >= cover) break;
+                const int64_t row = (int64_t)(u.seq.q0 + tok) * A.n1 + u.head * G + k % G;
                 const bool pad = tok >= u.seq.qlen;
                 // lane p holds rank p's maximum and sum; a rank that saw nothing has (-inf, 0) and no O
                 float2 v = make_float2(-INFINITY, 0.f);
@@ -362,15 +384,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         some ? xpack<kFp16>(acc[e].x * inv, acc[e].y * inv) : 0u;
                 if (lane == 0) A.lse[row] = pad ? 0.f : some ? (top - kShift) * kLn2 + logf(sum) : -INFINITY;
             }
+            cluster_sync();                              // peers are done with this CTA's shared memory
         }
-        cluster_sync();                                  // peers are done with this CTA's shared memory
-    }
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kFwdMma) {
         tc::tc_fence_after();
-        tc::tmem_dealloc(tmem, 512);
+        tc::tmem_dealloc(tmem, 256);
     }
     if (threadIdx.x == 0) {
         A.status[blockIdx.x] = *abort_flag ? SAG_ERR_TIMEOUT : SAG_OK;
@@ -384,7 +405,7 @@ cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, int unit
     if (!x_map_q(&mq, io.query, d, a, d.q_stride) || !x_map_k(&mk, io.key, io.query, d, a, d.k_stride) ||
         !x_map_k(&mv, io.value, io.query, d, a, d.v_stride))
         return cudaErrorInvalidValue;
-    return x_launch(k_xfwd<kFp16, D>, units * a.nsplit, kFwdThreads, a.nsplit, FwdSmem<D>::TOTAL, s, mq, mk, mv, a);
+    return x_launch(k_xfwd<kFp16, D>, units * a.nsplit, kFwdThreads, a.nsplit, FwdShape<D>::TOTAL, s, mq, mk, mv, a);
 }
 
 }  // namespace
