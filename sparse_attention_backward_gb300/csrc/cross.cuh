@@ -112,6 +112,31 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Waits of a whole (convergent) warp for one to three barriers: a test of a completed phase costs about 60 cycles, three
+// independent ones little more, and one after the other three times that, which the MMA warps do not have.  Bounded like
+// tc::mbar_wait; false when the limit ran out or *abort was set.  A barrier that has been seen complete stays so until
+// this warp goes on, so testing it again with the others is safe.
+struct Phase {
+    uint64_t *bar;
+    uint32_t parity;
+};
+template <class... P>
+__device__ __forceinline__ bool warp_wait(volatile int *abort, const P &...p) {
+    auto done = [&]() {
+        bool all = true;
+        ((all = tc::mbar_try_wait(p.bar, p.parity) && all), ...);
+        return __all_sync(0xffffffffu, all) != 0;
+    };
+    if (done()) return true;
+    const uint64_t t0 = tc::globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (done()) return true;
+        if ((i & 63) == 0 &&
+            __any_sync(0xffffffffu, *abort != 0 || tc::globaltimer_ns() - t0 > kXWaitNs))
+            return false;
+    }
+}
+
 // One arrival for a warp whose lanes have all done what the barrier stands for.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
     __syncwarp();
@@ -210,69 +235,79 @@ __device__ __forceinline__ XUnit x_decode(const XArgs &A, int unit) {
     return x;
 }
 
-// Which of the 128 keys from key `first` of a sequence are there, as four
-// words.  Collective over a warp when there is a mask.
+// Which of the kWords * 32 keys from key `first` of a sequence are there.
+// Collective over a warp when there is a mask.
+template <int kWords>
 struct KeyBits {
-    uint32_t w[4];
-    __device__ __forceinline__ bool all() const { return (w[0] & w[1] & w[2] & w[3]) == 0xffffffffu; }
+    uint32_t w[kWords];
+    __device__ __forceinline__ bool all() const {
+        uint32_t x = w[0];
+#pragma unroll
+        for (int j = 1; j < kWords; ++j) x &= w[j];
+        return x == 0xffffffffu;
+    }
+    // the first n
+    __device__ __forceinline__ void set_first(int n) {
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+            const int k = n - 32 * j;
+            w[j] = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
+        }
+    }
 };
-__device__ __forceinline__ KeyBits key_bits(const uint8_t *mask, const SeqRow &seq, int first, int lane) {
-    KeyBits k;
+template <int kWords>
+__device__ __forceinline__ KeyBits<kWords> key_bits(const uint8_t *mask, const SeqRow &seq, int first, int lane) {
+    KeyBits<kWords> k;
     const int left = seq.klen - first;
     if (!mask) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = left - 32 * j;
-            k.w[j] = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-        }
+        k.set_first(left);
         return k;
     }
     const uint8_t *m = mask + (int64_t)seq.k0 + first;
-    bool on[4];
+    bool on[kWords];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) on[j] = 32 * j + lane < left && m[32 * j + lane] != 0;
+    for (int j = 0; j < kWords; ++j) on[j] = 32 * j + lane < left && m[32 * j + lane] != 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) k.w[j] = __ballot_sync(0xffffffffu, on[j]);
+    for (int j = 0; j < kWords; ++j) k.w[j] = __ballot_sync(0xffffffffu, on[j]);
     return k;
 }
 
-// Zeros the rows of a [128 x 64 * kChunks] shared tile whose bit is not set, before the matrix product reads it: a
+// Zeros the rows of a [32 * kWords x 64 * kChunks] shared tile whose bit is not set, before the matrix product reads it: a
 // probability of 0 does not cancel a NaN.  Collective over the MMA warp.
-template <int kChunks>
-__device__ __forceinline__ void zero_rows(uint8_t *tile, const KeyBits &k, int lane) {
+template <int kChunks, int kWords>
+__device__ __forceinline__ void zero_rows(uint8_t *tile, const KeyBits<kWords> &k, int lane) {
     // eight lanes a row, four rows a step, every step independent of the others
     uint8_t *at = tile + (lane >> 3) * 128 + (lane & 7) * 16;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kWords; ++j) {
         if (k.w[j] == 0xffffffffu) continue;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (!((k.w[j] >> (4 * i + (lane >> 3))) & 1u))
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c)
-                    *reinterpret_cast<uint4 *>(at + c * 16384 + (32 * j + 4 * i) * 128) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(at + c * kWords * 4096 + (32 * j + 4 * i) * 128) = make_uint4(0, 0, 0, 0);
     }
     tc::fence_proxy_async_smem();
     __syncwarp();
 }
 
-// Products over a tile pair, each with K = 16 steps; the operands' 64-column chunks are 16 KB apart.
-// A [128 x D] K-major, B [128 x D] K-major: D columns 0..127 of the accumulator.
-template <int D>
+// Products, each with K = 16 steps; a tile of R rows keeps its 64-column chunks 128 R bytes apart.
+// A [128 x D] K-major, B [kN x D] K-major: columns 0..kN-1 of the accumulator.
+template <int D, int kN>
 __device__ __forceinline__ void mma_abt(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc) {
     const uint32_t al = desc_lo(a, 16), bl = desc_lo(b, 16);
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t step = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-        xmma_ss(acc, al + step, bl + step, idesc, kk > 0);
-    }
+    for (int kk = 0; kk < D / 16; ++kk)
+        xmma_ss(acc, al + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), bl + (((kk >> 2) * kN * 128 + (kk & 3) * 32) >> 4),
+                idesc, kk > 0);
 }
-// A [128 x 128] in TMEM (16-bit pairs; the second half of K starts `gap` columns after the first), B [128 x D] MN-major.
-template <int kGap, int kFrom = 0, int kTo = 8>
+// A [128 x kK] in TMEM (16-bit pairs; the second half of kK = 128 starts kGap columns after the first), B [kK x D] MN-major.
+template <int kK, int kGap>
 __device__ __forceinline__ void mma_ab(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
-    const uint32_t bl = desc_lo(b, 16384);
+    const uint32_t bl = desc_lo(b, kK * 128);
 #pragma unroll
-    for (int kk = kFrom; kk < kTo; ++kk)
+    for (int kk = 0; kk < kK / 16; ++kk)
         xmma_ts(acc, a + (kk >> 2) * kGap + (kk & 3) * 8, bl + (kk * 2048 >> 4), idesc, accumulate || kk > 0);
 }
 

@@ -181,7 +181,7 @@ extern "C" sag_status cross_attn_fwd(const sca_desc *desc, const sca_io *io, voi
     XArgs a = x_args(desc, io, p, ws);
     if (x_table(&a, desc, p, ws, s) != cudaSuccess) return SAG_ERR_CUDA;
     const int units = (int)(p.q_tiles * desc->n2);
-    a.nsplit = split_of(units, p.max_k, 2 * current_device_sms());   // two CTAs an SM
+    a.nsplit = split_of(units, 2 * p.max_k, 2 * current_device_sms());   // two CTAs an SM
     const char *e = getenv("XSPLIT"); if (e) a.nsplit = atoi(e);
     a.n_status = units * a.nsplit;
     return launch_xfwd(a, *io, *desc, units, s) == cudaSuccess ? SAG_OK : SAG_ERR_CUDA;

@@ -291,16 +291,16 @@ __global__ void __launch_bounds__(kXThreads, 1)
         auto wait_v = [&](int i) { return wait(&rb.full[i % L::RB], (i / L::RB) & 1); };
         auto issue_s = [&](int i) {
             tc::tc_fence_after();
-            mma_abt<D>(tmem + (i & 1) * 128, sbase + L::OFF_X, sbase + L::OFF_A + i % L::RA * L::TILE, id_s);
+            mma_abt<D, kXRows>(tmem + (i & 1) * 128, sbase + L::OFF_X, sbase + L::OFF_A + i % L::RA * L::TILE, id_s);
             tc::mma_commit_warp(&bars[XB_S + (i & 1)]);
         };
         auto issue_dp = [&](int i) {
             tc::tc_fence_after();
-            mma_abt<D>(tmem + 256, sbase + L::OFF_Y, sbase + L::OFF_B + i % L::RB * L::TILE, id_s);
+            mma_abt<D, kXRows>(tmem + 256, sbase + L::OFF_Y, sbase + L::OFF_B + i % L::RB * L::TILE, id_s);
             tc::mma_commit_warp(&bars[XB_DP]);
             tc::mma_commit_warp(&rb.empty[i % L::RB]);
         };
-        KeyBits kb = key_bits(A.mask, u.seq, t0 * kXRows, lane);
+        KeyBits<4> kb = key_bits<4>(A.mask, u.seq, t0 * kXRows, lane);
         bool ok = n == 0 || (wait(&bars[XB_XY], 0) && wait_k(0));
         if (ok && n > 0) {
             issue_s(0);
@@ -323,14 +323,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
             const uint32_t kt = L::OFF_A + i % L::RA * L::TILE;
             // S(i) has read this tile already (dS(i) follows from it), so its dead rows may go
             if (!kb.all()) zero_rows<L::KC>(smem + kt, kb, lane);
-            mma_ab<64>(tmem + 384, tmem + (i & 1) * 128, sbase + kt, id_q, i > 0);
+            mma_ab<kXRows, 64>(tmem + 384, tmem + (i & 1) * 128, sbase + kt, id_q, i > 0);
             tc::mma_commit_warp(&ra.empty[i % L::RA]);
             if (i + 2 < n) {
                 if (!wait_k(i + 2)) { ok = false; break; }
                 issue_s(i + 2);
                 if (!wait_v(i + 2)) { ok = false; break; }
             }
-            if (i + 1 < n) kb = key_bits(A.mask, u.seq, (t0 + i + 1) * kXRows, lane);
+            if (i + 1 < n) kb = key_bits<4>(A.mask, u.seq, (t0 + i + 1) * kXRows, lane);
         }
         if (!ok && lane == 0) fail();
         tc::mma_commit_warp(&bars[XB_ACC]);
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         const float c = A.scale_log2, nl = st[r] + up, nd = st[128 + r];
         bool ok = true;
         for (int i = 0; i < n; ++i) {
-            const KeyBits kb = key_bits(A.mask, u.seq, (t0 + i) * kXRows, lane);
+            const KeyBits<4> kb = key_bits<4>(A.mask, u.seq, (t0 + i) * kXRows, lane);
             const uint32_t ts = trow + (i & 1) * 128 + h * 64;
             if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[XB_S + (i & 1)], (i >> 1) & 1, abort_flag, kXWaitNs))) {
                 ok = false;
@@ -552,12 +552,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
             const int left = u.seq.qlen - (t0 + i) * A.tpt;
             const int live = (left < A.tpt ? left : A.tpt) * G;
             if (live < kXRows) {
-                KeyBits kb;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = live - 32 * j;
-                    kb.w[j] = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
-                }
+                KeyBits<4> kb;
+                kb.set_first(live);
                 zero_rows<L::KC>(smem + off + s * L::TILE, kb, lane);
             }
             tc::tc_fence_after();
@@ -565,13 +561,13 @@ __global__ void __launch_bounds__(kXThreads, 1)
         };
         auto issue_s = [&](int i) -> bool {
             if (!take(ra, L::OFF_A, i)) return false;
-            mma_abt<D>(tmem, sbase + L::OFF_X, sbase + L::OFF_A + (i % L::RA) * L::TILE, id_s);
+            mma_abt<D, kXRows>(tmem, sbase + L::OFF_X, sbase + L::OFF_A + (i % L::RA) * L::TILE, id_s);
             tc::mma_commit_warp(&bars[XB_S]);
             return true;
         };
         auto issue_dp = [&](int i) -> bool {
             if (!take(rb, L::OFF_B, i)) return false;
-            mma_abt<D>(tmem + 128, sbase + L::OFF_Y, sbase + L::OFF_B + (i % L::RB) * L::TILE, id_s);
+            mma_abt<D, kXRows>(tmem + 128, sbase + L::OFF_Y, sbase + L::OFF_B + (i % L::RB) * L::TILE, id_s);
             tc::mma_commit_warp(&bars[XB_DP]);
             return true;
         };
@@ -579,12 +575,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
         for (int i = 0; i < n && ok; ++i) {
             if (!wait(&bars[XB_PF], i & 1)) { ok = false; break; }
             tc::tc_fence_after();
-            mma_ab<64>(tmem + 256, tmem, sbase + L::OFF_B + (i % L::RB) * L::TILE, id_g, i > 0);
+            mma_ab<kXRows, 64>(tmem + 256, tmem, sbase + L::OFF_B + (i % L::RB) * L::TILE, id_g, i > 0);
             tc::mma_commit_warp(&rb.empty[i % L::RB]);
             if (i + 1 < n && !issue_s(i + 1)) { ok = false; break; }
             if (!wait(&bars[XB_DS], i & 1)) { ok = false; break; }
             tc::tc_fence_after();
-            mma_ab<64>(tmem + 384, tmem + 128, sbase + L::OFF_A + (i % L::RA) * L::TILE, id_g, i > 0);
+            mma_ab<kXRows, 64>(tmem + 384, tmem + 128, sbase + L::OFF_A + (i % L::RA) * L::TILE, id_g, i > 0);
             tc::mma_commit_warp(&ra.empty[i % L::RA]);
             if (i + 1 < n && !issue_dp(i + 1)) { ok = false; break; }
         }
@@ -734,7 +730,8 @@ struct BwdMaps {
 };
 bool maps(BwdMaps *m, const XArgs &a, const sca_io &io, const sca_desc &d) {
     return x_map_q(&m->q, io.query, d, a, d.q_stride, io.key) && x_map_q(&m->dy, io.attention_out_grad, d, a, 0, io.key) &&
-           x_map_k(&m->k, io.key, io.query, d, a, d.k_stride) && x_map_k(&m->v, io.value, io.query, d, a, d.v_stride);
+           x_map_k(&m->k, io.key, io.query, d, d.k_stride, kXRows) &&
+           x_map_k(&m->v, io.value, io.query, d, d.v_stride, kXRows);
 }
 
 template <bool kFp16, int D>

@@ -2,14 +2,13 @@
 // each query row's sequence, one pass with a running maximum and sum.
 //
 // A CTA takes a tile of 128 query rows of one key/value head and walks over
-// the key tiles: S = Q K^T and O += P V on the tensor cores (tcgen05), S, P and
-// O in TMEM, P as the TMEM operand of the second product, so that scores and
-// probabilities never touch shared memory.  Softmax: four warps, a thread a
-// row, no shuffles.  Two CTAs share an SM (256 TMEM columns and about 100 KB
-// each), so one's softmax, start and end run beside the other's products.
-// One CTA of two tiles that read the keys together was built too: its softmax
-// warps wait for one MMA warp, and it measured slower at every size (largest
-// case 795 us against 778, 131072 keys 427 against 228).
+// tiles of 64 keys: S = Q K^T and O += P V on the tensor cores (tcgen05), S, P
+// and O in TMEM, P over its S as the TMEM operand of the second product, so
+// that scores and probabilities never touch shared memory.  Two score tiles
+// are in flight: while the softmax (four warps, a thread a row, no shuffles)
+// works on one, the MMA warp multiplies the other's P and forms the scores
+// after it.  Two CTAs share an SM (256 TMEM columns and at most 113 KB each),
+// so one's start and end run beside the other's loop as well.
 //
 // The running maximum is lazy: O and the sum are rescaled only when a row's
 // maximum grows by more than 2^8 over the reference in use, which any reference
@@ -32,33 +31,27 @@ namespace sag {
 
 namespace {
 
-// Warps 0-3: softmax and epilogue, 4: TMA, 5: MMA, 6-7: none (a warpgroup's
-// registers are handed over as a whole: 184 + 72 = 2 * 128, what the block is
-// launched with).
-constexpr int kFwdThreads = 256, kFwdTma = 4, kFwdMma = 5;
-constexpr int kRegsSoftmax = 184, kRegsOther = 72;
+constexpr int kFwdThreads = 192, kFwdTma = 4, kFwdMma = 5;   // warps 0-3 softmax and epilogue, then TMA and MMA
+constexpr int kFwdKeys = 64;
 
-// TMEM columns: S 0, O 128.  64-wide heads leave room for P beside S (column
-// 192): the next S is then formed while this tile's exponentials are, and the
-// chain from tile to tile is the softmax alone.  128-wide heads put P over S.
+// TMEM columns: S of even / odd tiles 0 / 64, O 128.
 template <int D>
 struct FwdShape {
-    static constexpr bool P_APART = D == 64;
-    static constexpr int COL_P = P_APART ? 192 : 0;
     static constexpr int KC = D / 64;
-    static constexpr int TILE = KC * 16384;
-    static constexpr int STAGES = D == 64 ? 5 : 2;                // K and V tiles in turn
-    static constexpr int OFF_RING = TILE;
-    static constexpr int OFF_ML = OFF_RING + STAGES * TILE;       // float2 [128]
-    static constexpr int OFF_BAR = OFF_ML + 1024;
+    static constexpr int Q_BYTES = KC * 16384;
+    static constexpr int TILE = KC * kFwdKeys * 128;
+    static constexpr int STAGES = D == 64 ? 8 : 5;                // K and V tiles
+    static constexpr int OFF_RING = Q_BYTES;
+    static constexpr int OFF_BAR = OFF_RING + STAGES * TILE;
     static constexpr int TOTAL = OFF_BAR + 256;
-    static constexpr int XROW = D + 4;                            // exchange rows, padded against bank conflicts
-    static_assert(kXRows * XROW * 4 <= OFF_ML, "the exchange overlays Q and the ring");
+    // split units, over Q and the ring: float [128][XROW] of O (padded against bank conflicts), float2 [128]
+    static constexpr int XROW = D + 4;
+    static constexpr int OFF_ML = kXRows * XROW * 4;
+    static_assert(OFF_ML + kXRows * 8 <= OFF_BAR, "the exchange overlays Q and the ring");
     static_assert(2 * (TOTAL + 1024) <= 228 * 1024, "two CTAs an SM");
 };
-// XF_S: scores formed (and, with P over S, the product before them complete); XF_R: scores read; XF_P: halves of P written;
-// XF_O: P V complete (P apart)
-enum { XF_Q = 0, XF_S = 1, XF_R = 2, XF_P = 3, XF_O = 5, XF_DRAIN = 6, XF_FULL = 7 };
+// XF_S: scores of an even / odd tile formed, and P V of the tile two before complete; XF_P: P written
+enum { XF_Q = 0, XF_S = 1, XF_P = 3, XF_DRAIN = 5, XF_FULL = 6 };
 
 template <bool kFp16, int D>
 __global__ void __launch_bounds__(kFwdThreads, 2)
@@ -76,7 +69,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         // one arrival a softmax warp, one of everything else
-        for (int i = 0; i < XF_FULL + 2 * ST; ++i) tc::mbar_init(&bars[i], i >= XF_R && i < XF_O ? 4 : 1);
+        for (int i = 0; i < XF_FULL + 2 * ST; ++i) tc::mbar_init(&bars[i], i == XF_P || i == XF_P + 1 ? 4 : 1);
         tc::fence_mbar_init();
     }
     if (warp == kFwdMma) {
@@ -97,15 +90,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     const uint32_t sbase = tc::smem_u32(smem);
     const int G = A.group, tok0 = u.tile * A.tpt;
     const int cover = A.s1_pad ? A.s1_pad : u.seq.qlen;
-    const int nkt = tok0 < u.seq.qlen ? (u.seq.klen + kXRows - 1) / kXRows : 0;
+    const int nkt = tok0 < u.seq.qlen ? (u.seq.klen + kFwdKeys - 1) / kFwdKeys : 0;
     const int t0 = (int)((int64_t)nkt * rank / ns), n = (int)((int64_t)nkt * (rank + 1) / ns) - t0;
+    const int partial = A.mask ? 0 : u.seq.klen / kFwdKeys - t0;    // tiles from this one on may lack keys
     auto fail = [&]() { *abort_flag = 1; };
 
-    // The softmax warps take registers from the others.  The two sides share
-    // no code up to the end of the kernel: what both run must fit the smaller
-    // number.
     if (warp >= kFwdTma) {
-        regs_fewer<kRegsOther>();
         if (warp == kFwdTma) {
             // -------------------------------------------------- TMA producer
             if (lane == 0 && n > 0) {
@@ -116,7 +106,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                     if (use > 0 && !tc::mbar_wait(&empty[s], (use - 1) & 1, abort_flag, kXWaitNs)) return false;
                     tc::mbar_arrive_expect_tx(&full[s], L::TILE);
                     for (int c = 0; c < L::KC; ++c)
-                        tc::tma_load_3d(smem + L::OFF_RING + s * L::TILE + c * 16384, map, c * 64, u.head,
+                        tc::tma_load_3d(smem + L::OFF_RING + s * L::TILE + c * kFwdKeys * 128, map, c * 64, u.head,
                                         u.seq.k0 + key, &full[s]);
                     ++loads;
                     return true;
@@ -124,9 +114,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                 tc::mbar_arrive_expect_tx(&bars[XF_Q], (uint32_t)L::KC * A.tpt * G * 128);
                 for (int c = 0; c < L::KC; ++c)
                     tc::tma_load_3d(smem + c * 16384, &map_q, c * 64, u.head * G, u.seq.q0 + tok0, &bars[XF_Q]);
-                for (int i = 0; i < n && ok; ++i) {
-                    const int key = (t0 + i) * kXRows;
-                    ok = stage(&map_k, key) && stage(&map_v, key);
+                // in the order the MMA warp takes them: K 0, K 1, then V i and K i + 2
+                for (int i = -2; i < n && ok; ++i) {
+                    if (i >= 0) ok = stage(&map_v, (t0 + i) * kFwdKeys);
+                    if (ok && i + 2 < n) ok = stage(&map_k, (t0 + i + 2) * kFwdKeys);
                 }
                 if (!ok) fail();
                 // every load issued must have landed before the CTA exits
@@ -140,59 +131,37 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             // The tensor pipe queues about four instructions (256 cycles),
             // which hides a wait, a commit or some arithmetic between two
             // products, but not all of a tile's together: they are spread.
-            constexpr uint32_t id_s = tc::idesc_f16(kXRows, kXRows, !kFp16, false, false);
+            constexpr uint32_t id_s = tc::idesc_f16(kXRows, kFwdKeys, !kFp16, false, false);
             constexpr uint32_t id_o = tc::idesc_f16(kXRows, D, !kFp16, false, true);
             const uint32_t ring = sbase + L::OFF_RING;
-            auto wait = [&](uint64_t *b, uint32_t parity) -> bool {
-                return __all_sync(0xffffffffu, tc::mbar_wait(b, parity, abort_flag, kXWaitNs));
+            // load j of the ring: K 0, K 1, then V i behind min(i + 2, n) tiles of K, and K i + 2
+            auto landed = [&](int j) { return Phase{&full[j % ST], (uint32_t)(j / ST) & 1u}; };
+            auto issue_s = [&](int i, int j) {
+                mma_abt<D, kFwdKeys>(tmem + (i & 1) * 64, sbase, ring + j % ST * L::TILE, id_s);
+                tc::mma_commit_warp(&bars[XF_S + (i & 1)]);
+                tc::mma_commit_warp(&empty[j % ST]);
             };
-            // load j of the ring (K of tile i: 2 i, V: 2 i + 1)
-            auto landed = [&](int j) { return wait(&full[j % ST], j / ST & 1); };
-            auto tile_at = [&](int j) { return (uint32_t)(j % ST * L::TILE); };
-            auto issue_s = [&](int i) {
+            bool ok = true;
+            for (int i = 0; i < 2 && i < n && ok; ++i) {
+                ok = warp_wait(abort_flag, Phase{&bars[XF_Q], 0}, landed(i));
                 tc::tc_fence_after();
-                mma_abt<D>(tmem, sbase, ring + tile_at(2 * i), id_s);
-            };
-            KeyBits kb = key_bits(A.mask, u.seq, t0 * kXRows, lane);
-            bool ok = n == 0 || (wait(&bars[XF_Q], 0) && landed(0));
-            if (ok && n > 0) {
-                issue_s(0);
-                tc::mma_commit_warp(&bars[XF_S]);
-                tc::mma_commit_warp(&empty[0]);
-                ok = landed(1);
-                if (ok && !kb.all()) zero_rows<L::KC>(smem + L::OFF_RING + tile_at(1), kb, lane);
+                if (ok) issue_s(i, i);
             }
             for (int i = 0; i < n && ok; ++i) {
-                const bool more = i + 1 < n;
-                if (L::P_APART && more) {
-                    if (!landed(2 * i + 2) || !wait(&bars[XF_R], i & 1)) { ok = false; break; }
-                    issue_s(i + 1);
-                    tc::mma_commit_warp(&bars[XF_S]);
-                    tc::mma_commit_warp(&empty[(2 * i + 2) % ST]);
+                const bool more = i + 2 < n;
+                const int jv = i + (i + 2 < n ? i + 2 : n);
+                const Phase pv{&bars[XF_P + (i & 1)], (uint32_t)(i >> 1) & 1u};
+                ok = more ? warp_wait(abort_flag, pv, landed(jv), landed(jv + 1)) : warp_wait(abort_flag, pv, landed(jv));
+                if (!ok) break;
+                if (i >= partial) {
+                    const KeyBits<2> kb = key_bits<2>(A.mask, u.seq, (t0 + i) * kFwdKeys, lane);
+                    if (!kb.all()) zero_rows<L::KC, 2>(smem + L::OFF_RING + jv % ST * L::TILE, kb, lane);
                 }
-                // the first half of the keys while the softmax forms the second half's probabilities
-                const uint32_t vt = ring + tile_at(2 * i + 1);
-                if (!wait(&bars[XF_P], i & 1)) { ok = false; break; }
                 tc::tc_fence_after();
-                mma_ab<32, 0, 4>(tmem + 128, tmem + L::COL_P, vt, id_o, i > 0);
-                if (!wait(&bars[XF_P + 1], i & 1)) { ok = false; break; }
-                tc::tc_fence_after();
-                mma_ab<32, 4, 8>(tmem + 128, tmem + L::COL_P, vt, id_o, true);
-                if (L::P_APART) tc::mma_commit_warp(&bars[XF_O]);
-                tc::mma_commit_warp(&empty[(2 * i + 1) % ST]);
-                if (!L::P_APART) {
-                    if (more) {
-                        if (!landed(2 * i + 2)) { ok = false; break; }
-                        issue_s(i + 1);
-                    }
-                    tc::mma_commit_warp(&bars[XF_S]);
-                    if (more) tc::mma_commit_warp(&empty[(2 * i + 2) % ST]);
-                }
-                if (more) {
-                    kb = key_bits(A.mask, u.seq, (t0 + i + 1) * kXRows, lane);
-                    if (!landed(2 * i + 3)) { ok = false; break; }
-                    if (!kb.all()) zero_rows<L::KC>(smem + L::OFF_RING + tile_at(2 * i + 3), kb, lane);
-                }
+                mma_ab<kFwdKeys, 32>(tmem + 128, tmem + (i & 1) * 64, ring + jv % ST * L::TILE, id_o, i > 0);
+                tc::mma_commit_warp(&empty[jv % ST]);
+                if (more) issue_s(i + 2, jv + 1);
+                else tc::mma_commit_warp(&bars[XF_S + (i & 1)]);
             }
             if (!ok && lane == 0) fail();
             // every MMA issued must be complete before TMEM is freed
@@ -205,49 +174,43 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             cluster_sync();
         }
     } else {
-        regs_more<kRegsSoftmax>();
         const int r = warp * 32 + lane;                  // query row = TMEM lane
         const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
-        const uint32_t tp = trow + L::COL_P, to = trow + 128;
+        const uint32_t to = trow + 128;
         float m = -INFINITY, l = 0.f;                    // reference maximum (log2 units), sum
         if (n > 0) {
             // -------------------------------------------------- softmax
             const float c = A.scale_log2;
             auto wait = [&](int b, uint32_t parity) {
-                return __all_sync(0xffffffffu, tc::mbar_wait(&bars[b], parity, abort_flag, kXWaitNs));
+                return warp_wait(abort_flag, Phase{&bars[b], parity});
             };
+            // tile i's scores (or, behind the last two tiles, just the products before) are complete
+            auto formed = [&](int i) { return wait(XF_S + (i & 1), i >> 1 & 1); };
             // One tile; a copy of its own for tiles with absent keys, whose
             // selects otherwise run for every tile.  Scalar fp32 operations:
             // paired ones (fma.f32x2) have no more throughput here and
             // measured 10 % slower.
-            auto tile = [&](auto masked, int i, const KeyBits &kb) -> bool {
-                float x[128];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) tmem_ld32(trow + j * 32, reinterpret_cast<uint32_t *>(x) + j * 32);
+            auto tile = [&](auto masked, int i) -> bool {
+                const uint32_t ts = trow + (i & 1) * 64;
+                float x[64];
+                tmem_ld32(ts, reinterpret_cast<uint32_t *>(x));
+                tmem_ld32(ts + 32, reinterpret_cast<uint32_t *>(x) + 32);
                 tc::tmem_wait_ld();
-                if (L::P_APART) {
-                    tc::tc_fence_before();
-                    warp_arrive(&bars[XF_R], lane);
-                }
                 if constexpr (decltype(masked)::value) {
+                    const KeyBits<2> kb = key_bits<2>(A.mask, u.seq, (t0 + i) * kFwdKeys, lane);
 #pragma unroll
-                    for (int j = 0; j < 128; ++j)
+                    for (int j = 0; j < 64; ++j)
                         if (!((kb.w[j >> 5] >> (j & 31)) & 1u)) x[j] = -INFINITY;
                 }
                 float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int j = 4; j < 124; j += 8) {
+                for (int j = 4; j < 60; j += 8) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], x[j + e]), x[j + 4 + e]);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[124 + e]);
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[60 + e]);
                 const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                // O and P may be written once the product of the tile before is complete
-                if (L::P_APART && i > 0) {
-                    if (!wait(XF_O, (i - 1) & 1)) return false;
-                    tc::tc_fence_after();
-                }
                 const bool grow = mt > m + 8.f;
                 if (__any_sync(0xffffffffu, grow)) {
                     const float mnew = grow ? mt : m;
@@ -255,6 +218,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                     l *= f;
                     m = mnew;
                     if (i > 0) {
+                        if (!formed(i + 1)) return false;   // P V of the tile before is complete
+                        tc::tc_fence_after();
 #pragma unroll 1
                         for (int j = 0; j < D; j += 16) {
                             uint32_t y[16];
@@ -268,36 +233,30 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                 }
                 const float base = m == -INFINITY ? 0.f : m - kShift;
                 float sum[4] = {};
+                uint32_t p[32];
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float a = xex2(fmaf(x[h * 32 + 2 * j], c, -base));
-                        const float b = xex2(fmaf(x[h * 32 + 2 * j + 1], c, -base));
-                        sum[2 * (j & 1)] += a;
-                        sum[2 * (j & 1) + 1] += b;
-                        p[j] = xpack<kFp16>(a, b);
-                    }
-                    tmem_st16(tp + h * 16, p);
-                    if (h & 1) {
-                        tmem_wait_st();
-                        tc::tc_fence_before();
-                        warp_arrive(&bars[XF_P + h / 2], lane);
-                    }
+                for (int j = 0; j < 32; ++j) {
+                    const float a = xex2(fmaf(x[2 * j], c, -base));
+                    const float b = xex2(fmaf(x[2 * j + 1], c, -base));
+                    sum[2 * (j & 1)] += a;
+                    sum[2 * (j & 1) + 1] += b;
+                    p[j] = xpack<kFp16>(a, b);
                 }
+                tmem_st32(ts, p);
+                tmem_wait_st();
+                tc::tc_fence_before();
+                warp_arrive(&bars[XF_P + (i & 1)], lane);
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 return true;
             };
             bool ok = true;
             for (int i = 0; i < n && ok; ++i) {
-                const KeyBits kb = key_bits(A.mask, u.seq, (t0 + i) * kXRows, lane);
-                ok = wait(XF_S, i & 1);
+                ok = formed(i);
                 if (!ok) break;
                 tc::tc_fence_after();
-                ok = kb.all() ? tile(std::false_type{}, i, kb) : tile(std::true_type{}, i, kb);
+                ok = i < partial ? tile(std::false_type{}, i) : tile(std::true_type{}, i);
             }
-            if (ok) ok = L::P_APART ? wait(XF_O, (n - 1) & 1) : wait(XF_S, n & 1);
+            if (ok) ok = formed(n + 1);
             if (!ok && lane == 0) fail();
             tc::tc_fence_after();
         }
@@ -402,8 +361,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 template <bool kFp16, int D>
 cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s) {
     CUtensorMap mq, mk, mv;
-    if (!x_map_q(&mq, io.query, d, a, d.q_stride) || !x_map_k(&mk, io.key, io.query, d, a, d.k_stride) ||
-        !x_map_k(&mv, io.value, io.query, d, a, d.v_stride))
+    if (!x_map_q(&mq, io.query, d, a, d.q_stride) || !x_map_k(&mk, io.key, io.query, d, d.k_stride, kFwdKeys) ||
+        !x_map_k(&mv, io.value, io.query, d, d.v_stride, kFwdKeys))
         return cudaErrorInvalidValue;
     return x_launch(k_xfwd<kFp16, D>, units * a.nsplit, kFwdThreads, a.nsplit, FwdShape<D>::TOTAL, s, mq, mk, mv, a);
 }

@@ -35,11 +35,11 @@ inline bool x_map_q(CUtensorMap *m, const void *base, const sca_desc &d, const X
     return x_map(m, rows ? base : other, d.dtype == SAG_FP16, d.d, rows ? d.n1 : d.n2, rows ? rows : 1,
                  rows && stride ? stride : (int64_t)(rows ? d.n1 : d.n2) * d.d, rows ? a.group : 1, a.tpt);
 }
-inline bool x_map_k(CUtensorMap *m, const void *base, const void *other, const sca_desc &d, const XArgs &a,
-                    int64_t stride) {
+inline bool x_map_k(CUtensorMap *m, const void *base, const void *other, const sca_desc &d, int64_t stride,
+                    int box_rows) {
     const int64_t rows = x_rows_k(d);
     return x_map(m, rows ? base : other, d.dtype == SAG_FP16, d.d, rows ? d.n2 : d.n1, rows ? rows : 1,
-                 rows && stride ? stride : (int64_t)(rows ? d.n2 : d.n1) * d.d, 1, kXRows);
+                 rows && stride ? stride : (int64_t)(rows ? d.n2 : d.n1) * d.d, 1, box_rows);
 }
 
 template <class... P, class... Args>
