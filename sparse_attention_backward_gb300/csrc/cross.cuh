@@ -41,7 +41,7 @@ struct XArgs {
 };
 
 // units: query (k_xdkv: key) tiles times key/value heads
-cudaError_t launch_xfwd(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s);
+cudaError_t launch_xfwd(const XArgs &a, const sca_io &io, const sca_desc &d, bool long_loops, int units, cudaStream_t s);
 cudaError_t launch_xpre(const XArgs &a, bool fp16, int d, cudaStream_t s);
 cudaError_t launch_xdq(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s);
 cudaError_t launch_xdkv(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s);
@@ -303,11 +303,12 @@ __device__ __forceinline__ void mma_abt(uint32_t acc, uint32_t a, uint32_t b, ui
                 idesc, kk > 0);
 }
 // A [128 x kK] in TMEM (16-bit pairs; the second half of kK = 128 starts kGap columns after the first), B [kK x D] MN-major.
-template <int kK, int kGap>
+// Steps kFrom .. kTo - 1 of kK / 16.
+template <int kK, int kGap, int kFrom = 0, int kTo = kK / 16>
 __device__ __forceinline__ void mma_ab(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
     const uint32_t bl = desc_lo(b, kK * 128);
 #pragma unroll
-    for (int kk = 0; kk < kK / 16; ++kk)
+    for (int kk = kFrom; kk < kTo; ++kk)
         xmma_ts(acc, a + (kk >> 2) * kGap + (kk & 3) * 8, bl + (kk * 2048 >> 4), idesc, accumulate || kk > 0);
 }
 

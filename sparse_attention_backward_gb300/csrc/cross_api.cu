@@ -1,7 +1,6 @@
 // C ABI of the cross attention: validation and workspace sizes (phase 1),
 // sequence tables and launches (phase 2).
 #include <math.h>
-#include <stdlib.h>
 
 #include "cross.cuh"
 #include "kernels.cuh"
@@ -182,9 +181,10 @@ extern "C" sag_status cross_attn_fwd(const sca_desc *desc, const sca_io *io, voi
     if (x_table(&a, desc, p, ws, s) != cudaSuccess) return SAG_ERR_CUDA;
     const int units = (int)(p.q_tiles * desc->n2);
     a.nsplit = split_of(units, 2 * p.max_k, 2 * current_device_sms());   // two CTAs an SM
-    const char *e = getenv("XSPLIT"); if (e) a.nsplit = atoi(e);
+    // full query tiles, and at least 2048 keys a CTA
+    const bool long_loops = p.max_q > 1 && p.max_k >= 16 * a.nsplit;
     a.n_status = units * a.nsplit;
-    return launch_xfwd(a, *io, *desc, units, s) == cudaSuccess ? SAG_OK : SAG_ERR_CUDA;
+    return launch_xfwd(a, *io, *desc, long_loops, units, s) == cudaSuccess ? SAG_OK : SAG_ERR_CUDA;
 }
 
 extern "C" sag_status cross_attn_grad(const sca_desc *desc, const sca_io *io, void *workspace, size_t workspace_bytes,

@@ -162,6 +162,7 @@ enum { XB_XY = 0, XB_S = 1, XB_DP = 3, XB_PF = 4, XB_DS = 5, XB_ACC = 6, XB_DRAI
 struct Ring {
     uint64_t *full, *empty;
     int n;
+    __device__ __forceinline__ Phase landed(int i) const { return Phase{&full[i % n], (uint32_t)(i / n) & 1u}; }
 };
 
 __device__ __forceinline__ bool ring_wait_free(const Ring &r, int i, volatile int *abort) {
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const int cover = A.s1_pad ? A.s1_pad : u.seq.qlen;
     const int nkt = tok0 < u.seq.qlen ? (u.seq.klen + kXRows - 1) / kXRows : 0;
     const int t0 = (int)((int64_t)nkt * rank / ns), n = (int)((int64_t)nkt * (rank + 1) / ns) - t0;
+    const int partial = A.mask ? 0 : u.seq.klen / kXRows - t0;   // tiles from this one on may lack keys
     float up = 0.f;                                      // exponent that dS is scaled by
     if constexpr (kFp16) {
         up = ds_exponent(A, u.seq, seq_row(A.seq, u.b + 1), u.head, reinterpret_cast<float *>(smem + L::OFF_STAT));
@@ -283,54 +285,50 @@ __global__ void __launch_bounds__(kXThreads, 1)
         // ------------------------------------------------------ MMA issuer
         constexpr uint32_t id_s = tc::idesc_f16(kXRows, kXRows, !kFp16, false, false);
         constexpr uint32_t id_q = tc::idesc_f16(kXRows, D, !kFp16, false, true);
-        auto wait = [&](uint64_t *b, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, tc::mbar_wait(b, parity, abort_flag, kXWaitNs));
-        };
-        // a product is issued behind its tile's wait, which another product's queue hides (see the forward)
-        auto wait_k = [&](int i) { return wait(&ra.full[i % L::RA], (i / L::RA) & 1); };
-        auto wait_v = [&](int i) { return wait(&rb.full[i % L::RB], (i / L::RB) & 1); };
+        auto k_in = [&](int i) { return ra.landed(i); };
+        auto v_in = [&](int i) { return rb.landed(i); };
         auto issue_s = [&](int i) {
-            tc::tc_fence_after();
             mma_abt<D, kXRows>(tmem + (i & 1) * 128, sbase + L::OFF_X, sbase + L::OFF_A + i % L::RA * L::TILE, id_s);
             tc::mma_commit_warp(&bars[XB_S + (i & 1)]);
         };
         auto issue_dp = [&](int i) {
-            tc::tc_fence_after();
             mma_abt<D, kXRows>(tmem + 256, sbase + L::OFF_Y, sbase + L::OFF_B + i % L::RB * L::TILE, id_s);
             tc::mma_commit_warp(&bars[XB_DP]);
             tc::mma_commit_warp(&rb.empty[i % L::RB]);
         };
-        KeyBits<4> kb = key_bits<4>(A.mask, u.seq, t0 * kXRows, lane);
-        bool ok = n == 0 || (wait(&bars[XB_XY], 0) && wait_k(0));
-        if (ok && n > 0) {
-            issue_s(0);
-            ok = wait_v(0);
+        bool ok = true;
+        if (n > 0) {
+            ok = warp_wait(abort_flag, Phase{&bars[XB_XY], 0}, k_in(0));
+            tc::tc_fence_after();
+            if (ok) issue_s(0);
+            ok = ok && warp_wait(abort_flag, v_in(0));
             if (ok) issue_dp(0);
             if (ok && n > 1) {
-                ok = wait_k(1);
+                ok = warp_wait(abort_flag, k_in(1));
                 if (ok) issue_s(1);
-                ok = ok && wait_v(1);
             }
         }
         for (int i = 0; i < n && ok; ++i) {
             // the next dP once this one has been read, then this tile's dQ, then the scores two tiles on
             if (i + 1 < n) {
-                if (!wait(&bars[XB_PF], i & 1)) { ok = false; break; }
+                ok = warp_wait(abort_flag, Phase{&bars[XB_PF], (uint32_t)i & 1u}, v_in(i + 1));
+                if (!ok) break;
+                tc::tc_fence_after();
                 issue_dp(i + 1);
             }
-            if (!wait(&bars[XB_DS], i & 1)) { ok = false; break; }
-            tc::tc_fence_after();
+            const Phase ds{&bars[XB_DS], (uint32_t)i & 1u};
+            ok = i + 2 < n ? warp_wait(abort_flag, ds, k_in(i + 2)) : warp_wait(abort_flag, ds);
+            if (!ok) break;
             const uint32_t kt = L::OFF_A + i % L::RA * L::TILE;
-            // S(i) has read this tile already (dS(i) follows from it), so its dead rows may go
-            if (!kb.all()) zero_rows<L::KC>(smem + kt, kb, lane);
+            if (i >= partial) {
+                // S(i) has read this tile already (dS(i) follows from it), so its dead rows may go
+                const KeyBits<4> kb = key_bits<4>(A.mask, u.seq, (t0 + i) * kXRows, lane);
+                if (!kb.all()) zero_rows<L::KC>(smem + kt, kb, lane);
+            }
+            tc::tc_fence_after();
             mma_ab<kXRows, 64>(tmem + 384, tmem + (i & 1) * 128, sbase + kt, id_q, i > 0);
             tc::mma_commit_warp(&ra.empty[i % L::RA]);
-            if (i + 2 < n) {
-                if (!wait_k(i + 2)) { ok = false; break; }
-                issue_s(i + 2);
-                if (!wait_v(i + 2)) { ok = false; break; }
-            }
-            if (i + 1 < n) kb = key_bits<4>(A.mask, u.seq, (t0 + i + 1) * kXRows, lane);
+            if (i + 2 < n) issue_s(i + 2);
         }
         if (!ok && lane == 0) fail();
         tc::mma_commit_warp(&bars[XB_ACC]);
@@ -346,12 +344,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
         const float c = A.scale_log2, nl = st[r] + up, nd = st[128 + r];
         bool ok = true;
         for (int i = 0; i < n; ++i) {
-            const KeyBits<4> kb = key_bits<4>(A.mask, u.seq, (t0 + i) * kXRows, lane);
             const uint32_t ts = trow + (i & 1) * 128 + h * 64;
-            if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[XB_S + (i & 1)], (i >> 1) & 1, abort_flag, kXWaitNs))) {
-                ok = false;
-                break;
-            }
+            ok = warp_wait(abort_flag, Phase{&bars[XB_S + (i & 1)], (uint32_t)(i >> 1) & 1u});
+            if (!ok) break;
             tc::tc_fence_after();
             // dS over the scores; a copy of its own for tiles with absent keys
             auto tile = [&](auto masked) -> bool {
@@ -361,7 +356,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 tc::tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 64; ++j) p[j] = xex2(fmaf(p[j], c, nl));
-                if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[XB_DP], i & 1, abort_flag, kXWaitNs))) return false;
+                if (!warp_wait(abort_flag, Phase{&bars[XB_DP], (uint32_t)i & 1u})) return false;
                 tc::tc_fence_after();
                 float y[64];
                 tmem_ld32(trow + 256 + h * 64, reinterpret_cast<uint32_t *>(y));
@@ -369,6 +364,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 tc::tmem_wait_ld();
                 tc::tc_fence_before();
                 warp_arrive(&bars[XB_PF], lane);           // dP has been read
+                KeyBits<4> kb{};
+                if constexpr (decltype(masked)::value) kb = key_bits<4>(A.mask, u.seq, (t0 + i) * kXRows, lane);
                 uint32_t q[32];
 #pragma unroll
                 for (int j = 0; j < 64; j += 2) {
@@ -386,10 +383,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 warp_arrive(&bars[XB_DS], lane);
                 return true;
             };
-            ok = kb.all() ? tile(std::false_type{}) : tile(std::true_type{});
+            ok = i < partial ? tile(std::false_type{}) : tile(std::true_type{});
             if (!ok) break;
         }
-        if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[XB_ACC], 0, abort_flag, kXWaitNs));
+        if (ok) ok = warp_wait(abort_flag, Phase{&bars[XB_ACC], 0});
         if (!ok && lane == 0) fail();
         tc::tc_fence_after();
     }
@@ -542,13 +539,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
         // ------------------------------------------------------ MMA issuer
         constexpr uint32_t id_s = tc::idesc_f16(kXRows, kXRows, !kFp16, false, false);
         constexpr uint32_t id_g = tc::idesc_f16(kXRows, D, !kFp16, false, true);
-        auto wait = [&](uint64_t *b, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, tc::mbar_wait(b, parity, abort_flag, kXWaitNs));
-        };
-        // a ring tile has landed; rows behind the sequence's (or the tile's) last one are zeroed
-        auto take = [&](const Ring &rg, int off, int i) -> bool {
-            const int s = i % rg.n;
-            if (!wait(&rg.full[s], (i / rg.n) & 1)) return false;
+        // rows behind the sequence's (or the tile's) last one are zeroed in a tile that has landed
+        auto clear = [&](int off, int s, int i) {
             const int left = u.seq.qlen - (t0 + i) * A.tpt;
             const int live = (left < A.tpt ? left : A.tpt) * G;
             if (live < kXRows) {
@@ -557,32 +549,39 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 zero_rows<L::KC>(smem + off + s * L::TILE, kb, lane);
             }
             tc::tc_fence_after();
-            return true;
         };
-        auto issue_s = [&](int i) -> bool {
-            if (!take(ra, L::OFF_A, i)) return false;
+        auto issue_s = [&](int i) {
+            clear(L::OFF_A, i % L::RA, i);
             mma_abt<D, kXRows>(tmem, sbase + L::OFF_X, sbase + L::OFF_A + (i % L::RA) * L::TILE, id_s);
             tc::mma_commit_warp(&bars[XB_S]);
-            return true;
         };
-        auto issue_dp = [&](int i) -> bool {
-            if (!take(rb, L::OFF_B, i)) return false;
+        auto issue_dp = [&](int i) {
+            clear(L::OFF_B, i % L::RB, i);
             mma_abt<D, kXRows>(tmem + 128, sbase + L::OFF_Y, sbase + L::OFF_B + (i % L::RB) * L::TILE, id_s);
             tc::mma_commit_warp(&bars[XB_DP]);
-            return true;
         };
-        bool ok = n == 0 || (wait(&bars[XB_XY], 0) && issue_s(0) && issue_dp(0));
+        bool ok = true;
+        if (n > 0) {
+            ok = warp_wait(abort_flag, Phase{&bars[XB_XY], 0}, ra.landed(0));
+            if (ok) issue_s(0);
+            ok = ok && warp_wait(abort_flag, rb.landed(0));
+            if (ok) issue_dp(0);
+        }
         for (int i = 0; i < n && ok; ++i) {
-            if (!wait(&bars[XB_PF], i & 1)) { ok = false; break; }
+            const Phase p{&bars[XB_PF], (uint32_t)i & 1u}, ds{&bars[XB_DS], (uint32_t)i & 1u};
+            const bool more = i + 1 < n;
+            ok = more ? warp_wait(abort_flag, p, ra.landed(i + 1)) : warp_wait(abort_flag, p);
+            if (!ok) break;
             tc::tc_fence_after();
             mma_ab<kXRows, 64>(tmem + 256, tmem, sbase + L::OFF_B + (i % L::RB) * L::TILE, id_g, i > 0);
             tc::mma_commit_warp(&rb.empty[i % L::RB]);
-            if (i + 1 < n && !issue_s(i + 1)) { ok = false; break; }
-            if (!wait(&bars[XB_DS], i & 1)) { ok = false; break; }
+            if (more) issue_s(i + 1);
+            ok = more ? warp_wait(abort_flag, ds, rb.landed(i + 1)) : warp_wait(abort_flag, ds);
+            if (!ok) break;
             tc::tc_fence_after();
             mma_ab<kXRows, 64>(tmem + 384, tmem + 128, sbase + L::OFF_A + (i % L::RA) * L::TILE, id_g, i > 0);
             tc::mma_commit_warp(&ra.empty[i % L::RA]);
-            if (i + 1 < n && !issue_dp(i + 1)) { ok = false; break; }
+            if (more) issue_dp(i + 1);
         }
         if (!ok && lane == 0) fail();
         tc::mma_commit_warp(&bars[XB_ACC]);
@@ -624,7 +623,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             tmem_wait_st();
             tc::tc_fence_before();
             warp_arrive(&bars[XB_PF], lane);
-            if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[XB_DP], i & 1, abort_flag, kXWaitNs))) return false;
+            if (!warp_wait(abort_flag, Phase{&bars[XB_DP], (uint32_t)i & 1u})) return false;
             tc::tc_fence_after();
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
@@ -657,13 +656,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
         const bool all = __all_sync(0xffffffffu, live);
         bool ok = true;
         for (int i = 0; i < n && ok; ++i) {
-            ok = tc::mbar_wait(&rs.full[i & 1], (i >> 1) & 1, abort_flag, kXWaitNs);
-            ok = ok && tc::mbar_wait(&bars[XB_S], i & 1, abort_flag, kXWaitNs);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            ok = warp_wait(abort_flag, rs.landed(i), Phase{&bars[XB_S], (uint32_t)i & 1u});
+            if (!ok) break;
             tc::tc_fence_after();
             ok = all ? tile(std::false_type{}, i) : tile(std::true_type{}, i);
         }
-        if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[XB_ACC], 0, abort_flag, kXWaitNs));
+        if (ok) ok = warp_wait(abort_flag, Phase{&bars[XB_ACC], 0});
         if (!ok && lane == 0) fail();
         tc::tc_fence_after();
     }

@@ -2,10 +2,10 @@
 // each query row's sequence, one pass with a running maximum and sum.
 //
 // A CTA takes a tile of 128 query rows of one key/value head and walks over
-// tiles of 64 keys: S = Q K^T and O += P V on the tensor cores (tcgen05), S, P
+// key tiles of 64 (or 128): S = Q K^T and O += P V on the tensor cores (tcgen05), S, P
 // and O in TMEM, P over its S as the TMEM operand of the second product, so
 // that scores and probabilities never touch shared memory.  Two score tiles
-// are in flight: while the softmax (four warps, a thread a row, no shuffles)
+// of 64 keys are in flight: while the softmax (four warps, a thread a row, no shuffles)
 // works on one, the MMA warp multiplies the other's P and forms the scores
 // after it.  Two CTAs share an SM (256 TMEM columns and at most 113 KB each),
 // so one's start and end run beside the other's loop as well.
@@ -32,15 +32,15 @@ namespace sag {
 namespace {
 
 constexpr int kFwdThreads = 192, kFwdTma = 4, kFwdMma = 5;   // warps 0-3 softmax and epilogue, then TMA and MMA
-constexpr int kFwdKeys = 64;
 
-// TMEM columns: S of even / odd tiles 0 / 64, O 128.
-template <int D>
+// kKeys: keys of a tile.  TMEM columns: S of BUFS tiles in flight from 0, O 128.
+template <int D, int kKeys>
 struct FwdShape {
+    static constexpr int BUFS = 128 / kKeys, HALVES = kKeys / 64;
     static constexpr int KC = D / 64;
     static constexpr int Q_BYTES = KC * 16384;
-    static constexpr int TILE = KC * kFwdKeys * 128;
-    static constexpr int STAGES = D == 64 ? 8 : 5;                // K and V tiles
+    static constexpr int TILE = KC * kKeys * 128;
+    static constexpr int STAGES = 81920 / TILE;                   // K and V tiles
     static constexpr int OFF_RING = Q_BYTES;
     static constexpr int OFF_BAR = OFF_RING + STAGES * TILE;
     static constexpr int TOTAL = OFF_BAR + 256;
@@ -53,11 +53,12 @@ struct FwdShape {
 // XF_S: scores of an even / odd tile formed, and P V of the tile two before complete; XF_P: P written
 enum { XF_Q = 0, XF_S = 1, XF_P = 3, XF_DRAIN = 5, XF_FULL = 6 };
 
-template <bool kFp16, int D>
+template <bool kFp16, int D, int kKeys>
 __global__ void __launch_bounds__(kFwdThreads, 2)
     k_xfwd(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
            const __grid_constant__ CUtensorMap map_v, const __grid_constant__ XArgs A) {
-    using L = FwdShape<D>;
+    using L = FwdShape<D, kKeys>;
+    constexpr int NB = L::BUFS;
     constexpr int ST = L::STAGES;
     constexpr float kShift = kFp16 ? kFwdShiftF16 : 0.f;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -90,9 +91,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     const uint32_t sbase = tc::smem_u32(smem);
     const int G = A.group, tok0 = u.tile * A.tpt;
     const int cover = A.s1_pad ? A.s1_pad : u.seq.qlen;
-    const int nkt = tok0 < u.seq.qlen ? (u.seq.klen + kFwdKeys - 1) / kFwdKeys : 0;
+    const int nkt = tok0 < u.seq.qlen ? (u.seq.klen + kKeys - 1) / kKeys : 0;
     const int t0 = (int)((int64_t)nkt * rank / ns), n = (int)((int64_t)nkt * (rank + 1) / ns) - t0;
-    const int partial = A.mask ? 0 : u.seq.klen / kFwdKeys - t0;    // tiles from this one on may lack keys
+    const int partial = A.mask ? 0 : u.seq.klen / kKeys - t0;    // tiles from this one on may lack keys
     auto fail = [&]() { *abort_flag = 1; };
 
     if (warp >= kFwdTma) {
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                     if (use > 0 && !tc::mbar_wait(&empty[s], (use - 1) & 1, abort_flag, kXWaitNs)) return false;
                     tc::mbar_arrive_expect_tx(&full[s], L::TILE);
                     for (int c = 0; c < L::KC; ++c)
-                        tc::tma_load_3d(smem + L::OFF_RING + s * L::TILE + c * kFwdKeys * 128, map, c * 64, u.head,
+                        tc::tma_load_3d(smem + L::OFF_RING + s * L::TILE + c * kKeys * 128, map, c * 64, u.head,
                                         u.seq.k0 + key, &full[s]);
                     ++loads;
                     return true;
@@ -114,10 +115,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                 tc::mbar_arrive_expect_tx(&bars[XF_Q], (uint32_t)L::KC * A.tpt * G * 128);
                 for (int c = 0; c < L::KC; ++c)
                     tc::tma_load_3d(smem + c * 16384, &map_q, c * 64, u.head * G, u.seq.q0 + tok0, &bars[XF_Q]);
-                // in the order the MMA warp takes them: K 0, K 1, then V i and K i + 2
-                for (int i = -2; i < n && ok; ++i) {
-                    if (i >= 0) ok = stage(&map_v, (t0 + i) * kFwdKeys);
-                    if (ok && i + 2 < n) ok = stage(&map_k, (t0 + i + 2) * kFwdKeys);
+                // in the order the MMA warp takes them: the first K, then V i and K i + NB
+                for (int i = -NB; i < n && ok; ++i) {
+                    if (i >= 0) ok = stage(&map_v, (t0 + i) * kKeys);
+                    if (ok && i + NB < n) ok = stage(&map_k, (t0 + i + NB) * kKeys);
                 }
                 if (!ok) fail();
                 // every load issued must have landed before the CTA exits
@@ -131,37 +132,49 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             // The tensor pipe queues about four instructions (256 cycles),
             // which hides a wait, a commit or some arithmetic between two
             // products, but not all of a tile's together: they are spread.
-            constexpr uint32_t id_s = tc::idesc_f16(kXRows, kFwdKeys, !kFp16, false, false);
+            constexpr uint32_t id_s = tc::idesc_f16(kXRows, kKeys, !kFp16, false, false);
             constexpr uint32_t id_o = tc::idesc_f16(kXRows, D, !kFp16, false, true);
             const uint32_t ring = sbase + L::OFF_RING;
-            // load j of the ring: K 0, K 1, then V i behind min(i + 2, n) tiles of K, and K i + 2
+            // load j of the ring: the first K tiles, then V i (behind min(i + NB, n) tiles of K) and K i + NB
             auto landed = [&](int j) { return Phase{&full[j % ST], (uint32_t)(j / ST) & 1u}; };
             auto issue_s = [&](int i, int j) {
-                mma_abt<D, kFwdKeys>(tmem + (i & 1) * 64, sbase, ring + j % ST * L::TILE, id_s);
-                tc::mma_commit_warp(&bars[XF_S + (i & 1)]);
+                mma_abt<D, kKeys>(tmem + i % NB * kKeys, sbase, ring + j % ST * L::TILE, id_s);
+                tc::mma_commit_warp(&bars[XF_S + i % NB]);
                 tc::mma_commit_warp(&empty[j % ST]);
             };
             bool ok = true;
-            for (int i = 0; i < 2 && i < n && ok; ++i) {
+            for (int i = 0; i < NB && i < n && ok; ++i) {
                 ok = warp_wait(abort_flag, Phase{&bars[XF_Q], 0}, landed(i));
                 tc::tc_fence_after();
                 if (ok) issue_s(i, i);
             }
             for (int i = 0; i < n && ok; ++i) {
-                const bool more = i + 2 < n;
-                const int jv = i + (i + 2 < n ? i + 2 : n);
-                const Phase pv{&bars[XF_P + (i & 1)], (uint32_t)(i >> 1) & 1u};
-                ok = more ? warp_wait(abort_flag, pv, landed(jv), landed(jv + 1)) : warp_wait(abort_flag, pv, landed(jv));
+                const bool more = i + NB < n;
+                const int jv = i + (more ? i + NB : n);
+                const uint32_t vt = ring + jv % ST * L::TILE, acc = tmem + 128, pt = tmem + i % NB * kKeys;
+                // P (its first half), V, and with the last half the K tile of the scores that follow
+                auto written = [&](int h) {
+                    return L::HALVES == 2 ? Phase{&bars[XF_P + h], (uint32_t)i & 1u}
+                                          : Phase{&bars[XF_P + (i & 1)], (uint32_t)(i >> 1) & 1u};
+                };
+                ok = L::HALVES == 1 && more ? warp_wait(abort_flag, written(0), landed(jv), landed(jv + 1))
+                                            : warp_wait(abort_flag, written(0), landed(jv));
                 if (!ok) break;
                 if (i >= partial) {
-                    const KeyBits<2> kb = key_bits<2>(A.mask, u.seq, (t0 + i) * kFwdKeys, lane);
-                    if (!kb.all()) zero_rows<L::KC, 2>(smem + L::OFF_RING + jv % ST * L::TILE, kb, lane);
+                    const KeyBits<kKeys / 32> kb = key_bits<kKeys / 32>(A.mask, u.seq, (t0 + i) * kKeys, lane);
+                    if (!kb.all()) zero_rows<L::KC>(smem + L::OFF_RING + jv % ST * L::TILE, kb, lane);
                 }
                 tc::tc_fence_after();
-                mma_ab<kFwdKeys, 32>(tmem + 128, tmem + (i & 1) * 64, ring + jv % ST * L::TILE, id_o, i > 0);
+                mma_ab<kKeys, 32, 0, 4>(acc, pt, vt, id_o, i > 0);
+                if (L::HALVES == 2) {
+                    ok = more ? warp_wait(abort_flag, written(1), landed(jv + 1)) : warp_wait(abort_flag, written(1));
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    mma_ab<kKeys, 32, 4, kKeys / 16>(acc, pt, vt, id_o, true);
+                }
                 tc::mma_commit_warp(&empty[jv % ST]);
-                if (more) issue_s(i + 2, jv + 1);
-                else tc::mma_commit_warp(&bars[XF_S + (i & 1)]);
+                if (more) issue_s(i + NB, jv + 1);
+                else tc::mma_commit_warp(&bars[XF_S + i % NB]);
             }
             if (!ok && lane == 0) fail();
             // every MMA issued must be complete before TMEM is freed
@@ -185,31 +198,31 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                 return warp_wait(abort_flag, Phase{&bars[b], parity});
             };
             // tile i's scores (or, behind the last two tiles, just the products before) are complete
-            auto formed = [&](int i) { return wait(XF_S + (i & 1), i >> 1 & 1); };
+            auto formed = [&](int i) { return wait(XF_S + i % NB, (uint32_t)(i / NB) & 1u); };
             // One tile; a copy of its own for tiles with absent keys, whose
             // selects otherwise run for every tile.  Scalar fp32 operations:
             // paired ones (fma.f32x2) have no more throughput here and
             // measured 10 % slower.
             auto tile = [&](auto masked, int i) -> bool {
-                const uint32_t ts = trow + (i & 1) * 64;
-                float x[64];
-                tmem_ld32(ts, reinterpret_cast<uint32_t *>(x));
-                tmem_ld32(ts + 32, reinterpret_cast<uint32_t *>(x) + 32);
+                const uint32_t ts = trow + i % NB * kKeys;
+                float x[kKeys];
+#pragma unroll
+                for (int j = 0; j < kKeys; j += 32) tmem_ld32(ts + j, reinterpret_cast<uint32_t *>(x) + j);
                 tc::tmem_wait_ld();
                 if constexpr (decltype(masked)::value) {
-                    const KeyBits<2> kb = key_bits<2>(A.mask, u.seq, (t0 + i) * kFwdKeys, lane);
+                    const KeyBits<kKeys / 32> kb = key_bits<kKeys / 32>(A.mask, u.seq, (t0 + i) * kKeys, lane);
 #pragma unroll
-                    for (int j = 0; j < 64; ++j)
+                    for (int j = 0; j < kKeys; ++j)
                         if (!((kb.w[j >> 5] >> (j & 31)) & 1u)) x[j] = -INFINITY;
                 }
                 float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int j = 4; j < 60; j += 8) {
+                for (int j = 4; j < kKeys - 4; j += 8) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], x[j + e]), x[j + 4 + e]);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[60 + e]);
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[kKeys - 4 + e]);
                 const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
                 const bool grow = mt > m + 8.f;
                 if (__any_sync(0xffffffffu, grow)) {
@@ -218,7 +231,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                     l *= f;
                     m = mnew;
                     if (i > 0) {
-                        if (!formed(i + 1)) return false;   // P V of the tile before is complete
+                        if (!formed(i - 1 + NB)) return false;   // P V of the tile before is complete
                         tc::tc_fence_after();
 #pragma unroll 1
                         for (int j = 0; j < D; j += 16) {
@@ -233,19 +246,22 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                 }
                 const float base = m == -INFINITY ? 0.f : m - kShift;
                 float sum[4] = {};
-                uint32_t p[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float a = xex2(fmaf(x[2 * j], c, -base));
-                    const float b = xex2(fmaf(x[2 * j + 1], c, -base));
-                    sum[2 * (j & 1)] += a;
-                    sum[2 * (j & 1) + 1] += b;
-                    p[j] = xpack<kFp16>(a, b);
+                for (int h = 0; h < L::HALVES; ++h) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float a = xex2(fmaf(x[h * 64 + 2 * j], c, -base));
+                        const float b = xex2(fmaf(x[h * 64 + 2 * j + 1], c, -base));
+                        sum[2 * (j & 1)] += a;
+                        sum[2 * (j & 1) + 1] += b;
+                        p[j] = xpack<kFp16>(a, b);
+                    }
+                    tmem_st32(ts + h * 32, p);
+                    tmem_wait_st();
+                    tc::tc_fence_before();
+                    warp_arrive(&bars[XF_P + (L::HALVES == 2 ? h : i & 1)], lane);
                 }
-                tmem_st32(ts, p);
-                tmem_wait_st();
-                tc::tc_fence_before();
-                warp_arrive(&bars[XF_P + (i & 1)], lane);
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 return true;
             };
@@ -256,7 +272,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                 tc::tc_fence_after();
                 ok = i < partial ? tile(std::false_type{}, i) : tile(std::true_type{}, i);
             }
-            if (ok) ok = formed(n + 1);
+            if (ok) ok = formed(n - 1 + NB);
             if (!ok && lane == 0) fail();
             tc::tc_fence_after();
         }
@@ -358,21 +374,28 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     }
 }
 
-template <bool kFp16, int D>
+template <bool kFp16, int D, int kKeys>
 cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s) {
     CUtensorMap mq, mk, mv;
-    if (!x_map_q(&mq, io.query, d, a, d.q_stride) || !x_map_k(&mk, io.key, io.query, d, d.k_stride, kFwdKeys) ||
-        !x_map_k(&mv, io.value, io.query, d, d.v_stride, kFwdKeys))
+    if (!x_map_q(&mq, io.query, d, a, d.q_stride) || !x_map_k(&mk, io.key, io.query, d, d.k_stride, kKeys) ||
+        !x_map_k(&mv, io.value, io.query, d, d.v_stride, kKeys))
         return cudaErrorInvalidValue;
-    return x_launch(k_xfwd<kFp16, D>, units * a.nsplit, kFwdThreads, a.nsplit, FwdShape<D>::TOTAL, s, mq, mk, mv, a);
+    return x_launch(k_xfwd<kFp16, D, kKeys>, units * a.nsplit, kFwdThreads, a.nsplit, FwdShape<D, kKeys>::TOTAL, s, mq, mk,
+                    mv, a);
 }
 
 }  // namespace
 
-cudaError_t launch_xfwd(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s) {
+// Tiles of 128 keys take 64 cycles a step for their scores where two of 64 take 96 (M = 128 rows re-read per instruction),
+// but leave one score tile in flight instead of two.  They are taken for 128-wide heads where products dominate: full
+// query tiles and long loops.  Measured, 64 against 128: 8192 x 4096 tokens 825 / 742 us, 130 x 131072 233 / 205;
+// 1024 x 1024 33 / 35, 2048 x 512 70 / 74, one token x 4096 69 / 74 us; 64-wide heads 582 / 596 us.
+cudaError_t launch_xfwd(const XArgs &a, const sca_io &io, const sca_desc &d, bool long_loops, int units, cudaStream_t s) {
     const bool fp16 = d.dtype == SAG_FP16;
-    if (d.d == 128) return fp16 ? launch<true, 128>(a, io, d, units, s) : launch<false, 128>(a, io, d, units, s);
-    return fp16 ? launch<true, 64>(a, io, d, units, s) : launch<false, 64>(a, io, d, units, s);
+    if (d.d == 128 && long_loops)
+        return fp16 ? launch<true, 128, 128>(a, io, d, units, s) : launch<false, 128, 128>(a, io, d, units, s);
+    if (d.d == 128) return fp16 ? launch<true, 128, 64>(a, io, d, units, s) : launch<false, 128, 64>(a, io, d, units, s);
+    return fp16 ? launch<true, 64, 64>(a, io, d, units, s) : launch<false, 64, 64>(a, io, d, units, s);
 }
 
 }  // namespace sag
