@@ -26,7 +26,10 @@ struct XArgs {
     int32_t n1, n2, group;
     int32_t tpt;                        // tokens per query tile
     int32_t s1_pad, s2_pad;             // BSND: padded lengths, else 0
+    int32_t units;                      // query (k_xdkv: key) tiles times key/value heads
     int32_t nsplit;                     // CTAs (one cluster) that share a unit
+    int32_t ctas;                       // of the launch: units * nsplit, or fewer that take unit after unit
+    unsigned *ticket;                   // next units of the two gradient kernels, zeroed by k_xpre
     float scale, scale_log2;
     const uint8_t *mask;
     const uint16_t *o_in, *dy, *v_in;   // preprocess
@@ -34,17 +37,16 @@ struct XArgs {
     uint16_t *o, *dq, *dk, *dv;
     float *lse;                         // forward: written, gradient: read
     float *stats;                       // [query tile][n2][256]: lse * log2(e), then Delta, of the tile's 128 rows
-    float *norms;                       // fp16: largest row norm of dY of each [query tile][n2], then of V of each [key tile][n2]
+    unsigned *norms;                    // fp16: [batch][n2][2] largest squared row norms of dY and of V, as float bits
     int32_t q_tiles, k_tiles;
     int32_t *count, *status;            // device status: number of words, one word for each CTA
     int32_t n_status;                   // value for *count
 };
 
-// units: query (k_xdkv: key) tiles times key/value heads
-cudaError_t launch_xfwd(const XArgs &a, const sca_io &io, const sca_desc &d, bool long_loops, int units, cudaStream_t s);
+cudaError_t launch_xfwd(const XArgs &a, const sca_io &io, const sca_desc &d, bool long_loops, cudaStream_t s);
 cudaError_t launch_xpre(const XArgs &a, bool fp16, int d, cudaStream_t s);
-cudaError_t launch_xdq(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s);
-cudaError_t launch_xdkv(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s);
+cudaError_t launch_xdq(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s);
+cudaError_t launch_xdkv(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s);
 
 namespace {
 
@@ -255,41 +257,49 @@ struct KeyBits {
         }
     }
 };
+// In two steps, so that a tile's mask bytes are on their way while the tile before is worked on.
 template <int kWords>
-__device__ __forceinline__ KeyBits<kWords> key_bits(const uint8_t *mask, const SeqRow &seq, int first, int lane) {
-    KeyBits<kWords> k;
-    const int left = seq.klen - first;
-    if (!mask) {
-        k.set_first(left);
+struct KeyLoad {
+    uint8_t byte[kWords];
+    int left;
+    bool masked;
+    __device__ __forceinline__ void start(const uint8_t *mask, const SeqRow &seq, int first, int lane) {
+        left = seq.klen - first;
+        masked = mask != nullptr;
+        if (!masked) return;
+        const uint8_t *m = mask + (int64_t)seq.k0 + first;
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) byte[j] = 32 * j + lane < left ? m[32 * j + lane] : (uint8_t)0;
+    }
+    __device__ __forceinline__ KeyBits<kWords> finish() const {
+        KeyBits<kWords> k;
+        if (!masked) {
+            k.set_first(left);
+            return k;
+        }
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) k.w[j] = __ballot_sync(0xffffffffu, byte[j] != 0);
         return k;
     }
-    const uint8_t *m = mask + (int64_t)seq.k0 + first;
-    bool on[kWords];
-#pragma unroll
-    for (int j = 0; j < kWords; ++j) on[j] = 32 * j + lane < left && m[32 * j + lane] != 0;
-#pragma unroll
-    for (int j = 0; j < kWords; ++j) k.w[j] = __ballot_sync(0xffffffffu, on[j]);
-    return k;
-}
+};
 
-// Zeros the rows of a [32 * kWords x 64 * kChunks] shared tile whose bit is not set, before the matrix product reads it: a
-// probability of 0 does not cancel a NaN.  Collective over the MMA warp.
-template <int kChunks, int kWords>
-__device__ __forceinline__ void zero_rows(uint8_t *tile, const KeyBits<kWords> &k, int lane) {
-    // eight lanes a row, four rows a step, every step independent of the others
-    uint8_t *at = tile + (lane >> 3) * 128 + (lane & 7) * 16;
+// Zeros the rows of a [32 * kWords x 64 * kChunks] shared tile whose bit is not set, before a matrix product reads it: a
+// probability of 0 does not cancel a NaN.  Shared by kThreads threads; each fences its writes for the products' proxy.
+template <int kChunks, int kWords, int kThreads>
+__device__ __forceinline__ void zero_rows(uint8_t *tile, const KeyBits<kWords> &k, int thread) {
+    constexpr int kRows = 32 * kWords, kPer = kThreads > kRows ? kThreads / kRows : 1;   // threads a row
 #pragma unroll
-    for (int j = 0; j < kWords; ++j) {
-        if (k.w[j] == 0xffffffffu) continue;
+    for (int j = 0; j < kRows * kPer / kThreads; ++j) {
+        const int row = (thread + j * kThreads) / kPer;
+        uint32_t w = k.w[0];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (!((k.w[j] >> (4 * i + (lane >> 3))) & 1u))
+        for (int i = 1; i < kWords; ++i) w = row >> 5 == i ? k.w[i] : w;
+        if (!((w >> (row & 31)) & 1u))
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c)
-                    *reinterpret_cast<uint4 *>(at + c * kWords * 4096 + (32 * j + 4 * i) * 128) = make_uint4(0, 0, 0, 0);
+            for (int c = thread % kPer; c < kChunks * 8; c += kPer)
+                *reinterpret_cast<uint4 *>(tile + (c >> 3) * kRows * 128 + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
     }
     tc::fence_proxy_async_smem();
-    __syncwarp();
 }
 
 // Products, each with K = 16 steps; a tile of R rows keeps its 64-column chunks 128 R bytes apart.
@@ -312,19 +322,44 @@ __device__ __forceinline__ void mma_ab(uint32_t acc, uint32_t a, uint32_t b, uin
         xmma_ts(acc, a + (kk >> 2) * kGap + (kk & 3) * 8, bl + (kk * 2048 >> 4), idesc, accumulate || kk > 0);
 }
 
-// 16-bit row piece of `n` (a multiple of 8) fp32 values
-template <bool kFp16, int n>
-__device__ __forceinline__ void store_row(uint16_t *dst, const float *x) {
+// Stores of accumulator rows.  A lane holds 32 columns of its own row; written as they stand, each instruction of a warp
+// would touch 32 lines for 16 bytes each.  Groups of four lanes swap their 16-byte pieces first (two steps of a 4 x 4
+// transposition), so that an instruction writes 64 consecutive bytes of eight rows.  Collective over a warp.
+template <bool kFp16>
+struct RowStore {
+    int64_t off[4];                     // elements from `base` to the rows of this lane's group; negative: not stored
+    __device__ __forceinline__ void rows(int64_t mine, int lane) {
 #pragma unroll
-    for (int j = 0; j < n; j += 8) {
-        uint4 v;
-        v.x = xpack<kFp16>(x[j], x[j + 1]);
-        v.y = xpack<kFp16>(x[j + 2], x[j + 3]);
-        v.z = xpack<kFp16>(x[j + 4], x[j + 5]);
-        v.w = xpack<kFp16>(x[j + 6], x[j + 7]);
-        *reinterpret_cast<uint4 *>(dst + j) = v;
+        for (int i = 0; i < 4; ++i) off[i] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + i);
     }
-}
+    // the lower lane of a pair gives b for the other's a
+    __device__ __forceinline__ static void trade(uint32_t &a, uint32_t &b, bool upper, int with) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? a : b, with);
+        a = upper ? got : a;
+        b = upper ? b : got;
+    }
+    __device__ __forceinline__ static void trade(uint4 &a, uint4 &b, bool upper, int with) {
+        trade(a.x, b.x, upper, with);
+        trade(a.y, b.y, upper, with);
+        trade(a.z, b.z, upper, with);
+        trade(a.w, b.w, upper, with);
+    }
+    __device__ __forceinline__ void store(uint16_t *base, const float *y, int col, int lane) const {
+        uint4 c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            c[k] = make_uint4(xpack<kFp16>(y[8 * k], y[8 * k + 1]), xpack<kFp16>(y[8 * k + 2], y[8 * k + 3]),
+                              xpack<kFp16>(y[8 * k + 4], y[8 * k + 5]), xpack<kFp16>(y[8 * k + 6], y[8 * k + 7]));
+        const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) trade(c[k], c[k + 1], odd, 1);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) trade(c[k], c[k + 2], high, 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (off[i] >= 0) *reinterpret_cast<uint4 *>(base + off[i] + col + 8 * (lane & 3)) = c[i];
+    }
+};
 
 }  // namespace
 }  // namespace sag

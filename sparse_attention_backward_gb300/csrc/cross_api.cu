@@ -10,6 +10,7 @@ namespace sag {
 namespace {
 
 constexpr size_t kAlign = 256;
+constexpr size_t kTicketAt = 16;            // two ticket counters
 constexpr size_t kStatusAt = 256;           // status words, behind the workspace's header
 size_t up256(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 // CTAs that splitting may add to a launch (it stops at one CTA per SM), for the status words
@@ -61,7 +62,7 @@ sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {
     take(sizeof(int32_t) * ctas);           // status words, one a CTA
     p->o_seq = take(seq_ws_bytes(d->batch));
     p->o_stats = take(grad ? sizeof(float) * 256 * p->q_tiles * d->n2 : 0);
-    p->o_norms = take(grad && p->fp16 ? sizeof(float) * (p->q_tiles + p->k_tiles) * d->n2 : 0);
+    p->o_norms = take(grad && p->fp16 ? sizeof(unsigned) * 2 * (size_t)d->batch * d->n2 : 0);
     p->total = o;
     return SAG_OK;
 }
@@ -96,10 +97,11 @@ XArgs x_args(const sca_desc *d, const sca_io *io, const XPlan &p, char *ws) {
     a.dv = static_cast<uint16_t *>(io->dv);
     a.lse = io->softmax_lse;
     a.stats = reinterpret_cast<float *>(ws + p.o_stats);
-    a.norms = reinterpret_cast<float *>(ws + p.o_norms);
+    a.norms = reinterpret_cast<unsigned *>(ws + p.o_norms);
     a.q_tiles = (int)p.q_tiles;
     a.k_tiles = (int)p.k_tiles;
     a.count = reinterpret_cast<int32_t *>(ws);
+    a.ticket = reinterpret_cast<unsigned *>(ws + kTicketAt);
     a.status = reinterpret_cast<int32_t *>(ws + kStatusAt);
     return a;
 }
@@ -179,12 +181,12 @@ extern "C" sag_status cross_attn_fwd(const sca_desc *desc, const sca_io *io, voi
         return cudaMemsetAsync(ws, 0, sizeof(int32_t), s) == cudaSuccess ? SAG_OK : SAG_ERR_CUDA;
     XArgs a = x_args(desc, io, p, ws);
     if (x_table(&a, desc, p, ws, s) != cudaSuccess) return SAG_ERR_CUDA;
-    const int units = (int)(p.q_tiles * desc->n2);
-    a.nsplit = split_of(units, 2 * p.max_k, 2 * current_device_sms());   // two CTAs an SM
+    a.units = (int)(p.q_tiles * desc->n2);
+    a.nsplit = split_of(a.units, 2 * p.max_k, 2 * current_device_sms());   // two CTAs an SM, tiles of 64 keys
+    a.n_status = a.ctas = a.units * a.nsplit;
     // full query tiles, and at least 2048 keys a CTA
     const bool long_loops = p.max_q > 1 && p.max_k >= 16 * a.nsplit;
-    a.n_status = units * a.nsplit;
-    return launch_xfwd(a, *io, *desc, long_loops, units, s) == cudaSuccess ? SAG_OK : SAG_ERR_CUDA;
+    return launch_xfwd(a, *io, *desc, long_loops, s) == cudaSuccess ? SAG_OK : SAG_ERR_CUDA;
 }
 
 extern "C" sag_status cross_attn_grad(const sca_desc *desc, const sca_io *io, void *workspace, size_t workspace_bytes,
@@ -203,17 +205,29 @@ extern "C" sag_status cross_attn_grad(const sca_desc *desc, const sca_io *io, vo
     XArgs a = x_args(desc, io, p, ws);
     if (x_table(&a, desc, p, ws, s) != cudaSuccess) return SAG_ERR_CUDA;
     const int sms = current_device_sms();
+    if (p.fp16 && cudaMemsetAsync(a.norms, 0, sizeof(unsigned) * 2 * (size_t)desc->batch * desc->n2, s) != cudaSuccess)
+        return SAG_ERR_CUDA;
     if (launch_xpre(a, p.fp16, desc->d, s) != cudaSuccess) return SAG_ERR_CUDA;
+    // one CTA an SM: a cluster for each unit, or CTAs that take unit after unit
+    auto share = [&](int units, int tiles) {
+        a.units = units;
+        a.nsplit = split_of(units, tiles, sms);
+        a.ctas = a.nsplit > 1 || units < sms ? units * a.nsplit : sms;
+    };
+    int before = 0;
+    // k_xpre zeroes the tickets; without query rows there is none
+    if (!q_units && cudaMemsetAsync(a.ticket, 0, 2 * sizeof(unsigned), s) != cudaSuccess) return SAG_ERR_CUDA;
     if (q_units) {
-        a.nsplit = split_of(q_units, p.max_k, sms);
-        if (launch_xdq(a, *io, *desc, q_units, s) != cudaSuccess) return SAG_ERR_CUDA;
-        a.status += (int64_t)q_units * a.nsplit;
+        share(q_units, p.max_k);
+        if (launch_xdq(a, *io, *desc, s) != cudaSuccess) return SAG_ERR_CUDA;
+        before = a.ctas;
     }
     if (k_units) {
-        const int64_t before = q_units ? (int64_t)q_units * a.nsplit : 0;
-        a.nsplit = split_of(k_units, p.max_q, sms);
-        a.n_status = (int32_t)(before + (int64_t)k_units * a.nsplit);
-        if (launch_xdkv(a, *io, *desc, k_units, s) != cudaSuccess) return SAG_ERR_CUDA;
+        a.status += before;
+        a.ticket += 1;
+        share(k_units, p.max_q);
+        a.n_status = before + a.ctas;
+        if (launch_xdkv(a, *io, *desc, s) != cudaSuccess) return SAG_ERR_CUDA;
     }
     return SAG_OK;
 }

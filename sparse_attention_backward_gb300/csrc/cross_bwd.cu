@@ -20,8 +20,10 @@
 // dY and V rows of the sequence and head: |dP - Delta| <= 2 |dY| |V|, so that
 // neither a loss scale overflows nor a long softmax vanishes.
 //
-// Few tiles: a cluster's CTAs split the loop and join their accumulators
-// through distributed shared memory, in rank order.
+// A CTA (one per SM) walks over units, so that the next unit's tiles land and
+// its first products run beside the last one's stores.  Few units: a cluster's
+// CTAs split one unit's loop and join their accumulators through distributed
+// shared memory, in rank order.
 #include <type_traits>
 
 #include "cross.cuh"
@@ -42,12 +44,13 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
     __shared__ float red[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = lane % LPR;
+    if (blockIdx.x == 0 && threadIdx.x < 2) A.ticket[threadIdx.x] = 0;
     const int q_units = A.q_tiles * A.n2;
     float top = 0.f;
     int64_t slot;
     if ((int)blockIdx.x < q_units) {
         const XUnit u = x_decode<&SeqRow::qtile0>(A, blockIdx.x);
-        slot = u.tile_id;
+        slot = ((int64_t)u.b * A.n2 + u.head) * 2;
         float *st = A.stats + u.tile_id * 256;
         for (int r = warp * RPW + lane / LPR; r < kXRows; r += 8 * RPW) {
             const int tok = u.tile * A.tpt + r / A.group;
@@ -81,7 +84,7 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
     } else {
         // fp16 only: row norms of V
         const XUnit u = x_decode<&SeqRow::ktile0>(A, blockIdx.x - q_units);
-        slot = q_units + u.tile_id;
+        slot = ((int64_t)u.b * A.n2 + u.head) * 2 + 1;
         for (int r = warp * RPW + lane / LPR; r < kXRows; r += 8 * RPW) {
             const int key = u.tile * kXRows + r;
             const int64_t row = (int64_t)u.seq.k0 + key;
@@ -107,37 +110,19 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
         __syncthreads();
         if (threadIdx.x == 0) {
             for (int i = 1; i < 8; ++i) top = fmaxf(top, red[i]);
-            A.norms[slot] = sqrtf(top);
+            atomicMax(A.norms + slot, __float_as_uint(top));   // a maximum does not depend on the order
         }
     }
 }
 
-// fp16: exponent e such that 2^e |dS| <= 2^15 for every dS of the sequence and head.  `red` is [kXThreads / 32] floats of
-// shared memory; holds a __syncthreads.
-__device__ __forceinline__ float ds_exponent(const XArgs &A, const SeqRow &a, const SeqRow &b, int head, float *red) {
-    float ny = 0.f, nv = 0.f;
-    for (int t = a.qtile0 + threadIdx.x; t < b.qtile0; t += kXThreads) ny = fmaxf(ny, A.norms[(int64_t)t * A.n2 + head]);
-    for (int t = a.ktile0 + threadIdx.x; t < b.ktile0; t += kXThreads)
-        nv = fmaxf(nv, A.norms[(int64_t)(A.q_tiles + t) * A.n2 + head]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        ny = fmaxf(ny, __shfl_xor_sync(0xffffffffu, ny, o));
-        nv = fmaxf(nv, __shfl_xor_sync(0xffffffffu, nv, o));
-    }
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) {
-        red[2 * warp] = ny;
-        red[2 * warp + 1] = nv;
-    }
-    __syncthreads();
-    ny = nv = 0.f;
-    for (int i = 0; i < kXThreads / 32; ++i) {
-        ny = fmaxf(ny, red[2 * i]);
-        nv = fmaxf(nv, red[2 * i + 1]);
-    }
-    const float bound = 2.f * ny * nv;
+// fp16: exponent e such that 2^e |dS| <= 2^15 for every dS of a sequence and head.
+__device__ __forceinline__ float ds_exponent(uint2 norms) {
+    const float bound = 2.f * sqrtf(__uint_as_float(norms.x)) * sqrtf(__uint_as_float(norms.y));
     if (!(bound > 0.f) || !(bound < INFINITY)) return 0.f;
     return fminf(fmaxf(14.f - (float)ilogbf(bound), -40.f), 40.f);
+}
+__device__ __forceinline__ uint2 ds_norms(const XArgs &A, const XUnit &u) {
+    return *reinterpret_cast<const uint2 *>(A.norms + ((int64_t)u.b * A.n2 + u.head) * 2);
 }
 
 // ------------------------------------------------------------------- shared
@@ -156,8 +141,39 @@ struct BwdSmem {
     static_assert(2 * kXRows * XROW * 4 <= OFF_STAT, "the exchange overlays the tiles");
     static_assert(TOTAL <= 227 * 1024, "shared memory of one CTA");
 };
-// barriers
-enum { XB_XY = 0, XB_S = 1, XB_DP = 3, XB_PF = 4, XB_DS = 5, XB_ACC = 6, XB_DRAIN = 7, XB_STF = 8, XB_STE = 10, XB_RING = 12 };
+// barriers; XB_XYE: the resident tiles may be overwritten; XB_UF, XB_UE: units handed out
+enum {
+    XB_XY = 0, XB_XYE, XB_S, XB_DP = XB_S + 2, XB_PF, XB_DS, XB_ACC, XB_STF, XB_STE = XB_STF + 2, XB_UF = XB_STE + 2,
+    XB_UE = XB_UF + 2, XB_RING = XB_UE + 2
+};
+// arrivals that complete a phase: one a softmax warp; every reader's for the units; one of everything else
+__device__ __forceinline__ int bwd_arrivals(int i) {
+    return i == XB_PF || i == XB_DS || i == XB_STE || i == XB_STE + 1 ? 8 : i == XB_UE || i == XB_UE + 1 ? 9 : 1;
+}
+
+// Units of a CTA, one after the other: the first by its number, the others from a ticket counter, since units differ (short
+// sequences, masked and padding tiles) and a fixed order left SMs idle: 142 us against 101 for k_xdkv of a padded batch.
+// The producer takes a unit when it has issued the loads of the one before, and hands it to the MMA and softmax warps
+// through two slots.  A split unit is its cluster's only one.
+struct Units {
+    volatile int *slot;
+    uint64_t *full, *empty;
+    __device__ __forceinline__ int take(const XArgs &A, int k, volatile int *abort) const {   // one thread; -1: timeout
+        if (k >= 2 && !tc::mbar_wait(&empty[k & 1], (k / 2 - 1) & 1, abort, kXWaitNs)) return -1;
+        int unit = A.units;
+        if (k == 0) unit = blockIdx.x / A.nsplit;
+        else if (A.ctas < A.units) unit = (int)(gridDim.x + atomicAdd(A.ticket, 1u));
+        slot[k & 1] = unit;
+        tc::mbar_arrive(&full[k & 1]);
+        return unit;
+    }
+    __device__ __forceinline__ int read(int k, volatile int *abort, int lane) const {         // a warp; -1: timeout
+        if (!warp_wait(abort, Phase{&full[k & 1], (uint32_t)(k >> 1) & 1u})) return -1;
+        const int unit = slot[k & 1];
+        warp_arrive(&empty[k & 1], lane);
+        return unit;
+    }
+};
 
 struct Ring {
     uint64_t *full, *empty;
@@ -174,14 +190,14 @@ __device__ __forceinline__ bool ring_drain(const Ring &r, int loads) {
     return ok;
 }
 
-// Joins the ranks' partial accumulators: `rows` rows of D columns each, in xo[row][XROW] of every rank; row k of this
-// rank's share goes to out(k) (nullptr: not stored), scaled by mul(k).
-template <bool kFp16, int D, class Out, class Mul>
-__device__ __forceinline__ void join_rows(float *xo, int rows, int ns, int rank, int warp, int lane, Out &&out, Mul &&mul) {
+// Joins the ranks' partial accumulators: 128 rows of D columns each, in xo[row][XROW] of every rank; row k of this
+// rank's share goes to dst + out(k) (negative: not stored), scaled by f.
+template <bool kFp16, int D, class Out>
+__device__ __forceinline__ void join_rows(float *xo, uint16_t *dst, int ns, int rank, int warp, int lane, Out &&out, float f) {
     constexpr int E = D / 64;
-    for (int k = rank + ns * warp; k < rows; k += ns * 8) {
-        uint16_t *dst = out(k);
-        if (!dst) continue;
+    for (int k = rank + ns * warp; k < kXRows; k += ns * 8) {
+        const int64_t at = out(k);
+        if (at < 0) continue;
         float2 y[kMaxSplit][E], acc[E] = {};
 #pragma unroll
         for (int p = 0; p < kMaxSplit; ++p)
@@ -195,15 +211,15 @@ __device__ __forceinline__ void join_rows(float *xo, int rows, int ns, int rank,
             if (p < ns)
 #pragma unroll
                 for (int e = 0; e < E; ++e) acc[e] = add2(acc[e], y[p][e]);
-        const float f = mul(k);
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            *reinterpret_cast<uint32_t *>(dst + e * 64 + lane * 2) = xpack<kFp16>(acc[e].x * f, acc[e].y * f);
+            *reinterpret_cast<uint32_t *>(dst + at + e * 64 + lane * 2) = xpack<kFp16>(acc[e].x * f, acc[e].y * f);
     }
 }
 
 // ------------------------------------------------------------------- k_xdq
 // TMEM columns: S of even / odd key tiles at 0 / 128 (dS over them, the second half of K 64 columns on), dP 256, dQ 384.
+// Tiles are counted through all units (g): buffers and phases follow the count.
 template <bool kFp16, int D>
 __global__ void __launch_bounds__(kXThreads, 1)
     k_xdq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_dy,
@@ -216,11 +232,11 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const Ring rb = {ra.empty + L::RA, ra.empty + L::RA + L::RB, L::RB};
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rb.empty + L::RB);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const Units units = {abort_flag + 1, bars + XB_UF, bars + XB_UE};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        for (int i = 0; i < XB_RING; ++i) tc::mbar_init(&bars[i], i == XB_DS || i == XB_PF ? 8 : 1);   // one arrival a warp
-        for (int i = 0; i < 2 * (L::RA + L::RB); ++i) tc::mbar_init(&ra.full[i], 1);
+        for (int i = 0; i < XB_RING + 2 * (L::RA + L::RB); ++i) tc::mbar_init(&bars[i], bwd_arrivals(i));
         tc::fence_mbar_init();
     }
     if (warp == 9) {
@@ -233,50 +249,67 @@ __global__ void __launch_bounds__(kXThreads, 1)
         tc::prefetch_tmap(&map_k);
         tc::prefetch_tmap(&map_v);
     }
-    const int ns = A.nsplit, rank = blockIdx.x % ns;
-    const XUnit u = x_decode<&SeqRow::qtile0>(A, blockIdx.x / ns);
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot, sbase = tc::smem_u32(smem);
-    const int G = A.group, tok0 = u.tile * A.tpt;
-    const int cover = A.s1_pad ? A.s1_pad : u.seq.qlen;
-    const int nkt = tok0 < u.seq.qlen ? (u.seq.klen + kXRows - 1) / kXRows : 0;
-    const int t0 = (int)((int64_t)nkt * rank / ns), n = (int)((int64_t)nkt * (rank + 1) / ns) - t0;
-    const int partial = A.mask ? 0 : u.seq.klen / kXRows - t0;   // tiles from this one on may lack keys
-    float up = 0.f;                                      // exponent that dS is scaled by
-    if constexpr (kFp16) {
-        up = ds_exponent(A, u.seq, seq_row(A.seq, u.b + 1), u.head, reinterpret_cast<float *>(smem + L::OFF_STAT));
-    }
+    const int ns = A.nsplit, rank = blockIdx.x % ns;
+    const int G = A.group;
     auto fail = [&]() { *abort_flag = 1; };
+    struct Work {
+        XUnit u;
+        int tok0, t0, n;                                 // first token; this rank's first key tile and their number
+    };
+    auto decode = [&](int unit) {
+        Work w;
+        w.u = x_decode<&SeqRow::qtile0>(A, unit);
+        w.tok0 = w.u.tile * A.tpt;
+        const int nkt = w.tok0 < w.u.seq.qlen ? (w.u.seq.klen + kXRows - 1) / kXRows : 0;
+        w.t0 = (int)((int64_t)nkt * rank / ns);
+        w.n = (int)((int64_t)nkt * (rank + 1) / ns) - w.t0;
+        return w;
+    };
 
     if (warp == 8) {
         // ------------------------------------------------------ TMA producer
-        if (lane == 0 && n > 0) {
+        if (lane == 0) {
             const uint32_t qbytes = (uint32_t)L::KC * A.tpt * G * 128;
-            tc::mbar_arrive_expect_tx(&bars[XB_XY], 2 * qbytes);
-            for (int c = 0; c < L::KC; ++c) {
-                tc::tma_load_3d(smem + L::OFF_X + c * 16384, &map_q, c * 64, u.head * G, u.seq.q0 + tok0, &bars[XB_XY]);
-                tc::tma_load_3d(smem + L::OFF_Y + c * 16384, &map_dy, c * 64, u.head * G, u.seq.q0 + tok0, &bars[XB_XY]);
-            }
-            int la = 0, lb = 0;
-            auto load = [&](const Ring &r, int off, const CUtensorMap *map, int &i, int key) {
-                if (!ring_wait_free(r, i, abort_flag)) return false;
-                const int s = i % r.n;
-                tc::mbar_arrive_expect_tx(&r.full[s], L::TILE);
-                for (int c = 0; c < L::KC; ++c)
-                    tc::tma_load_3d(smem + off + s * L::TILE + c * 16384, map, c * 64, u.head, u.seq.k0 + key, &r.full[s]);
-                ++i;
-                return true;
-            };
-            // keys run one tile ahead of values, as the MMA warp takes them
-            bool ok = load(ra, L::OFF_A, &map_k, la, t0 * kXRows);
-            for (int i = 0; i < n && ok; ++i) {
-                ok = load(rb, L::OFF_B, &map_v, lb, (t0 + i) * kXRows);
-                if (ok && i + 1 < n) ok = load(ra, L::OFF_A, &map_k, la, (t0 + i + 1) * kXRows);
+            int la = 0, lb = 0, lx = 0;                  // loads so far
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const int unit = units.take(A, k, abort_flag);
+                ok = unit >= 0;
+                if (!ok || unit >= A.units) break;
+                const Work w = decode(unit);
+                if (w.n == 0) continue;
+                auto load = [&](const Ring &r, int off, const CUtensorMap *map, int &i, int key) {
+                    if (!ring_wait_free(r, i, abort_flag)) return false;
+                    const int s = i % r.n;
+                    tc::mbar_arrive_expect_tx(&r.full[s], L::TILE);
+                    for (int c = 0; c < L::KC; ++c)
+                        tc::tma_load_3d(smem + off + s * L::TILE + c * 16384, map, c * 64, w.u.head, w.u.seq.k0 + key,
+                                        &r.full[s]);
+                    ++i;
+                    return true;
+                };
+                ok = lx == 0 || tc::mbar_wait(&bars[XB_XYE], (lx - 1) & 1, abort_flag, kXWaitNs);
+                if (!ok) break;
+                tc::mbar_arrive_expect_tx(&bars[XB_XY], 2 * qbytes);
+                for (int c = 0; c < L::KC; ++c) {
+                    const int row = w.u.seq.q0 + w.tok0;
+                    tc::tma_load_3d(smem + L::OFF_X + c * 16384, &map_q, c * 64, w.u.head * G, row, &bars[XB_XY]);
+                    tc::tma_load_3d(smem + L::OFF_Y + c * 16384, &map_dy, c * 64, w.u.head * G, row, &bars[XB_XY]);
+                }
+                ++lx;
+                // keys run one tile ahead of values, as the MMA warp takes them
+                ok = load(ra, L::OFF_A, &map_k, la, w.t0 * kXRows);
+                for (int i = 0; i < w.n && ok; ++i) {
+                    ok = load(rb, L::OFF_B, &map_v, lb, (w.t0 + i) * kXRows);
+                    if (ok && i + 1 < w.n) ok = load(ra, L::OFF_A, &map_k, la, (w.t0 + i + 1) * kXRows);
+                }
             }
             if (!ok) fail();
-            bool drained = tc::drain_armed(&bars[XB_XY], 1, kXWaitNs);
+            bool drained = tc::drain_armed(&bars[XB_XY], lx, kXWaitNs);
             drained = ring_drain(ra, la) && drained;
             drained = ring_drain(rb, lb) && drained;
             if (!drained) fail();
@@ -285,123 +318,163 @@ __global__ void __launch_bounds__(kXThreads, 1)
         // ------------------------------------------------------ MMA issuer
         constexpr uint32_t id_s = tc::idesc_f16(kXRows, kXRows, !kFp16, false, false);
         constexpr uint32_t id_q = tc::idesc_f16(kXRows, D, !kFp16, false, true);
-        auto k_in = [&](int i) { return ra.landed(i); };
-        auto v_in = [&](int i) { return rb.landed(i); };
-        auto issue_s = [&](int i) {
-            mma_abt<D, kXRows>(tmem + (i & 1) * 128, sbase + L::OFF_X, sbase + L::OFF_A + i % L::RA * L::TILE, id_s);
-            tc::mma_commit_warp(&bars[XB_S + (i & 1)]);
+        auto issue_s = [&](int g) {
+            mma_abt<D, kXRows>(tmem + (g & 1) * 128, sbase + L::OFF_X, sbase + L::OFF_A + g % L::RA * L::TILE, id_s);
+            tc::mma_commit_warp(&bars[XB_S + (g & 1)]);
         };
-        auto issue_dp = [&](int i) {
-            mma_abt<D, kXRows>(tmem + 256, sbase + L::OFF_Y, sbase + L::OFF_B + i % L::RB * L::TILE, id_s);
+        auto issue_dp = [&](int g) {
+            mma_abt<D, kXRows>(tmem + 256, sbase + L::OFF_Y, sbase + L::OFF_B + g % L::RB * L::TILE, id_s);
             tc::mma_commit_warp(&bars[XB_DP]);
-            tc::mma_commit_warp(&rb.empty[i % L::RB]);
+            tc::mma_commit_warp(&rb.empty[g % L::RB]);
         };
         bool ok = true;
-        if (n > 0) {
-            ok = warp_wait(abort_flag, Phase{&bars[XB_XY], 0}, k_in(0));
-            tc::tc_fence_after();
-            if (ok) issue_s(0);
-            ok = ok && warp_wait(abort_flag, v_in(0));
-            if (ok) issue_dp(0);
-            if (ok && n > 1) {
-                ok = warp_wait(abort_flag, k_in(1));
-                if (ok) issue_s(1);
-            }
-        }
-        for (int i = 0; i < n && ok; ++i) {
-            // the next dP once this one has been read, then this tile's dQ, then the scores two tiles on
-            if (i + 1 < n) {
-                ok = warp_wait(abort_flag, Phase{&bars[XB_PF], (uint32_t)i & 1u}, v_in(i + 1));
-                if (!ok) break;
-                tc::tc_fence_after();
-                issue_dp(i + 1);
-            }
-            const Phase ds{&bars[XB_DS], (uint32_t)i & 1u};
-            ok = i + 2 < n ? warp_wait(abort_flag, ds, k_in(i + 2)) : warp_wait(abort_flag, ds);
+        int g = 0, nonempty = 0;
+        for (int k = 0; ok; ++k) {
+            const int unit = units.read(k, abort_flag, lane);
+            ok = unit >= 0;
+            if (!ok || unit >= A.units) break;
+            const Work w = decode(unit);
+            const int n = w.n;
+            if (n == 0) continue;
+            ok = warp_wait(abort_flag, Phase{&bars[XB_XY], (uint32_t)nonempty & 1u}, ra.landed(g));
             if (!ok) break;
-            const uint32_t kt = L::OFF_A + i % L::RA * L::TILE;
-            if (i >= partial) {
-                // S(i) has read this tile already (dS(i) follows from it), so its dead rows may go
-                const KeyBits<4> kb = key_bits<4>(A.mask, u.seq, (t0 + i) * kXRows, lane);
-                if (!kb.all()) zero_rows<L::KC>(smem + kt, kb, lane);
-            }
             tc::tc_fence_after();
-            mma_ab<kXRows, 64>(tmem + 384, tmem + (i & 1) * 128, sbase + kt, id_q, i > 0);
-            tc::mma_commit_warp(&ra.empty[i % L::RA]);
-            if (i + 2 < n) issue_s(i + 2);
+            issue_s(g);
+            ok = warp_wait(abort_flag, rb.landed(g));
+            if (!ok) break;
+            issue_dp(g);
+            if (n > 1) {
+                ok = warp_wait(abort_flag, ra.landed(g + 1));
+                if (!ok) break;
+                issue_s(g + 1);
+            } else {
+                tc::mma_commit_warp(&bars[XB_XYE]);
+            }
+            for (int i = 0; i < n; ++i, ++g) {
+                // the next dP once this one has been read, then this tile's dQ, then the scores two tiles on
+                if (i + 1 < n) {
+                    ok = warp_wait(abort_flag, Phase{&bars[XB_PF], (uint32_t)g & 1u}, rb.landed(g + 1));
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    issue_dp(g + 1);
+                    if (i + 2 == n) tc::mma_commit_warp(&bars[XB_XYE]);
+                }
+                const Phase ds{&bars[XB_DS], (uint32_t)g & 1u};
+                ok = i + 2 < n ? warp_wait(abort_flag, ds, ra.landed(g + 2)) : warp_wait(abort_flag, ds);
+                if (!ok) break;
+                const uint32_t kt = L::OFF_A + g % L::RA * L::TILE;
+                tc::tc_fence_after();
+                mma_ab<kXRows, 64>(tmem + 384, tmem + (g & 1) * 128, sbase + kt, id_q, i > 0);
+                tc::mma_commit_warp(&ra.empty[g % L::RA]);
+                if (i + 2 < n) issue_s(g + 2);
+            }
+            if (!ok) break;
+            tc::mma_commit_warp(&bars[XB_ACC]);
+            ++nonempty;
         }
         if (!ok && lane == 0) fail();
-        tc::mma_commit_warp(&bars[XB_ACC]);
-        if (!__all_sync(0xffffffffu, tc::mbar_wait_drain(&bars[XB_ACC], 0, kXWaitNs)) && lane == 0) fail();
+        // every MMA issued must be complete before TMEM is freed: one more phase of XB_ACC
+        if (!ok) tc::mma_commit_warp(&bars[XB_ACC]);
+        const int phases = nonempty + (ok ? 0 : 1);
+        if (!__all_sync(0xffffffffu, tc::drain_armed(&bars[XB_ACC], phases, kXWaitNs)) && lane == 0) fail();
     }
 
     const int h = warp >> 2;                             // softmax warps: half of the columns
     const int r = (warp & 3) * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    if (warp < 8 && n > 0) {
-        // ------------------------------------------------------ softmax
-        const float *st = A.stats + u.tile_id * 256;
-        const float c = A.scale_log2, nl = st[r] + up, nd = st[128 + r];
-        bool ok = true;
-        for (int i = 0; i < n; ++i) {
-            const uint32_t ts = trow + (i & 1) * 128 + h * 64;
-            ok = warp_wait(abort_flag, Phase{&bars[XB_S + (i & 1)], (uint32_t)(i >> 1) & 1u});
-            if (!ok) break;
-            tc::tc_fence_after();
-            // dS over the scores; a copy of its own for tiles with absent keys
-            auto tile = [&](auto masked) -> bool {
-                float p[64];
-                tmem_ld32(ts, reinterpret_cast<uint32_t *>(p));
-                tmem_ld32(ts + 32, reinterpret_cast<uint32_t *>(p) + 32);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 64; ++j) p[j] = xex2(fmaf(p[j], c, nl));
-                if (!warp_wait(abort_flag, Phase{&bars[XB_DP], (uint32_t)i & 1u})) return false;
-                tc::tc_fence_after();
-                float y[64];
-                tmem_ld32(trow + 256 + h * 64, reinterpret_cast<uint32_t *>(y));
-                tmem_ld32(trow + 256 + h * 64 + 32, reinterpret_cast<uint32_t *>(y) + 32);
-                tc::tmem_wait_ld();
-                tc::tc_fence_before();
-                warp_arrive(&bars[XB_PF], lane);           // dP has been read
-                KeyBits<4> kb{};
-                if constexpr (decltype(masked)::value) kb = key_bits<4>(A.mask, u.seq, (t0 + i) * kXRows, lane);
-                uint32_t q[32];
-#pragma unroll
-                for (int j = 0; j < 64; j += 2) {
-                    float a = p[j] * (y[j] + nd), b = p[j + 1] * (y[j + 1] + nd);
-                    if constexpr (decltype(masked)::value) {
-                        const uint32_t w = h ? kb.w[2 + (j >> 5)] : kb.w[j >> 5];
-                        if (!((w >> (j & 31)) & 1u)) a = 0.f;
-                        if (!((w >> ((j + 1) & 31)) & 1u)) b = 0.f;
-                    }
-                    q[j / 2] = xpack<kFp16>(a, b);
-                }
-                tmem_st32(ts, q);
-                tmem_wait_st();
-                tc::tc_fence_before();
-                warp_arrive(&bars[XB_DS], lane);
-                return true;
-            };
-            ok = i < partial ? tile(std::false_type{}) : tile(std::true_type{});
-            if (!ok) break;
-        }
-        if (ok) ok = warp_wait(abort_flag, Phase{&bars[XB_ACC], 0});
-        if (!ok && lane == 0) fail();
-        tc::tc_fence_after();
-    }
-
-    // ---------------------------------------------------------- epilogue
-    const float f = A.scale * (kFp16 ? exp2f(-up) : 1.f);
-    auto out = [&](int k) -> uint16_t * {
-        const int tok = tok0 + k / G;
-        if (k >= A.tpt * G || tok >= cover) return nullptr;
-        return A.dq + ((int64_t)(u.seq.q0 + tok) * A.n1 + u.head * G + k % G) * D;
+    Work w{};
+    float up = 0.f;                                      // exponent that dS is scaled by
+    auto out = [&](int k) -> int64_t {                   // place of row k in dQ; negative: none
+        const int tok = w.tok0 + k / G;
+        if (k >= A.tpt * G || tok >= (A.s1_pad ? A.s1_pad : w.u.seq.qlen)) return -1;
+        return ((int64_t)(w.u.seq.q0 + tok) * A.n1 + w.u.head * G + k % G) * D;
     };
-    if (ns == 1) {
-        if (warp < 8) {
-            uint16_t *dst = out(r);
-            const bool pad = n == 0 || tok0 + r / G >= u.seq.qlen;
+    if (warp < 8) {
+        bool ok = true;
+        int g = 0, nonempty = 0;
+        // the next unit's statistics are on their way while this one is stored
+        int unit = units.read(0, abort_flag, lane);
+        float st_nl = 0.f, st_nd = 0.f;
+        uint2 norms{};
+        auto begin = [&]() {
+            w = decode(unit);
+            st_nl = A.stats[w.u.tile_id * 256 + r];
+            st_nd = A.stats[w.u.tile_id * 256 + 128 + r];
+            if constexpr (kFp16) norms = ds_norms(A, w.u);
+        };
+        ok = unit >= 0;
+        if (ok && unit < A.units) begin();
+        for (int k = 0; ok && unit < A.units; ++k) {
+            const int n = w.n;
+            if constexpr (kFp16) up = ds_exponent(norms);
+            const float nl = st_nl + up, nd = st_nd;
+            if (n > 0) {
+                // ---------------------------------------------- softmax
+                const float c = A.scale_log2;
+                const int partial = A.mask ? 0 : w.u.seq.klen / kXRows - w.t0;
+                KeyLoad<4> keys{};                       // of the next tile that may lack keys
+                if (partial < n)
+                    keys.start(A.mask, w.u.seq, (w.t0 + (partial > 0 ? partial : 0)) * kXRows, lane);
+                // dS over the scores; a copy of its own for tiles with absent keys
+                auto tile = [&](auto masked, int i) -> bool {
+                    const uint32_t ts = trow + (g & 1) * 128 + h * 64;
+                    float p[64];
+                    tmem_ld32(ts, reinterpret_cast<uint32_t *>(p));
+                    tmem_ld32(ts + 32, reinterpret_cast<uint32_t *>(p) + 32);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) p[j] = xex2(fmaf(p[j], c, nl));
+                    if (!warp_wait(abort_flag, Phase{&bars[XB_DP], (uint32_t)g & 1u})) return false;
+                    tc::tc_fence_after();
+                    float y[64];
+                    tmem_ld32(trow + 256 + h * 64, reinterpret_cast<uint32_t *>(y));
+                    tmem_ld32(trow + 256 + h * 64 + 32, reinterpret_cast<uint32_t *>(y) + 32);
+                    tc::tmem_wait_ld();
+                    tc::tc_fence_before();
+                    warp_arrive(&bars[XB_PF], lane);     // dP has been read
+                    KeyBits<4> kb{};
+                    if constexpr (decltype(masked)::value) {
+                        kb = keys.finish();
+                        if (i + 1 < n) keys.start(A.mask, w.u.seq, (w.t0 + i + 1) * kXRows, lane);
+                        // the scores have read this tile's keys, so its dead rows may go before dS K
+                        if (!kb.all()) zero_rows<L::KC, 4, 256>(smem + L::OFF_A + g % L::RA * L::TILE, kb, threadIdx.x);
+                    }
+                    uint32_t q[32];
+#pragma unroll
+                    for (int j = 0; j < 64; j += 2) {
+                        float a = p[j] * (y[j] + nd), b = p[j + 1] * (y[j + 1] + nd);
+                        if constexpr (decltype(masked)::value) {
+                            const uint32_t bits = h ? kb.w[2 + (j >> 5)] : kb.w[j >> 5];
+                            if (!((bits >> (j & 31)) & 1u)) a = 0.f;
+                            if (!((bits >> ((j + 1) & 31)) & 1u)) b = 0.f;
+                        }
+                        q[j / 2] = xpack<kFp16>(a, b);
+                    }
+                    tmem_st32(ts, q);
+                    tmem_wait_st();
+                    tc::tc_fence_before();
+                    warp_arrive(&bars[XB_DS], lane);
+                    return true;
+                };
+                for (int i = 0; i < n && ok; ++i, ++g) {
+                    ok = warp_wait(abort_flag, Phase{&bars[XB_S + (g & 1)], (uint32_t)(g >> 1) & 1u});
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    ok = i < partial ? tile(std::false_type{}, i) : tile(std::true_type{}, i);
+                }
+                if (ok) ok = warp_wait(abort_flag, Phase{&bars[XB_ACC], (uint32_t)nonempty & 1u});
+                ++nonempty;
+                tc::tc_fence_after();
+            }
+            if (ns > 1 || !ok) break;                    // stored below
+            // -------------------------------------------------- epilogue
+            const float f = A.scale * (kFp16 ? exp2f(-up) : 1.f);
+            const bool pad = n == 0 || w.tok0 + r / G >= w.u.seq.qlen;
+            RowStore<kFp16> rows;
+            rows.rows(out(r), lane);
+            unit = units.read(k + 1, abort_flag, lane);
+            ok = unit >= 0;
+            if (ok && unit < A.units) begin();
 #pragma unroll
             for (int j = 0; j < D / 2; j += 32) {
                 float y[32];
@@ -411,18 +484,22 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = pad ? 0.f : y[e] * f;
-                if (dst) store_row<kFp16, 32>(dst + h * (D / 2) + j, y);
+                rows.store(A.dq, y, h * (D / 2) + j, lane);
             }
+            tc::tc_fence_before();                       // read before the next unit's products may follow
         }
-    } else {
+        if (!ok && lane == 0) fail();
+    }
+    if (ns > 1) {
+        // the CTA's only unit: partial sums into shared memory, then each rank joins its share of the rows
         float *xo = reinterpret_cast<float *>(smem);
         __syncthreads();                                 // loads and products on this memory are complete
         if (warp < 8) {
-            const bool pad = n == 0 || tok0 + r / G >= u.seq.qlen;
+            const bool pad = w.n == 0 || w.tok0 + r / G >= w.u.seq.qlen;
 #pragma unroll
             for (int j = 0; j < D / 2; j += 32) {
                 float y[32];
-                if (n > 0) {
+                if (w.n > 0) {
                     tmem_ld32(trow + 384 + h * (D / 2) + j, reinterpret_cast<uint32_t *>(y));
                     tc::tmem_wait_ld();
                 }
@@ -433,7 +510,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
             }
         }
         cluster_sync();
-        if (warp < 8) join_rows<kFp16, D>(xo, kXRows, ns, rank, warp, lane, out, [&](int) { return f; });
+        if (warp < 8) {
+            const float f = A.scale * (kFp16 ? exp2f(-up) : 1.f);
+            join_rows<kFp16, D>(xo, A.dq, ns, rank, warp, lane, out, f);
+        }
         cluster_sync();                                  // peers are done with this CTA's shared memory
     }
     tc::tc_fence_before();
@@ -461,12 +541,11 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const Ring rs = {bars + XB_STF, bars + XB_STE, 2};
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rb.empty + L::RB);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const Units units = {abort_flag + 1, bars + XB_UF, bars + XB_UE};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        for (int i = 0; i < XB_RING; ++i)
-            tc::mbar_init(&bars[i], i == XB_DS || i == XB_PF || i == XB_STE || i == XB_STE + 1 ? 8 : 1);   // one arrival a warp
-        for (int i = 0; i < 2 * (L::RA + L::RB); ++i) tc::mbar_init(&ra.full[i], 1);
+        for (int i = 0; i < XB_RING + 2 * (L::RA + L::RB); ++i) tc::mbar_init(&bars[i], bwd_arrivals(i));
         tc::fence_mbar_init();
     }
     if (warp == 9) {
@@ -479,57 +558,80 @@ __global__ void __launch_bounds__(kXThreads, 1)
         tc::prefetch_tmap(&map_k);
         tc::prefetch_tmap(&map_v);
     }
-    const int ns = A.nsplit, rank = blockIdx.x % ns;
-    const XUnit u = x_decode<&SeqRow::ktile0>(A, blockIdx.x / ns);
+    if (A.tpt * A.group < kXRows) {
+        // groups that do not divide 128 leave rows that no load writes: they stay zero
+        KeyBits<4> kb;
+        kb.set_first(A.tpt * A.group);
+        if (warp < 8)
+            for (int i = 0; i < L::RA + L::RB; ++i)
+                zero_rows<L::KC, 4, 256>(smem + L::OFF_A + i * L::TILE, kb, threadIdx.x);
+    }
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot, sbase = tc::smem_u32(smem);
-    const int G = A.group, key0 = u.tile * kXRows;
-    const int cover = A.s2_pad ? A.s2_pad : u.seq.klen;
-    const int nqt = key0 < u.seq.klen ? (u.seq.qlen + A.tpt - 1) / A.tpt : 0;
-    const int t0 = (int)((int64_t)nqt * rank / ns), n = (int)((int64_t)nqt * (rank + 1) / ns) - t0;
-    float up = 0.f;
-    if constexpr (kFp16) {
-        up = ds_exponent(A, u.seq, seq_row(A.seq, u.b + 1), u.head, reinterpret_cast<float *>(smem + L::OFF_STAT));
-        __syncthreads();                                 // the scratch becomes the ring of statistics
-    }
+    const int ns = A.nsplit, rank = blockIdx.x % ns;
+    const int G = A.group;
     auto fail = [&]() { *abort_flag = 1; };
+    struct Work {
+        XUnit u;
+        int key0, t0, n;                                 // first key; this rank's first query tile and their number
+    };
+    auto decode = [&](int unit) {
+        Work w;
+        w.u = x_decode<&SeqRow::ktile0>(A, unit);
+        w.key0 = w.u.tile * kXRows;
+        const int nqt = w.key0 < w.u.seq.klen ? (w.u.seq.qlen + A.tpt - 1) / A.tpt : 0;
+        w.t0 = (int)((int64_t)nqt * rank / ns);
+        w.n = (int)((int64_t)nqt * (rank + 1) / ns) - w.t0;
+        return w;
+    };
 
     if (warp == 8) {
         // ------------------------------------------------------ TMA producer
-        if (lane == 0 && n > 0) {
-            if (kFp16) tc::fence_proxy_async_smem();     // the scratch was written by plain stores
-            tc::mbar_arrive_expect_tx(&bars[XB_XY], 2 * L::TILE);
-            for (int c = 0; c < L::KC; ++c) {
-                tc::tma_load_3d(smem + L::OFF_X + c * 16384, &map_k, c * 64, u.head, u.seq.k0 + key0, &bars[XB_XY]);
-                tc::tma_load_3d(smem + L::OFF_Y + c * 16384, &map_v, c * 64, u.head, u.seq.k0 + key0, &bars[XB_XY]);
-            }
+        if (lane == 0) {
             const uint32_t qbytes = (uint32_t)L::KC * A.tpt * G * 128;
-            int la = 0, lb = 0, ls = 0;
+            int la = 0, lb = 0, ls = 0, lx = 0;          // loads so far
             bool ok = true;
-            auto load = [&](const Ring &r, int off, const CUtensorMap *map, int &i) {
-                if (!ring_wait_free(r, i, abort_flag)) return false;
-                const int s = i % r.n;
-                tc::mbar_arrive_expect_tx(&r.full[s], qbytes);
-                for (int c = 0; c < L::KC; ++c)
-                    tc::tma_load_3d(smem + off + s * L::TILE + c * 16384, map, c * 64, u.head * G,
-                                    u.seq.q0 + (t0 + i) * A.tpt, &r.full[s]);
-                ++i;
-                return true;
-            };
-            for (int i = 0; i < n && ok; ++i) {
-                ok = load(ra, L::OFF_A, &map_q, la);
-                if (ok) ok = ring_wait_free(rs, i, abort_flag);
+            for (int k = 0; ok; ++k) {
+                const int unit = units.take(A, k, abort_flag);
+                ok = unit >= 0;
+                if (!ok || unit >= A.units) break;
+                const Work w = decode(unit);
+                if (w.n == 0) continue;
+                auto load = [&](const Ring &r, int off, const CUtensorMap *map, int &i, int tile) {
+                    if (!ring_wait_free(r, i, abort_flag)) return false;
+                    const int s = i % r.n;
+                    tc::mbar_arrive_expect_tx(&r.full[s], qbytes);
+                    for (int c = 0; c < L::KC; ++c)
+                        tc::tma_load_3d(smem + off + s * L::TILE + c * 16384, map, c * 64, w.u.head * G,
+                                        w.u.seq.q0 + tile * A.tpt, &r.full[s]);
+                    ++i;
+                    return true;
+                };
+                ok = lx == 0 || tc::mbar_wait(&bars[XB_XYE], (lx - 1) & 1, abort_flag, kXWaitNs);
                 if (!ok) break;
-                tc::mbar_arrive_expect_tx(&rs.full[i & 1], 1024);
-                bulk_load(smem + L::OFF_STAT + (i & 1) * 1024,
-                          A.stats + ((int64_t)(u.seq.qtile0 + t0 + i) * A.n2 + u.head) * 256, 1024, &rs.full[i & 1]);
-                ++ls;
-                ok = load(rb, L::OFF_B, &map_dy, lb);
+                tc::mbar_arrive_expect_tx(&bars[XB_XY], 2 * L::TILE);
+                for (int c = 0; c < L::KC; ++c) {
+                    const int row = w.u.seq.k0 + w.key0;
+                    tc::tma_load_3d(smem + L::OFF_X + c * 16384, &map_k, c * 64, w.u.head, row, &bars[XB_XY]);
+                    tc::tma_load_3d(smem + L::OFF_Y + c * 16384, &map_v, c * 64, w.u.head, row, &bars[XB_XY]);
+                }
+                ++lx;
+                for (int i = 0; i < w.n && ok; ++i) {
+                    ok = load(ra, L::OFF_A, &map_q, la, w.t0 + i);
+                    if (ok) ok = ring_wait_free(rs, ls, abort_flag);
+                    if (!ok) break;
+                    tc::mbar_arrive_expect_tx(&rs.full[ls & 1], 1024);
+                    bulk_load(smem + L::OFF_STAT + (ls & 1) * 1024,
+                              A.stats + ((int64_t)(w.u.seq.qtile0 + w.t0 + i) * A.n2 + w.u.head) * 256, 1024,
+                              &rs.full[ls & 1]);
+                    ++ls;
+                    ok = load(rb, L::OFF_B, &map_dy, lb, w.t0 + i);
+                }
             }
             if (!ok) fail();
-            bool drained = tc::drain_armed(&bars[XB_XY], 1, kXWaitNs);
+            bool drained = tc::drain_armed(&bars[XB_XY], lx, kXWaitNs);
             drained = ring_drain(ra, la) && drained;
             drained = ring_drain(rb, lb) && drained;
             drained = ring_drain(rs, ls) && drained;
@@ -539,144 +641,179 @@ __global__ void __launch_bounds__(kXThreads, 1)
         // ------------------------------------------------------ MMA issuer
         constexpr uint32_t id_s = tc::idesc_f16(kXRows, kXRows, !kFp16, false, false);
         constexpr uint32_t id_g = tc::idesc_f16(kXRows, D, !kFp16, false, true);
-        // rows behind the sequence's (or the tile's) last one are zeroed in a tile that has landed
-        auto clear = [&](int off, int s, int i) {
-            const int left = u.seq.qlen - (t0 + i) * A.tpt;
-            const int live = (left < A.tpt ? left : A.tpt) * G;
-            if (live < kXRows) {
-                KeyBits<4> kb;
-                kb.set_first(live);
-                zero_rows<L::KC>(smem + off + s * L::TILE, kb, lane);
-            }
-            tc::tc_fence_after();
-        };
-        auto issue_s = [&](int i) {
-            clear(L::OFF_A, i % L::RA, i);
-            mma_abt<D, kXRows>(tmem, sbase + L::OFF_X, sbase + L::OFF_A + (i % L::RA) * L::TILE, id_s);
-            tc::mma_commit_warp(&bars[XB_S]);
-        };
-        auto issue_dp = [&](int i) {
-            clear(L::OFF_B, i % L::RB, i);
-            mma_abt<D, kXRows>(tmem + 128, sbase + L::OFF_Y, sbase + L::OFF_B + (i % L::RB) * L::TILE, id_s);
-            tc::mma_commit_warp(&bars[XB_DP]);
-        };
         bool ok = true;
-        if (n > 0) {
-            ok = warp_wait(abort_flag, Phase{&bars[XB_XY], 0}, ra.landed(0));
-            if (ok) issue_s(0);
-            ok = ok && warp_wait(abort_flag, rb.landed(0));
-            if (ok) issue_dp(0);
-        }
-        for (int i = 0; i < n && ok; ++i) {
-            const Phase p{&bars[XB_PF], (uint32_t)i & 1u}, ds{&bars[XB_DS], (uint32_t)i & 1u};
-            const bool more = i + 1 < n;
-            ok = more ? warp_wait(abort_flag, p, ra.landed(i + 1)) : warp_wait(abort_flag, p);
+        int g = 0, nonempty = 0;
+        for (int k = 0; ok; ++k) {
+            const int unit = units.read(k, abort_flag, lane);
+            ok = unit >= 0;
+            if (!ok || unit >= A.units) break;
+            const Work w = decode(unit);
+            const int n = w.n;
+            if (n == 0) continue;
+            // rows behind the sequence's last one are zeroed in a tile that has landed
+            auto clear = [&](int off, int s, int i) {
+                const int left = w.u.seq.qlen - (w.t0 + i) * A.tpt;
+                if (left < A.tpt) {
+                    KeyBits<4> kb;
+                    kb.set_first(left * G);
+                    zero_rows<L::KC, 4, 32>(smem + off + s * L::TILE, kb, lane);
+                    __syncwarp();
+                }
+                tc::tc_fence_after();
+            };
+            auto issue_s = [&](int i, int gi) {
+                clear(L::OFF_A, gi % L::RA, i);
+                mma_abt<D, kXRows>(tmem, sbase + L::OFF_X, sbase + L::OFF_A + (gi % L::RA) * L::TILE, id_s);
+                tc::mma_commit_warp(&bars[XB_S]);
+            };
+            auto issue_dp = [&](int i, int gi) {
+                clear(L::OFF_B, gi % L::RB, i);
+                mma_abt<D, kXRows>(tmem + 128, sbase + L::OFF_Y, sbase + L::OFF_B + (gi % L::RB) * L::TILE, id_s);
+                tc::mma_commit_warp(&bars[XB_DP]);
+                if (i + 1 == n) tc::mma_commit_warp(&bars[XB_XYE]);
+            };
+            ok = warp_wait(abort_flag, Phase{&bars[XB_XY], (uint32_t)nonempty & 1u}, ra.landed(g));
             if (!ok) break;
-            tc::tc_fence_after();
-            mma_ab<kXRows, 64>(tmem + 256, tmem, sbase + L::OFF_B + (i % L::RB) * L::TILE, id_g, i > 0);
-            tc::mma_commit_warp(&rb.empty[i % L::RB]);
-            if (more) issue_s(i + 1);
-            ok = more ? warp_wait(abort_flag, ds, rb.landed(i + 1)) : warp_wait(abort_flag, ds);
+            issue_s(0, g);
+            ok = warp_wait(abort_flag, rb.landed(g));
             if (!ok) break;
-            tc::tc_fence_after();
-            mma_ab<kXRows, 64>(tmem + 384, tmem + 128, sbase + L::OFF_A + (i % L::RA) * L::TILE, id_g, i > 0);
-            tc::mma_commit_warp(&ra.empty[i % L::RA]);
-            if (more) issue_dp(i + 1);
+            issue_dp(0, g);
+            for (int i = 0; i < n; ++i, ++g) {
+                const Phase p{&bars[XB_PF], (uint32_t)g & 1u}, ds{&bars[XB_DS], (uint32_t)g & 1u};
+                const bool more = i + 1 < n;
+                ok = more ? warp_wait(abort_flag, p, ra.landed(g + 1)) : warp_wait(abort_flag, p);
+                if (!ok) break;
+                tc::tc_fence_after();
+                mma_ab<kXRows, 64>(tmem + 256, tmem, sbase + L::OFF_B + (g % L::RB) * L::TILE, id_g, i > 0);
+                tc::mma_commit_warp(&rb.empty[g % L::RB]);
+                if (more) issue_s(i + 1, g + 1);
+                ok = more ? warp_wait(abort_flag, ds, rb.landed(g + 1)) : warp_wait(abort_flag, ds);
+                if (!ok) break;
+                tc::tc_fence_after();
+                mma_ab<kXRows, 64>(tmem + 384, tmem + 128, sbase + L::OFF_A + (g % L::RA) * L::TILE, id_g, i > 0);
+                tc::mma_commit_warp(&ra.empty[g % L::RA]);
+                if (more) issue_dp(i + 1, g + 1);
+            }
+            if (!ok) break;
+            tc::mma_commit_warp(&bars[XB_ACC]);
+            ++nonempty;
         }
         if (!ok && lane == 0) fail();
-        tc::mma_commit_warp(&bars[XB_ACC]);
-        if (!__all_sync(0xffffffffu, tc::mbar_wait_drain(&bars[XB_ACC], 0, kXWaitNs)) && lane == 0) fail();
+        // every MMA issued must be complete before TMEM is freed: one more phase of XB_ACC
+        if (!ok) tc::mma_commit_warp(&bars[XB_ACC]);
+        const int phases = nonempty + (ok ? 0 : 1);
+        if (!__all_sync(0xffffffffu, tc::drain_armed(&bars[XB_ACC], phases, kXWaitNs)) && lane == 0) fail();
     }
 
     const int h = warp >> 2;
     const int r = (warp & 3) * 32 + lane;                // key = TMEM lane
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    if (warp < 8 && n > 0) {
-        // ------------------------------------------------------ softmax
-        const float c = A.scale_log2;
-        const bool live = key0 + r < u.seq.klen && (!A.mask || A.mask[(int64_t)u.seq.k0 + key0 + r]);
-        const float k = kFp16 ? exp2f(up - kShift) : 1.f;
-        // One query tile; a copy of its own for key tiles with absent keys.
-        auto tile = [&](auto masked, int i) -> bool {
-            constexpr bool kMasked = decltype(masked)::value;
-            const float4 *st = reinterpret_cast<const float4 *>(smem + L::OFF_STAT + (i & 1) * 1024) + h * 16;
-            float p[64];
-            tmem_ld32(trow + h * 64, reinterpret_cast<uint32_t *>(p));
-            tmem_ld32(trow + h * 64 + 32, reinterpret_cast<uint32_t *>(p) + 32);
-            tc::tmem_wait_ld();
-            uint32_t q[32];
-#pragma unroll
-            for (int j = 0; j < 64; j += 4) {
-                const float4 nl4 = st[j / 4];
-                const float nl[4] = {nl4.x, nl4.y, nl4.z, nl4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = fmaf(p[j + e], c, nl[e]);
-                    if (kFp16) x += kShift;
-                    p[j + e] = xex2(x);
-                    if (kMasked && !live) p[j + e] = 0.f;
-                }
-                q[j / 2] = xpack<kFp16>(p[j], p[j + 1]);
-                q[j / 2 + 1] = xpack<kFp16>(p[j + 2], p[j + 3]);
-            }
-            tmem_st32(trow + h * 64, q);
-            tmem_wait_st();
-            tc::tc_fence_before();
-            warp_arrive(&bars[XB_PF], lane);
-            if (!warp_wait(abort_flag, Phase{&bars[XB_DP], (uint32_t)i & 1u})) return false;
-            tc::tc_fence_after();
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                float y[32];
-                tmem_ld32(trow + 128 + h * 64 + g * 32, reinterpret_cast<uint32_t *>(y));
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 nd4 = st[32 + (g * 32 + j) / 4];
-                    const float nd[4] = {nd4.x, nd4.y, nd4.z, nd4.w};
-                    float a[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        a[e] = y[j + e] + nd[e];
-                        if (kFp16) a[e] *= k;
-                        a[e] *= p[g * 32 + j + e];
-                        if (kMasked && !live) a[e] = 0.f;
-                    }
-                    q[(g * 32 + j) / 2] = xpack<kFp16>(a[0], a[1]);
-                    q[(g * 32 + j) / 2 + 1] = xpack<kFp16>(a[2], a[3]);
-                }
-            }
-            tmem_st32(trow + 128 + h * 64, q);
-            tmem_wait_st();
-            tc::tc_fence_before();
-            warp_arrive(&bars[XB_DS], lane);
-            if (lane == 0) tc::mbar_arrive(&rs.empty[i & 1]);
-            return true;
-        };
-        const bool all = __all_sync(0xffffffffu, live);
-        bool ok = true;
-        for (int i = 0; i < n && ok; ++i) {
-            ok = warp_wait(abort_flag, rs.landed(i), Phase{&bars[XB_S], (uint32_t)i & 1u});
-            if (!ok) break;
-            tc::tc_fence_after();
-            ok = all ? tile(std::false_type{}, i) : tile(std::true_type{}, i);
-        }
-        if (ok) ok = warp_wait(abort_flag, Phase{&bars[XB_ACC], 0});
-        if (!ok && lane == 0) fail();
-        tc::tc_fence_after();
-    }
-
-    // ---------------------------------------------------------- epilogue: warps 0-3 dV, warps 4-7 dK
-    const float fv = kFp16 ? exp2f(-kShift) : 1.f, fk = A.scale * (kFp16 ? exp2f(-up) : 1.f);
-    auto out = [&](int k) -> uint16_t * {
-        const int key = key0 + k % kXRows;
-        if (key >= cover) return nullptr;
-        return (k < kXRows ? A.dv : A.dk) + (((int64_t)u.seq.k0 + key) * A.n2 + u.head) * D;
+    const float fv = kFp16 ? exp2f(-kShift) : 1.f;
+    Work w{};
+    float up = 0.f;                                      // exponent that dS is scaled by
+    auto out = [&](int k) -> int64_t {                   // place of key row k in dK and dV; negative: none
+        const int key = w.key0 + k;
+        if (key >= (A.s2_pad ? A.s2_pad : w.u.seq.klen)) return -1;
+        return (((int64_t)w.u.seq.k0 + key) * A.n2 + w.u.head) * D;
     };
-    if (ns == 1) {
-        if (warp < 8) {
-            uint16_t *dst = out(h * kXRows + r);
-            const float f = h ? fk : fv;
+    if (warp < 8) {
+        bool ok = true;
+        int g = 0, nonempty = 0;
+        // what the next unit needs from memory is on its way while this one is stored
+        int unit = units.read(0, abort_flag, lane);
+        bool st_live = false;
+        uint2 norms{};
+        auto begin = [&]() {
+            w = decode(unit);
+            st_live = w.key0 + r < w.u.seq.klen && (!A.mask || A.mask[(int64_t)w.u.seq.k0 + w.key0 + r] != 0);
+            if constexpr (kFp16) norms = ds_norms(A, w.u);
+        };
+        ok = unit >= 0;
+        if (ok && unit < A.units) begin();
+        for (int turn = 0; ok && unit < A.units; ++turn) {
+            const int n = w.n;
+            if constexpr (kFp16) up = ds_exponent(norms);
+            const bool live = st_live;
+            if (n > 0) {
+                // ---------------------------------------------- softmax
+                const float c = A.scale_log2;
+                const float k = kFp16 ? exp2f(up - kShift) : 1.f;
+                // One query tile; a copy of its own for key tiles with absent keys.
+                auto tile = [&](auto masked) -> bool {
+                    constexpr bool kMasked = decltype(masked)::value;
+                    const float4 *st = reinterpret_cast<const float4 *>(smem + L::OFF_STAT + (g & 1) * 1024) + h * 16;
+                    float p[64];
+                    tmem_ld32(trow + h * 64, reinterpret_cast<uint32_t *>(p));
+                    tmem_ld32(trow + h * 64 + 32, reinterpret_cast<uint32_t *>(p) + 32);
+                    tc::tmem_wait_ld();
+                    uint32_t q[32];
+#pragma unroll
+                    for (int j = 0; j < 64; j += 4) {
+                        const float4 nl4 = st[j / 4];
+                        const float nl[4] = {nl4.x, nl4.y, nl4.z, nl4.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float x = fmaf(p[j + e], c, nl[e]);
+                            if (kFp16) x += kShift;
+                            p[j + e] = xex2(x);
+                            if (kMasked && !live) p[j + e] = 0.f;
+                        }
+                        q[j / 2] = xpack<kFp16>(p[j], p[j + 1]);
+                        q[j / 2 + 1] = xpack<kFp16>(p[j + 2], p[j + 3]);
+                    }
+                    tmem_st32(trow + h * 64, q);
+                    tmem_wait_st();
+                    tc::tc_fence_before();
+                    warp_arrive(&bars[XB_PF], lane);
+                    if (!warp_wait(abort_flag, Phase{&bars[XB_DP], (uint32_t)g & 1u})) return false;
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        float y[32];
+                        tmem_ld32(trow + 128 + h * 64 + f * 32, reinterpret_cast<uint32_t *>(y));
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 nd4 = st[32 + (f * 32 + j) / 4];
+                            const float nd[4] = {nd4.x, nd4.y, nd4.z, nd4.w};
+                            float a[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                a[e] = y[j + e] + nd[e];
+                                if (kFp16) a[e] *= k;
+                                a[e] *= p[f * 32 + j + e];
+                                if (kMasked && !live) a[e] = 0.f;
+                            }
+                            q[(f * 32 + j) / 2] = xpack<kFp16>(a[0], a[1]);
+                            q[(f * 32 + j) / 2 + 1] = xpack<kFp16>(a[2], a[3]);
+                        }
+                    }
+                    tmem_st32(trow + 128 + h * 64, q);
+                    tmem_wait_st();
+                    tc::tc_fence_before();
+                    warp_arrive(&bars[XB_DS], lane);
+                    if (lane == 0) tc::mbar_arrive(&rs.empty[g & 1]);
+                    return true;
+                };
+                const bool all = __all_sync(0xffffffffu, live);
+                for (int i = 0; i < n && ok; ++i, ++g) {
+                    ok = warp_wait(abort_flag, rs.landed(g), Phase{&bars[XB_S], (uint32_t)g & 1u});
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    ok = all ? tile(std::false_type{}) : tile(std::true_type{});
+                }
+                if (ok) ok = warp_wait(abort_flag, Phase{&bars[XB_ACC], (uint32_t)nonempty & 1u});
+                ++nonempty;
+                tc::tc_fence_after();
+            }
+            if (ns > 1 || !ok) break;                    // stored below
+            // -------------------------------------------------- epilogue: warps 0-3 dV, warps 4-7 dK
+            const float f = h ? A.scale * (kFp16 ? exp2f(-up) : 1.f) : fv;
+            RowStore<kFp16> rows;
+            rows.rows(out(r), lane);
+            unit = units.read(turn + 1, abort_flag, lane);
+            ok = unit >= 0;
+            if (ok && unit < A.units) begin();
 #pragma unroll
             for (int j = 0; j < D; j += 32) {
                 float y[32];
@@ -686,29 +823,36 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = n > 0 ? y[e] * f : 0.f;
-                if (dst) store_row<kFp16, 32>(dst + j, y);
+                rows.store(h ? A.dk : A.dv, y, j, lane);
             }
+            tc::tc_fence_before();                       // read before the next unit's products may follow
         }
-    } else {
+        if (!ok && lane == 0) fail();
+    }
+    if (ns > 1) {
+        // the CTA's only unit: partial sums into shared memory, then each rank joins its share of the rows
         float *xo = reinterpret_cast<float *>(smem);
         __syncthreads();                                 // loads and products on this memory are complete
         if (warp < 8) {
 #pragma unroll
             for (int j = 0; j < D; j += 32) {
                 float y[32];
-                if (n > 0) {
+                if (w.n > 0) {
                     tmem_ld32(trow + 256 + h * 128 + j, reinterpret_cast<uint32_t *>(y));
                     tc::tmem_wait_ld();
                 }
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                     *reinterpret_cast<float4 *>(xo + (h * kXRows + r) * L::XROW + j + e) =
-                        n > 0 ? make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        w.n > 0 ? make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
         cluster_sync();
-        if (warp < 8)
-            join_rows<kFp16, D>(xo, 2 * kXRows, ns, rank, warp, lane, out, [&](int k) { return k < kXRows ? fv : fk; });
+        if (warp < 8) {
+            const float fk = A.scale * (kFp16 ? exp2f(-up) : 1.f);
+            join_rows<kFp16, D>(xo, A.dv, ns, rank, warp, lane, out, fv);
+            join_rows<kFp16, D>(xo + kXRows * L::XROW, A.dk, ns, rank, warp, lane, out, fk);
+        }
         cluster_sync();                                  // peers are done with this CTA's shared memory
     }
     tc::tc_fence_before();
@@ -733,11 +877,16 @@ bool maps(BwdMaps *m, const XArgs &a, const sca_io &io, const sca_desc &d) {
 }
 
 template <bool kFp16, int D>
-cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, bool dkv, int units, cudaStream_t s) {
+cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, bool dkv, cudaStream_t s) {
     BwdMaps m;
     if (!maps(&m, a, io, d)) return cudaErrorInvalidValue;
-    return x_launch(dkv ? k_xdkv<kFp16, D> : k_xdq<kFp16, D>, units * a.nsplit, kXThreads, a.nsplit, BwdSmem<D>::TOTAL, s, m.q, m.dy,
+    return x_launch(dkv ? k_xdkv<kFp16, D> : k_xdq<kFp16, D>, a.ctas, kXThreads, a.nsplit, BwdSmem<D>::TOTAL, s, m.q, m.dy,
                     m.k, m.v, a);
+}
+
+template <bool kFp16>
+cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, bool dkv, cudaStream_t s) {
+    return d.d == 128 ? launch<kFp16, 128>(a, io, d, dkv, s) : launch<kFp16, 64>(a, io, d, dkv, s);
 }
 
 }  // namespace
@@ -755,16 +904,12 @@ cudaError_t launch_xpre(const XArgs &a, bool fp16, int d, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_xdq(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s) {
-    const bool fp16 = d.dtype == SAG_FP16;
-    if (d.d == 128) return fp16 ? launch<true, 128>(a, io, d, false, units, s) : launch<false, 128>(a, io, d, false, units, s);
-    return fp16 ? launch<true, 64>(a, io, d, false, units, s) : launch<false, 64>(a, io, d, false, units, s);
+cudaError_t launch_xdq(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s) {
+    return d.dtype == SAG_FP16 ? launch<true>(a, io, d, false, s) : launch<false>(a, io, d, false, s);
 }
 
-cudaError_t launch_xdkv(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s) {
-    const bool fp16 = d.dtype == SAG_FP16;
-    if (d.d == 128) return fp16 ? launch<true, 128>(a, io, d, true, units, s) : launch<false, 128>(a, io, d, true, units, s);
-    return fp16 ? launch<true, 64>(a, io, d, true, units, s) : launch<false, 64>(a, io, d, true, units, s);
+cudaError_t launch_xdkv(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s) {
+    return d.dtype == SAG_FP16 ? launch<true>(a, io, d, true, s) : launch<false>(a, io, d, true, s);
 }
 
 }  // namespace sag

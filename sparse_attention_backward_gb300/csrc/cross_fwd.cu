@@ -37,6 +37,7 @@ constexpr int kFwdThreads = 192, kFwdTma = 4, kFwdMma = 5;   // warps 0-3 softma
 template <int D, int kKeys>
 struct FwdShape {
     static constexpr int BUFS = 128 / kKeys, HALVES = kKeys / 64;
+    static constexpr bool MASK_AHEAD = kKeys == 64;              // 128 scores a thread leave no registers for it
     static constexpr int KC = D / 64;
     static constexpr int Q_BYTES = KC * 16384;
     static constexpr int TILE = KC * kKeys * 128;
@@ -160,10 +161,6 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                 ok = L::HALVES == 1 && more ? warp_wait(abort_flag, written(0), landed(jv), landed(jv + 1))
                                             : warp_wait(abort_flag, written(0), landed(jv));
                 if (!ok) break;
-                if (i >= partial) {
-                    const KeyBits<kKeys / 32> kb = key_bits<kKeys / 32>(A.mask, u.seq, (t0 + i) * kKeys, lane);
-                    if (!kb.all()) zero_rows<L::KC>(smem + L::OFF_RING + jv % ST * L::TILE, kb, lane);
-                }
                 tc::tc_fence_after();
                 mma_ab<kKeys, 32, 0, 4>(acc, pt, vt, id_o, i > 0);
                 if (L::HALVES == 2) {
@@ -203,6 +200,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             // selects otherwise run for every tile.  Scalar fp32 operations:
             // paired ones (fma.f32x2) have no more throughput here and
             // measured 10 % slower.
+            KeyLoad<kKeys / 32> keys{};                  // of the next tile that may lack keys
             auto tile = [&](auto masked, int i) -> bool {
                 const uint32_t ts = trow + i % NB * kKeys;
                 float x[kKeys];
@@ -210,10 +208,17 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                 for (int j = 0; j < kKeys; j += 32) tmem_ld32(ts + j, reinterpret_cast<uint32_t *>(x) + j);
                 tc::tmem_wait_ld();
                 if constexpr (decltype(masked)::value) {
-                    const KeyBits<kKeys / 32> kb = key_bits<kKeys / 32>(A.mask, u.seq, (t0 + i) * kKeys, lane);
+                    if (!L::MASK_AHEAD) keys.start(A.mask, u.seq, (t0 + i) * kKeys, lane);
+                    const KeyBits<kKeys / 32> kb = keys.finish();
+                    if (L::MASK_AHEAD && i + 1 < n) keys.start(A.mask, u.seq, (t0 + i + 1) * kKeys, lane);
 #pragma unroll
                     for (int j = 0; j < kKeys; ++j)
                         if (!((kb.w[j >> 5] >> (j & 31)) & 1u)) x[j] = -INFINITY;
+                    if (!kb.all()) {
+                        const int jv = i + (i + NB < n ? i + NB : n);   // V's place in the ring, as in the MMA warp
+                        if (!warp_wait(abort_flag, Phase{&full[jv % ST], (uint32_t)(jv / ST) & 1u})) return false;
+                        zero_rows<L::KC, kKeys / 32, 128>(smem + L::OFF_RING + jv % ST * L::TILE, kb, r);
+                    }
                 }
                 float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -265,6 +270,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 return true;
             };
+            if (L::MASK_AHEAD && partial < n) keys.start(A.mask, u.seq, (t0 + (partial > 0 ? partial : 0)) * kKeys, lane);
             bool ok = true;
             for (int i = 0; i < n && ok; ++i) {
                 ok = formed(i);
@@ -286,6 +292,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             const int64_t row = (int64_t)(u.seq.q0 + tok) * A.n1 + u.head * G + r % G;
             const bool some = l > 0.f || l != l;         // l is NaN when a score was
             const float inv = some ? 1.f / l : 0.f;
+            RowStore<kFp16> rows;
+            rows.rows(mine ? row * D : -1, lane);
 #pragma unroll
             for (int j = 0; j < D; j += 32) {
                 float y[32];
@@ -295,7 +303,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = some && !pad ? y[e] * inv : 0.f;
-                if (mine) store_row<kFp16, 32>(A.o + row * D + j, y);
+                rows.store(A.o, y, j, lane);
             }
             if (mine) A.lse[row] = pad ? 0.f : some ? (m - kShift) * kLn2 + logf(l) : -INFINITY;
         } else {
@@ -375,12 +383,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 }
 
 template <bool kFp16, int D, int kKeys>
-cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, int units, cudaStream_t s) {
+cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s) {
     CUtensorMap mq, mk, mv;
     if (!x_map_q(&mq, io.query, d, a, d.q_stride) || !x_map_k(&mk, io.key, io.query, d, d.k_stride, kKeys) ||
         !x_map_k(&mv, io.value, io.query, d, d.v_stride, kKeys))
         return cudaErrorInvalidValue;
-    return x_launch(k_xfwd<kFp16, D, kKeys>, units * a.nsplit, kFwdThreads, a.nsplit, FwdShape<D, kKeys>::TOTAL, s, mq, mk,
+    return x_launch(k_xfwd<kFp16, D, kKeys>, a.ctas, kFwdThreads, a.nsplit, FwdShape<D, kKeys>::TOTAL, s, mq, mk,
                     mv, a);
 }
 
@@ -390,12 +398,12 @@ cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, int unit
 // but leave one score tile in flight instead of two.  They are taken for 128-wide heads where products dominate: full
 // query tiles and long loops.  Measured, 64 against 128: 8192 x 4096 tokens 825 / 742 us, 130 x 131072 233 / 205;
 // 1024 x 1024 33 / 35, 2048 x 512 70 / 74, one token x 4096 69 / 74 us; 64-wide heads 582 / 596 us.
-cudaError_t launch_xfwd(const XArgs &a, const sca_io &io, const sca_desc &d, bool long_loops, int units, cudaStream_t s) {
+cudaError_t launch_xfwd(const XArgs &a, const sca_io &io, const sca_desc &d, bool long_loops, cudaStream_t s) {
     const bool fp16 = d.dtype == SAG_FP16;
     if (d.d == 128 && long_loops)
-        return fp16 ? launch<true, 128, 128>(a, io, d, units, s) : launch<false, 128, 128>(a, io, d, units, s);
-    if (d.d == 128) return fp16 ? launch<true, 128, 64>(a, io, d, units, s) : launch<false, 128, 64>(a, io, d, units, s);
-    return fp16 ? launch<true, 64, 64>(a, io, d, units, s) : launch<false, 64, 64>(a, io, d, units, s);
+        return fp16 ? launch<true, 128, 128>(a, io, d, s) : launch<false, 128, 128>(a, io, d, s);
+    if (d.d == 128) return fp16 ? launch<true, 128, 64>(a, io, d, s) : launch<false, 128, 64>(a, io, d, s);
+    return fp16 ? launch<true, 64, 64>(a, io, d, s) : launch<false, 64, 64>(a, io, d, s);
 }
 
 }  // namespace sag
