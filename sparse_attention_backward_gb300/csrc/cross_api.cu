@@ -75,6 +75,12 @@ int split_of(int64_t units, int tiles, int room) {
     return ns;
 }
 
+void set_split(XArgs *a, int ns) {
+    a->nsplit = ns;
+    a->split_log2 = 0;
+    while (1 << a->split_log2 < ns) ++a->split_log2;
+}
+
 XArgs x_args(const sca_desc *d, const sca_io *io, const XPlan &p, char *ws) {
     XArgs a{};
     a.n1 = d->n1;
@@ -182,7 +188,7 @@ extern "C" sag_status cross_attn_fwd(const sca_desc *desc, const sca_io *io, voi
     XArgs a = x_args(desc, io, p, ws);
     if (x_table(&a, desc, p, ws, s) != cudaSuccess) return SAG_ERR_CUDA;
     a.units = (int)(p.q_tiles * desc->n2);
-    a.nsplit = split_of(a.units, 2 * p.max_k, 2 * current_device_sms());   // two CTAs an SM, tiles of 64 keys
+    set_split(&a, split_of(a.units, 2 * p.max_k, 2 * current_device_sms()));   // two CTAs an SM, tiles of 64 keys
     a.n_status = a.ctas = a.units * a.nsplit;
     // full query tiles, and at least 2048 keys a CTA
     const bool long_loops = p.max_q > 1 && p.max_k >= 16 * a.nsplit;
@@ -211,7 +217,7 @@ extern "C" sag_status cross_attn_grad(const sca_desc *desc, const sca_io *io, vo
     // one CTA an SM: a cluster for each unit, or CTAs that take unit after unit
     auto share = [&](int units, int tiles) {
         a.units = units;
-        a.nsplit = split_of(units, tiles, sms);
+        set_split(&a, split_of(units, tiles, sms));
         a.ctas = a.nsplit > 1 || units < sms ? units * a.nsplit : sms;
     };
     int before = 0;

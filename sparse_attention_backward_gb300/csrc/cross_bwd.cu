@@ -161,7 +161,7 @@ struct Units {
     __device__ __forceinline__ int take(const XArgs &A, int k, volatile int *abort) const {   // one thread; -1: timeout
         if (k >= 2 && !tc::mbar_wait(&empty[k & 1], (k / 2 - 1) & 1, abort, kXWaitNs)) return -1;
         int unit = A.units;
-        if (k == 0) unit = blockIdx.x / A.nsplit;
+        if (k == 0) unit = blockIdx.x >> A.split_log2;
         else if (A.ctas < A.units) unit = (int)(gridDim.x + atomicAdd(A.ticket, 1u));
         slot[k & 1] = unit;
         tc::mbar_arrive(&full[k & 1]);
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot, sbase = tc::smem_u32(smem);
-    const int ns = A.nsplit, rank = blockIdx.x % ns;
+    const int ns = A.nsplit, rank = blockIdx.x & (ns - 1);
     const int G = A.group;
     auto fail = [&]() { *abort_flag = 1; };
     struct Work {
@@ -265,8 +265,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         w.u = x_decode<&SeqRow::qtile0>(A, unit);
         w.tok0 = w.u.tile * A.tpt;
         const int nkt = w.tok0 < w.u.seq.qlen ? (w.u.seq.klen + kXRows - 1) / kXRows : 0;
-        w.t0 = (int)((int64_t)nkt * rank / ns);
-        w.n = (int)((int64_t)nkt * (rank + 1) / ns) - w.t0;
+        x_share(A, nkt, rank, &w.t0, &w.n);
         return w;
     };
 
@@ -384,11 +383,13 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     Work w{};
     float up = 0.f;                                      // exponent that dS is scaled by
-    auto out = [&](int k) -> int64_t {                   // place of row k in dQ; negative: none
-        const int tok = w.tok0 + k / G;
-        if (k >= A.tpt * G || tok >= (A.s1_pad ? A.s1_pad : w.u.seq.qlen)) return -1;
-        return ((int64_t)(w.u.seq.q0 + tok) * A.n1 + w.u.head * G + k % G) * D;
+    auto place = [&](int tok_in, int head_in) -> int64_t {   // place of a row (token and head in the tile) in dQ
+        const int tok = w.tok0 + tok_in;
+        if (tok_in >= A.tpt || tok >= (A.s1_pad ? A.s1_pad : w.u.seq.qlen)) return -1;
+        return ((int64_t)(w.u.seq.q0 + tok) * A.n1 + w.u.head * G + head_in) * D;
     };
+    auto out = [&](int k) { return place(k / G, k % G); };
+    const int my_tok = r / G, my_head = r % G;
     if (warp < 8) {
         bool ok = true;
         int g = 0, nonempty = 0;
@@ -426,29 +427,34 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     for (int j = 0; j < 64; ++j) p[j] = xex2(fmaf(p[j], c, nl));
                     if (!warp_wait(abort_flag, Phase{&bars[XB_DP], (uint32_t)g & 1u})) return false;
                     tc::tc_fence_after();
-                    float y[64];
-                    tmem_ld32(trow + 256 + h * 64, reinterpret_cast<uint32_t *>(y));
-                    tmem_ld32(trow + 256 + h * 64 + 32, reinterpret_cast<uint32_t *>(y) + 32);
-                    tc::tmem_wait_ld();
-                    tc::tc_fence_before();
-                    warp_arrive(&bars[XB_PF], lane);     // dP has been read
-                    KeyBits<4> kb{};
+                    uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
                     if constexpr (decltype(masked)::value) {
-                        kb = keys.finish();
+                        const KeyBits<4> kb = keys.finish();
                         if (i + 1 < n) keys.start(A.mask, w.u.seq, (w.t0 + i + 1) * kXRows, lane);
                         // the scores have read this tile's keys, so its dead rows may go before dS K
                         if (!kb.all()) zero_rows<L::KC, 4, 256>(smem + L::OFF_A + g % L::RA * L::TILE, kb, threadIdx.x);
+                        bits[0] = h ? kb.w[2] : kb.w[0];
+                        bits[1] = h ? kb.w[3] : kb.w[1];
                     }
                     uint32_t q[32];
 #pragma unroll
-                    for (int j = 0; j < 64; j += 2) {
-                        float a = p[j] * (y[j] + nd), b = p[j + 1] * (y[j + 1] + nd);
-                        if constexpr (decltype(masked)::value) {
-                            const uint32_t bits = h ? kb.w[2 + (j >> 5)] : kb.w[j >> 5];
-                            if (!((bits >> (j & 31)) & 1u)) a = 0.f;
-                            if (!((bits >> ((j + 1) & 31)) & 1u)) b = 0.f;
+                    for (int f = 0; f < 2; ++f) {
+                        float y[32];
+                        tmem_ld32(trow + 256 + h * 64 + f * 32, reinterpret_cast<uint32_t *>(y));
+                        tc::tmem_wait_ld();
+                        if (f) {
+                            tc::tc_fence_before();
+                            warp_arrive(&bars[XB_PF], lane);   // dP has been read
                         }
-                        q[j / 2] = xpack<kFp16>(a, b);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float a = p[f * 32 + j] * (y[j] + nd), b = p[f * 32 + j + 1] * (y[j + 1] + nd);
+                            if constexpr (decltype(masked)::value) {
+                                if (!((bits[f] >> j) & 1u)) a = 0.f;
+                                if (!((bits[f] >> (j + 1)) & 1u)) b = 0.f;
+                            }
+                            q[(f * 32 + j) / 2] = xpack<kFp16>(a, b);
+                        }
                     }
                     tmem_st32(ts, q);
                     tmem_wait_st();
@@ -469,9 +475,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
             if (ns > 1 || !ok) break;                    // stored below
             // -------------------------------------------------- epilogue
             const float f = A.scale * (kFp16 ? exp2f(-up) : 1.f);
-            const bool pad = n == 0 || w.tok0 + r / G >= w.u.seq.qlen;
+            const bool pad = n == 0 || w.tok0 + my_tok >= w.u.seq.qlen;
             RowStore<kFp16> rows;
-            rows.rows(out(r), lane);
+            rows.rows(place(my_tok, my_head), lane);
             unit = units.read(k + 1, abort_flag, lane);
             ok = unit >= 0;
             if (ok && unit < A.units) begin();
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         float *xo = reinterpret_cast<float *>(smem);
         __syncthreads();                                 // loads and products on this memory are complete
         if (warp < 8) {
-            const bool pad = w.n == 0 || w.tok0 + r / G >= w.u.seq.qlen;
+            const bool pad = w.n == 0 || w.tok0 + my_tok >= w.u.seq.qlen;
 #pragma unroll
             for (int j = 0; j < D / 2; j += 32) {
                 float y[32];
@@ -570,7 +576,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot, sbase = tc::smem_u32(smem);
-    const int ns = A.nsplit, rank = blockIdx.x % ns;
+    const int ns = A.nsplit, rank = blockIdx.x & (ns - 1);
     const int G = A.group;
     auto fail = [&]() { *abort_flag = 1; };
     struct Work {
@@ -582,8 +588,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         w.u = x_decode<&SeqRow::ktile0>(A, unit);
         w.key0 = w.u.tile * kXRows;
         const int nqt = w.key0 < w.u.seq.klen ? (w.u.seq.qlen + A.tpt - 1) / A.tpt : 0;
-        w.t0 = (int)((int64_t)nqt * rank / ns);
-        w.n = (int)((int64_t)nqt * (rank + 1) / ns) - w.t0;
+        x_share(A, nqt, rank, &w.t0, &w.n);
         return w;
     };
 

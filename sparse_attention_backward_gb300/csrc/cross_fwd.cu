@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         tc::prefetch_tmap(&map_k);
         tc::prefetch_tmap(&map_v);
     }
-    const int ns = A.nsplit, rank = blockIdx.x % ns;
-    const XUnit u = x_decode<&SeqRow::qtile0>(A, blockIdx.x / ns);
+    const int ns = A.nsplit, rank = blockIdx.x & (ns - 1);
+    const XUnit u = x_decode<&SeqRow::qtile0>(A, blockIdx.x >> A.split_log2);
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
@@ -93,7 +93,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     const int G = A.group, tok0 = u.tile * A.tpt;
     const int cover = A.s1_pad ? A.s1_pad : u.seq.qlen;
     const int nkt = tok0 < u.seq.qlen ? (u.seq.klen + kKeys - 1) / kKeys : 0;
-    const int t0 = (int)((int64_t)nkt * rank / ns), n = (int)((int64_t)nkt * (rank + 1) / ns) - t0;
+    int t0, n;
+    x_share(A, nkt, rank, &t0, &n);
     const int partial = A.mask ? 0 : u.seq.klen / kKeys - t0;    // tiles from this one on may lack keys
     auto fail = [&]() { *abort_flag = 1; };
 
