@@ -121,8 +121,8 @@ __device__ __forceinline__ float ds_exponent(uint2 norms) {
     if (!(bound > 0.f) || !(bound < INFINITY)) return 0.f;
     return fminf(fmaxf(14.f - (float)ilogbf(bound), -40.f), 40.f);
 }
-__device__ __forceinline__ uint2 ds_norms(const XArgs &A, const XUnit &u) {
-    return *reinterpret_cast<const uint2 *>(A.norms + ((int64_t)u.b * A.n2 + u.head) * 2);
+__device__ __forceinline__ uint2 ds_norms(const XArgs &A, int b, int head) {
+    return *reinterpret_cast<const uint2 *>(A.norms + ((int64_t)b * A.n2 + head) * 2);
 }
 
 // ------------------------------------------------------------------- shared
@@ -140,6 +140,7 @@ struct BwdSmem {
     static constexpr int XROW = D + 4;
     static_assert(2 * kXRows * XROW * 4 <= OFF_STAT, "the exchange overlays the tiles");
     static_assert(TOTAL <= 227 * 1024, "shared memory of one CTA");
+    // 512 bytes behind OFF_BAR: barriers, TMEM address, abort flag; from 320 on the two slots of units
 };
 // barriers; XB_XYE: the resident tiles may be overwritten; XB_UF, XB_UE: units handed out
 enum {
@@ -151,27 +152,42 @@ __device__ __forceinline__ int bwd_arrivals(int i) {
     return i == XB_PF || i == XB_DS || i == XB_STE || i == XB_STE + 1 ? 8 : i == XB_UE || i == XB_UE + 1 ? 9 : 1;
 }
 
+// A unit as its roles need it, in shared memory.
+struct alignas(16) Work {
+    SeqRow seq;
+    int32_t b, head;
+    int32_t first;                      // k_xdq: first token, k_xdkv: first key, within the sequence
+    int32_t t0, n;                      // this rank's first tile of the loop and their number; n < 0: no more units
+    int32_t stat;                       // k_xdq: (query tile of all sequences) * n2 + head
+    int32_t pad[4];
+};
+
 // Units of a CTA, one after the other: the first by its number, the others from a ticket counter, since units differ (short
 // sequences, masked and padding tiles) and a fixed order left SMs idle: 142 us against 101 for k_xdkv of a padded batch.
-// The producer takes a unit when it has issued the loads of the one before, and hands it to the MMA and softmax warps
-// through two slots.  A split unit is its cluster's only one.
+// The producer takes and decodes a unit when it has issued the loads of the one before, and hands it to the MMA and softmax
+// warps through two slots.  A split unit is its cluster's only one.
 struct Units {
-    volatile int *slot;
+    Work *slot;
     uint64_t *full, *empty;
-    __device__ __forceinline__ int take(const XArgs &A, int k, volatile int *abort) const {   // one thread; -1: timeout
-        if (k >= 2 && !tc::mbar_wait(&empty[k & 1], (k / 2 - 1) & 1, abort, kXWaitNs)) return -1;
+    // one thread; false: timeout
+    template <class Decode>
+    __device__ __forceinline__ bool take(const XArgs &A, int k, volatile int *abort, Work *w, Decode &&decode) const {
+        if (k >= 2 && !tc::mbar_wait(&empty[k & 1], (k / 2 - 1) & 1, abort, kXWaitNs)) return false;
         int unit = A.units;
         if (k == 0) unit = blockIdx.x >> A.split_log2;
         else if (A.ctas < A.units) unit = (int)(gridDim.x + atomicAdd(A.ticket, 1u));
-        slot[k & 1] = unit;
+        if (unit < A.units) *w = decode(unit);
+        else w->n = -1;
+        slot[k & 1] = *w;
         tc::mbar_arrive(&full[k & 1]);
-        return unit;
+        return true;
     }
-    __device__ __forceinline__ int read(int k, volatile int *abort, int lane) const {         // a warp; -1: timeout
-        if (!warp_wait(abort, Phase{&full[k & 1], (uint32_t)(k >> 1) & 1u})) return -1;
-        const int unit = slot[k & 1];
+    // a warp; false: timeout
+    __device__ __forceinline__ bool read(int k, volatile int *abort, int lane, Work *w) const {
+        if (!warp_wait(abort, Phase{&full[k & 1], (uint32_t)(k >> 1) & 1u})) return false;
+        *w = slot[k & 1];
         warp_arrive(&empty[k & 1], lane);
-        return unit;
+        return true;
     }
 };
 
@@ -232,7 +248,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const Ring rb = {ra.empty + L::RA, ra.empty + L::RA + L::RB, L::RB};
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rb.empty + L::RB);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const Units units = {abort_flag + 1, bars + XB_UF, bars + XB_UE};
+    const Units units = {reinterpret_cast<Work *>(smem + L::OFF_BAR + 320), bars + XB_UF, bars + XB_UE};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         *abort_flag = 0;
@@ -256,16 +272,15 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const int ns = A.nsplit, rank = blockIdx.x & (ns - 1);
     const int G = A.group;
     auto fail = [&]() { *abort_flag = 1; };
-    struct Work {
-        XUnit u;
-        int tok0, t0, n;                                 // first token; this rank's first key tile and their number
-    };
     auto decode = [&](int unit) {
-        Work w;
-        w.u = x_decode<&SeqRow::qtile0>(A, unit);
-        w.tok0 = w.u.tile * A.tpt;
-        const int nkt = w.tok0 < w.u.seq.qlen ? (w.u.seq.klen + kXRows - 1) / kXRows : 0;
-        x_share(A, nkt, rank, &w.t0, &w.n);
+        const XUnit u = x_decode<&SeqRow::qtile0>(A, unit);
+        Work w{};
+        w.seq = u.seq;
+        w.b = u.b;
+        w.head = u.head;
+        w.first = u.tile * A.tpt;
+        w.stat = (int32_t)u.tile_id;
+        x_share(A, w.first < u.seq.qlen ? (u.seq.klen + kXRows - 1) / kXRows : 0, rank, &w.t0, &w.n);
         return w;
     };
 
@@ -276,17 +291,16 @@ __global__ void __launch_bounds__(kXThreads, 1)
             int la = 0, lb = 0, lx = 0;                  // loads so far
             bool ok = true;
             for (int k = 0; ok; ++k) {
-                const int unit = units.take(A, k, abort_flag);
-                ok = unit >= 0;
-                if (!ok || unit >= A.units) break;
-                const Work w = decode(unit);
+                Work w{};
+                ok = units.take(A, k, abort_flag, &w, decode);
+                if (!ok || w.n < 0) break;
                 if (w.n == 0) continue;
                 auto load = [&](const Ring &r, int off, const CUtensorMap *map, int &i, int key) {
                     if (!ring_wait_free(r, i, abort_flag)) return false;
                     const int s = i % r.n;
                     tc::mbar_arrive_expect_tx(&r.full[s], L::TILE);
                     for (int c = 0; c < L::KC; ++c)
-                        tc::tma_load_3d(smem + off + s * L::TILE + c * 16384, map, c * 64, w.u.head, w.u.seq.k0 + key,
+                        tc::tma_load_3d(smem + off + s * L::TILE + c * 16384, map, c * 64, w.head, w.seq.k0 + key,
                                         &r.full[s]);
                     ++i;
                     return true;
@@ -295,9 +309,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 if (!ok) break;
                 tc::mbar_arrive_expect_tx(&bars[XB_XY], 2 * qbytes);
                 for (int c = 0; c < L::KC; ++c) {
-                    const int row = w.u.seq.q0 + w.tok0;
-                    tc::tma_load_3d(smem + L::OFF_X + c * 16384, &map_q, c * 64, w.u.head * G, row, &bars[XB_XY]);
-                    tc::tma_load_3d(smem + L::OFF_Y + c * 16384, &map_dy, c * 64, w.u.head * G, row, &bars[XB_XY]);
+                    const int row = w.seq.q0 + w.first;
+                    tc::tma_load_3d(smem + L::OFF_X + c * 16384, &map_q, c * 64, w.head * G, row, &bars[XB_XY]);
+                    tc::tma_load_3d(smem + L::OFF_Y + c * 16384, &map_dy, c * 64, w.head * G, row, &bars[XB_XY]);
                 }
                 ++lx;
                 // keys run one tile ahead of values, as the MMA warp takes them
@@ -329,10 +343,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
         bool ok = true;
         int g = 0, nonempty = 0;
         for (int k = 0; ok; ++k) {
-            const int unit = units.read(k, abort_flag, lane);
-            ok = unit >= 0;
-            if (!ok || unit >= A.units) break;
-            const Work w = decode(unit);
+            Work w;
+            ok = units.read(k, abort_flag, lane, &w);
+            if (!ok || w.n < 0) break;
             const int n = w.n;
             if (n == 0) continue;
             ok = warp_wait(abort_flag, Phase{&bars[XB_XY], (uint32_t)nonempty & 1u}, ra.landed(g));
@@ -384,9 +397,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
     Work w{};
     float up = 0.f;                                      // exponent that dS is scaled by
     auto place = [&](int tok_in, int head_in) -> int64_t {   // place of a row (token and head in the tile) in dQ
-        const int tok = w.tok0 + tok_in;
-        if (tok_in >= A.tpt || tok >= (A.s1_pad ? A.s1_pad : w.u.seq.qlen)) return -1;
-        return ((int64_t)(w.u.seq.q0 + tok) * A.n1 + w.u.head * G + head_in) * D;
+        const int tok = w.first + tok_in;
+        if (tok_in >= A.tpt || tok >= (A.s1_pad ? A.s1_pad : w.seq.qlen)) return -1;
+        return ((int64_t)(w.seq.q0 + tok) * A.n1 + w.head * G + head_in) * D;
     };
     auto out = [&](int k) { return place(k / G, k % G); };
     const int my_tok = r / G, my_head = r % G;
@@ -394,28 +407,27 @@ __global__ void __launch_bounds__(kXThreads, 1)
         bool ok = true;
         int g = 0, nonempty = 0;
         // the next unit's statistics are on their way while this one is stored
-        int unit = units.read(0, abort_flag, lane);
         float st_nl = 0.f, st_nd = 0.f;
         uint2 norms{};
-        auto begin = [&]() {
-            w = decode(unit);
-            st_nl = A.stats[w.u.tile_id * 256 + r];
-            st_nd = A.stats[w.u.tile_id * 256 + 128 + r];
-            if constexpr (kFp16) norms = ds_norms(A, w.u);
+        auto begin = [&](int k) {
+            ok = units.read(k, abort_flag, lane, &w);
+            if (!ok || w.n < 0) return;
+            st_nl = A.stats[(int64_t)w.stat * 256 + r];
+            st_nd = A.stats[(int64_t)w.stat * 256 + 128 + r];
+            if constexpr (kFp16) norms = ds_norms(A, w.b, w.head);
         };
-        ok = unit >= 0;
-        if (ok && unit < A.units) begin();
-        for (int k = 0; ok && unit < A.units; ++k) {
+        begin(0);
+        for (int k = 0; ok && w.n >= 0; ++k) {
             const int n = w.n;
             if constexpr (kFp16) up = ds_exponent(norms);
             const float nl = st_nl + up, nd = st_nd;
             if (n > 0) {
                 // ---------------------------------------------- softmax
                 const float c = A.scale_log2;
-                const int partial = A.mask ? 0 : w.u.seq.klen / kXRows - w.t0;
+                const int partial = A.mask ? 0 : w.seq.klen / kXRows - w.t0;
                 KeyLoad<4> keys{};                       // of the next tile that may lack keys
                 if (partial < n)
-                    keys.start(A.mask, w.u.seq, (w.t0 + (partial > 0 ? partial : 0)) * kXRows, lane);
+                    keys.start(A.mask, w.seq, (w.t0 + (partial > 0 ? partial : 0)) * kXRows, lane);
                 // dS over the scores; a copy of its own for tiles with absent keys
                 auto tile = [&](auto masked, int i) -> bool {
                     const uint32_t ts = trow + (g & 1) * 128 + h * 64;
@@ -430,7 +442,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
                     if constexpr (decltype(masked)::value) {
                         const KeyBits<4> kb = keys.finish();
-                        if (i + 1 < n) keys.start(A.mask, w.u.seq, (w.t0 + i + 1) * kXRows, lane);
+                        if (i + 1 < n) keys.start(A.mask, w.seq, (w.t0 + i + 1) * kXRows, lane);
                         // the scores have read this tile's keys, so its dead rows may go before dS K
                         if (!kb.all()) zero_rows<L::KC, 4, 256>(smem + L::OFF_A + g % L::RA * L::TILE, kb, threadIdx.x);
                         bits[0] = h ? kb.w[2] : kb.w[0];
@@ -475,12 +487,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
             if (ns > 1 || !ok) break;                    // stored below
             // -------------------------------------------------- epilogue
             const float f = A.scale * (kFp16 ? exp2f(-up) : 1.f);
-            const bool pad = n == 0 || w.tok0 + my_tok >= w.u.seq.qlen;
+            const bool pad = n == 0 || w.first + my_tok >= w.seq.qlen;
             RowStore<kFp16> rows;
             rows.rows(place(my_tok, my_head), lane);
-            unit = units.read(k + 1, abort_flag, lane);
-            ok = unit >= 0;
-            if (ok && unit < A.units) begin();
+            begin(k + 1);
 #pragma unroll
             for (int j = 0; j < D / 2; j += 32) {
                 float y[32];
@@ -501,7 +511,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         float *xo = reinterpret_cast<float *>(smem);
         __syncthreads();                                 // loads and products on this memory are complete
         if (warp < 8) {
-            const bool pad = w.n == 0 || w.tok0 + my_tok >= w.u.seq.qlen;
+            const bool pad = w.n == 0 || w.first + my_tok >= w.seq.qlen;
 #pragma unroll
             for (int j = 0; j < D / 2; j += 32) {
                 float y[32];
@@ -547,7 +557,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const Ring rs = {bars + XB_STF, bars + XB_STE, 2};
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rb.empty + L::RB);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const Units units = {abort_flag + 1, bars + XB_UF, bars + XB_UE};
+    const Units units = {reinterpret_cast<Work *>(smem + L::OFF_BAR + 320), bars + XB_UF, bars + XB_UE};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         *abort_flag = 0;
@@ -579,16 +589,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const int ns = A.nsplit, rank = blockIdx.x & (ns - 1);
     const int G = A.group;
     auto fail = [&]() { *abort_flag = 1; };
-    struct Work {
-        XUnit u;
-        int key0, t0, n;                                 // first key; this rank's first query tile and their number
-    };
     auto decode = [&](int unit) {
-        Work w;
-        w.u = x_decode<&SeqRow::ktile0>(A, unit);
-        w.key0 = w.u.tile * kXRows;
-        const int nqt = w.key0 < w.u.seq.klen ? (w.u.seq.qlen + A.tpt - 1) / A.tpt : 0;
-        x_share(A, nqt, rank, &w.t0, &w.n);
+        const XUnit u = x_decode<&SeqRow::ktile0>(A, unit);
+        Work w{};
+        w.seq = u.seq;
+        w.b = u.b;
+        w.head = u.head;
+        w.first = u.tile * kXRows;
+        x_share(A, w.first < u.seq.klen ? (u.seq.qlen + A.tpt - 1) / A.tpt : 0, rank, &w.t0, &w.n);
         return w;
     };
 
@@ -599,18 +607,17 @@ __global__ void __launch_bounds__(kXThreads, 1)
             int la = 0, lb = 0, ls = 0, lx = 0;          // loads so far
             bool ok = true;
             for (int k = 0; ok; ++k) {
-                const int unit = units.take(A, k, abort_flag);
-                ok = unit >= 0;
-                if (!ok || unit >= A.units) break;
-                const Work w = decode(unit);
+                Work w{};
+                ok = units.take(A, k, abort_flag, &w, decode);
+                if (!ok || w.n < 0) break;
                 if (w.n == 0) continue;
                 auto load = [&](const Ring &r, int off, const CUtensorMap *map, int &i, int tile) {
                     if (!ring_wait_free(r, i, abort_flag)) return false;
                     const int s = i % r.n;
                     tc::mbar_arrive_expect_tx(&r.full[s], qbytes);
                     for (int c = 0; c < L::KC; ++c)
-                        tc::tma_load_3d(smem + off + s * L::TILE + c * 16384, map, c * 64, w.u.head * G,
-                                        w.u.seq.q0 + tile * A.tpt, &r.full[s]);
+                        tc::tma_load_3d(smem + off + s * L::TILE + c * 16384, map, c * 64, w.head * G,
+                                        w.seq.q0 + tile * A.tpt, &r.full[s]);
                     ++i;
                     return true;
                 };
@@ -618,9 +625,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 if (!ok) break;
                 tc::mbar_arrive_expect_tx(&bars[XB_XY], 2 * L::TILE);
                 for (int c = 0; c < L::KC; ++c) {
-                    const int row = w.u.seq.k0 + w.key0;
-                    tc::tma_load_3d(smem + L::OFF_X + c * 16384, &map_k, c * 64, w.u.head, row, &bars[XB_XY]);
-                    tc::tma_load_3d(smem + L::OFF_Y + c * 16384, &map_v, c * 64, w.u.head, row, &bars[XB_XY]);
+                    const int row = w.seq.k0 + w.first;
+                    tc::tma_load_3d(smem + L::OFF_X + c * 16384, &map_k, c * 64, w.head, row, &bars[XB_XY]);
+                    tc::tma_load_3d(smem + L::OFF_Y + c * 16384, &map_v, c * 64, w.head, row, &bars[XB_XY]);
                 }
                 ++lx;
                 for (int i = 0; i < w.n && ok; ++i) {
@@ -629,7 +636,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     if (!ok) break;
                     tc::mbar_arrive_expect_tx(&rs.full[ls & 1], 1024);
                     bulk_load(smem + L::OFF_STAT + (ls & 1) * 1024,
-                              A.stats + ((int64_t)(w.u.seq.qtile0 + w.t0 + i) * A.n2 + w.u.head) * 256, 1024,
+                              A.stats + ((int64_t)(w.seq.qtile0 + w.t0 + i) * A.n2 + w.head) * 256, 1024,
                               &rs.full[ls & 1]);
                     ++ls;
                     ok = load(rb, L::OFF_B, &map_dy, lb, w.t0 + i);
@@ -649,15 +656,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
         bool ok = true;
         int g = 0, nonempty = 0;
         for (int k = 0; ok; ++k) {
-            const int unit = units.read(k, abort_flag, lane);
-            ok = unit >= 0;
-            if (!ok || unit >= A.units) break;
-            const Work w = decode(unit);
+            Work w;
+            ok = units.read(k, abort_flag, lane, &w);
+            if (!ok || w.n < 0) break;
             const int n = w.n;
             if (n == 0) continue;
             // rows behind the sequence's last one are zeroed in a tile that has landed
             auto clear = [&](int off, int s, int i) {
-                const int left = w.u.seq.qlen - (w.t0 + i) * A.tpt;
+                const int left = w.seq.qlen - (w.t0 + i) * A.tpt;
                 if (left < A.tpt) {
                     KeyBits<4> kb;
                     kb.set_first(left * G);
@@ -717,25 +723,24 @@ __global__ void __launch_bounds__(kXThreads, 1)
     Work w{};
     float up = 0.f;                                      // exponent that dS is scaled by
     auto out = [&](int k) -> int64_t {                   // place of key row k in dK and dV; negative: none
-        const int key = w.key0 + k;
-        if (key >= (A.s2_pad ? A.s2_pad : w.u.seq.klen)) return -1;
-        return (((int64_t)w.u.seq.k0 + key) * A.n2 + w.u.head) * D;
+        const int key = w.first + k;
+        if (key >= (A.s2_pad ? A.s2_pad : w.seq.klen)) return -1;
+        return (((int64_t)w.seq.k0 + key) * A.n2 + w.head) * D;
     };
     if (warp < 8) {
         bool ok = true;
         int g = 0, nonempty = 0;
         // what the next unit needs from memory is on its way while this one is stored
-        int unit = units.read(0, abort_flag, lane);
         bool st_live = false;
         uint2 norms{};
-        auto begin = [&]() {
-            w = decode(unit);
-            st_live = w.key0 + r < w.u.seq.klen && (!A.mask || A.mask[(int64_t)w.u.seq.k0 + w.key0 + r] != 0);
-            if constexpr (kFp16) norms = ds_norms(A, w.u);
+        auto begin = [&](int k) {
+            ok = units.read(k, abort_flag, lane, &w);
+            if (!ok || w.n < 0) return;
+            st_live = w.first + r < w.seq.klen && (!A.mask || A.mask[(int64_t)w.seq.k0 + w.first + r] != 0);
+            if constexpr (kFp16) norms = ds_norms(A, w.b, w.head);
         };
-        ok = unit >= 0;
-        if (ok && unit < A.units) begin();
-        for (int turn = 0; ok && unit < A.units; ++turn) {
+        begin(0);
+        for (int turn = 0; ok && w.n >= 0; ++turn) {
             const int n = w.n;
             if constexpr (kFp16) up = ds_exponent(norms);
             const bool live = st_live;
@@ -816,9 +821,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             const float f = h ? A.scale * (kFp16 ? exp2f(-up) : 1.f) : fv;
             RowStore<kFp16> rows;
             rows.rows(out(r), lane);
-            unit = units.read(turn + 1, abort_flag, lane);
-            ok = unit >= 0;
-            if (ok && unit < A.units) begin();
+            begin(turn + 1);
 #pragma unroll
             for (int j = 0; j < D; j += 32) {
                 float y[32];
