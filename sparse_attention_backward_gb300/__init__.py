@@ -558,12 +558,18 @@ def _dense(name, t, like, shape, dtype):
     return t.data_ptr()
 
 
+def _new(like):
+    """A dense tensor of the same shape, type and device."""
+    import torch
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
+
+
 def _with(desc, **fields):
     """The descriptor, or a copy where a field differs (a kept one is never changed)."""
     if all(getattr(desc, k) == v for k, v in fields.items()):
         return desc
     new = type(desc).from_buffer_copy(desc)
-    new.__dict__.update(desc.__dict__)
+    new.__dict__.update(desc.__dict__, _dense=False)
     for k, v in fields.items():
         setattr(new, k, v)
     return new
@@ -576,7 +582,7 @@ def _launch(device, stream, call):
     if stream is not None:
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
-    if torch.cuda.current_device() != device:
+    if torch._C._cuda_getDevice() != device:
         with torch.cuda.device(device):
             return call(torch.cuda.current_stream().cuda_stream)
     return call(torch._C._cuda_getCurrentRawStream(device))   # a stream object costs several microseconds
@@ -630,6 +636,7 @@ def make_rotary_desc(rotary: Rotary, cu_seqlens, n1, n2, d, dtype=SAG_BF16, layo
     lead = (desc.batch, int(s_max)) if layout == SAG_LAYOUT_BSND else (cu[len(cu) - 1],)
     desc._shapes = (lead + (n1, d), lead + (n2, d))
     desc._dtype = _torch_dtype(desc)
+    desc._dense = True      # strides as made, 0
     return desc
 
 
@@ -660,16 +667,18 @@ def _rotary(entry, q, k, rotary, cu_seqlens, positions, out, workspace, stream, 
 
     def call(handle):
         if out is None:
-            qo = torch.empty(q.shape, dtype=dtype, device=q.device)
-            ko = torch.empty(k.shape, dtype=dtype, device=q.device) if k is not None else None
+            qo = _new(q)
+            ko = _new(k) if k is not None else None
         else:
             qo, ko = (out, None) if k is None and not isinstance(out, (tuple, list)) else out
             _check("out", qo, q, q.shape, dtype)
             if k is not None:
                 _check("out", ko, q, k.shape, dtype)
-        use = _with(desc, q_stride=_row_stride("q", q, n1, d), q_out_stride=_row_stride("out", qo, n1, d),
-                    k_stride=_row_stride("k", k, n2, d) if n2 else 0,
-                    k_out_stride=_row_stride("out", ko, n2, d) if n2 else 0)
+        use = desc
+        if not (out is None and q.is_contiguous() and (k is None or k.is_contiguous()) and desc._dense):
+            use = _with(desc, q_stride=_row_stride("q", q, n1, d), q_out_stride=_row_stride("out", qo, n1, d),
+                        k_stride=_row_stride("k", k, n2, d) if n2 else 0,
+                        k_out_stride=_row_stride("out", ko, n2, d) if n2 else 0)
         io = SrtIo(q.data_ptr(), k.data_ptr() if n2 else None, pos, qo.data_ptr(), ko.data_ptr() if n2 else None)
         ws, need = workspace, 0
         if use.batch > 64:          # smaller tables travel with the launch
@@ -717,6 +726,7 @@ def make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, dtype=SAG_BF1
     desc._shapes = (((desc.batch, int(s1_max)) if bsnd else (cq[len(cq) - 1],)) + (n1, d),
                     ((desc.batch, int(s2_max)) if bsnd else (ck[len(ck) - 1],)) + (n2, d))
     desc._dtype = _torch_dtype(desc)
+    desc._dense = True      # strides as made, 0
     return desc
 
 
@@ -756,8 +766,10 @@ def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, w
     _check("q", q, q, q.shape, dtype)
     _check("k", k, q, k.shape, dtype)
     _check("v", v, q, k.shape, dtype)
-    use = _with(desc, q_stride=_row_stride("q", q, n1, d), k_stride=_row_stride("k", k, n2, d),
-                v_stride=_row_stride("v", v, n2, d))
+    use = desc
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and desc._dense):
+        use = _with(desc, q_stride=_row_stride("q", q, n1, d), k_stride=_row_stride("k", k, n2, d),
+                    v_stride=_row_stride("v", v, n2, d))
     io = ScaIo(q.data_ptr(), k.data_ptr(), v.data_ptr())
     if key_mask is not None:
         if key_mask.dtype not in (torch.bool, torch.uint8):
@@ -795,8 +807,7 @@ def cross_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, ke
     """
     def tensors(io, dtype):
         import torch
-        o, lse = out if out is not None else (torch.empty(q.shape, dtype=dtype, device=q.device),
-                                              torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device))
+        o, lse = out if out is not None else (_new(q), q.new_empty(q.shape[:-1], dtype=torch.float32))
         io.attention_out = _dense("attention_out", o, q, q.shape, dtype)
         io.softmax_lse = _dense("softmax_lse", lse, q, q.shape[:-1], torch.float32)
         return o, lse
@@ -814,9 +825,10 @@ def cross_backward(q, k, v, o, dy, lse, cu_seqlens_q=None, cu_seqlens_kv=None, s
         io.attention_out = _dense("o", o, q, q.shape, dtype)
         io.attention_out_grad = _dense("dy", dy, q, q.shape, dtype)
         io.softmax_lse = _dense("lse", lse, q, q.shape[:-1], torch.float32)
-        shapes = (q.shape, k.shape, k.shape)
-        outs = out if out is not None else tuple(torch.empty(s, dtype=dtype, device=q.device) for s in shapes)
-        io.dq, io.dk, io.dv = (_dense(n, t, q, s, dtype) for n, t, s in zip(("dq", "dk", "dv"), outs, shapes))
+        outs = dq, dk, dv = out if out is not None else (_new(q), _new(k), _new(v))
+        io.dq = _dense("dq", dq, q, q.shape, dtype)
+        io.dk = _dense("dk", dk, q, k.shape, dtype)
+        io.dv = _dense("dv", dv, q, k.shape, dtype)
         return outs
 
     return _cross("cross_attn_grad", cross_grad_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,

@@ -27,7 +27,7 @@ struct XArgs {
     int32_t tpt;                        // tokens per query tile
     int32_t s1_pad, s2_pad;             // BSND: padded lengths, else 0
     int32_t units;                      // query (k_xdkv: key) tiles times key/value heads
-    int32_t nsplit, split_log2;         // CTAs (one cluster, a power of two) that share a unit
+    int32_t nsplit;                     // CTAs (one cluster) that share a unit
     int32_t ctas;                       // of the launch: units * nsplit, or fewer that take unit after unit
     unsigned *ticket;                   // next units of the two gradient kernels, zeroed by k_xpre
     float scale, scale_log2;
@@ -239,8 +239,12 @@ __device__ __forceinline__ XUnit x_decode(const XArgs &A, int unit) {
 
 // A rank's share of `tiles`: first tile and number.
 __device__ __forceinline__ void x_share(const XArgs &A, int tiles, int rank, int *first, int *n) {
-    *first = (tiles * rank) >> A.split_log2;
-    *n = ((tiles * (rank + 1)) >> A.split_log2) - *first;
+    *first = 0;
+    *n = tiles;
+    if (A.nsplit > 1) {
+        *first = tiles * rank / A.nsplit;
+        *n = tiles * (rank + 1) / A.nsplit - *first;
+    }
 }
 
 // Which of the kWords * 32 keys from key `first` of a sequence are there.

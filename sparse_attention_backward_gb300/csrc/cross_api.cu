@@ -67,18 +67,15 @@ sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {
     return SAG_OK;
 }
 
-// CTAs that share a unit: while SMs are idle, as long as each has a tile of the loop
+// CTAs that share a unit: as many as run at once, up to a cluster's 8, as long as each has a tile of the loop.  A cluster
+// lies within one of the GPU's parts (GPCs), so not every size fills all SMs: the shares, in thousandths, are what
+// cudaOccupancyMaxActiveClusters gives on GB300 (304, 304, 291, 296, 290, 276, 266, 288 of 304 CTAs at two an SM).
 int split_of(int64_t units, int tiles, int room) {
+    static const int share[kMaxSplit + 1] = {0, 1000, 1000, 957, 974, 954, 908, 875, 948};
     if (room > kSplitCtas) room = kSplitCtas;
-    int ns = 1;
-    while (ns < kMaxSplit && units * ns * 2 <= room && tiles >= 2 * ns) ns *= 2;
-    return ns;
-}
-
-void set_split(XArgs *a, int ns) {
-    a->nsplit = ns;
-    a->split_log2 = 0;
-    while (1 << a->split_log2 < ns) ++a->split_log2;
+    for (int ns = kMaxSplit; ns > 1; --ns)
+        if (ns <= tiles && units * ns * 1000 <= (int64_t)room * share[ns]) return ns;
+    return 1;
 }
 
 XArgs x_args(const sca_desc *d, const sca_io *io, const XPlan &p, char *ws) {
@@ -188,7 +185,7 @@ extern "C" sag_status cross_attn_fwd(const sca_desc *desc, const sca_io *io, voi
     XArgs a = x_args(desc, io, p, ws);
     if (x_table(&a, desc, p, ws, s) != cudaSuccess) return SAG_ERR_CUDA;
     a.units = (int)(p.q_tiles * desc->n2);
-    set_split(&a, split_of(a.units, 2 * p.max_k, 2 * current_device_sms()));   // two CTAs an SM, tiles of 64 keys
+    a.nsplit = split_of(a.units, 2 * p.max_k, 2 * current_device_sms());   // two CTAs an SM, tiles of 64 keys
     a.n_status = a.ctas = a.units * a.nsplit;
     // full query tiles, and at least 2048 keys a CTA
     const bool long_loops = p.max_q > 1 && p.max_k >= 16 * a.nsplit;
@@ -217,7 +214,7 @@ extern "C" sag_status cross_attn_grad(const sca_desc *desc, const sca_io *io, vo
     // one CTA an SM: a cluster for each unit, or CTAs that take unit after unit
     auto share = [&](int units, int tiles) {
         a.units = units;
-        set_split(&a, split_of(units, tiles, sms));
+        a.nsplit = split_of(units, tiles, sms);
         a.ctas = a.nsplit > 1 || units < sms ? units * a.nsplit : sms;
     };
     int before = 0;

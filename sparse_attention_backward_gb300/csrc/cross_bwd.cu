@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
         const XUnit u = x_decode<&SeqRow::qtile0>(A, blockIdx.x);
         slot = ((int64_t)u.b * A.n2 + u.head) * 2;
         float *st = A.stats + u.tile_id * 256;
+#pragma unroll 4
         for (int r = warp * RPW + lane / LPR; r < kXRows; r += 8 * RPW) {
             const int tok = u.tile * A.tpt + r / A.group;
             const bool live = r < A.tpt * A.group && tok < u.seq.qlen;
@@ -85,6 +86,7 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
         // fp16 only: row norms of V
         const XUnit u = x_decode<&SeqRow::ktile0>(A, blockIdx.x - q_units);
         slot = ((int64_t)u.b * A.n2 + u.head) * 2 + 1;
+#pragma unroll 4
         for (int r = warp * RPW + lane / LPR; r < kXRows; r += 8 * RPW) {
             const int key = u.tile * kXRows + r;
             const int64_t row = (int64_t)u.seq.k0 + key;
@@ -174,7 +176,7 @@ struct Units {
     __device__ __forceinline__ bool take(const XArgs &A, int k, volatile int *abort, Work *w, Decode &&decode) const {
         if (k >= 2 && !tc::mbar_wait(&empty[k & 1], (k / 2 - 1) & 1, abort, kXWaitNs)) return false;
         int unit = A.units;
-        if (k == 0) unit = blockIdx.x >> A.split_log2;
+        if (k == 0) unit = blockIdx.x / A.nsplit;
         else if (A.ctas < A.units) unit = (int)(gridDim.x + atomicAdd(A.ticket, 1u));
         if (unit < A.units) *w = decode(unit);
         else w->n = -1;
@@ -210,26 +212,36 @@ __device__ __forceinline__ bool ring_drain(const Ring &r, int loads) {
 // rank's share goes to dst + out(k) (negative: not stored), scaled by f.
 template <bool kFp16, int D, class Out>
 __device__ __forceinline__ void join_rows(float *xo, uint16_t *dst, int ns, int rank, int warp, int lane, Out &&out, float f) {
-    constexpr int E = D / 64;
-    for (int k = rank + ns * warp; k < kXRows; k += ns * 8) {
-        const int64_t at = out(k);
-        if (at < 0) continue;
-        float2 y[kMaxSplit][E], acc[E] = {};
+    constexpr int E = D / 64, R = 2;                     // float2 a lane and row; rows at a time, for the remote reads' latency
+    for (int k0 = rank + ns * warp; k0 < kXRows; k0 += ns * 8 * R) {
+        float2 y[R][kMaxSplit][E];
+        int64_t at[R];
 #pragma unroll
-        for (int p = 0; p < kMaxSplit; ++p)
-            if (p < ns) {
-                const uint32_t a = peer_addr(tc::smem_u32(xo + k * (D + 4) + lane * 2), p);
+        for (int i = 0; i < R; ++i) {
+            const int k = k0 + i * ns * 8;
+            at[i] = k < kXRows ? out(k) : -1;
+            if (at[i] < 0) continue;
 #pragma unroll
-                for (int e = 0; e < E; ++e) y[p][e] = peer_ld2(a + e * 256);
-            }
+            for (int p = 0; p < kMaxSplit; ++p)
+                if (p < ns) {
+                    const uint32_t a = peer_addr(tc::smem_u32(xo + k * (D + 4) + lane * 2), p);
 #pragma unroll
-        for (int p = 0; p < kMaxSplit; ++p)
-            if (p < ns)
+                    for (int e = 0; e < E; ++e) y[i][p][e] = peer_ld2(a + e * 256);
+                }
+        }
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = add2(acc[e], y[p][e]);
+        for (int i = 0; i < R; ++i) {
+            if (at[i] < 0) continue;
+            float2 acc[E] = {};
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            *reinterpret_cast<uint32_t *>(dst + at + e * 64 + lane * 2) = xpack<kFp16>(acc[e].x * f, acc[e].y * f);
+            for (int p = 0; p < kMaxSplit; ++p)
+                if (p < ns)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = add2(acc[e], y[i][p][e]);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                *reinterpret_cast<uint32_t *>(dst + at[i] + e * 64 + lane * 2) = xpack<kFp16>(acc[e].x * f, acc[e].y * f);
+        }
     }
 }
 
@@ -269,7 +281,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot, sbase = tc::smem_u32(smem);
-    const int ns = A.nsplit, rank = blockIdx.x & (ns - 1);
+    const int ns = A.nsplit, rank = blockIdx.x % ns;
     const int G = A.group;
     auto fail = [&]() { *abort_flag = 1; };
     auto decode = [&](int unit) {
@@ -586,7 +598,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot, sbase = tc::smem_u32(smem);
-    const int ns = A.nsplit, rank = blockIdx.x & (ns - 1);
+    const int ns = A.nsplit, rank = blockIdx.x % ns;
     const int G = A.group;
     auto fail = [&]() { *abort_flag = 1; };
     auto decode = [&](int unit) {

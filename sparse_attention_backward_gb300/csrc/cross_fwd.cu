@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         tc::prefetch_tmap(&map_k);
         tc::prefetch_tmap(&map_v);
     }
-    const int ns = A.nsplit, rank = blockIdx.x & (ns - 1);
-    const XUnit u = x_decode<&SeqRow::qtile0>(A, blockIdx.x >> A.split_log2);
+    const int ns = A.nsplit, rank = blockIdx.x % ns;
+    const XUnit u = x_decode<&SeqRow::qtile0>(A, blockIdx.x / A.nsplit);
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
