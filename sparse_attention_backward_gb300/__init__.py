@@ -14,6 +14,11 @@ Tensors are TND ([T, N, D]) or, given as 4-D tensors, BSND ([B, S, N, D] with
 every batch padded to S rows; cu_seqlens then give the valid lengths).  With
 ``q_rope`` / ``k_rope`` the head dim is split (Q = [q, q_rope] along D) and
 the gradients come back as (dq, dk, dv, dq_rope, dk_rope).
+
+Next to it, in the same layouts: ``forward`` and ``indexer_backward``; rotary
+positions (``Rotary``, ``rotary_forward`` / ``rotary_backward``, or ``rotary=``
+of forward and backward); cross attention to an encoder's states
+(``cross_forward`` / ``cross_backward``).
 """
 from __future__ import annotations
 
@@ -229,17 +234,21 @@ def query_error(workspace, stream) -> int:
 
 def backward(q, k, v, o, dy, softmax_max, softmax_sum, topk, cu_seqlens_q, cu_seqlens_kv, scale,
              block_size, block_count, deterministic=False, out=None, workspace=None, stream=None,
-             check=False, q_rope=None, k_rope=None):
+             check=False, q_rope=None, k_rope=None, rotary=None, q_positions=None, k_positions=None):
     """torch-tensor convenience over the C ABI (allocation and marshalling only).
 
     All tensors must be contiguous CUDA tensors, TND ([T, N, D]) or BSND
     ([B, S, N, D], 4-D); returns (dq, dk, dv), or (dq, dk, dv, dq_rope,
     dk_rope) with the rope split.  With ``check`` the device status is read
-    back (this synchronizes the stream).
+    back (this synchronizes the stream).  With ``rotary`` (see ``forward``) q
+    and k, and their gradients, are those before the rotation.
     """
     import torch
     if not q.is_cuda:
         raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
+    if rotary is not None:
+        q, k, q_rope, k_rope = _rotated(q, k, q_rope, k_rope, rotary, cu_seqlens_q, cu_seqlens_kv, q_positions,
+                                        k_positions, stream)
     dtype = SAG_FP16 if q.dtype == torch.float16 else SAG_BF16
     layout, s1_max, s2_max, n1, d_qk, n2, d_rope = _layout_of(q, k, q_rope)
     d_v = v.shape[-1]
@@ -263,11 +272,24 @@ def backward(q, k, v, o, dy, softmax_max, softmax_sum, topk, cu_seqlens_q, cu_se
             raise ValueError("all tensors must be contiguous")
     io = make_io(**{k_: t.data_ptr() for k_, t in named.items()})
     sel_attn_grad_ex(desc, io, workspace.data_ptr(), need, stream.cuda_stream)
+    if rotary is not None:      # the gradients of the tensors that were rotated, in place
+        dq, dk = (out[3], out[4]) if d_rope else (out[0], out[1])
+        rotary_backward(dq, None, rotary, cu_seqlens_q, q_positions, out=dq, stream=stream)
+        rotary_backward(dk, None, rotary, cu_seqlens_kv, k_positions, out=dk, stream=stream)
     if check:
         st = query_error(workspace.data_ptr(), stream.cuda_stream)
         if st != SAG_OK:
             raise SagError(st, "device")
     return out
+
+
+def _rotated(q, k, q_rope, k_rope, rotary, cu_seqlens_q, cu_seqlens_kv, q_positions, k_positions, stream):
+    """(q, k, q_rope, k_rope) with the rotation applied to the rope tensors, or
+    to q and k where there are none."""
+    turn = lambda x, cu, pos: rotary_forward(x, None, rotary, cu, pos, stream=stream)  # noqa: E731
+    if q_rope is not None:
+        return q, k, turn(q_rope, cu_seqlens_q, q_positions), turn(k_rope, cu_seqlens_kv, k_positions)
+    return turn(q, cu_seqlens_q, q_positions), turn(k, cu_seqlens_kv, k_positions), None, None
 
 
 def fwd_workspace_size(desc: SagDesc) -> int:
@@ -296,13 +318,21 @@ def sel_attn_fwd(desc: SagDesc, query, key, value, topk_indices, attention_out, 
 
 
 def forward(q, k, v, topk, cu_seqlens_q, cu_seqlens_kv, scale, block_size, block_count,
-            out=None, workspace=None, stream=None, check=False, q_rope=None, k_rope=None):
+            out=None, workspace=None, stream=None, check=False, q_rope=None, k_rope=None, rotary=None,
+            q_positions=None, k_positions=None):
     """torch-tensor convenience over the forward's C ABI: returns
     (attention_out [.., n1, d_v], softmax_max [.., n1, 8], softmax_sum [.., n1, 8])
-    in the layout of q (TND or 4-D BSND)."""
+    in the layout of q (TND or 4-D BSND).
+
+    ``rotary`` (a ``Rotary``) rotates q_rope and k_rope, or q and k where there
+    is no rope split, before the attention; ``q_positions`` / ``k_positions``
+    as in ``rotary_forward``."""
     import torch
     if not q.is_cuda:
         raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
+    if rotary is not None:
+        q, k, q_rope, k_rope = _rotated(q, k, q_rope, k_rope, rotary, cu_seqlens_q, cu_seqlens_kv, q_positions,
+                                        k_positions, stream)
     dtype = SAG_FP16 if q.dtype == torch.float16 else SAG_BF16
     layout, s1_max, s2_max, n1, d_qk, n2, d_rope = _layout_of(q, k, q_rope)
     d_v = v.shape[-1]
@@ -468,23 +498,28 @@ class ScaIo(ctypes.Structure):
         "query", "key", "value", "attention_out", "attention_out_grad", "softmax_lse", "key_mask", "dq", "dk", "dv")]
 
 
+_neighbours = None
+
+
 def _lib_neighbours():
+    global _neighbours
+    if _neighbours is not None:
+        return _neighbours
     lib = load()
-    if not getattr(lib, "_neighbours_ready", False):
-        vp, sz = ctypes.c_void_p, ctypes.c_size_t
-        dbl, psz = ctypes.c_double, ctypes.POINTER(ctypes.c_size_t)
-        lib.rotary_frequencies.argtypes = [ctypes.c_int32, dbl, ctypes.c_int32] + [dbl] * 6 + [ctypes.POINTER(dbl)] * 2
-        lib.cross_attn_query_error.argtypes = [vp, vp]
-        for prefix, desc, io, names in (("rotary", SrtDesc, SrtIo, ("fwd", "grad")),
-                                        ("cross_attn", ScaDesc, ScaIo, ("fwd", "grad"))):
-            for n in names:
-                getattr(lib, f"{prefix}_{n}").argtypes = [ctypes.POINTER(desc), ctypes.POINTER(io), vp, sz, vp]
-        lib.rotary_workspace_size.argtypes = [ctypes.POINTER(SrtDesc), psz]
-        lib.cross_attn_fwd_workspace_size.argtypes = [ctypes.POINTER(ScaDesc), psz]
-        lib.cross_attn_grad_workspace_size.argtypes = [ctypes.POINTER(ScaDesc), psz]
-        for n in EXPORTED_NEIGHBOURS:
-            getattr(lib, n).restype = ctypes.c_int
-        lib._neighbours_ready = True
+    vp, sz = ctypes.c_void_p, ctypes.c_size_t
+    dbl, psz = ctypes.c_double, ctypes.POINTER(ctypes.c_size_t)
+    lib.rotary_frequencies.argtypes = [ctypes.c_int32, dbl, ctypes.c_int32] + [dbl] * 6 + [ctypes.POINTER(dbl)] * 2
+    lib.cross_attn_query_error.argtypes = [vp, vp]
+    for prefix, desc, io, names in (("rotary", SrtDesc, SrtIo, ("fwd", "grad")),
+                                    ("cross_attn", ScaDesc, ScaIo, ("fwd", "grad"))):
+        for n in names:
+            getattr(lib, f"{prefix}_{n}").argtypes = [ctypes.POINTER(desc), ctypes.POINTER(io), vp, sz, vp]
+    lib.rotary_workspace_size.argtypes = [ctypes.POINTER(SrtDesc), psz]
+    lib.cross_attn_fwd_workspace_size.argtypes = [ctypes.POINTER(ScaDesc), psz]
+    lib.cross_attn_grad_workspace_size.argtypes = [ctypes.POINTER(ScaDesc), psz]
+    for n in EXPORTED_NEIGHBOURS:
+        getattr(lib, n).restype = ctypes.c_int
+    _neighbours = lib
     return lib
 
 
@@ -533,26 +568,28 @@ def _row_stride(name, t, heads, d):
     return step
 
 
-def _check_rows(name, t, shape):
-    """A tensor of the descriptor's rows: a padded batch of just its shape, or
-    packed rows, possibly with more behind them."""
-    if tuple(t.shape) == shape:
+def _check_rows(name, t, shape, dtype):
+    """A tensor of the descriptor's rows and type: a padded batch of just its
+    shape, or packed rows, possibly with more behind them."""
+    if t.dtype is not dtype:
+        raise SagError(SAG_ERR_DTYPE, f"{name}: tensor of {t.dtype}, expected {dtype}")
+    if t.shape == shape:
         return
     if len(shape) == 4 or t.dim() != 3 or tuple(t.shape[1:]) != shape[1:] or t.shape[0] < shape[0]:
         raise ValueError(f"{name}: shape {tuple(t.shape)} does not hold the descriptor's {shape}")
 
 
-def _check(name, t, like, shape, dtype):
-    if t.dtype != dtype:
+def _check(name, t, device, shape, dtype):
+    if t.dtype is not dtype:
         raise SagError(SAG_ERR_DTYPE, f"{name}: tensor of {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.get_device() != like.get_device():
-        raise ValueError(f"{name}: on {t.device}, not on {like.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, not on device {device}")
 
 
-def _dense(name, t, like, shape, dtype):
-    _check(name, t, like, shape, dtype)
+def _dense(name, t, device, shape, dtype):
+    _check(name, t, device, shape, dtype)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -656,26 +693,28 @@ def _rotary(entry, q, k, rotary, cu_seqlens, positions, out, workspace, stream, 
         desc = make_rotary_desc(rotary, cu_seqlens, n1, n2, d, _sag_dtype(q), SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND,
                                 q.shape[1] if bsnd else 0)
     qs, ks = desc._shapes
-    dtype = desc._dtype
-    _check_rows("q", q, qs)
-    _check("q", q, q, q.shape, dtype)
+    dtype, device = desc._dtype, q.get_device()
+    _check_rows("q", q, qs, dtype)
+    lead = q.shape[:-2]
     if k is not None:
-        _check("k", k, q, q.shape[:-2] + ks[-2:], dtype)
+        _check("k", k, device, lead + ks[-2:], dtype)
     elif ks[-2]:
         raise ValueError("the descriptor has a key")
-    pos = _dense("positions", positions, q, q.shape[:-2], torch.int32) if positions is not None else None
+    pos = _dense("positions", positions, device, lead, torch.int32) if positions is not None else None
 
     def call(handle):
+        use = desc
         if out is None:
             qo = _new(q)
             ko = _new(k) if k is not None else None
+            plain = desc._dense and q.is_contiguous() and (k is None or k.is_contiguous())
         else:
             qo, ko = (out, None) if k is None and not isinstance(out, (tuple, list)) else out
-            _check("out", qo, q, q.shape, dtype)
+            _check("out", qo, device, q.shape, dtype)
             if k is not None:
-                _check("out", ko, q, k.shape, dtype)
-        use = desc
-        if not (out is None and q.is_contiguous() and (k is None or k.is_contiguous()) and desc._dense):
+                _check("out", ko, device, k.shape, dtype)
+            plain = False
+        if not plain:
             use = _with(desc, q_stride=_row_stride("q", q, n1, d), q_out_stride=_row_stride("out", qo, n1, d),
                         k_stride=_row_stride("k", k, n2, d) if n2 else 0,
                         k_out_stride=_row_stride("out", ko, n2, d) if n2 else 0)
@@ -685,12 +724,12 @@ def _rotary(entry, q, k, rotary, cu_seqlens, positions, out, workspace, stream, 
             need = rotary_workspace_size(use)
             if ws is None or ws.numel() < need:
                 ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        st = getattr(_lib_neighbours(), entry)(use, io, ws.data_ptr() if need else None, need, handle)
+        st = entry(use, io, ws.data_ptr() if need else None, need, handle)
         if st != SAG_OK:
-            raise SagError(st, entry)
+            raise SagError(st, entry.__name__)
         return (qo, ko) if k is not None else qo
 
-    return _launch(q.get_device(), stream, call)
+    return _launch(device, stream, call)
 
 
 def rotary_forward(q, k, rotary, cu_seqlens=None, positions=None, out=None, workspace=None, stream=None, desc=None):
@@ -702,13 +741,13 @@ def rotary_forward(q, k, rotary, cu_seqlens=None, positions=None, out=None, work
     ``out=(q, k)`` rotates in place; rows may be strided (slices of a fused
     projection).  ``desc`` (make_rotary_desc) replaces rotary and cu_seqlens.
     """
-    return _rotary("rotary_fwd", q, k, rotary, cu_seqlens, positions, out, workspace, stream, desc)
+    return _rotary(_lib_neighbours().rotary_fwd, q, k, rotary, cu_seqlens, positions, out, workspace, stream, desc)
 
 
 def rotary_backward(dq, dk, rotary, cu_seqlens=None, positions=None, out=None, workspace=None, stream=None, desc=None):
     """Gradient of ``rotary_forward``: the gradients of its outputs to those of
     its inputs; arguments alike."""
-    return _rotary("rotary_grad", dq, dk, rotary, cu_seqlens, positions, out, workspace, stream, desc)
+    return _rotary(_lib_neighbours().rotary_grad, dq, dk, rotary, cu_seqlens, positions, out, workspace, stream, desc)
 
 
 def make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, dtype=SAG_BF16, layout=SAG_LAYOUT_TND, s1_max=0,
@@ -746,8 +785,8 @@ def cross_query_error(workspace, stream) -> int:
 
 
 def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, workspace, stream, check, desc, tensors):
-    """Shared by the two directions: ``tensors(io, dtype)`` fills in the
-    remaining sca_io pointers and gives the outputs."""
+    """Shared by the two directions: ``tensors(io, device, dtype)`` fills in
+    the remaining sca_io pointers and gives the outputs."""
     import torch
     if not q.is_cuda:
         raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
@@ -760,38 +799,38 @@ def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, w
         desc = make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, _sag_dtype(q),
                                SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND, q.shape[1] if bsnd else 0,
                                k.shape[1] if bsnd else 0)
-    dtype = desc._dtype
-    _check_rows("q", q, desc._shapes[0])
-    _check_rows("k", k, desc._shapes[1])
-    _check("q", q, q, q.shape, dtype)
-    _check("k", k, q, k.shape, dtype)
-    _check("v", v, q, k.shape, dtype)
+    dtype, device = desc._dtype, q.get_device()
+    _check_rows("q", q, desc._shapes[0], dtype)
+    _check_rows("k", k, desc._shapes[1], dtype)
+    _check("v", v, device, k.shape, dtype)
+    if k.get_device() != device:
+        raise ValueError(f"k: on {k.device}, not on {q.device}")
     use = desc
-    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and desc._dense):
+    if not (desc._dense and q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
         use = _with(desc, q_stride=_row_stride("q", q, n1, d), k_stride=_row_stride("k", k, n2, d),
                     v_stride=_row_stride("v", v, n2, d))
     io = ScaIo(q.data_ptr(), k.data_ptr(), v.data_ptr())
     if key_mask is not None:
         if key_mask.dtype not in (torch.bool, torch.uint8):
             raise ValueError("key_mask must be a bool or uint8 tensor")
-        io.key_mask = _dense("key_mask", key_mask, q, k.shape[:-2], key_mask.dtype)
+        io.key_mask = _dense("key_mask", key_mask, device, k.shape[:-2], key_mask.dtype)
 
     def call(handle):
-        outs = tensors(io, dtype)
-        need = desc.__dict__.get(entry)
+        outs = tensors(io, device, dtype)
+        need = desc.__dict__.get(size)
         if need is None:
-            need = desc.__dict__[entry] = size(desc)
+            need = desc.__dict__[size] = size(desc)
         ws = workspace
         if ws is None or ws.numel() < need:
             ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        st = getattr(_lib_neighbours(), entry)(use, io, ws.data_ptr(), need, handle)
+        st = entry(use, io, ws.data_ptr(), need, handle)
         if st == SAG_OK and check:
             st = cross_query_error(ws.data_ptr(), handle)
         if st != SAG_OK:
-            raise SagError(st, entry)
+            raise SagError(st, entry.__name__)
         return outs
 
-    return _launch(q.get_device(), stream, call)
+    return _launch(device, stream, call)
 
 
 def cross_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, key_mask=None, out=None, workspace=None,
@@ -805,14 +844,18 @@ def cross_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, ke
     ``desc`` (make_cross_desc) replaces cu_seqlens_* and scale; ``check`` reads
     the device status back (this synchronizes the stream).
     """
-    def tensors(io, dtype):
+    def tensors(io, device, dtype):
         import torch
-        o, lse = out if out is not None else (_new(q), q.new_empty(q.shape[:-1], dtype=torch.float32))
-        io.attention_out = _dense("attention_out", o, q, q.shape, dtype)
-        io.softmax_lse = _dense("softmax_lse", lse, q, q.shape[:-1], torch.float32)
+        if out is None:
+            o, lse = _new(q), q.new_empty(q.shape[:-1], dtype=torch.float32)
+            io.attention_out, io.softmax_lse = o.data_ptr(), lse.data_ptr()
+        else:
+            o, lse = out
+            io.attention_out = _dense("attention_out", o, device, q.shape, dtype)
+            io.softmax_lse = _dense("softmax_lse", lse, device, q.shape[:-1], torch.float32)
         return o, lse
 
-    return _cross("cross_attn_fwd", cross_fwd_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,
+    return _cross(_lib_neighbours().cross_attn_fwd, cross_fwd_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,
                   workspace, stream, check, desc, tensors)
 
 
@@ -820,16 +863,20 @@ def cross_backward(q, k, v, o, dy, lse, cu_seqlens_q=None, cu_seqlens_kv=None, s
                    workspace=None, stream=None, check=False, desc=None):
     """Gradient of ``cross_forward``: returns (dq, dk, dv), from the forward's o
     and lse and the gradient dy of o; the other arguments as there."""
-    def tensors(io, dtype):
+    def tensors(io, device, dtype):
         import torch
-        io.attention_out = _dense("o", o, q, q.shape, dtype)
-        io.attention_out_grad = _dense("dy", dy, q, q.shape, dtype)
-        io.softmax_lse = _dense("lse", lse, q, q.shape[:-1], torch.float32)
-        outs = dq, dk, dv = out if out is not None else (_new(q), _new(k), _new(v))
-        io.dq = _dense("dq", dq, q, q.shape, dtype)
-        io.dk = _dense("dk", dk, q, k.shape, dtype)
-        io.dv = _dense("dv", dv, q, k.shape, dtype)
+        io.attention_out = _dense("o", o, device, q.shape, dtype)
+        io.attention_out_grad = _dense("dy", dy, device, q.shape, dtype)
+        io.softmax_lse = _dense("lse", lse, device, q.shape[:-1], torch.float32)
+        if out is None:
+            outs = dq, dk, dv = _new(q), _new(k), _new(v)
+            io.dq, io.dk, io.dv = dq.data_ptr(), dk.data_ptr(), dv.data_ptr()
+        else:
+            outs = dq, dk, dv = out
+            io.dq = _dense("dq", dq, device, q.shape, dtype)
+            io.dk = _dense("dk", dk, device, k.shape, dtype)
+            io.dv = _dense("dv", dv, device, k.shape, dtype)
         return outs
 
-    return _cross("cross_attn_grad", cross_grad_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,
+    return _cross(_lib_neighbours().cross_attn_grad, cross_grad_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,
                   workspace, stream, check, desc, tensors)
