@@ -847,7 +847,7 @@ def cross_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, ke
     def tensors(io, device, dtype):
         import torch
         if out is None:
-            o, lse = _new(q), q.new_empty(q.shape[:-1], dtype=torch.float32)
+            o, lse = _new(q), torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
             io.attention_out, io.softmax_lse = o.data_ptr(), lse.data_ptr()
         else:
             o, lse = out

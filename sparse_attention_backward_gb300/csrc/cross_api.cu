@@ -185,7 +185,7 @@ extern "C" sag_status cross_attn_fwd(const sca_desc *desc, const sca_io *io, voi
     XArgs a = x_args(desc, io, p, ws);
     if (x_table(&a, desc, p, ws, s) != cudaSuccess) return SAG_ERR_CUDA;
     a.units = (int)(p.q_tiles * desc->n2);
-    a.nsplit = split_of(a.units, 2 * p.max_k, 2 * current_device_sms());   // two CTAs an SM, tiles of 64 keys
+    a.nsplit = split_of(a.units, 2 * p.max_k, (desc->d == 64 ? 4 : 2) * current_device_sms());   // CTAs an SM; tiles of 64 keys
     a.n_status = a.ctas = a.units * a.nsplit;
     // full query tiles, and at least 2048 keys a CTA
     const bool long_loops = p.max_q > 1 && p.max_k >= 16 * a.nsplit;

@@ -7,8 +7,8 @@
 // that scores and probabilities never touch shared memory.  Two score tiles
 // of 64 keys are in flight: while the softmax (four warps, a thread a row, no shuffles)
 // works on one, the MMA warp multiplies the other's P and forms the scores
-// after it.  Two CTAs share an SM (256 TMEM columns and at most 113 KB each),
-// so one's start and end run beside the other's loop as well.
+// after it.  Two CTAs (64-wide heads: four) share an SM, so one's start and end
+// run beside the other's loop as well.
 //
 // The running maximum is lazy: O and the sum are rescaled only when a row's
 // maximum grows by more than 2^8 over the reference in use, which any reference
@@ -33,15 +33,22 @@ namespace {
 
 constexpr int kFwdThreads = 192, kFwdTma = 4, kFwdMma = 5;   // warps 0-3 softmax and epilogue, then TMA and MMA
 
-// kKeys: keys of a tile.  TMEM columns: S of BUFS tiles in flight from 0, O 128.
+// kKeys: keys of a tile, BUFS: score tiles in flight, CTAS: of an SM.  TMEM columns: S of tile i from (i % BUFS) * kKeys,
+// P over it from column P_AT of it on, O from COL_O.  64-wide heads spend most of their time in the softmax, whose
+// latencies more warps hide: four CTAs with one score tile each (128 columns) instead of two with two.  They have 80
+// registers a thread, so a tile's scores are taken in halves, the first one twice.
 template <int D, int kKeys>
 struct FwdShape {
-    static constexpr int BUFS = 128 / kKeys, HALVES = kKeys / 64;
-    static constexpr bool MASK_AHEAD = kKeys == 64;              // 128 scores a thread leave no registers for it
+    static constexpr bool NARROW = D == 64;
+    static constexpr int CTAS = NARROW ? 4 : 2;
+    static constexpr int BUFS = NARROW ? 1 : 128 / kKeys, HALVES = kKeys / 64;
+    static constexpr int P_AT = NARROW ? 32 : 0;
+    static constexpr int COL_O = BUFS * kKeys, TMEM = 512 / CTAS;
+    static constexpr bool MASK_AHEAD = kKeys == 64 && !NARROW;   // elsewhere registers are wanting
     static constexpr int KC = D / 64;
     static constexpr int Q_BYTES = KC * 16384;
     static constexpr int TILE = KC * kKeys * 128;
-    static constexpr int STAGES = 81920 / TILE;                   // K and V tiles
+    static constexpr int STAGES = NARROW ? 4 : 81920 / TILE;      // K and V tiles
     static constexpr int OFF_RING = Q_BYTES;
     static constexpr int OFF_BAR = OFF_RING + STAGES * TILE;
     static constexpr int TOTAL = OFF_BAR + 256;
@@ -49,13 +56,13 @@ struct FwdShape {
     static constexpr int XROW = D + 4;
     static constexpr int OFF_ML = kXRows * XROW * 4;
     static_assert(OFF_ML + kXRows * 8 <= OFF_BAR, "the exchange overlays Q and the ring");
-    static_assert(2 * (TOTAL + 1024) <= 228 * 1024, "two CTAs an SM");
+    static_assert(CTAS * (TOTAL + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 // XF_S: scores of an even / odd tile formed, and P V of the tile two before complete; XF_P: P written
 enum { XF_Q = 0, XF_S = 1, XF_P = 3, XF_DRAIN = 5, XF_FULL = 6 };
 
 template <bool kFp16, int D, int kKeys>
-__global__ void __launch_bounds__(kFwdThreads, 2)
+__global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
     k_xfwd(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
            const __grid_constant__ CUtensorMap map_v, const __grid_constant__ XArgs A) {
     using L = FwdShape<D, kKeys>;
@@ -75,7 +82,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         tc::fence_mbar_init();
     }
     if (warp == kFwdMma) {
-        tc::tmem_alloc(tmem_slot, 256);
+        tc::tmem_alloc(tmem_slot, L::TMEM);
         tc::tmem_relinquish();
     }
     if (threadIdx.x == kFwdTma * 32) {
@@ -153,11 +160,11 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             for (int i = 0; i < n && ok; ++i) {
                 const bool more = i + NB < n;
                 const int jv = i + (more ? i + NB : n);
-                const uint32_t vt = ring + jv % ST * L::TILE, acc = tmem + 128, pt = tmem + i % NB * kKeys;
+                const uint32_t vt = ring + jv % ST * L::TILE, acc = tmem + L::COL_O, pt = tmem + i % NB * kKeys + L::P_AT;
                 // P (its first half), V, and with the last half the K tile of the scores that follow
                 auto written = [&](int h) {
                     return L::HALVES == 2 ? Phase{&bars[XF_P + h], (uint32_t)i & 1u}
-                                          : Phase{&bars[XF_P + (i & 1)], (uint32_t)(i >> 1) & 1u};
+                                          : Phase{&bars[XF_P + i % NB], (uint32_t)(i / NB) & 1u};
                 };
                 ok = L::HALVES == 1 && more ? warp_wait(abort_flag, written(0), landed(jv), landed(jv + 1))
                                             : warp_wait(abort_flag, written(0), landed(jv));
@@ -187,7 +194,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     } else {
         const int r = warp * 32 + lane;                  // query row = TMEM lane
         const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
-        const uint32_t to = trow + 128;
+        const uint32_t to = trow + L::COL_O;
         float m = -INFINITY, l = 0.f;                    // reference maximum (log2 units), sum
         if (n > 0) {
             // -------------------------------------------------- softmax
@@ -204,31 +211,40 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             KeyLoad<kKeys / 32> keys{};                  // of the next tile that may lack keys
             auto tile = [&](auto masked, int i) -> bool {
                 const uint32_t ts = trow + i % NB * kKeys;
-                float x[kKeys];
-#pragma unroll
-                for (int j = 0; j < kKeys; j += 32) tmem_ld32(ts + j, reinterpret_cast<uint32_t *>(x) + j);
-                tc::tmem_wait_ld();
+                KeyBits<kKeys / 32> kb{};
                 if constexpr (decltype(masked)::value) {
                     if (!L::MASK_AHEAD) keys.start(A.mask, u.seq, (t0 + i) * kKeys, lane);
-                    const KeyBits<kKeys / 32> kb = keys.finish();
+                    kb = keys.finish();
                     if (L::MASK_AHEAD && i + 1 < n) keys.start(A.mask, u.seq, (t0 + i + 1) * kKeys, lane);
-#pragma unroll
-                    for (int j = 0; j < kKeys; ++j)
-                        if (!((kb.w[j >> 5] >> (j & 31)) & 1u)) x[j] = -INFINITY;
                     if (!kb.all()) {
                         const int jv = i + (i + NB < n ? i + NB : n);   // V's place in the ring, as in the MMA warp
                         if (!warp_wait(abort_flag, Phase{&full[jv % ST], (uint32_t)(jv / ST) & 1u})) return false;
                         zero_rows<L::KC, kKeys / 32, 128>(smem + L::OFF_RING + jv % ST * L::TILE, kb, r);
                     }
                 }
-                float mx[4] = {x[0], x[1], x[2], x[3]};
+                constexpr int kHeld = L::NARROW ? 32 : kKeys;           // scores held in registers at a time
+                float x[kHeld];
+                // columns `from` .. from + kHeld - 1
+                auto scores = [&](int from) {
 #pragma unroll
-                for (int j = 4; j < kKeys - 4; j += 8) {
+                    for (int j = 0; j < kHeld; j += 32) tmem_ld32(ts + from + j, reinterpret_cast<uint32_t *>(x) + j);
+                    tc::tmem_wait_ld();
+                    if constexpr (decltype(masked)::value) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], x[j + e]), x[j + 4 + e]);
+                        for (int j = 0; j < kHeld; ++j)
+                            if (!((kb.w[(from + j) >> 5] >> (j & 31)) & 1u)) x[j] = -INFINITY;
+                    }
+                };
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int from = 0; from < kKeys; from += kHeld) {
+                    scores(from);
+#pragma unroll
+                    for (int j = 0; j < kHeld; j += 8) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], x[j + e]), x[j + 4 + e]);
+                    }
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[kKeys - 4 + e]);
                 const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
                 const bool grow = mt > m + 8.f;
                 if (__any_sync(0xffffffffu, grow)) {
@@ -252,21 +268,38 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                 }
                 const float base = m == -INFINITY ? 0.f : m - kShift;
                 float sum[4] = {};
-#pragma unroll
-                for (int h = 0; h < L::HALVES; ++h) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float a = xex2(fmaf(x[h * 64 + 2 * j], c, -base));
-                        const float b = xex2(fmaf(x[h * 64 + 2 * j + 1], c, -base));
-                        sum[2 * (j & 1)] += a;
-                        sum[2 * (j & 1) + 1] += b;
-                        p[j] = xpack<kFp16>(a, b);
-                    }
-                    tmem_st32(ts + h * 32, p);
+                // two rounded probabilities
+                auto pair = [&](int j) {
+                    const float a = xex2(fmaf(x[j], c, -base)), b = xex2(fmaf(x[j + 1], c, -base));
+                    sum[j & 2] += a;
+                    sum[(j & 2) + 1] += b;
+                    return xpack<kFp16>(a, b);
+                };
+                auto written = [&](int which) {
                     tmem_wait_st();
                     tc::tc_fence_before();
-                    warp_arrive(&bars[XF_P + (L::HALVES == 2 ? h : i & 1)], lane);
+                    warp_arrive(&bars[XF_P + which], lane);
+                };
+                if constexpr (L::NARROW) {
+                    // the second half's scores are at hand, and P lies over them
+                    uint32_t p[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) p[j] = pair(2 * j);
+                    tmem_st16(ts + 48, p);
+                    scores(0);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) p[j] = pair(2 * j);
+                    tmem_st16(ts + 32, p);
+                    written(0);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < L::HALVES; ++h) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) p[j] = pair(h * 64 + 2 * j);
+                        tmem_st32(ts + h * 32, p);
+                        written(L::HALVES == 2 ? h : i % NB);
+                    }
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 return true;
@@ -375,7 +408,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     __syncthreads();
     if (warp == kFwdMma) {
         tc::tc_fence_after();
-        tc::tmem_dealloc(tmem, 256);
+        tc::tmem_dealloc(tmem, L::TMEM);
     }
     if (threadIdx.x == 0) {
         A.status[blockIdx.x] = *abort_flag ? SAG_ERR_TIMEOUT : SAG_OK;
