@@ -160,6 +160,9 @@ template <int n> __device__ __forceinline__ void regs_fewer() { asm volatile("se
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Kernels of one call: the next one's CTAs may be placed as this one's leave, and wait there for all its results.
+__device__ __forceinline__ void grid_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // address of the same shared-memory variable in CTA `rank` of the cluster
 __device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, int rank) {
     uint32_t a;

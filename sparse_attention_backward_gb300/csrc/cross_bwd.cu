@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = lane % LPR;
     if (blockIdx.x == 0 && threadIdx.x < 2) A.ticket[threadIdx.x] = 0;
+    grid_next();
     const int q_units = A.q_tiles * A.n2;
     float top = 0.f;
     int64_t slot;
@@ -281,8 +282,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot, sbase = tc::smem_u32(smem);
+    grid_wait();                                         // statistics and tickets of the kernel before
     const int ns = A.nsplit, rank = blockIdx.x % ns;
     const int G = A.group;
+    grid_next();
     auto fail = [&]() { *abort_flag = 1; };
     auto decode = [&](int unit) {
         const XUnit u = x_decode<&SeqRow::qtile0>(A, unit);
@@ -598,6 +601,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot, sbase = tc::smem_u32(smem);
+    grid_wait();                                         // statistics and tickets of the kernel before
     const int ns = A.nsplit, rank = blockIdx.x % ns;
     const int G = A.group;
     auto fail = [&]() { *abort_flag = 1; };
@@ -897,16 +901,16 @@ bool maps(BwdMaps *m, const XArgs &a, const sca_io &io, const sca_desc &d) {
 }
 
 template <bool kFp16, int D>
-cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, bool dkv, cudaStream_t s) {
+cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, bool dkv, bool after, cudaStream_t s) {
     BwdMaps m;
     if (!maps(&m, a, io, d)) return cudaErrorInvalidValue;
-    return x_launch(dkv ? k_xdkv<kFp16, D> : k_xdq<kFp16, D>, a.ctas, kXThreads, a.nsplit, BwdSmem<D>::TOTAL, s, m.q, m.dy,
+    return x_launch(dkv ? k_xdkv<kFp16, D> : k_xdq<kFp16, D>, a.ctas, kXThreads, a.nsplit, BwdSmem<D>::TOTAL, after, s, m.q, m.dy,
                     m.k, m.v, a);
 }
 
 template <bool kFp16>
-cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, bool dkv, cudaStream_t s) {
-    return d.d == 128 ? launch<kFp16, 128>(a, io, d, dkv, s) : launch<kFp16, 64>(a, io, d, dkv, s);
+cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, bool dkv, bool after, cudaStream_t s) {
+    return d.d == 128 ? launch<kFp16, 128>(a, io, d, dkv, after, s) : launch<kFp16, 64>(a, io, d, dkv, after, s);
 }
 
 }  // namespace
@@ -925,11 +929,13 @@ cudaError_t launch_xpre(const XArgs &a, bool fp16, int d, cudaStream_t s) {
 }
 
 cudaError_t launch_xdq(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s) {
-    return d.dtype == SAG_FP16 ? launch<true>(a, io, d, false, s) : launch<false>(a, io, d, false, s);
+    return d.dtype == SAG_FP16 ? launch<true>(a, io, d, false, true, s) : launch<false>(a, io, d, false, true, s);
 }
 
 cudaError_t launch_xdkv(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s) {
-    return d.dtype == SAG_FP16 ? launch<true>(a, io, d, true, s) : launch<false>(a, io, d, true, s);
+    // without query rows there is no kernel of this call before it
+    const bool after = a.q_tiles > 0;
+    return d.dtype == SAG_FP16 ? launch<true>(a, io, d, true, after, s) : launch<false>(a, io, d, true, after, s);
 }
 
 }  // namespace sag

@@ -422,8 +422,8 @@ cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStre
     if (!x_map_q(&mq, io.query, d, a, d.q_stride) || !x_map_k(&mk, io.key, io.query, d, d.k_stride, kKeys) ||
         !x_map_k(&mv, io.value, io.query, d, d.v_stride, kKeys))
         return cudaErrorInvalidValue;
-    return x_launch(k_xfwd<kFp16, D, kKeys>, a.ctas, kFwdThreads, a.nsplit, FwdShape<D, kKeys>::TOTAL, s, mq, mk,
-                    mv, a);
+    return x_launch(k_xfwd<kFp16, D, kKeys>, a.ctas, kFwdThreads, a.nsplit, FwdShape<D, kKeys>::TOTAL, false, s, mq,
+                    mk, mv, a);
 }
 
 }  // namespace

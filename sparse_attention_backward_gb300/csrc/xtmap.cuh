@@ -42,8 +42,11 @@ inline bool x_map_k(CUtensorMap *m, const void *base, const void *other, const s
                  rows && stride ? stride : (int64_t)(rows ? d.n2 : d.n1) * d.d, 1, box_rows);
 }
 
+// `after`: a kernel of this call that starts while the one before it ends (its CTAs set up, then wait for that one's
+// results with grid_wait).
 template <class... P, class... Args>
-cudaError_t x_launch(void (*kernel)(P...), int ctas, int threads, int cluster, int smem, cudaStream_t s, const Args &...args) {
+cudaError_t x_launch(void (*kernel)(P...), int ctas, int threads, int cluster, int smem, bool after, cudaStream_t s,
+                     const Args &...args) {
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -52,13 +55,22 @@ cudaError_t x_launch(void (*kernel)(P...), int ctas, int threads, int cluster, i
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (after) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
