@@ -313,3 +313,21 @@ def test_large_batch_captured():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("drop", [None, 0.2])
+@pytest.mark.parametrize("l1,l2", [([300], [2100]), ([200, 64], [5000, 2300]), ([260], [9000])])
+def test_long_loops_of_wide_heads(dtype, drop, l1, l2):
+    # full query tiles and at least 2048 keys: the forward's tiles of 128 keys
+    run(Case(l1, l2, 16, 8, 128, dtype, mask=drop, seed=21))
+
+
+def test_growing_maximum_in_long_loops():
+    # every few tiles the maximum grows beyond the lazy reference, in either half of a tile
+    c = Case([256], [4096], 16, 8, 128, BF, seed=22)
+    ramp = torch.linspace(0.02, 2.5, 4096)[:, None, None]
+    ramp = ramp.reshape(64, 64, 1, 1)[torch.arange(64) ^ 1].reshape(4096, 1, 1)      # the larger half first
+    c.k = (torch.randn(1, 8, 128, generator=torch.Generator().manual_seed(4)) * ramp).to(BF).contiguous()
+    c.q = (c.q * 0.4).to(BF)
+    run(c)
