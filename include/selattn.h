@@ -520,7 +520,8 @@ sag_status rotary_frequencies(int32_t d_rot, double base, int32_t scaling, doubl
 /* Phase 1 (host only): validation and workspace size (0 for batches of up to 64 sequences). */
 sag_status rotary_workspace_size(const srt_desc *desc, size_t *workspace_bytes);
 
-/* Phase 2: the rotation and its gradient, enqueued on `stream`.  The workspace may be NULL where phase 1 said 0. */
+/* Phase 2: the rotation and its gradient, enqueued on `stream`; ownership and errors as for sel_attn_grad.  The workspace may
+ * be NULL where phase 1 said 0.  SAG_ERR_UNSUPPORTED for interleaved pairs where d, offset, d_rot or a row stride is odd. */
 sag_status rotary_fwd(const srt_desc *desc, const srt_io *io, void *workspace, size_t workspace_bytes, void *stream);
 sag_status rotary_grad(const srt_desc *desc, const srt_io *io, void *workspace, size_t workspace_bytes, void *stream);
 
@@ -582,8 +583,9 @@ typedef struct sca_io {
 sag_status cross_attn_fwd_workspace_size(const sca_desc *desc, size_t *workspace_bytes);
 sag_status cross_attn_grad_workspace_size(const sca_desc *desc, size_t *workspace_bytes);
 
-/* Phase 2: enqueue on `stream`; ownership and host-side errors as for sel_attn_grad.  Every output is bit-identical run to
- * run (sums are taken in a fixed order). */
+/* Phase 2: enqueue on `stream`; ownership and host-side errors as for sel_attn_grad.  Outputs must not overlap inputs.  Every
+ * output is bit-identical run to run (sums are taken in a fixed order).  These calls and the rotary ones may be captured into
+ * a graph; the legacy default stream runs them on the device that owns the workspace (rotary: the output). */
 sag_status cross_attn_fwd(const sca_desc *desc, const sca_io *io, void *workspace, size_t workspace_bytes, void *stream);
 sag_status cross_attn_grad(const sca_desc *desc, const sca_io *io, void *workspace, size_t workspace_bytes, void *stream);
 

@@ -253,6 +253,10 @@ sag_status run_rotary(const srt_desc *d, const srt_io *io, void *workspace, size
     a.in_stride[1] = d->k_stride ? d->k_stride : (int64_t)d->n2 * d->d;
     a.out_stride[0] = d->q_out_stride ? d->q_out_stride : (int64_t)d->n1 * d->d;
     a.out_stride[1] = d->k_out_stride ? d->k_out_stride : (int64_t)d->n2 * d->d;
+    // an output over its own input has to have its rows where the input has them
+    if ((io->query == io->query_out && a.in_stride[0] != a.out_stride[0]) ||
+        (d->n2 && io->key == io->key_out && a.in_stride[1] != a.out_stride[1]))
+        return SAG_ERR_SHAPE;
     for (int i = 0; i < d->d_rot / 2; ++i) {
         // fraction of a turn per position, then 64 bits of it
         double t = d->inv_freq[i] / (2.0 * M_PI);

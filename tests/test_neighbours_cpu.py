@@ -139,6 +139,14 @@ def test_rotary_phase2_host_checks(lib):
     assert call(_rot(cu=[0, 0]), sab.SrtIo()) == OK        # no rows: nothing to do
 
 
+def test_rotary_in_place_with_another_stride(lib):
+    # the device is asked for only after the argument checks, and there is none here; with one, the strides are refused
+    d = _rot()
+    d.q_out_stride = 1024
+    io = sab.SrtIo(query=4096, key=8192, query_out=4096, key_out=16384)
+    assert lib.rotary_fwd(ctypes.byref(d), ctypes.byref(io), None, 0, None) in (SHAPE, sab.SAG_ERR_CUDA)
+
+
 # --------------------------------------------------------- cross attention
 def _cross(**kw):
     a = dict(cu_seqlens_q=[0, 3, 10], cu_seqlens_kv=[0, 7, 7], n1=8, n2=2, d=128, scale=0.1)
