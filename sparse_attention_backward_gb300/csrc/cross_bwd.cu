@@ -451,7 +451,11 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     tmem_ld32(ts + 32, reinterpret_cast<uint32_t *>(p) + 32);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) p[j] = xex2(fmaf(p[j], c, nl));
+                    for (int j = 0; j < 64; j += 2) {
+                        const float2 e = fma2(make_float2(p[j], p[j + 1]), make_float2(c, c), make_float2(nl, nl));
+                        p[j] = xex2(e.x);
+                        p[j + 1] = xex2(e.y);
+                    }
                     if (!warp_wait(abort_flag, Phase{&bars[XB_DP], (uint32_t)g & 1u})) return false;
                     tc::tc_fence_after();
                     uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
@@ -475,7 +479,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
                         }
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
-                            float a = p[f * 32 + j] * (y[j] + nd), b = p[f * 32 + j + 1] * (y[j + 1] + nd);
+                            const float2 e = mul2(make_float2(p[f * 32 + j], p[f * 32 + j + 1]),
+                                                  add2(make_float2(y[j], y[j + 1]), make_float2(nd, nd)));
+                            float a = e.x, b = e.y;
                             if constexpr (decltype(masked)::value) {
                                 if (!((bits[f] >> j) & 1u)) a = 0.f;
                                 if (!((bits[f] >> (j + 1)) & 1u)) b = 0.f;
@@ -776,14 +782,18 @@ __global__ void __launch_bounds__(kXThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 64; j += 4) {
                         const float4 nl4 = st[j / 4];
-                        const float nl[4] = {nl4.x, nl4.y, nl4.z, nl4.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float x = fmaf(p[j + e], c, nl[e]);
-                            if (kFp16) x += kShift;
-                            p[j + e] = xex2(x);
-                            if (kMasked && !live) p[j + e] = 0.f;
+                        const float2 c2 = make_float2(c, c), shift = make_float2(kShift, kShift);
+                        float2 e = fma2(make_float2(p[j], p[j + 1]), c2, make_float2(nl4.x, nl4.y));
+                        float2 o = fma2(make_float2(p[j + 2], p[j + 3]), c2, make_float2(nl4.z, nl4.w));
+                        if (kFp16) {
+                            e = add2(e, shift);
+                            o = add2(o, shift);
                         }
+                        p[j] = xex2(e.x);
+                        p[j + 1] = xex2(e.y);
+                        p[j + 2] = xex2(o.x);
+                        p[j + 3] = xex2(o.y);
+                        if (kMasked && !live) p[j] = p[j + 1] = p[j + 2] = p[j + 3] = 0.f;
                         q[j / 2] = xpack<kFp16>(p[j], p[j + 1]);
                         q[j / 2 + 1] = xpack<kFp16>(p[j + 2], p[j + 3]);
                     }
@@ -801,17 +811,19 @@ __global__ void __launch_bounds__(kXThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; j += 4) {
                             const float4 nd4 = st[32 + (f * 32 + j) / 4];
-                            const float nd[4] = {nd4.x, nd4.y, nd4.z, nd4.w};
-                            float a[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                a[e] = y[j + e] + nd[e];
-                                if (kFp16) a[e] *= k;
-                                a[e] *= p[f * 32 + j + e];
-                                if (kMasked && !live) a[e] = 0.f;
+                            const float2 k2 = make_float2(k, k);
+                            const float *pp = p + f * 32 + j;
+                            float2 e = add2(make_float2(y[j], y[j + 1]), make_float2(nd4.x, nd4.y));
+                            float2 o = add2(make_float2(y[j + 2], y[j + 3]), make_float2(nd4.z, nd4.w));
+                            if (kFp16) {
+                                e = mul2(e, k2);
+                                o = mul2(o, k2);
                             }
-                            q[(f * 32 + j) / 2] = xpack<kFp16>(a[0], a[1]);
-                            q[(f * 32 + j) / 2 + 1] = xpack<kFp16>(a[2], a[3]);
+                            e = mul2(e, make_float2(pp[0], pp[1]));
+                            o = mul2(o, make_float2(pp[2], pp[3]));
+                            if (kMasked && !live) e.x = e.y = o.x = o.y = 0.f;
+                            q[(f * 32 + j) / 2] = xpack<kFp16>(e.x, e.y);
+                            q[(f * 32 + j) / 2 + 1] = xpack<kFp16>(o.x, o.y);
                         }
                     }
                     tmem_st32(trow + 128 + h * 64, q);
