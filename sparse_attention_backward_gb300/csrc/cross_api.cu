@@ -13,7 +13,7 @@ constexpr size_t kAlign = 256;
 constexpr size_t kTicketAt = 16;            // two ticket counters
 constexpr size_t kStatusAt = 256;           // status words, behind the workspace's header
 size_t up256(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-// CTAs that splitting may add to a launch (it stops at one CTA per SM), for the status words
+// most CTAs of a launch whose units are split, for the status words
 constexpr int64_t kSplitCtas = 1024;
 
 struct XPlan {
