@@ -149,14 +149,15 @@ struct BwdSmem {
     static_assert(TOTAL <= 227 * 1024, "shared memory of one CTA");
     // 512 bytes behind OFF_BAR: barriers, TMEM address, abort flag; from 320 on the two slots of units
 };
-// barriers; XB_XYE: the resident tiles may be overwritten; XB_UF, XB_UE: units handed out
+// barriers; XB_XYE: the resident tiles may be overwritten; XB_UF, XB_UE: units handed out; XB_DS: two in k_xdq, where the
+// softmax warps may be done with the next tile before the MMA warp looks for this one (modelled in the tests)
 enum {
-    XB_XY = 0, XB_XYE, XB_S, XB_DP = XB_S + 2, XB_PF, XB_DS, XB_ACC, XB_STF, XB_STE = XB_STF + 2, XB_UF = XB_STE + 2,
+    XB_XY = 0, XB_XYE, XB_S, XB_DP = XB_S + 2, XB_PF, XB_DS, XB_ACC = XB_DS + 2, XB_STF, XB_STE = XB_STF + 2, XB_UF = XB_STE + 2,
     XB_UE = XB_UF + 2, XB_RING = XB_UE + 2
 };
 // arrivals that complete a phase: one a softmax warp; every reader's for the units; one of everything else
 __device__ __forceinline__ int bwd_arrivals(int i) {
-    return i == XB_PF || i == XB_DS || i == XB_STE || i == XB_STE + 1 ? 8 : i == XB_UE || i == XB_UE + 1 ? 9 : 1;
+    return i == XB_PF || i == XB_DS || i == XB_DS + 1 || i == XB_STE || i == XB_STE + 1 ? 8 : i == XB_UE || i == XB_UE + 1 ? 9 : 1;
 }
 
 // A unit as its roles need it, in shared memory.
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     issue_dp(g + 1);
                     if (i + 2 == n) tc::mma_commit_warp(&bars[XB_XYE]);
                 }
-                const Phase ds{&bars[XB_DS], (uint32_t)g & 1u};
+                const Phase ds{&bars[XB_DS + (g & 1)], (uint32_t)(g >> 1) & 1u};
                 ok = i + 2 < n ? warp_wait(abort_flag, ds, ra.landed(g + 2)) : warp_wait(abort_flag, ds);
                 if (!ok) break;
                 const uint32_t kt = L::OFF_A + g % L::RA * L::TILE;
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     tmem_st32(ts, q);
                     tmem_wait_st();
                     tc::tc_fence_before();
-                    warp_arrive(&bars[XB_DS], lane);
+                    warp_arrive(&bars[XB_DS + (g & 1)], lane);
                     return true;
                 };
                 for (int i = 0; i < n && ok; ++i, ++g) {
