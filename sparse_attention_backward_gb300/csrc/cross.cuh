@@ -13,7 +13,8 @@
 namespace sag {
 
 constexpr int kXRows = 128;             // rows of a query tile, keys of a key tile
-constexpr int kMaxSplit = 8;            // CTAs of a cluster
+constexpr int kMaxSplit = 8;            // CTAs of a cluster, pieces of a unit
+constexpr int kMaxPieces = 304;         // pieces of a launch: each has its partial sums in the workspace
 constexpr int kXThreads = 320;          // warps 0-7 softmax and epilogue, 8 TMA, 9 MMA
 constexpr uint64_t kXWaitNs = 2000000000ull;
 // A half keeps 11 bits down to 2^-14 only, and a probability of a long sequence lies below that.  Both passes shift
@@ -29,7 +30,12 @@ struct XArgs {
     int32_t units;                      // query (k_xdkv: key) tiles times key/value heads
     int32_t nsplit;                     // CTAs (one cluster) that share a unit
     int32_t ctas;                       // of the launch: units * nsplit, or fewer that take unit after unit
-    unsigned *ticket;                   // next units of the two gradient kernels, zeroed by k_xpre
+    // gradient kernels: work items are `full` whole units, then pieces of the others, `pieces` each
+    int32_t items, full, pieces;
+    float *parts;                       // partial sums of the pieces
+    unsigned *arrived;                  // pieces of a unit whose sums are there, for each softmax warp
+    int32_t n_arrived;                  // such counters of the call
+    unsigned *ticket;                   // next items of the two gradient kernels; zeroed by k_xpre, like the counters
     float scale, scale_log2;
     const uint8_t *mask;
     const uint16_t *o_in, *dy, *v_in;   // preprocess
@@ -237,12 +243,12 @@ __device__ __forceinline__ XUnit x_decode(const XArgs &A, int unit) {
 }
 
 // A rank's share of `tiles`: first tile and number.
-__device__ __forceinline__ void x_share(const XArgs &A, int tiles, int rank, int *first, int *n) {
+__device__ __forceinline__ void x_share(int tiles, int rank, int ranks, int *first, int *n) {
     *first = 0;
     *n = tiles;
-    if (A.nsplit > 1) {
-        *first = tiles * rank / A.nsplit;
-        *n = tiles * (rank + 1) / A.nsplit - *first;
+    if (ranks > 1) {
+        *first = tiles * rank / ranks;
+        *n = tiles * (rank + 1) / ranks - *first;
     }
 }
 

@@ -21,7 +21,9 @@ struct XPlan {
     int tpt;
     int64_t q_tiles, k_tiles;               // query and key tiles of all sequences, padding included
     int max_q, max_k;                       // most query / key tiles of one sequence that have work
-    size_t o_seq, o_stats, o_norms, total;
+    int min_q, min_k;                       // fewest
+    bool padding;                           // some tiles are padding
+    size_t o_seq, o_stats, o_norms, o_parts, o_arrived, total;
 };
 
 sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {
@@ -45,6 +47,8 @@ sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {
     p->tpt = kXRows / (d->n1 / d->n2);
     p->q_tiles = p->k_tiles = 0;
     p->max_q = p->max_k = 0;
+    p->min_q = p->min_k = 1 << 30;
+    p->padding = false;
     for (int b = 0; b < d->batch; ++b) {
         const int ql = d->cu_seqlens_q[b + 1] - d->cu_seqlens_q[b], kl = d->cu_seqlens_kv[b + 1] - d->cu_seqlens_kv[b];
         const int qt = ((p->bsnd ? d->s1_max : ql) + p->tpt - 1) / p->tpt;
@@ -54,6 +58,9 @@ sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {
         const int qw = (ql + p->tpt - 1) / p->tpt, kw = (kl + kXRows - 1) / kXRows;
         if (qw > p->max_q) p->max_q = qw;
         if (kw > p->max_k) p->max_k = kw;
+        if (qw < p->min_q) p->min_q = qw;
+        if (kw < p->min_k) p->min_k = kw;
+        if (qw < qt || kw < kt) p->padding = true;
     }
     size_t o = 0;
     auto take = [&](size_t bytes) { const size_t at = o; o = up256(o + bytes); return at; };
@@ -63,6 +70,10 @@ sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {
     p->o_seq = take(seq_ws_bytes(d->batch));
     p->o_stats = take(grad ? sizeof(float) * 256 * p->q_tiles * d->n2 : 0);
     p->o_norms = take(grad && p->fp16 ? sizeof(unsigned) * 2 * (size_t)d->batch * d->n2 : 0);
+    const int64_t most = (p->q_tiles > p->k_tiles ? p->q_tiles : p->k_tiles) * d->n2;
+    const int64_t pieces = most < kMaxPieces / kMaxSplit ? most * kMaxSplit : kMaxPieces;
+    p->o_parts = take(grad ? sizeof(float) * 2 * kXRows * d->d * pieces : 0);
+    p->o_arrived = take(grad ? sizeof(unsigned) * 2 * 8 * kMaxPieces : 0);
     p->total = o;
     return SAG_OK;
 }
@@ -76,6 +87,25 @@ int split_of(int64_t units, int tiles, int room) {
     for (int ns = kMaxSplit; ns > 1; --ns)
         if (ns <= tiles && units * ns * 1000 <= (int64_t)room * share[ns]) return ns;
     return 1;
+}
+
+// Units of a gradient kernel beyond full rounds of the SMs are cut into pieces of their loops if those fill the last round
+// better: `full` whole units, then `pieces` of each other one.  Times in tiles of the loop: a piece costs about six more
+// for its start, its sums' way to the workspace and the last one's adding up, which takes one for each piece.  160 units of
+// 64 tiles: 260 -> 207 us, 512 units of 256 tiles: 2320 -> 2150 us, 320 units of 24 tiles: 190 -> 179 us.  Only where units
+// take alike: short ones fill the last round as it is (a ragged padded batch: 155 -> 165 us).
+void tail_of(int units, int tiles, int least, int sms, int *full, int *pieces) {
+    *full = units;
+    *pieces = 1;
+    const int rest = least * 8 >= tiles * 7 ? units % sms : 0;
+    int best = tiles + 1;
+    for (int s = 2; s <= kMaxSplit && s <= tiles && rest * s <= kMaxPieces; ++s) {
+        const int t = (rest * s + sms - 1) / sms * ((tiles + s - 1) / s + 6) + s;
+        if (rest == 0 || t >= best) continue;
+        best = t;
+        *full = units - rest;
+        *pieces = s;
+    }
 }
 
 XArgs x_args(const sca_desc *d, const sca_io *io, const XPlan &p, char *ws) {
@@ -101,6 +131,8 @@ XArgs x_args(const sca_desc *d, const sca_io *io, const XPlan &p, char *ws) {
     a.lse = io->softmax_lse;
     a.stats = reinterpret_cast<float *>(ws + p.o_stats);
     a.norms = reinterpret_cast<unsigned *>(ws + p.o_norms);
+    a.parts = reinterpret_cast<float *>(ws + p.o_parts);
+    a.arrived = reinterpret_cast<unsigned *>(ws + p.o_arrived);
     a.q_tiles = (int)p.q_tiles;
     a.k_tiles = (int)p.k_tiles;
     a.count = reinterpret_cast<int32_t *>(ws);
@@ -210,25 +242,45 @@ extern "C" sag_status cross_attn_grad(const sca_desc *desc, const sca_io *io, vo
     const int sms = current_device_sms();
     if (p.fp16 && cudaMemsetAsync(a.norms, 0, sizeof(unsigned) * 2 * (size_t)desc->batch * desc->n2, s) != cudaSuccess)
         return SAG_ERR_CUDA;
-    if (launch_xpre(a, p.fp16, desc->d, s) != cudaSuccess) return SAG_ERR_CUDA;
-    // one CTA an SM: a cluster for each unit, or CTAs that take unit after unit
-    auto share = [&](int units, int tiles) {
-        a.units = units;
-        a.nsplit = split_of(units, tiles, sms);
-        a.ctas = a.nsplit > 1 || units < sms ? units * a.nsplit : sms;
+    // one CTA an SM: a cluster for each unit, or CTAs that take item after item
+    struct Share {
+        int units, nsplit, full, pieces, items, ctas;
     };
+    auto share = [&](int units, int tiles, int least) {
+        Share x;
+        x.units = x.full = units;
+        x.nsplit = split_of(units, tiles, sms);
+        x.pieces = 1;
+        if (x.nsplit == 1 && !p.padding) tail_of(units, tiles, least, sms, &x.full, &x.pieces);
+        x.items = x.full + (units - x.full) * x.pieces;
+        x.ctas = x.nsplit > 1 ? units * x.nsplit : x.items < sms ? x.items : sms;
+        return x;
+    };
+    auto use = [&](const Share &x) {
+        a.units = x.units;
+        a.nsplit = x.nsplit;
+        a.full = x.full;
+        a.pieces = x.pieces;
+        a.items = x.items;
+        a.ctas = x.ctas;
+    };
+    const Share sq = share(q_units, p.max_k, p.min_k), sk = share(k_units, p.max_q, p.min_q);
+    const int counts = (sq.units - sq.full) * 8;
+    a.n_arrived = counts + (sk.units - sk.full) * 8;
+    if (launch_xpre(a, p.fp16, desc->d, s) != cudaSuccess) return SAG_ERR_CUDA;
     int before = 0;
     // k_xpre zeroes the tickets; without query rows there is none
     if (!q_units && cudaMemsetAsync(a.ticket, 0, 2 * sizeof(unsigned), s) != cudaSuccess) return SAG_ERR_CUDA;
     if (q_units) {
-        share(q_units, p.max_k);
+        use(sq);
         if (launch_xdq(a, *io, *desc, s) != cudaSuccess) return SAG_ERR_CUDA;
         before = a.ctas;
     }
     if (k_units) {
         a.status += before;
         a.ticket += 1;
-        share(k_units, p.max_q);
+        use(sk);
+        a.arrived += counts;
         a.n_status = before + a.ctas;
         if (launch_xdkv(a, *io, *desc, s) != cudaSuccess) return SAG_ERR_CUDA;
     }

@@ -1,5 +1,5 @@
 // Cross attention, gradient: three launches, no fp32 accumulators in memory, no
-// atomics but a maximum and a ticket, so the same bits on every run.
+// atomics but a maximum, tickets and counters, so the same bits on every run.
 //
 //   k_xpre  Delta = rowsum(dY * O) and lse in log2 units, packed by query tile
 //   k_xdq   per query tile:  S = Q K^T, dP = dY V^T, dS = P (dP - Delta),  dQ += dS K      (over key tiles)
@@ -23,7 +23,10 @@
 // A CTA (one per SM) walks over units, so that the next unit's tiles land and
 // its first products run beside the last one's stores.  Few units: a cluster's
 // CTAs split one unit's loop and join their accumulators through distributed
-// shared memory, in rank order.
+// shared memory, in rank order.  More: the units beyond full rounds of the SMs
+// are cut into pieces, joined through the workspace in their order.  (Clusters
+// there cost 2269 us against 2271 without and 2100 with pieces for the gradient
+// below: a cluster's CTAs cannot take unit after unit.)
 //
 // Measured on one GB300, 2 x 8192 x 4096 tokens, 32 heads of 128 (bf16): k_xpre 51
 // us (5.3 TB/s), k_xdq 920 us (the tensor pipe 75 % active), k_xdkv 1267 us (85 %),
@@ -48,7 +51,10 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
     __shared__ float red[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = lane % LPR;
-    if (blockIdx.x == 0 && threadIdx.x < 2) A.ticket[threadIdx.x] = 0;
+    if (blockIdx.x == 0) {
+        if (threadIdx.x < 2) A.ticket[threadIdx.x] = 0;
+        for (int i = threadIdx.x; i < A.n_arrived; i += 256) A.arrived[i] = 0;
+    }
     grid_next();
     const int q_units = A.q_tiles * A.n2;
     float top = 0.f;
@@ -167,7 +173,68 @@ struct alignas(16) Work {
     int32_t first;                      // k_xdq: first token, k_xdkv: first key, within the sequence
     int32_t t0, n;                      // this rank's first tile of the loop and their number; n < 0: no more units
     int32_t stat;                       // k_xdq: (query tile of all sequences) * n2 + head
-    int32_t pad[4];
+    int32_t piece;                      // number of the piece; -1: a whole unit, or a cluster's; -2: nothing to do
+    int32_t pad[3];
+};
+
+// Work item -> unit, and the share of its loop.
+struct Item {
+    int unit, rank, ranks, piece;
+    __device__ __forceinline__ Item(const XArgs &A, int item, int rank_, int ranks_)
+        : unit(item), rank(rank_), ranks(ranks_), piece(-1) {
+        if (item >= A.full) {
+            piece = item - A.full;
+            unit = A.full + piece / A.pieces;
+            rank = piece % A.pieces;
+            ranks = A.pieces;
+        }
+    }
+    // of a loop of `tiles`; a unit without work is its first piece's alone
+    __device__ __forceinline__ void share(int tiles, Work *w) const {
+        x_share(tiles, rank, ranks, &w->t0, &w->n);
+        w->piece = piece >= 0 && tiles == 0 ? (rank ? -2 : -1) : piece;
+    }
+};
+
+// A piece's sums: a thread's 32-bit accumulators of COLS columns go to the workspace; of each warp's rows, the warp that
+// arrives last adds all pieces up in their order, so the order of arrival does not show in the result.
+template <int COLS>
+struct Pieces {
+    float4 *mine;                       // [piece][warp][COLS / 4][lane]
+    unsigned *arrived;
+    int pieces, rank;
+    __device__ __forceinline__ Pieces(const XArgs &A, int piece, int warp, int lane)
+        : mine(reinterpret_cast<float4 *>(A.parts) + ((int64_t)piece * 8 + warp) * (COLS * 8) + lane),
+          arrived(A.arrived + piece / A.pieces * 8 + warp), pieces(A.pieces), rank(piece % A.pieces) {}
+    __device__ __forceinline__ void put(int j, const float *y) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            __stcg(mine + (j / 4 + e) * 32, make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]));
+    }
+    __device__ __forceinline__ bool last(int lane) const {
+        __threadfence();
+        __syncwarp();
+        unsigned before = 0;
+        if (lane == 0) before = atomicAdd(arrived, 1u);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        __threadfence();
+        return before + 1 == (unsigned)pieces;
+    }
+    __device__ __forceinline__ void sum(int j, float *y) const {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = 0.f;
+        const float4 *p = mine - (int64_t)rank * 8 * (COLS * 8) + j / 4 * 32;
+        for (int k = 0; k < pieces; ++k, p += 8 * (COLS * 8)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float4 v = __ldcg(p + e * 32);
+                y[4 * e] += v.x;
+                y[4 * e + 1] += v.y;
+                y[4 * e + 2] += v.z;
+                y[4 * e + 3] += v.w;
+            }
+        }
+    }
 };
 
 // Units of a CTA, one after the other: the first by its number, the others from a ticket counter, since units differ (short
@@ -181,10 +248,10 @@ struct Units {
     template <class Decode>
     __device__ __forceinline__ bool take(const XArgs &A, int k, volatile int *abort, Work *w, Decode &&decode) const {
         if (k >= 2 && !tc::mbar_wait(&empty[k & 1], (k / 2 - 1) & 1, abort, kXWaitNs)) return false;
-        int unit = A.units;
-        if (k == 0) unit = blockIdx.x / A.nsplit;
-        else if (A.ctas < A.units) unit = (int)(gridDim.x + atomicAdd(A.ticket, 1u));
-        if (unit < A.units) *w = decode(unit);
+        int item = A.items;
+        if (k == 0) item = blockIdx.x / A.nsplit;
+        else if (A.ctas < A.items) item = (int)(gridDim.x + atomicAdd(A.ticket, 1u));
+        if (item < A.items) *w = decode(item);
         else w->n = -1;
         slot[k & 1] = *w;
         tc::mbar_arrive(&full[k & 1]);
@@ -292,15 +359,16 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const int G = A.group;
     grid_next();
     auto fail = [&]() { *abort_flag = 1; };
-    auto decode = [&](int unit) {
-        const XUnit u = x_decode<&SeqRow::qtile0>(A, unit);
+    auto decode = [&](int number) {
+        const Item item(A, number, rank, ns);
+        const XUnit u = x_decode<&SeqRow::qtile0>(A, item.unit);
         Work w{};
         w.seq = u.seq;
         w.b = u.b;
         w.head = u.head;
         w.first = u.tile * A.tpt;
         w.stat = (int32_t)u.tile_id;
-        x_share(A, w.first < u.seq.qlen ? (u.seq.klen + kXRows - 1) / kXRows : 0, rank, &w.t0, &w.n);
+        item.share(w.first < u.seq.qlen ? (u.seq.klen + kXRows - 1) / kXRows : 0, &w);
         return w;
     };
 
@@ -461,8 +529,6 @@ __global__ void __launch_bounds__(kXThreads, 1)
                         p[j] = xex2(e.x);
                         p[j + 1] = xex2(e.y);
                     }
-                    if (!warp_wait(abort_flag, Phase{&bars[XB_DP], (uint32_t)g & 1u})) return false;
-                    tc::tc_fence_after();
                     uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
                     if constexpr (decltype(masked)::value) {
                         const KeyBits<4> kb = keys.finish();
@@ -472,6 +538,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
                         bits[0] = h ? kb.w[2] : kb.w[0];
                         bits[1] = h ? kb.w[3] : kb.w[1];
                     }
+                    if (!warp_wait(abort_flag, Phase{&bars[XB_DP], (uint32_t)g & 1u})) return false;
+                    tc::tc_fence_after();
                     uint32_t q[32];
 #pragma unroll
                     for (int f = 0; f < 2; ++f) {
@@ -513,20 +581,47 @@ __global__ void __launch_bounds__(kXThreads, 1)
             if (ns > 1 || !ok) break;                    // stored below
             // -------------------------------------------------- epilogue
             const float f = A.scale * (kFp16 ? exp2f(-up) : 1.f);
-            const bool pad = n == 0 || w.first + my_tok >= w.seq.qlen;
+            const int piece = w.piece;
+            const bool pad = (n == 0 && piece < 0) || w.first + my_tok >= w.seq.qlen;
             RowStore<kFp16> rows;
-            rows.rows(place(my_tok, my_head), lane);
+            rows.rows(piece == -2 ? -1 : place(my_tok, my_head), lane);
             begin(k + 1);
-#pragma unroll
-            for (int j = 0; j < D / 2; j += 32) {
-                float y[32];
+            auto sums = [&](int j, float *y) {
                 if (n > 0) {
                     tmem_ld32(trow + 384 + h * (D / 2) + j, reinterpret_cast<uint32_t *>(y));
                     tc::tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) y[e] = 0.f;
                 }
+            };
+            auto store = [&](int j, float *y) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = pad ? 0.f : y[e] * f;
                 rows.store(A.dq, y, h * (D / 2) + j, lane);
+            };
+            if (piece < 0) {
+#pragma unroll
+                for (int j = 0; j < D / 2; j += 32) {
+                    float y[32];
+                    sums(j, y);
+                    store(j, y);
+                }
+            } else {
+                const Pieces<D / 2> part(A, piece, warp, lane);
+#pragma unroll 1
+                for (int j = 0; j < D / 2; j += 32) {
+                    float y[32];
+                    sums(j, y);
+                    part.put(j, y);
+                }
+                if (part.last(lane))
+#pragma unroll 1
+                    for (int j = 0; j < D / 2; j += 32) {
+                        float y[32];
+                        part.sum(j, y);
+                        store(j, y);
+                    }
             }
             tc::tc_fence_before();                       // read before the next unit's products may follow
         }
@@ -616,14 +711,15 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const int ns = A.nsplit, rank = blockIdx.x % ns;
     const int G = A.group;
     auto fail = [&]() { *abort_flag = 1; };
-    auto decode = [&](int unit) {
-        const XUnit u = x_decode<&SeqRow::ktile0>(A, unit);
+    auto decode = [&](int number) {
+        const Item item(A, number, rank, ns);
+        const XUnit u = x_decode<&SeqRow::ktile0>(A, item.unit);
         Work w{};
         w.seq = u.seq;
         w.b = u.b;
         w.head = u.head;
         w.first = u.tile * kXRows;
-        x_share(A, w.first < u.seq.klen ? (u.seq.qlen + A.tpt - 1) / A.tpt : 0, rank, &w.t0, &w.n);
+        item.share(w.first < u.seq.klen ? (u.seq.qlen + A.tpt - 1) / A.tpt : 0, &w);
         return w;
     };
 
@@ -852,19 +948,46 @@ __global__ void __launch_bounds__(kXThreads, 1)
             if (ns > 1 || !ok) break;                    // stored below
             // -------------------------------------------------- epilogue: warps 0-3 dV, warps 4-7 dK
             const float f = h ? A.scale * (kFp16 ? exp2f(-up) : 1.f) : fv;
+            const int piece = w.piece;
             RowStore<kFp16> rows;
-            rows.rows(out(r), lane);
+            rows.rows(piece == -2 ? -1 : out(r), lane);
             begin(turn + 1);
-#pragma unroll
-            for (int j = 0; j < D; j += 32) {
-                float y[32];
+            auto sums = [&](int j, float *y) {
                 if (n > 0) {
                     tmem_ld32(trow + 256 + h * 128 + j, reinterpret_cast<uint32_t *>(y));
                     tc::tmem_wait_ld();
-                }
+                } else {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = n > 0 ? y[e] * f : 0.f;
+                    for (int e = 0; e < 32; ++e) y[e] = 0.f;
+                }
+            };
+            auto store = [&](int j, float *y) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] *= f;
                 rows.store(h ? A.dk : A.dv, y, j, lane);
+            };
+            if (piece < 0) {
+#pragma unroll
+                for (int j = 0; j < D; j += 32) {
+                    float y[32];
+                    sums(j, y);
+                    store(j, y);
+                }
+            } else {
+                const Pieces<D> part(A, piece, warp, lane);
+#pragma unroll 1
+                for (int j = 0; j < D; j += 32) {
+                    float y[32];
+                    sums(j, y);
+                    part.put(j, y);
+                }
+                if (part.last(lane))
+#pragma unroll 1
+                    for (int j = 0; j < D; j += 32) {
+                        float y[32];
+                        part.sum(j, y);
+                        store(j, y);
+                    }
             }
             tc::tc_fence_before();                       // read before the next unit's products may follow
         }

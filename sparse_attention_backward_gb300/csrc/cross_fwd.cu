@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
     const int cover = A.s1_pad ? A.s1_pad : u.seq.qlen;
     const int nkt = tok0 < u.seq.qlen ? (u.seq.klen + kKeys - 1) / kKeys : 0;
     int t0, n;
-    x_share(A, nkt, rank, &t0, &n);
+    x_share(nkt, rank, ns, &t0, &n);
     const int partial = A.mask ? 0 : u.seq.klen / kKeys - t0;    // tiles from this one on may lack keys
     auto fail = [&]() { *abort_flag = 1; };
 

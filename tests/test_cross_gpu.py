@@ -331,3 +331,35 @@ def test_growing_maximum_in_long_loops():
     c.k = (torch.randn(1, 8, 128, generator=torch.Generator().manual_seed(4)) * ramp).to(BF).contiguous()
     c.q = (c.q * 0.4).to(BF)
     run(c)
+
+
+# units beyond full rounds of 152 SMs, with loops long enough that they are cut: (key tiles, query tiles, both kernels'
+# last round, no full round before it)
+@pytest.mark.parametrize("dtype,drop", [(BF, None), (HF, 0.3)])
+@pytest.mark.parametrize("l1,l2,n1,n2,d", [
+    ([2000], [1280], 16, 16, 128), ([640], [2000], 32, 16, 128), ([1050, 1100], [2100, 2050], 32, 8, 64),
+    ([8192], [1300], 8, 8, 64)])
+def test_last_units_in_pieces(dtype, drop, l1, l2, n1, n2, d):
+    run(Case(l1, l2, n1, n2, d, dtype, mask=drop, seed=l1[0]))
+
+
+def test_pieces_are_added_up_in_their_order():
+    c = Case([2048], [1280], 16, 16, 128, BF, seed=5)
+    q, k, v, dy = (x.cuda() for x in (c.q, c.k, c.v, c.dy))
+    o, lse = sab.cross_forward(q, k, v, c.cu1, c.cu2, c.scale)
+    want = sab.cross_backward(q, k, v, o, dy, lse, c.cu1, c.cu2, c.scale, check=True)
+    for _ in range(20):
+        for x, y in zip(want, sab.cross_backward(q, k, v, o, dy, lse, c.cu1, c.cu2, c.scale)):
+            assert torch.equal(x, y)
+
+
+def test_pieces_without_work():
+    # all states of one sequence masked, and a piece's whole share of the other's
+    c = Case([2048, 2040], [640, 640], 16, 16, 64, BF, mask=0.0, seed=6)
+    c.mask[:640] = False
+    c.k[:640], c.v[:640] = float("nan"), float("inf")
+    run(c)
+    c = Case([640], [2048], 32, 16, 64, HF, mask=0.0, seed=7)
+    c.mask[1024:] = False
+    c.k[1024:], c.v[1024:] = float("nan"), float("inf")
+    run(c)
