@@ -302,18 +302,15 @@ struct KeyLoad {
 // probability of 0 does not cancel a NaN.  Shared by kThreads threads; each fences its writes for the products' proxy.
 template <int kChunks, int kWords, int kThreads>
 __device__ __forceinline__ void zero_rows(uint8_t *tile, const KeyBits<kWords> &k, int thread) {
-    constexpr int kRows = 32 * kWords, kPer = kThreads > kRows ? kThreads / kRows : 1;   // threads a row
+    // consecutive threads take consecutive 16-byte pieces, so a pass of kPass rows has no bank conflicts (with a thread or
+    // two a row this took 700 to 1000 cycles of a masked tile)
+    constexpr int kRows = 32 * kWords, kPass = kThreads / (kChunks * 8);
+    static_assert(kPass >= 1 && 32 % kPass == 0, "a pass lies within a word");
+    const int c = thread % (kChunks * 8), r = thread / (kChunks * 8);
+    uint8_t *at = tile + (c >> 3) * kRows * 128 + r * 128 + (c & 7) * 16;
 #pragma unroll
-    for (int j = 0; j < kRows * kPer / kThreads; ++j) {
-        const int row = (thread + j * kThreads) / kPer;
-        uint32_t w = k.w[0];
-#pragma unroll
-        for (int i = 1; i < kWords; ++i) w = row >> 5 == i ? k.w[i] : w;
-        if (!((w >> (row & 31)) & 1u))
-#pragma unroll
-            for (int c = thread % kPer; c < kChunks * 8; c += kPer)
-                *reinterpret_cast<uint4 *>(tile + (c >> 3) * kRows * 128 + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-    }
+    for (int j = 0; j < kRows; j += kPass)
+        if (!((k.w[j >> 5] >> ((j & 31) + r)) & 1u)) *reinterpret_cast<uint4 *>(at + j * 128) = make_uint4(0, 0, 0, 0);
     tc::fence_proxy_async_smem();
 }
 

@@ -139,14 +139,15 @@ __device__ __forceinline__ uint2 ds_norms(const XArgs &A, int b, int head) {
 }
 
 // ------------------------------------------------------------------- shared
-// Two resident tiles (X, Y) and two rings: tiles that live long (A: keys in k_xdq, queries in k_xdkv) and tiles that one
+// Resident tiles (X, Y) of a unit and two rings: tiles that live long (A: keys in k_xdq, queries in k_xdkv) and tiles that one
 // product reads (B: values, or output gradients, which two read).
 template <int D>
 struct BwdSmem {
     static constexpr int KC = D / 64;
     static constexpr int TILE = KC * 16384;
     static constexpr int RA = D == 128 ? 3 : 4, RB = D == 128 ? 2 : 4;
-    static constexpr int OFF_X = 0, OFF_Y = TILE, OFF_A = 2 * TILE, OFF_B = OFF_A + RA * TILE;
+    static constexpr int RX = D == 128 ? 1 : 2;          // pairs of resident tiles: the next unit's land early (1588 -> 1540 us)
+    static constexpr int OFF_Y = TILE, OFF_A = RX * 2 * TILE, OFF_B = OFF_A + RA * TILE;
     static constexpr int OFF_STAT = OFF_B + RB * TILE;   // k_xdkv: [2][256] floats
     static constexpr int OFF_BAR = OFF_STAT + 2048;
     static constexpr int TOTAL = OFF_BAR + 512;
@@ -158,8 +159,8 @@ struct BwdSmem {
 // barriers; XB_XYE: the resident tiles may be overwritten; XB_UF, XB_UE: units handed out; XB_DS: two in k_xdq, where the
 // softmax warps may be done with the next tile before the MMA warp looks for this one (modelled in the tests)
 enum {
-    XB_XY = 0, XB_XYE, XB_S, XB_DP = XB_S + 2, XB_PF, XB_DS, XB_ACC = XB_DS + 2, XB_STF, XB_STE = XB_STF + 2, XB_UF = XB_STE + 2,
-    XB_UE = XB_UF + 2, XB_RING = XB_UE + 2
+    XB_XY = 0, XB_XYE = XB_XY + 2, XB_S = XB_XYE + 2, XB_DP = XB_S + 2, XB_PF, XB_DS, XB_ACC = XB_DS + 2,
+    XB_STF, XB_STE = XB_STF + 2, XB_UF = XB_STE + 2, XB_UE = XB_UF + 2, XB_RING = XB_UE + 2
 };
 // arrivals that complete a phase: one a softmax warp; every reader's for the units; one of everything else
 __device__ __forceinline__ int bwd_arrivals(int i) {
@@ -329,6 +330,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     using L = BwdSmem<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
+    const Ring rx = {bars + XB_XY, bars + XB_XYE, L::RX};
     const Ring ra = {bars + XB_RING, bars + XB_RING + L::RA, L::RA};
     const Ring rb = {ra.empty + L::RA, ra.empty + L::RA + L::RB, L::RB};
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rb.empty + L::RB);
@@ -393,13 +395,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     ++i;
                     return true;
                 };
-                ok = lx == 0 || tc::mbar_wait(&bars[XB_XYE], (lx - 1) & 1, abort_flag, kXWaitNs);
+                ok = ring_wait_free(rx, lx, abort_flag);
                 if (!ok) break;
-                tc::mbar_arrive_expect_tx(&bars[XB_XY], 2 * qbytes);
+                const int x = lx % L::RX;
+                tc::mbar_arrive_expect_tx(&rx.full[x], 2 * qbytes);
                 for (int c = 0; c < L::KC; ++c) {
                     const int row = w.seq.q0 + w.first;
-                    tc::tma_load_3d(smem + L::OFF_X + c * 16384, &map_q, c * 64, w.head * G, row, &bars[XB_XY]);
-                    tc::tma_load_3d(smem + L::OFF_Y + c * 16384, &map_dy, c * 64, w.head * G, row, &bars[XB_XY]);
+                    tc::tma_load_3d(smem + x * 2 * L::TILE + c * 16384, &map_q, c * 64, w.head * G, row, &rx.full[x]);
+                    tc::tma_load_3d(smem + x * 2 * L::TILE + L::OFF_Y + c * 16384, &map_dy, c * 64, w.head * G, row, &rx.full[x]);
                 }
                 ++lx;
                 // keys run one tile ahead of values, as the MMA warp takes them
@@ -410,7 +413,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
             }
             if (!ok) fail();
-            bool drained = tc::drain_armed(&bars[XB_XY], lx, kXWaitNs);
+            bool drained = ring_drain(rx, lx);
             drained = ring_drain(ra, la) && drained;
             drained = ring_drain(rb, lb) && drained;
             if (!drained) fail();
@@ -419,24 +422,25 @@ __global__ void __launch_bounds__(kXThreads, 1)
         // ------------------------------------------------------ MMA issuer
         constexpr uint32_t id_s = tc::idesc_f16(kXRows, kXRows, !kFp16, false, false);
         constexpr uint32_t id_q = tc::idesc_f16(kXRows, D, !kFp16, false, true);
+        bool ok = true;
+        int g = 0, nonempty = 0;
+        auto resident = [&]() { return sbase + nonempty % L::RX * 2 * L::TILE; };
         auto issue_s = [&](int g) {
-            mma_abt<D, kXRows>(tmem + (g & 1) * 128, sbase + L::OFF_X, sbase + L::OFF_A + g % L::RA * L::TILE, id_s);
+            mma_abt<D, kXRows>(tmem + (g & 1) * 128, resident(), sbase + L::OFF_A + g % L::RA * L::TILE, id_s);
             tc::mma_commit_warp(&bars[XB_S + (g & 1)]);
         };
         auto issue_dp = [&](int g) {
-            mma_abt<D, kXRows>(tmem + 256, sbase + L::OFF_Y, sbase + L::OFF_B + g % L::RB * L::TILE, id_s);
+            mma_abt<D, kXRows>(tmem + 256, resident() + L::OFF_Y, sbase + L::OFF_B + g % L::RB * L::TILE, id_s);
             tc::mma_commit_warp(&bars[XB_DP]);
             tc::mma_commit_warp(&rb.empty[g % L::RB]);
         };
-        bool ok = true;
-        int g = 0, nonempty = 0;
         for (int k = 0; ok; ++k) {
             Work w;
             ok = units.read(k, abort_flag, lane, &w);
             if (!ok || w.n < 0) break;
             const int n = w.n;
             if (n == 0) continue;
-            ok = warp_wait(abort_flag, Phase{&bars[XB_XY], (uint32_t)nonempty & 1u}, ra.landed(g));
+            ok = warp_wait(abort_flag, rx.landed(nonempty), ra.landed(g));
             if (!ok) break;
             tc::tc_fence_after();
             issue_s(g);
@@ -448,7 +452,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 if (!ok) break;
                 issue_s(g + 1);
             } else {
-                tc::mma_commit_warp(&bars[XB_XYE]);
+                tc::mma_commit_warp(&rx.empty[nonempty % L::RX]);
             }
             for (int i = 0; i < n; ++i, ++g) {
                 // the next dP once this one has been read, then this tile's dQ, then the scores two tiles on
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     if (!ok) break;
                     tc::tc_fence_after();
                     issue_dp(g + 1);
-                    if (i + 2 == n) tc::mma_commit_warp(&bars[XB_XYE]);
+                    if (i + 2 == n) tc::mma_commit_warp(&rx.empty[nonempty % L::RX]);
                 }
                 const Phase ds{&bars[XB_DS + (g & 1)], (uint32_t)(g >> 1) & 1u};
                 ok = i + 2 < n ? warp_wait(abort_flag, ds, ra.landed(g + 2)) : warp_wait(abort_flag, ds);
@@ -574,6 +578,17 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     tc::tc_fence_after();
                     ok = i < partial ? tile(std::false_type{}, i) : tile(std::true_type{}, i);
                 }
+            }
+            // beside the last product: the places of this unit's rows, and the next unit (they took 600 of a unit's 5400 cycles
+            // after it, with one tile a unit)
+            const int piece = w.piece;
+            const bool pad = (n == 0 && piece < 0) || w.first + my_tok >= w.seq.qlen;
+            RowStore<kFp16> rows;
+            if (ns == 1 && ok) {
+                rows.rows(piece == -2 ? -1 : place(my_tok, my_head), lane);
+                begin(k + 1);
+            }
+            if (n > 0) {
                 if (ok) ok = warp_wait(abort_flag, Phase{&bars[XB_ACC], (uint32_t)nonempty & 1u});
                 ++nonempty;
                 tc::tc_fence_after();
@@ -581,11 +596,6 @@ __global__ void __launch_bounds__(kXThreads, 1)
             if (ns > 1 || !ok) break;                    // stored below
             // -------------------------------------------------- epilogue
             const float f = A.scale * (kFp16 ? exp2f(-up) : 1.f);
-            const int piece = w.piece;
-            const bool pad = (n == 0 && piece < 0) || w.first + my_tok >= w.seq.qlen;
-            RowStore<kFp16> rows;
-            rows.rows(piece == -2 ? -1 : place(my_tok, my_head), lane);
-            begin(k + 1);
             auto sums = [&](int j, float *y) {
                 if (n > 0) {
                     tmem_ld32(trow + 384 + h * (D / 2) + j, reinterpret_cast<uint32_t *>(y));
@@ -673,6 +683,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     constexpr float kShift = kFp16 ? kGradShiftF16 : 0.f;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
+    const Ring rx = {bars + XB_XY, bars + XB_XYE, L::RX};
     const Ring ra = {bars + XB_RING, bars + XB_RING + L::RA, L::RA};
     const Ring rb = {ra.empty + L::RA, ra.empty + L::RA + L::RB, L::RB};
     const Ring rs = {bars + XB_STF, bars + XB_STE, 2};
@@ -744,13 +755,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     ++i;
                     return true;
                 };
-                ok = lx == 0 || tc::mbar_wait(&bars[XB_XYE], (lx - 1) & 1, abort_flag, kXWaitNs);
+                ok = ring_wait_free(rx, lx, abort_flag);
                 if (!ok) break;
-                tc::mbar_arrive_expect_tx(&bars[XB_XY], 2 * L::TILE);
+                const int x = lx % L::RX;
+                tc::mbar_arrive_expect_tx(&rx.full[x], 2 * L::TILE);
                 for (int c = 0; c < L::KC; ++c) {
                     const int row = w.seq.k0 + w.first;
-                    tc::tma_load_3d(smem + L::OFF_X + c * 16384, &map_k, c * 64, w.head, row, &bars[XB_XY]);
-                    tc::tma_load_3d(smem + L::OFF_Y + c * 16384, &map_v, c * 64, w.head, row, &bars[XB_XY]);
+                    tc::tma_load_3d(smem + x * 2 * L::TILE + c * 16384, &map_k, c * 64, w.head, row, &rx.full[x]);
+                    tc::tma_load_3d(smem + x * 2 * L::TILE + L::OFF_Y + c * 16384, &map_v, c * 64, w.head, row, &rx.full[x]);
                 }
                 ++lx;
                 for (int i = 0; i < w.n && ok; ++i) {
@@ -766,7 +778,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
             }
             if (!ok) fail();
-            bool drained = tc::drain_armed(&bars[XB_XY], lx, kXWaitNs);
+            bool drained = ring_drain(rx, lx);
             drained = ring_drain(ra, la) && drained;
             drained = ring_drain(rb, lb) && drained;
             drained = ring_drain(rs, ls) && drained;
@@ -795,18 +807,19 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
                 tc::tc_fence_after();
             };
+            const uint32_t resident = sbase + nonempty % L::RX * 2 * L::TILE;
             auto issue_s = [&](int i, int gi) {
                 clear(L::OFF_A, gi % L::RA, i);
-                mma_abt<D, kXRows>(tmem, sbase + L::OFF_X, sbase + L::OFF_A + (gi % L::RA) * L::TILE, id_s);
+                mma_abt<D, kXRows>(tmem, resident, sbase + L::OFF_A + (gi % L::RA) * L::TILE, id_s);
                 tc::mma_commit_warp(&bars[XB_S]);
             };
             auto issue_dp = [&](int i, int gi) {
                 clear(L::OFF_B, gi % L::RB, i);
-                mma_abt<D, kXRows>(tmem + 128, sbase + L::OFF_Y, sbase + L::OFF_B + (gi % L::RB) * L::TILE, id_s);
+                mma_abt<D, kXRows>(tmem + 128, resident + L::OFF_Y, sbase + L::OFF_B + (gi % L::RB) * L::TILE, id_s);
                 tc::mma_commit_warp(&bars[XB_DP]);
-                if (i + 1 == n) tc::mma_commit_warp(&bars[XB_XYE]);
+                if (i + 1 == n) tc::mma_commit_warp(&rx.empty[nonempty % L::RX]);
             };
-            ok = warp_wait(abort_flag, Phase{&bars[XB_XY], (uint32_t)nonempty & 1u}, ra.landed(g));
+            ok = warp_wait(abort_flag, rx.landed(nonempty), ra.landed(g));
             if (!ok) break;
             issue_s(0, g);
             ok = warp_wait(abort_flag, rb.landed(g));
@@ -941,6 +954,15 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     tc::tc_fence_after();
                     ok = all ? tile(std::false_type{}) : tile(std::true_type{});
                 }
+            }
+            // beside the last product: the places of this unit's rows, and the next unit
+            const int piece = w.piece;
+            RowStore<kFp16> rows;
+            if (ns == 1 && ok) {
+                rows.rows(piece == -2 ? -1 : out(r), lane);
+                begin(turn + 1);
+            }
+            if (n > 0) {
                 if (ok) ok = warp_wait(abort_flag, Phase{&bars[XB_ACC], (uint32_t)nonempty & 1u});
                 ++nonempty;
                 tc::tc_fence_after();
@@ -948,10 +970,6 @@ __global__ void __launch_bounds__(kXThreads, 1)
             if (ns > 1 || !ok) break;                    // stored below
             // -------------------------------------------------- epilogue: warps 0-3 dV, warps 4-7 dK
             const float f = h ? A.scale * (kFp16 ? exp2f(-up) : 1.f) : fv;
-            const int piece = w.piece;
-            RowStore<kFp16> rows;
-            rows.rows(piece == -2 ? -1 : out(r), lane);
-            begin(turn + 1);
             auto sums = [&](int j, float *y) {
                 if (n > 0) {
                     tmem_ld32(trow + 256 + h * 128 + j, reinterpret_cast<uint32_t *>(y));

@@ -122,9 +122,9 @@ def _mma_tile(m, reads, place, tag):
         first = False
 
 
-def _gradient_q(seed, units, ra_n, rb_n, ds_bars):
+def _gradient_q(seed, units, ra_n, rb_n, rx_n, ds_bars):
     m = _Model(seed, {"pf": WARPS, "ds": WARPS})
-    ra, rb = _Ring(m, "k", ra_n), _Ring(m, "v", rb_n)
+    ra, rb, rx = _Ring(m, "k", ra_n), _Ring(m, "v", rb_n), _Ring(m, "x", rx_n)
 
     def ds(g):
         return (("ds", g % ds_bars), (g // ds_bars) & 1)
@@ -132,8 +132,8 @@ def _gradient_q(seed, units, ra_n, rb_n, ds_bars):
     def producer():
         la = lb = 0
         for u, n in enumerate(units):
-            yield ((("xye", 0), (u - 1) & 1),) if u else ()
-            m.load(("xy", 0), "x", u)
+            yield rx.free(u)
+            rx.load(u, u)
             yield ra.free(la)
             ra.load(la, la)
             la += 1
@@ -148,17 +148,17 @@ def _gradient_q(seed, units, ra_n, rb_n, ds_bars):
 
     def mma():
         def issue_s(g, u):
-            _mma_tile(m, {"x": u, ("k", g % ra_n): g}, ("s", g & 1), ("s", g))
+            _mma_tile(m, {("x", u % rx_n): u, ("k", g % ra_n): g}, ("s", g & 1), ("s", g))
             m.commit(("s", g & 1))
 
         def issue_dp(g, u):
-            _mma_tile(m, {"x": u, ("v", g % rb_n): g}, "dp", ("dp", g))
+            _mma_tile(m, {("x", u % rx_n): u, ("v", g % rb_n): g}, "dp", ("dp", g))
             m.commit(("dp", 0))
             rb.release(g)
 
         g = 0
         for u, n in enumerate(units):
-            yield ((("xy", 0), u & 1), ra.landed(g))
+            yield (rx.landed(u), ra.landed(g))
             issue_s(g, u)
             yield (rb.landed(g),)
             issue_dp(g, u)
@@ -166,13 +166,13 @@ def _gradient_q(seed, units, ra_n, rb_n, ds_bars):
                 yield (ra.landed(g + 1),)
                 issue_s(g + 1, u)
             else:
-                m.commit(("xye", 0))
+                rx.release(u)
             for i in range(n):
                 if i + 1 < n:
                     yield ((("pf", 0), g & 1), rb.landed(g + 1))
                     issue_dp(g + 1, u)
                     if i + 2 == n:
-                        m.commit(("xye", 0))
+                        rx.release(u)
                 yield (ds(g), ra.landed(g + 2)) if i + 2 < n else (ds(g),)
                 m.mma(_halves(m, ("s", g & 1), ("ds", g)) | {("k", g % ra_n): g}, "dq", u)
                 ra.release(g)
@@ -200,15 +200,15 @@ def _gradient_q(seed, units, ra_n, rb_n, ds_bars):
     return m.run(dict({w: softmax(w) for w in range(WARPS)}, producer=producer(), mma=mma()))
 
 
-def _gradient_kv(seed, units, ra_n, rb_n):
+def _gradient_kv(seed, units, ra_n, rb_n, rx_n):
     m = _Model(seed, {"pf": WARPS, "ds": WARPS, "st_empty": WARPS})
-    ra, rb, rs = _Ring(m, "q", ra_n), _Ring(m, "dy", rb_n), _Ring(m, "st", 2)
+    ra, rb, rs, rx = _Ring(m, "q", ra_n), _Ring(m, "dy", rb_n), _Ring(m, "st", 2), _Ring(m, "x", rx_n)
 
     def producer():
         g = 0
         for u, n in enumerate(units):
-            yield ((("xye", 0), (u - 1) & 1),) if u else ()
-            m.load(("xy", 0), "x", u)
+            yield rx.free(u)
+            rx.load(u, u)
             for _ in range(n):
                 yield ra.free(g)
                 ra.load(g, g)
@@ -220,18 +220,18 @@ def _gradient_kv(seed, units, ra_n, rb_n):
 
     def mma():
         def issue_s(g, u):
-            _mma_tile(m, {"x": u, ("q", g % ra_n): g}, "s", ("s", g))
+            _mma_tile(m, {("x", u % rx_n): u, ("q", g % ra_n): g}, "s", ("s", g))
             m.commit(("s", 0))
 
         def issue_dp(g, u, last):
-            _mma_tile(m, {"x": u, ("dy", g % rb_n): g}, "dp", ("dp", g))
+            _mma_tile(m, {("x", u % rx_n): u, ("dy", g % rb_n): g}, "dp", ("dp", g))
             m.commit(("dp", 0))
             if last:
-                m.commit(("xye", 0))
+                rx.release(u)
 
         g = 0
         for u, n in enumerate(units):
-            yield ((("xy", 0), u & 1), ra.landed(g))
+            yield (rx.landed(u), ra.landed(g))
             issue_s(g, u)
             yield (rb.landed(g),)
             issue_dp(g, u, n == 1)
@@ -344,19 +344,19 @@ def _forward(seed, n, stages, bufs, halves):
     return m.run(dict({w: softmax(w) for w in range(WARPS)}, producer=producer(), mma=mma()))
 
 
-@pytest.mark.parametrize("ra,rb", [(3, 2), (4, 4)])
+@pytest.mark.parametrize("ra,rb,rx", [(3, 2, 1), (4, 4, 2)])
 @pytest.mark.parametrize("units", [[1], [2], [5], [1, 2, 3, 1, 4], [2, 2, 1, 7]])
-def test_gradient_hand_offs(ra, rb, units):
+def test_gradient_hand_offs(ra, rb, rx, units):
     for seed in range(60):
-        assert _gradient_q(seed, units, ra, rb, 2) == "ok"
-        assert _gradient_kv(seed, units, ra, rb) == "ok"
+        assert _gradient_q(seed, units, ra, rb, rx, 2) == "ok"
+        assert _gradient_kv(seed, units, ra, rb, rx) == "ok"
 
 
 def test_one_barrier_for_two_ds_tiles_fails():
     ends = set()
     for seed in range(300):
         try:
-            ends.add(_gradient_q(seed, [5], 3, 2, 1).split(":")[0])
+            ends.add(_gradient_q(seed, [5], 3, 2, 1, 1).split(":")[0])
         except AssertionError:
             ends.add("wrong tile")      # warps arrive for the next tile in place of slower ones
     assert ends == {"ok", "blocked", "wrong tile"}
