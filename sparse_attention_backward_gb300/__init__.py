@@ -499,12 +499,15 @@ class ScaIo(ctypes.Structure):
 
 
 _neighbours = None
+_torch = None       # the module, for calls that take microseconds: an import statement costs a quarter of one
 
 
 def _lib_neighbours():
-    global _neighbours
+    global _neighbours, _torch
     if _neighbours is not None:
         return _neighbours
+    import torch
+    _torch = torch
     lib = load()
     vp, sz = ctypes.c_void_p, ctypes.c_size_t
     dbl, psz = ctypes.c_double, ctypes.POINTER(ctypes.c_size_t)
@@ -597,8 +600,7 @@ def _dense(name, t, device, shape, dtype):
 
 def _new(like):
     """A dense tensor of the same shape, type and device."""
-    import torch
-    return torch.empty_like(like, memory_format=torch.contiguous_format)
+    return _torch.empty_like(like, memory_format=_torch.contiguous_format)
 
 
 def _with(desc, **fields):
@@ -615,14 +617,13 @@ def _with(desc, **fields):
 def _launch(device, stream, call):
     """call(raw stream) with the tensors' device current; what the call
     allocates comes from the pool of the stream that it runs on."""
-    import torch
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _torch.cuda.stream(stream):
             return call(stream.cuda_stream)
-    if torch._C._cuda_getDevice() != device:
-        with torch.cuda.device(device):
-            return call(torch.cuda.current_stream().cuda_stream)
-    return call(torch._C._cuda_getCurrentRawStream(device))   # a stream object costs several microseconds
+    if _torch._C._cuda_getDevice() != device:
+        with _torch.cuda.device(device):
+            return call(_torch.cuda.current_stream().cuda_stream)
+    return call(_torch._C._cuda_getCurrentRawStream(device))   # a stream object costs several microseconds
 
 
 class Rotary:
@@ -683,24 +684,25 @@ def rotary_workspace_size(desc: SrtDesc) -> int:
 
 
 def _rotary(entry, q, k, rotary, cu_seqlens, positions, out, workspace, stream, desc):
-    import torch
     if not q.is_cuda:
         raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
-    n1, d = q.shape[-2:]
+    shape = q.shape
+    n1, d = shape[-2:]
     n2 = k.shape[-2] if k is not None else 0
     if desc is None:
         bsnd = q.dim() == 4
         desc = make_rotary_desc(rotary, cu_seqlens, n1, n2, d, _sag_dtype(q), SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND,
-                                q.shape[1] if bsnd else 0)
+                                shape[1] if bsnd else 0)
     qs, ks = desc._shapes
     dtype, device = desc._dtype, q.get_device()
-    _check_rows("q", q, qs, dtype)
-    lead = q.shape[:-2]
+    if q.dtype is not dtype or shape != qs:
+        _check_rows("q", q, qs, dtype)
+    lead = shape[:-2]
     if k is not None:
         _check("k", k, device, lead + ks[-2:], dtype)
     elif ks[-2]:
         raise ValueError("the descriptor has a key")
-    pos = _dense("positions", positions, device, lead, torch.int32) if positions is not None else None
+    pos = _dense("positions", positions, device, lead, _torch.int32) if positions is not None else None
 
     def call(handle):
         use = desc
@@ -723,7 +725,7 @@ def _rotary(entry, q, k, rotary, cu_seqlens, positions, out, workspace, stream, 
         if use.batch > 64:          # smaller tables travel with the launch
             need = rotary_workspace_size(use)
             if ws is None or ws.numel() < need:
-                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+                ws = _torch.empty(need, dtype=_torch.uint8, device=q.device)
         st = entry(use, io, ws.data_ptr() if need else None, need, handle)
         if st != SAG_OK:
             raise SagError(st, entry.__name__)
@@ -787,22 +789,25 @@ def cross_query_error(workspace, stream) -> int:
 def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, workspace, stream, check, desc, tensors):
     """Shared by the two directions: ``tensors(io, device, dtype)`` fills in
     the remaining sca_io pointers and gives the outputs."""
-    import torch
     if not q.is_cuda:
         raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
-    n1, d = q.shape[-2:]
-    n2 = k.shape[-2]
+    q_shape, k_shape = q.shape, k.shape
+    n1, d = q_shape[-2:]
+    n2 = k_shape[-2]
     if desc is None:
         bsnd = q.dim() == 4
         if bsnd and k.dim() != 4:
             raise ValueError("BSND needs 4-D query and key tensors")
         desc = make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, _sag_dtype(q),
-                               SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND, q.shape[1] if bsnd else 0,
-                               k.shape[1] if bsnd else 0)
+                               SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND, q_shape[1] if bsnd else 0,
+                               k_shape[1] if bsnd else 0)
     dtype, device = desc._dtype, q.get_device()
-    _check_rows("q", q, desc._shapes[0], dtype)
-    _check_rows("k", k, desc._shapes[1], dtype)
-    _check("v", v, device, k.shape, dtype)
+    qs, ks = desc._shapes
+    if q.dtype is not dtype or q_shape != qs:
+        _check_rows("q", q, qs, dtype)
+    if k.dtype is not dtype or k_shape != ks:
+        _check_rows("k", k, ks, dtype)
+    _check("v", v, device, k_shape, dtype)
     if k.get_device() != device:
         raise ValueError(f"k: on {k.device}, not on {q.device}")
     use = desc
@@ -811,9 +816,9 @@ def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, w
                     v_stride=_row_stride("v", v, n2, d))
     io = ScaIo(q.data_ptr(), k.data_ptr(), v.data_ptr())
     if key_mask is not None:
-        if key_mask.dtype not in (torch.bool, torch.uint8):
+        if key_mask.dtype not in (_torch.bool, _torch.uint8):
             raise ValueError("key_mask must be a bool or uint8 tensor")
-        io.key_mask = _dense("key_mask", key_mask, device, k.shape[:-2], key_mask.dtype)
+        io.key_mask = _dense("key_mask", key_mask, device, k_shape[:-2], key_mask.dtype)
 
     def call(handle):
         outs = tensors(io, device, dtype)
@@ -822,7 +827,7 @@ def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, w
             need = desc.__dict__[size] = size(desc)
         ws = workspace
         if ws is None or ws.numel() < need:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws = _torch.empty(need, dtype=_torch.uint8, device=q.device)
         st = entry(use, io, ws.data_ptr(), need, handle)
         if st == SAG_OK and check:
             st = cross_query_error(ws.data_ptr(), handle)
@@ -845,14 +850,13 @@ def cross_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, ke
     the device status back (this synchronizes the stream).
     """
     def tensors(io, device, dtype):
-        import torch
         if out is None:
-            o, lse = _new(q), torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+            o, lse = _new(q), _torch.empty(q.shape[:-1], dtype=_torch.float32, device=q.device)
             io.attention_out, io.softmax_lse = o.data_ptr(), lse.data_ptr()
         else:
             o, lse = out
             io.attention_out = _dense("attention_out", o, device, q.shape, dtype)
-            io.softmax_lse = _dense("softmax_lse", lse, device, q.shape[:-1], torch.float32)
+            io.softmax_lse = _dense("softmax_lse", lse, device, q.shape[:-1], _torch.float32)
         return o, lse
 
     return _cross(_lib_neighbours().cross_attn_fwd, cross_fwd_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,
@@ -864,10 +868,9 @@ def cross_backward(q, k, v, o, dy, lse, cu_seqlens_q=None, cu_seqlens_kv=None, s
     """Gradient of ``cross_forward``: returns (dq, dk, dv), from the forward's o
     and lse and the gradient dy of o; the other arguments as there."""
     def tensors(io, device, dtype):
-        import torch
         io.attention_out = _dense("o", o, device, q.shape, dtype)
         io.attention_out_grad = _dense("dy", dy, device, q.shape, dtype)
-        io.softmax_lse = _dense("lse", lse, device, q.shape[:-1], torch.float32)
+        io.softmax_lse = _dense("lse", lse, device, q.shape[:-1], _torch.float32)
         if out is None:
             outs = dq, dk, dv = _new(q), _new(k), _new(v)
             io.dq, io.dk, io.dv = dq.data_ptr(), dk.data_ptr(), dv.data_ptr()
