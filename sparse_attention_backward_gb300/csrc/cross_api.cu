@@ -26,6 +26,10 @@ struct XPlan {
     size_t o_seq, o_stats, o_norms, o_parts, o_arrived, total;
 };
 
+// Whether units with loops of `least` to `longest` tiles may be cut (tail_of): below 14 a piece never pays, and short units
+// fill the last round as it is (a ragged padded batch: 155 -> 165 us with pieces).
+bool may_cut(const XPlan &p, int longest, int least) { return !p.padding && longest >= 14 && least * 8 >= longest * 7; }
+
 sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {
     if (!d || !d->cu_seqlens_q || !d->cu_seqlens_kv) return SAG_ERR_NULL;
     if (d->dtype != SAG_BF16 && d->dtype != SAG_FP16) return SAG_ERR_DTYPE;
@@ -72,8 +76,9 @@ sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {
     p->o_norms = take(grad && p->fp16 ? sizeof(unsigned) * 2 * (size_t)d->batch * d->n2 : 0);
     const int64_t most = (p->q_tiles > p->k_tiles ? p->q_tiles : p->k_tiles) * d->n2;
     const int64_t pieces = most < kMaxPieces / kMaxSplit ? most * kMaxSplit : kMaxPieces;
-    p->o_parts = take(grad ? sizeof(float) * 2 * kXRows * d->d * pieces : 0);
-    p->o_arrived = take(grad ? sizeof(unsigned) * 2 * 8 * kMaxPieces : 0);
+    const bool cut = grad && (may_cut(*p, p->max_k, p->min_k) || may_cut(*p, p->max_q, p->min_q));
+    p->o_parts = take(cut ? sizeof(float) * 2 * kXRows * d->d * pieces : 0);
+    p->o_arrived = take(cut ? sizeof(unsigned) * 2 * 8 * kMaxPieces : 0);
     p->total = o;
     return SAG_OK;
 }
@@ -92,12 +97,11 @@ int split_of(int64_t units, int tiles, int room) {
 // Units of a gradient kernel beyond full rounds of the SMs are cut into pieces of their loops if those fill the last round
 // better: `full` whole units, then `pieces` of each other one.  Times in tiles of the loop: a piece costs about six more
 // for its start, its sums' way to the workspace and the last one's adding up, which takes one for each piece.  160 units of
-// 64 tiles: 260 -> 207 us, 512 units of 256 tiles: 2320 -> 2150 us, 320 units of 24 tiles: 190 -> 179 us.  Only where units
-// take alike: short ones fill the last round as it is (a ragged padded batch: 155 -> 165 us).
-void tail_of(int units, int tiles, int least, int sms, int *full, int *pieces) {
+// 64 tiles: 260 -> 207 us, 512 units of 256 tiles: 2320 -> 2150 us, 320 units of 24 tiles: 190 -> 179 us.
+void tail_of(int units, int tiles, int sms, int *full, int *pieces) {
     *full = units;
     *pieces = 1;
-    const int rest = least * 8 >= tiles * 7 ? units % sms : 0;
+    const int rest = units % sms;
     int best = tiles + 1;
     for (int s = 2; s <= kMaxSplit && s <= tiles && rest * s <= kMaxPieces; ++s) {
         const int t = (rest * s + sms - 1) / sms * ((tiles + s - 1) / s + 6) + s;
@@ -251,7 +255,7 @@ extern "C" sag_status cross_attn_grad(const sca_desc *desc, const sca_io *io, vo
         x.units = x.full = units;
         x.nsplit = split_of(units, tiles, sms);
         x.pieces = 1;
-        if (x.nsplit == 1 && !p.padding) tail_of(units, tiles, least, sms, &x.full, &x.pieces);
+        if (x.nsplit == 1 && may_cut(p, tiles, least)) tail_of(units, tiles, sms, &x.full, &x.pieces);
         x.items = x.full + (units - x.full) * x.pieces;
         x.ctas = x.nsplit > 1 ? units * x.nsplit : x.items < sms ? x.items : sms;
         return x;

@@ -208,3 +208,14 @@ def test_cross_arguments():
         sab.cross_forward(x, x, x, [0, 4], [0, 4], 0.1)
     with pytest.raises(ValueError):
         sab.cross_backward(x, x, x, x, x, torch.zeros(4, 2), [0, 4], [0, 4], 0.1)
+
+
+def test_workspace_of_partial_sums():
+    """Only gradients with long, alike loops hold the sums of pieces (304 x 128 KB at most)."""
+    def size(cu1, cu2, **kw):
+        return sab.cross_grad_workspace_size(sab.make_cross_desc(cu1, cu2, 16, 16, 128, 0.1, **kw))
+
+    assert size([0, 1600], [0, 1600]) < 4 << 20
+    assert 304 * (128 << 10) <= size([0, 4096], [0, 4096]) < 304 * (128 << 10) + (8 << 20)
+    assert size([0, 4096, 5000], [0, 4096, 5000]) < 8 << 20
+    assert size([0, 4096, 4096], [0, 4096, 4100], layout=sab.SAG_LAYOUT_BSND, s1_max=4096, s2_max=4096) < 16 << 20
