@@ -123,17 +123,24 @@ def _mma_tile(m, reads, place, tag):
 
 
 def _gradient_q(seed, units, ra_n, rb_n, rx_n, ds_bars):
-    m = _Model(seed, {"pf": WARPS, "ds": WARPS})
-    ra, rb, rx = _Ring(m, "k", ra_n), _Ring(m, "v", rb_n), _Ring(m, "x", rx_n)
+    """`units`: tiles of each, 0 without work."""
+    m = _Model(seed, {"pf": WARPS, "ds": WARPS, "unit_empty": WARPS + 1})
+    ra, rb, rx, ru = _Ring(m, "k", ra_n), _Ring(m, "v", rb_n), _Ring(m, "x", rx_n), _Ring(m, "unit", 2)
+    units = units + [-1]
 
     def ds(g):
         return (("ds", g % ds_bars), (g // ds_bars) & 1)
 
     def producer():
-        la = lb = 0
-        for u, n in enumerate(units):
+        la = lb = u = 0
+        for k, n in enumerate(units):
+            yield ru.free(k)
+            m.arrive(("unit_full", k % 2))
+            if n <= 0:
+                continue
             yield rx.free(u)
             rx.load(u, u)
+            u += 1
             yield ra.free(la)
             ra.load(la, la)
             la += 1
@@ -156,8 +163,12 @@ def _gradient_q(seed, units, ra_n, rb_n, rx_n, ds_bars):
             m.commit(("dp", 0))
             rb.release(g)
 
-        g = 0
-        for u, n in enumerate(units):
+        g = u = 0
+        for k, n in enumerate(units):
+            yield (ru.landed(k),)
+            m.arrive(("unit_empty", k % 2))
+            if n <= 0:
+                continue
             yield (rx.landed(u), ra.landed(g))
             issue_s(g, u)
             yield (rb.landed(g),)
@@ -180,10 +191,17 @@ def _gradient_q(seed, units, ra_n, rb_n, rx_n, ds_bars):
                     issue_s(g + 2, u)
                 g += 1
             m.commit(("acc", 0))
+            u += 1
 
     def softmax(w):
-        g = 0
-        for u, n in enumerate(units):
+        g = u = 0
+
+        def begin(k):
+            yield (ru.landed(k),)
+            m.arrive(("unit_empty", k % 2))
+
+        yield from begin(0)
+        for k, n in enumerate(units[:-1]):
             for _ in range(n):
                 yield ((("s", g & 1), (g >> 1) & 1),)
                 m.check((("s", g & 1), w), ("s", g))
@@ -194,8 +212,12 @@ def _gradient_q(seed, units, ra_n, rb_n, rx_n, ds_bars):
                 m.mem[(("s", g & 1), w)] = ("ds", g)
                 m.arrive(ds(g)[0])
                 g += 1
-            yield ((("acc", 0), u & 1),)
-            m.check("dq", u)
+            yield from begin(k + 1)
+            if n:
+                yield ((("acc", 0), u & 1),)
+                yield ()                        # stores
+                m.check("dq", u)
+                u += 1
 
     return m.run(dict({w: softmax(w) for w in range(WARPS)}, producer=producer(), mma=mma()))
 
@@ -267,6 +289,7 @@ def _gradient_kv(seed, units, ra_n, rb_n, rx_n):
                 m.arrive(("st_empty", g % 2))
                 g += 1
             yield ((("acc", 0), u & 1),)
+            yield ()
             m.check("dv", u)
             m.check("dk", u)
 
@@ -345,11 +368,21 @@ def _forward(seed, n, stages, bufs, halves):
 
 
 @pytest.mark.parametrize("ra,rb,rx", [(3, 2, 1), (4, 4, 2)])
-@pytest.mark.parametrize("units", [[1], [2], [5], [1, 2, 3, 1, 4], [2, 2, 1, 7]])
+@pytest.mark.parametrize("units", [[1], [2], [5], [1, 2, 3, 1, 4], [2, 2, 1, 7], [1] * 9])
 def test_gradient_hand_offs(ra, rb, rx, units):
     for seed in range(60):
         assert _gradient_q(seed, units, ra, rb, rx, 2) == "ok"
         assert _gradient_kv(seed, units, ra, rb, rx) == "ok"
+
+
+EMPTY = [[0], [0, 0, 0], [1, 0, 0, 0, 0, 1], [0, 3, 0, 0, 0, 2, 1, 0, 0, 0, 0], [1, 1, 0, 0, 0, 0, 1, 1, 0, 1]]
+
+
+@pytest.mark.parametrize("ra,rb,rx", [(3, 2, 1), (4, 4, 2)])
+@pytest.mark.parametrize("units", EMPTY)
+def test_units_without_work(ra, rb, rx, units):
+    for seed in range(60):
+        assert _gradient_q(seed, units, ra, rb, rx, 2) == "ok"
 
 
 def test_one_barrier_for_two_ds_tiles_fails():
