@@ -1,4 +1,5 @@
-// Cross attention, gradient: three launches, no fp32 accumulators in memory, no
+// Cross attention, gradient: three launches, no fp32 accumulators in memory (but
+// for the sums of a cut unit's pieces), no
 // atomics but a maximum, tickets and counters, so the same bits on every run.
 //
 //   k_xpre  Delta = rowsum(dY * O) and lse in log2 units, packed by query tile
