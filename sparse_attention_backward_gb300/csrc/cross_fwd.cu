@@ -390,12 +390,14 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
 #pragma unroll
                 for (int o = kMaxSplit / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 top = __shfl_sync(0xffffffffu, top, 0);
+                // A rank that saw something counts even where its weight underflows: 0 times its NaN is NaN, as in an undivided
+                // loop.  (A rank of NaN scores alone has -inf and NaN.)
                 const float w = v.y == 0.f ? 0.f : xex2(v.x - top);
                 float sum = 0.f;
 #pragma unroll
                 for (int p = 0; p < kMaxSplit; ++p) {
                     const float wp = __shfl_sync(0xffffffffu, w, p), lp = __shfl_sync(0xffffffffu, v.y, p);
-                    if (wp == 0.f) continue;
+                    if (lp == 0.f) continue;
                     sum += lp * wp;
 #pragma unroll
                     for (int e = 0; e < E; ++e) {

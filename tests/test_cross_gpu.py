@@ -363,3 +363,30 @@ def test_pieces_without_work():
     c.mask[1024:] = False
     c.k[1024:], c.v[1024:] = float("nan"), float("inf")
     run(c)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (HF, 64), (BF, 128), (HF, 128)])
+@pytest.mark.parametrize("what", ["states", "far", "value"])
+@pytest.mark.parametrize("l1,l2,first,last", [
+    ([3], [64], 16, 37), ([3], [577], 144, 336), ([3], [577], 128, 192), ([130], [577], 128, 192), ([256], [4097], 1024, 2048)])
+def test_nan_in_states_that_are_there(dtype, d, what, l1, l2, first, last):
+    # loops split over a cluster, where in the last three cases some CTAs see these states and no others: every score is NaN
+    # ("states"), or one is and the others lie so far below the maximum that their share underflows ("far"), or a column of V
+    # is NaN there ("value")
+    c = Case(l1, l2, 4, 2, d, dtype, seed=31)
+    there = slice(first, last)
+    c.q, c.k = torch.ones_like(c.q), torch.zeros_like(c.k)
+    if what != "states":
+        c.k[there] = -20.0          # scores of -20 sqrt(d): 2^-230 of the others and less
+    if what == "value":
+        c.v[there, :, 5] = float("nan")
+    else:
+        c.k[there if what == "states" else first, 0] = float("nan")
+    o, lse = sab.cross_forward(c.q.cuda(), c.k.cuda(), c.v.cuda(), c.cu1, c.cu2, c.scale, check=True)
+    wo, wl, mag = c.forward()
+    o, lse = o.cpu(), lse.cpu()
+    assert torch.equal(lse.isnan(), wl.isnan()) and torch.equal(o.isnan(), wo.isnan())
+    assert bool(wo.isnan().any()) and not bool(wo.isnan().all())
+    u = torch.finfo(dtype).eps / 2
+    _within("o", o.nan_to_num(0.0), wo.nan_to_num(0.0), (u + S32) * mag.nan_to_num(0.0), dtype)
+    assert bool(((lse - wl).nan_to_num(0.0).abs() <= S32 + 2.0 ** -20 * wl.nan_to_num(0.0).abs()).all())
