@@ -44,6 +44,7 @@ struct XArgs {
     float *lse;                         // forward: written, gradient: read
     float *stats;                       // [query tile][n2][256]: lse * log2(e), then Delta, of the tile's 128 rows
     unsigned *norms;                    // fp16: [batch][n2][2] largest squared row norms of dY and of V, as float bits
+    float *row_norms;                   // fp16: [query tile][n2][128] squared norms of the rows of dY
     int32_t q_tiles, k_tiles;
     int32_t *count, *status;            // device status: number of words, one word for each CTA
     int32_t n_status;                   // value for *count

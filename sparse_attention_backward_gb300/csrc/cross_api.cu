@@ -23,7 +23,7 @@ struct XPlan {
     int max_q, max_k;                       // most query / key tiles of one sequence that have work
     int min_q, min_k;                       // fewest
     bool padding;                           // some tiles are padding
-    size_t o_seq, o_stats, o_norms, o_parts, o_arrived, total;
+    size_t o_seq, o_stats, o_norms, o_row_norms, o_parts, o_arrived, total;
 };
 
 // Whether units with loops of `least` to `longest` tiles may be cut (tail_of): below 14 a piece never pays, and short units
@@ -74,6 +74,7 @@ sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {
     p->o_seq = take(seq_ws_bytes(d->batch));
     p->o_stats = take(grad ? sizeof(float) * 256 * p->q_tiles * d->n2 : 0);
     p->o_norms = take(grad && p->fp16 ? sizeof(unsigned) * 2 * (size_t)d->batch * d->n2 : 0);
+    p->o_row_norms = take(grad && p->fp16 ? sizeof(float) * kXRows * p->q_tiles * d->n2 : 0);
     const int64_t most = (p->q_tiles > p->k_tiles ? p->q_tiles : p->k_tiles) * d->n2;
     const int64_t pieces = most < kMaxPieces / kMaxSplit ? most * kMaxSplit : kMaxPieces;
     const bool cut = grad && (may_cut(*p, p->max_k, p->min_k) || may_cut(*p, p->max_q, p->min_q));
@@ -135,6 +136,7 @@ XArgs x_args(const sca_desc *d, const sca_io *io, const XPlan &p, char *ws) {
     a.lse = io->softmax_lse;
     a.stats = reinterpret_cast<float *>(ws + p.o_stats);
     a.norms = reinterpret_cast<unsigned *>(ws + p.o_norms);
+    a.row_norms = reinterpret_cast<float *>(ws + p.o_row_norms);
     a.parts = reinterpret_cast<float *>(ws + p.o_parts);
     a.arrived = reinterpret_cast<unsigned *>(ws + p.o_arrived);
     a.q_tiles = (int)p.q_tiles;

@@ -17,9 +17,13 @@
 // warp: exp beside dK and the next dP, dS beside dV and the next S.
 //
 // P and dS are rounded to the 16-bit type as operands; fp16 ones are scaled by
-// powers of two first (cross.cuh), dS by one found from the largest norms of
-// dY and V rows of the sequence and head: |dP - Delta| <= 2 |dY| |V|, so that
-// neither a loss scale overflows nor a long softmax vanishes.
+// powers of two first (cross.cuh), so that neither a loss scale overflows nor a
+// long softmax vanishes.  |dP - Delta| <= 2 |dY| max|V| gives the one of dS.  In
+// k_xdq each query row has its own, from its dY: with one for the sequence, rows
+// of small dY lost their bits to subnormals (30000 states, dY 2^-18 of the
+// largest: dQ off by 12 %, now by 0.03 %; 1500 states: 0.6 %).  k_xdkv sums over
+// the rows of a sequence, where the largest count most, and takes one exponent
+// from the largest |dY|.
 //
 // A CTA (one per SM) walks over units, so that the next unit's tiles land and
 // its first products run beside the last one's stores.  Few units: a cluster's
@@ -95,6 +99,7 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
                 const bool some = live && lse != -INFINITY;
                 st[r] = some ? -lse * kLog2e : -INFINITY;   // makes P = 0 where there is nothing
                 st[128 + r] = some ? -dot : 0.f;
+                if constexpr (kFp16) A.row_norms[u.tile_id * kXRows + r] = nrm;
             }
             if (nrm < INFINITY) top = fmaxf(top, nrm);
         }
@@ -133,14 +138,14 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
     }
 }
 
-// fp16: exponent e such that 2^e |dS| <= 2^15 for every dS of a sequence and head.
-__device__ __forceinline__ float ds_exponent(uint2 norms) {
-    const float bound = 2.f * sqrtf(__uint_as_float(norms.x)) * sqrtf(__uint_as_float(norms.y));
+// fp16: exponent e such that 2^e |dS| <= 2^15 for every dS of rows of dY and V whose largest squared norms are given.
+__device__ __forceinline__ float ds_exponent(float dy, float v) {
+    const float bound = 2.f * sqrtf(dy) * sqrtf(v);
     if (!(bound > 0.f) || !(bound < INFINITY)) return 0.f;
     return fminf(fmaxf(14.f - (float)ilogbf(bound), -40.f), 40.f);
 }
-__device__ __forceinline__ uint2 ds_norms(const XArgs &A, int b, int head) {
-    return *reinterpret_cast<const uint2 *>(A.norms + ((int64_t)b * A.n2 + head) * 2);
+__device__ __forceinline__ float2 ds_norms(const XArgs &A, int b, int head) {
+    return *reinterpret_cast<const float2 *>(A.norms + ((int64_t)b * A.n2 + head) * 2);
 }
 
 // ------------------------------------------------------------------- shared
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const int r = (warp & 3) * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     Work w{};
-    float up = 0.f;                                      // exponent that dS is scaled by
+    float up = 0.f;                                      // exponent that the row's dS is scaled by
     auto place = [&](int tok_in, int head_in) -> int64_t {   // place of a row (token and head in the tile) in dQ
         const int tok = w.first + tok_in;
         if (tok_in >= A.tpt || tok >= (A.s1_pad ? A.s1_pad : w.seq.qlen)) return -1;
@@ -505,18 +510,19 @@ __global__ void __launch_bounds__(kXThreads, 1)
         int g = 0, nonempty = 0;
         // the next unit's statistics are on their way while this one is stored
         float st_nl = 0.f, st_nd = 0.f;
-        uint2 norms{};
+        float2 norms{};
         auto begin = [&](int k) {
             ok = units.read(k, abort_flag, lane, &w);
             if (!ok || w.n < 0) return;
             st_nl = A.stats[(int64_t)w.stat * 256 + r];
             st_nd = A.stats[(int64_t)w.stat * 256 + 128 + r];
-            if constexpr (kFp16) norms = ds_norms(A, w.b, w.head);
+            if constexpr (kFp16)
+                norms = make_float2(A.row_norms[(int64_t)w.stat * kXRows + r], ds_norms(A, w.b, w.head).y);
         };
         begin(0);
         for (int k = 0; ok && w.n >= 0; ++k) {
             const int n = w.n;
-            if constexpr (kFp16) up = ds_exponent(norms);
+            if constexpr (kFp16) up = ds_exponent(norms.x, norms.y);
             const float nl = st_nl + up, nd = st_nd;
             if (n > 0) {
                 // ---------------------------------------------- softmax
@@ -648,6 +654,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         __syncthreads();                                 // loads and products on this memory are complete
         if (warp < 8) {
             const bool pad = w.n == 0 || w.first + my_tok >= w.seq.qlen;
+            const float down = kFp16 ? exp2f(-up) : 1.f; // of this row, undone before rows change threads
 #pragma unroll
             for (int j = 0; j < D / 2; j += 32) {
                 float y[32];
@@ -658,14 +665,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                     *reinterpret_cast<float4 *>(xo + r * L::XROW + h * (D / 2) + j + e) =
-                        pad ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                        pad ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : make_float4(y[e] * down, y[e + 1] * down, y[e + 2] * down, y[e + 3] * down);
             }
         }
         cluster_sync();
-        if (warp < 8) {
-            const float f = A.scale * (kFp16 ? exp2f(-up) : 1.f);
-            join_rows<kFp16, D>(xo, A.dq, ns, rank, warp, lane, out, f);
-        }
+        if (warp < 8) join_rows<kFp16, D>(xo, A.dq, ns, rank, warp, lane, out, A.scale);
         cluster_sync();                                  // peers are done with this CTA's shared memory
     }
     tc::tc_fence_before();
@@ -873,7 +878,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         int g = 0, nonempty = 0;
         // what the next unit needs from memory is on its way while this one is stored
         bool st_live = false;
-        uint2 norms{};
+        float2 norms{};
         auto begin = [&](int k) {
             ok = units.read(k, abort_flag, lane, &w);
             if (!ok || w.n < 0) return;
@@ -883,7 +888,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         begin(0);
         for (int turn = 0; ok && w.n >= 0; ++turn) {
             const int n = w.n;
-            if constexpr (kFp16) up = ds_exponent(norms);
+            if constexpr (kFp16) up = ds_exponent(norms.x, norms.y);
             const bool live = st_live;
             if (n > 0) {
                 // ---------------------------------------------- softmax

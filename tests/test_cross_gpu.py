@@ -390,3 +390,35 @@ def test_nan_in_states_that_are_there(dtype, d, what, l1, l2, first, last):
     u = torch.finfo(dtype).eps / 2
     _within("o", o.nan_to_num(0.0), wo.nan_to_num(0.0), (u + S32) * mag.nan_to_num(0.0), dtype)
     assert bool(((lse - wl).nan_to_num(0.0).abs() <= S32 + 2.0 ** -20 * wl.nan_to_num(0.0).abs()).all())
+
+
+# a cluster's unit, whole units, pieces
+@pytest.mark.parametrize("l1,l2,n1,n2,d", [([64], [30000], 2, 1, 64), ([640], [1500], 16, 16, 128), ([640], [3001], 32, 16, 128)])
+def test_rows_of_small_output_gradients_in_fp16(l1, l2, n1, n2, d):
+    """dY rows that differ by 2^18 in one sequence: each row of dQ keeps its bits.
+
+    Rounding dS (u of each, independent) gives a row an error of at most u c sqrt(sum_j dS_j^2 |K_j|^2) in the root mean
+    square, the fp32 part s c sqrt(sum_j A_j^2 |K_j|^2); four times that, plus the rounding of dQ itself."""
+    c = Case(l1, l2, n1, n2, d, HF, seed=33)
+    spread = 2.0 ** (13 - 18 * torch.arange(l1[0]) / (l1[0] - 1))
+    spread = spread[torch.randperm(l1[0], generator=torch.Generator().manual_seed(34))]
+    c.dy = (torch.randn(c.dy.shape, generator=torch.Generator().manual_seed(35)) * spread[:, None, None]).to(HF)
+    q, k, v, dy = (x.cuda() for x in (c.q, c.k, c.v, c.dy))
+    o, lse = sab.cross_forward(q, k, v, c.cu1, c.cu2, c.scale)
+    got = sab.cross_backward(q, k, v, o, dy, lse, c.cu1, c.cu2, c.scale, check=True)
+    o, lse = o.cpu(), lse.cpu()
+    want, tol = c.backward(o, lse)
+    for name, x, w, t in zip(("dq", "dk", "dv"), got, want, tol):
+        _within(name, x, w, t, HF)
+    u = 2.0 ** -11
+    for h in range(n1):
+        n = h // (n1 // n2)
+        x, y, w, kk, vv = c.q[:, h].double(), c.dy[:, h].double(), o[:, h].double(), c.k[:, n].double(), c.v[:, n].double()
+        p = (x @ kk.T * c.scale - lse[:, h].double()[:, None]).exp()
+        ds = p * (y @ vv.T - (y * w).sum(1, keepdim=True))
+        a = p * (y.abs() @ vv.abs().T + (y * w).abs().sum(1, keepdim=True))
+        kn = kk.norm(dim=1)
+        lim = 4 * c.scale * (u * (ds * kn).norm(dim=1) + S32 * (a * kn).norm(dim=1)) + u * want[0][:, h].norm(dim=1)
+        err = (got[0][:, h].cpu().double() - want[0][:, h]).norm(dim=1)
+        over = err - lim - d ** 0.5 * 2.0 ** -25
+        assert bool((over <= 0).all()), (h, float((err / want[0][:, h].norm(dim=1)).max()))
