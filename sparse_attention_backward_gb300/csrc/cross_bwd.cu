@@ -868,6 +868,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const float fv = kFp16 ? exp2f(-kShift) : 1.f;
     Work w{};
     float up = 0.f;                                      // exponent that dS is scaled by
+    bool st_live = false;                                // the thread's key is there
     auto out = [&](int k) -> int64_t {                   // place of key row k in dK and dV; negative: none
         const int key = w.first + k;
         if (key >= (A.s2_pad ? A.s2_pad : w.seq.klen)) return -1;
@@ -877,7 +878,6 @@ __global__ void __launch_bounds__(kXThreads, 1)
         bool ok = true;
         int g = 0, nonempty = 0;
         // what the next unit needs from memory is on its way while this one is stored
-        bool st_live = false;
         float2 norms{};
         auto begin = [&](int k) {
             ok = units.read(k, abort_flag, lane, &w);
@@ -991,7 +991,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             };
             auto store = [&](int j, float *y) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] *= f;
+                for (int e = 0; e < 32; ++e) y[e] = live ? y[e] * f : 0.f;   // P = 0 does not cancel a NaN of dY
                 rows.store(h ? A.dk : A.dv, y, j, lane);
             };
             if (piece < 0) {
@@ -1036,7 +1036,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                     *reinterpret_cast<float4 *>(xo + (h * kXRows + r) * L::XROW + j + e) =
-                        w.n > 0 ? make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        w.n > 0 && st_live ? make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
         cluster_sync();

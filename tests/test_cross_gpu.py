@@ -422,3 +422,28 @@ def test_rows_of_small_output_gradients_in_fp16(l1, l2, n1, n2, d):
         err = (got[0][:, h].cpu().double() - want[0][:, h]).norm(dim=1)
         over = err - lim - d ** 0.5 * 2.0 ** -25
         assert bool((over <= 0).all()), (h, float((err / want[0][:, h].norm(dim=1)).max()))
+
+
+# whole units, a cluster's, and pieces
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("l1,l2,n1,n2,d", [([20, 30], [400, 90], 4, 2, 128), ([900], [400], 4, 2, 64), ([2048], [1280], 16, 16, 64)])
+@pytest.mark.parametrize("padded", [False, True])
+def test_absent_states_get_zeros_whatever_the_queries_hold(dtype, l1, l2, n1, n2, d, padded):
+    c = Case(l1, l2, n1, n2, d, dtype, padded=padded, mask=0.3, seed=32)
+    q, k, v = c.q.cuda(), c.k.cuda(), c.v.cuda()
+    o, lse = sab.cross_forward(q, k, v, c.cu1, c.cu2, c.scale, **c.args())
+    first = (0, 7) if padded else (7,)
+    c.dy[first] = float("inf")      # an overflowed loss scale
+    dq, dk, dv = sab.cross_backward(q, k, v, o, c.dy.cuda(), lse, c.cu1, c.cu2, c.scale, check=True, **c.args())
+    there = c.mask.clone()
+    if padded:
+        for b, n in enumerate(l2):
+            there[b, n:] = False
+    for x in (dk.cpu(), dv.cpu()):
+        assert bool((x[~there] == 0).all())
+        seen = x[0][there[0]] if padded else x[:l2[0]][there[:l2[0]]]
+        assert not bool(seen.isfinite().all())      # the others of that sequence show it
+    rest = dq.cpu().reshape(-1, n1, d).clone()
+    assert not bool(rest[7].isfinite().any())
+    rest[7] = 0
+    assert bool(rest.isfinite().all())
