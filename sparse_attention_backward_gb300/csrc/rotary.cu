@@ -233,11 +233,19 @@ sag_status run_rotary(const srt_desc *d, const srt_io *io, void *workspace, size
     if (off16(io->query, 15) || off16(io->query_out, 15) || off16(io->positions, 3) ||
         (d->n2 && (off16(io->key, 15) || off16(io->key_out, 15))))
         return SAG_ERR_ALIGN;
+    RotArgs a;
+    a.in_stride[0] = d->q_stride ? d->q_stride : (int64_t)d->n1 * d->d;
+    a.in_stride[1] = d->k_stride ? d->k_stride : (int64_t)d->n2 * d->d;
+    a.out_stride[0] = d->q_out_stride ? d->q_out_stride : (int64_t)d->n1 * d->d;
+    a.out_stride[1] = d->k_out_stride ? d->k_out_stride : (int64_t)d->n2 * d->d;
+    // an output over its own input has to have its rows where the input has them
+    if ((io->query == io->query_out && a.in_stride[0] != a.out_stride[0]) ||
+        (d->n2 && io->key == io->key_out && a.in_stride[1] != a.out_stride[1]))
+        return SAG_ERR_SHAPE;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     DeviceGuard dg;
     if (!dg.bind_memory(io->query_out)) return SAG_ERR_CUDA;
-    RotArgs a;
     a.n1 = d->n1;
     a.d = d->d;
     a.d_rot = d->d_rot;
@@ -250,14 +258,6 @@ sag_status run_rotary(const srt_desc *d, const srt_io *io, void *workspace, size
     a.in[1] = static_cast<const uint16_t *>(io->key);
     a.out[0] = static_cast<uint16_t *>(io->query_out);
     a.out[1] = static_cast<uint16_t *>(io->key_out);
-    a.in_stride[0] = d->q_stride ? d->q_stride : (int64_t)d->n1 * d->d;
-    a.in_stride[1] = d->k_stride ? d->k_stride : (int64_t)d->n2 * d->d;
-    a.out_stride[0] = d->q_out_stride ? d->q_out_stride : (int64_t)d->n1 * d->d;
-    a.out_stride[1] = d->k_out_stride ? d->k_out_stride : (int64_t)d->n2 * d->d;
-    // an output over its own input has to have its rows where the input has them
-    if ((io->query == io->query_out && a.in_stride[0] != a.out_stride[0]) ||
-        (d->n2 && io->key == io->key_out && a.in_stride[1] != a.out_stride[1]))
-        return SAG_ERR_SHAPE;
     for (int i = 0; i < d->d_rot / 2; ++i) {
         // fraction of a turn per position, then 64 bits of it
         double t = d->inv_freq[i] / (2.0 * M_PI);

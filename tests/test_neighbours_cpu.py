@@ -219,3 +219,21 @@ def test_workspace_of_partial_sums():
     assert 304 * (128 << 10) <= size([0, 4096], [0, 4096]) < 304 * (128 << 10) + (8 << 20)
     assert size([0, 4096, 5000], [0, 4096, 5000]) < 8 << 20
     assert size([0, 4096, 4096], [0, 4096, 4100], layout=sab.SAG_LAYOUT_BSND, s1_max=4096, s2_max=4096) < 16 << 20
+
+
+@pytest.mark.parametrize("entry", ["rotary_fwd", "rotary_grad"])
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_rows_of_an_output_over_its_input_lie_where_the_inputs_do(lib, entry, which):
+    """Refused before the device is looked for (these addresses belong to none), and nothing else is."""
+    width = dict(q=512, k=256)[which]
+    io = sab.SrtIo(query=4096, key=8192, query_out=4096 if which == "q" else 12288, key_out=8192 if which == "k" else 16384)
+
+    def call(**strides):
+        d = _rot()
+        for name, value in strides.items():
+            setattr(d, f"{which}_{name}", value)
+        return getattr(lib, entry)(ctypes.byref(d), ctypes.byref(io), None, 0, None)
+
+    assert call(out_stride=width + 8) == call(stride=width + 8) == call(stride=width + 8, out_stride=width + 16) == SHAPE
+    for legal in (dict(), dict(out_stride=width), dict(stride=width + 8, out_stride=width + 8)):
+        assert call(**legal) == sab.SAG_ERR_CUDA
