@@ -447,3 +447,55 @@ def test_absent_states_get_zeros_whatever_the_queries_hold(dtype, l1, l2, n1, n2
     assert not bool(rest[7].isfinite().any())
     rest[7] = 0
     assert bool(rest.isfinite().all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("drop", [None, 0.3])
+def test_gradient_of_the_forward_definition(d, drop):
+    """Against 64-bit autograd of the definition of O, element by element, and against its central differences.
+
+    The kernel gets its own o and lse: o is off by e = u |O| + (u + s) P |V|, which moves Delta by |dY| . e and dS by P times
+    that; lse is off by r = s + 2^-20 |lse|, which moves P, and so dS and dV, by a factor of 1 + r."""
+    c = Case([9, 20], [33, 60], 4, 2, d, HF, mask=drop, seed=36)
+    q, k, v, dy = (x.cuda() for x in (c.q, c.k, c.v, c.dy))
+    o, lse = sab.cross_forward(q, k, v, c.cu1, c.cu2, c.scale, **c.args())
+    got = [x.cpu().double() for x in sab.cross_backward(q, k, v, o, dy, lse, c.cu1, c.cu2, c.scale, check=True, **c.args())]
+    u, s, g = 2.0 ** -11, c.scale, c.n1 // c.n2
+
+    def value(x):
+        total = 0.0
+        for i, j, h in c.parts():
+            total = total + (((x[0][i, h] @ x[1][j, h // g].T * s).softmax(1) @ x[2][j, h // g]) * c.dy[i, h].double()).sum()
+        return total
+
+    base = [x.double() for x in (c.q, c.k, c.v)]
+    if c.mask is not None:      # absent rows are not read: any finite value
+        base[1][~c.mask], base[2][~c.mask] = 0.0, 0.0
+    leaves = [x.clone().requires_grad_() for x in base]
+    want = torch.autograd.grad(value(leaves), leaves)
+    lim = [torch.zeros_like(x) for x in base]
+    for i, j, h in c.parts():
+        n = h // g
+        x, y, kk, vv = base[0][i, h], c.dy[i, h].double(), base[1][j, n], base[2][j, n]
+        sc = x @ kk.T * s
+        p, r = sc.softmax(1), S32 + 2.0 ** -20 * sc.logsumexp(1, keepdim=True).abs()
+        w = p @ vv
+        ds = p * (y @ vv.T - (y * w).sum(1, keepdim=True))
+        a = p * (y.abs() @ vv.abs().T + (y * w).abs().sum(1, keepdim=True))
+        moved = p * (y.abs() * (u * w.abs() + (u + S32) * (p @ vv.abs()))).sum(1, keepdim=True)
+        ds = (u + S32 + r) * ds.abs() + S32 * a + moved
+        lim[0][i, h] = s * ds @ kk.abs()
+        lim[1][j, n] += s * ds.T @ x.abs()
+        lim[2][j, n] += ((u + S32 + r) * p).T @ y.abs()
+    for at, name in enumerate(("dq", "dk", "dv")):
+        bound = 1.01 * (u * want[at].abs() + lim[at]) + 2.0 ** -25
+        assert float(bound.norm()) < 0.1 * float(want[at].norm())       # zeros would fail
+        assert bool(((got[at] - want[at]).abs() <= bound).all()), name
+        # along the gradient itself, where the difference is its norm
+        e, h = want[at] / want[at].norm(), 1e-3
+        up, down = list(base), list(base)
+        up[at], down[at] = base[at] + h * e, base[at] - h * e
+        diff = float(value(up) - value(down)) / (2 * h)
+        allowed = float((bound * e.abs()).sum())
+        assert allowed < 0.1 * abs(diff)
+        assert abs(float((got[at] * e).sum()) - diff) <= allowed + 1e-4 * abs(diff), name
