@@ -2,7 +2,7 @@
 // for the sums of a cut unit's pieces), no
 // atomics but a maximum, tickets and counters, so the same bits on every run.
 //
-//   k_xpre  Delta = rowsum(dY * O) and lse in log2 units, packed by query tile
+//   k_xpre  Delta = rowsum(dY * O) and lse in log2 units, packed by query tile; zeros for absent states
 //   k_xdq   per query tile:  S = Q K^T, dP = dY V^T, dS = P (dP - Delta),  dQ += dS K      (over key tiles)
 //   k_xdkv  per key tile:    S^T = K Q^T, dP^T = V dY^T,  dV += P^T dY,  dK += dS^T Q      (over query tiles)
 //
@@ -104,26 +104,34 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
             if (nrm < INFINITY) top = fmaxf(top, nrm);
         }
     } else {
-        // fp16 only: row norms of V
+        // zeros for the gradients of absent states; fp16: row norms of V
         const XUnit u = x_decode<&SeqRow::ktile0>(A, blockIdx.x - q_units);
         slot = ((int64_t)u.b * A.n2 + u.head) * 2 + 1;
+        const int cover = A.s2_pad ? A.s2_pad : u.seq.klen;
 #pragma unroll 4
         for (int r = warp * RPW + lane / LPR; r < kXRows; r += 8 * RPW) {
             const int key = u.tile * kXRows + r;
             const int64_t row = (int64_t)u.seq.k0 + key;
-            float nrm = 0.f;
-            if (key < u.seq.klen && (!A.mask || A.mask[row])) {
-                uint4 a = *reinterpret_cast<const uint4 *>(A.v_in + row * A.v_stride + u.head * D + part * 8);
-                const uint32_t *pa = &a.x;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float y0 = u16_to_f<kFp16>((uint16_t)pa[i]), y1 = u16_to_f<kFp16>((uint16_t)(pa[i] >> 16));
-                    nrm += y0 * y0 + y1 * y1;
-                }
+            const bool there = key < u.seq.klen && (!A.mask || A.mask[row]);
+            if (!there && key < cover) {
+                const int64_t at = (row * A.n2 + u.head) * D + part * 8;
+                *reinterpret_cast<uint4 *>(A.dk + at) = *reinterpret_cast<uint4 *>(A.dv + at) = make_uint4(0, 0, 0, 0);
             }
+            if constexpr (kFp16) {
+                float nrm = 0.f;
+                if (there) {
+                    uint4 a = *reinterpret_cast<const uint4 *>(A.v_in + row * A.v_stride + u.head * D + part * 8);
+                    const uint32_t *pa = &a.x;
 #pragma unroll
-            for (int o = LPR / 2; o; o >>= 1) nrm += __shfl_xor_sync(0xffffffffu, nrm, o);
-            if (nrm < INFINITY) top = fmaxf(top, nrm);
+                    for (int i = 0; i < 4; ++i) {
+                        const float y0 = u16_to_f<kFp16>((uint16_t)pa[i]), y1 = u16_to_f<kFp16>((uint16_t)(pa[i] >> 16));
+                        nrm += y0 * y0 + y1 * y1;
+                    }
+                }
+#pragma unroll
+                for (int o = LPR / 2; o; o >>= 1) nrm += __shfl_xor_sync(0xffffffffu, nrm, o);
+                if (nrm < INFINITY) top = fmaxf(top, nrm);
+            }
         }
     }
     if constexpr (kFp16) {
@@ -969,7 +977,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
             const int piece = w.piece;
             RowStore<kFp16> rows;
             if (ns == 1 && ok) {
-                rows.rows(piece == -2 ? -1 : out(r), lane);
+                // k_xpre has zeroed the rows of absent states, whose sums are not 0 where dY holds a NaN (P = 0 does not cancel
+                // it).  Zeroing them here made one-tile loops 2 % longer (selects: 5 %) and masked ones 3 %.
+                rows.rows(piece == -2 || !live ? -1 : out(r), lane);
                 begin(turn + 1);
             }
             if (n > 0) {
@@ -991,7 +1001,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             };
             auto store = [&](int j, float *y) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = live ? y[e] * f : 0.f;   // P = 0 does not cancel a NaN of dY
+                for (int e = 0; e < 32; ++e) y[e] *= f;
                 rows.store(h ? A.dk : A.dv, y, j, lane);
             };
             if (piece < 0) {
@@ -1084,7 +1094,7 @@ cudaError_t launch(const XArgs &a, const sca_io &io, const sca_desc &d, bool dkv
 }  // namespace
 
 cudaError_t launch_xpre(const XArgs &a, bool fp16, int d, cudaStream_t s) {
-    const int64_t ctas = (int64_t)a.q_tiles * a.n2 + (fp16 ? (int64_t)a.k_tiles * a.n2 : 0);
+    const int64_t ctas = (int64_t)a.q_tiles * a.n2 + (fp16 || a.mask || a.s2_pad ? (int64_t)a.k_tiles * a.n2 : 0);
     if (ctas == 0) return cudaSuccess;
     if (d == 128) {
         if (fp16) k_xpre<true, 128><<<(unsigned)ctas, 256, 0, s>>>(a);
