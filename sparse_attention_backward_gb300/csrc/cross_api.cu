@@ -85,13 +85,20 @@ sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {
 }
 
 // CTAs that share a unit: as many as run at once, up to a cluster's 8, as long as each has a tile of the loop.  A cluster
-// lies within one of the GPU's parts (GPCs), so not every size fills all SMs: the shares, in thousandths, are what
-// cudaOccupancyMaxActiveClusters gives on GB300 (304, 304, 291, 296, 290, 276, 266, 288 of 304 CTAs at two an SM).
-int split_of(int64_t units, int tiles, int room) {
-    static const int share[kMaxSplit + 1] = {0, 1000, 1000, 957, 974, 954, 908, 875, 948};
-    if (room > kSplitCtas) room = kSplitCtas;
+// lies within one of the GPU's parts (GPCs), so not every size fills all SMs, and with fewer CTAs an SM fewer sizes do.
+// Most clusters that run at once on 152 SMs: with one and two CTAs an SM what cudaOccupancyMaxActiveClusters gives for
+// that shared memory (asked for the kernels themselves it counts one CTA an SM), with four up to where the next smaller size
+// is faster.  The limits show in the times of one query tile against 4096 states, us at them and one cluster beyond:
+//   gradient, 128 wide (one an SM)   15 of 8: 36.4 | 47.9   23 of 6: 51.4 | 65.7   28 of 5: 58.9 | 75.3   36 of 4: 69.7 | 85.7
+//   forward, 128 wide (two)          36 of 8: 18.6 | 29.1   46 of 6: 22.1 | 34.9   58 of 5: 30.0 | 44.5   74 of 4: 38.4 | 54.9
+//   forward, 64 wide (four)          64 of 8: 22.2, 66: 25.3, 69: 33.7, where 7 take 27.1
+// They are fixed, not asked for, so that a call's sums have the same order on every GB300.
+int split_of(int64_t units, int tiles, int per_sm, int sms) {
+    static const int fits[3][kMaxSplit + 1] = {
+        {0, 152, 76, 46, 36, 28, 23, 15, 15}, {0, 304, 152, 97, 74, 58, 46, 38, 36}, {0, 608, 304, 194, 146, 114, 94, 77, 66}};
+    const int *row = fits[per_sm >> 1];
     for (int ns = kMaxSplit; ns > 1; --ns)
-        if (ns <= tiles && units * ns * 1000 <= (int64_t)room * share[ns]) return ns;
+        if (ns <= tiles && units * ns <= kSplitCtas && units * 152 <= (int64_t)row[ns] * sms) return ns;
     return 1;
 }
 
@@ -223,7 +230,7 @@ extern "C" sag_status cross_attn_fwd(const sca_desc *desc, const sca_io *io, voi
     XArgs a = x_args(desc, io, p, ws);
     if (x_table(&a, desc, p, ws, s) != cudaSuccess) return SAG_ERR_CUDA;
     a.units = (int)(p.q_tiles * desc->n2);
-    a.nsplit = split_of(a.units, 2 * p.max_k, (desc->d == 64 ? 4 : 2) * current_device_sms());   // CTAs an SM; tiles of 64 keys
+    a.nsplit = split_of(a.units, 2 * p.max_k, desc->d == 64 ? 4 : 2, current_device_sms());   // tiles of 64 keys; CTAs an SM
     a.n_status = a.ctas = a.units * a.nsplit;
     // full query tiles, and at least 2048 keys a CTA
     const bool long_loops = p.max_q > 1 && p.max_k >= 16 * a.nsplit;
@@ -255,7 +262,7 @@ extern "C" sag_status cross_attn_grad(const sca_desc *desc, const sca_io *io, vo
     auto share = [&](int units, int tiles, int least) {
         Share x;
         x.units = x.full = units;
-        x.nsplit = split_of(units, tiles, sms);
+        x.nsplit = split_of(units, tiles, 1, sms);
         x.pieces = 1;
         if (x.nsplit == 1 && may_cut(p, tiles, least)) tail_of(units, tiles, sms, &x.full, &x.pieces);
         x.items = x.full + (units - x.full) * x.pieces;

@@ -499,3 +499,20 @@ def test_gradient_of_the_forward_definition(d, drop):
         allowed = float((bound * e.abs()).sum())
         assert allowed < 0.1 * abs(diff)
         assert abs(float((got[at] * e).sum()) - diff) <= allowed + 1e-4 * abs(diff), name
+
+
+@pytest.mark.parametrize("d,grad,heads", [
+    (128, True, {15: 8, 16: 6, 23: 6, 24: 5, 29: 4, 37: 3, 47: 2, 77: 1}), (128, False, {36: 8, 37: 7, 39: 6, 47: 5, 59: 4, 75: 3, 98: 2}),
+    (64, True, {15: 8, 16: 6, 76: 2, 77: 1}), (64, False, {66: 8, 72: 7, 78: 6, 95: 5, 115: 4})])
+def test_clusters_of_a_launch_run_at_once(d, grad, heads):
+    """One query tile a head and long loops: as many CTAs a head as fit the GPU beside the other heads', by the number of
+    status words that a call leaves (the first word of its workspace; k_xdkv, with 16 tiles a head, has more units than SMs)."""
+    for n, split in heads.items():
+        q, k = (torch.zeros(rows, n, d, dtype=BF, device="cuda") for rows in (128, 2048))
+        desc = sab.make_cross_desc([0, 128], [0, 2048], n, n, d, 0.1)
+        ws = torch.zeros((sab.cross_grad_workspace_size if grad else sab.cross_fwd_workspace_size)(desc), dtype=torch.uint8, device="cuda")
+        o, lse = sab.cross_forward(q, k, k, desc=desc, workspace=None if grad else ws)
+        if grad:
+            sab.cross_backward(q, k, k, o, q, lse, desc=desc, workspace=ws, check=True)
+        ctas = int(ws[:4].view(torch.int32)) - (152 if grad else 0)
+        assert ctas == n * split, (n, ctas)
