@@ -27,7 +27,8 @@ struct XPlan {
 };
 
 // Whether units with loops of `least` to `longest` tiles may be cut (tail_of): below 14 a piece never pays, and short units
-// fill the last round as it is (a ragged padded batch: 155 -> 165 us with pieces).
+// fill the last round as it is (a ragged padded batch: 155 -> 165 us with pieces).  The shortest loop then has 13 tiles, one
+// at least for each of up to 8 pieces, which the kernels rely on.
 bool may_cut(const XPlan &p, int longest, int least) { return !p.padding && longest >= 14 && least * 8 >= longest * 7; }
 
 sag_status x_plan(const sca_desc *d, bool grad, XPlan *p) {

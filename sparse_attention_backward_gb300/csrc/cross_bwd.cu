@@ -192,7 +192,7 @@ struct alignas(16) Work {
     int32_t first;                      // k_xdq: first token, k_xdkv: first key, within the sequence
     int32_t t0, n;                      // this rank's first tile of the loop and their number; n < 0: no more units
     int32_t stat;                       // k_xdq: (query tile of all sequences) * n2 + head
-    int32_t piece;                      // number of the piece; -1: a whole unit, or a cluster's; -2: nothing to do
+    int32_t piece;                      // number of the piece; -1: a whole unit, or a cluster's
     int32_t pad[3];
 };
 
@@ -208,10 +208,10 @@ struct Item {
             ranks = A.pieces;
         }
     }
-    // of a loop of `tiles`; a unit without work is its first piece's alone
+    // of a loop of `tiles`; a piece always has some (only units of long, alike loops are cut)
     __device__ __forceinline__ void share(int tiles, Work *w) const {
         x_share(tiles, rank, ranks, &w->t0, &w->n);
-        w->piece = piece >= 0 && tiles == 0 ? (rank ? -2 : -1) : piece;
+        w->piece = piece;
     }
 };
 
@@ -601,10 +601,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
             // beside the last product: the places of this unit's rows, and the next unit (they took 600 of a unit's 5400 cycles
             // after it, with one tile a unit)
             const int piece = w.piece;
-            const bool pad = (n == 0 && piece < 0) || w.first + my_tok >= w.seq.qlen;
+            const bool pad = n == 0 || w.first + my_tok >= w.seq.qlen;
             RowStore<kFp16> rows;
             if (ns == 1 && ok) {
-                rows.rows(piece == -2 ? -1 : place(my_tok, my_head), lane);
+                rows.rows(place(my_tok, my_head), lane);
                 begin(k + 1);
             }
             if (n > 0) {
@@ -979,7 +979,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             if (ns == 1 && ok) {
                 // k_xpre has zeroed the rows of absent states, whose sums are not 0 where dY holds a NaN (P = 0 does not cancel
                 // it).  Zeroing them here made one-tile loops 2 % longer (selects: 5 %) and masked ones 3 %.
-                rows.rows(piece == -2 || !live ? -1 : out(r), lane);
+                rows.rows(live ? out(r) : -1, lane);
                 begin(turn + 1);
             }
             if (n > 0) {
