@@ -244,7 +244,8 @@ sag_status run_rotary(const srt_desc *d, const srt_io *io, void *workspace, size
         return SAG_ERR_SHAPE;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    DeviceGuard dg;
+    DeviceGuard wg, dg;
+    if (need && !wg.bind_memory(workspace)) return SAG_ERR_CUDA;         // a kernel writes there: host memory is refused
     if (!dg.bind_memory(io->query_out)) return SAG_ERR_CUDA;
     a.n1 = d->n1;
     a.d = d->d;

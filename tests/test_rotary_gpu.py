@@ -160,3 +160,20 @@ def test_streams_and_graph_replay():
 def test_no_rows():
     q = torch.empty((0, 4, 64), dtype=torch.bfloat16, device="cuda")
     assert sab.rotary_forward(q, None, sab.Rotary(64), [0, 0, 0]).shape == (0, 4, 64)
+
+
+def test_workspace_in_host_memory_is_refused():
+    # 65 sequences: the table of them goes through the workspace
+    cu = list(range(66))
+    q = _x((65, 2, 64), torch.bfloat16, 10).cuda()
+    rot = sab.Rotary(64)
+    desc = sab.make_rotary_desc(rot, cu, 2, 0, 64)
+    need = sab.rotary_workspace_size(desc)
+    host = torch.empty(need + 16, dtype=torch.uint8)
+    host = host[-host.data_ptr() % 16:][:need]
+    for call in (sab.rotary_forward, sab.rotary_backward):
+        with pytest.raises(sab.SagError) as e:
+            call(q, None, rot, desc=desc, workspace=host)
+        assert e.value.status == sab.SAG_ERR_CUDA
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert torch.equal(sab.rotary_forward(q, None, rot, desc=desc, workspace=ws), sab.rotary_forward(q, None, rot, cu))
