@@ -603,6 +603,34 @@ def _new(like):
     return _torch.empty_like(like, memory_format=_torch.contiguous_format)
 
 
+def _rows_of(desc, cu, s_max):
+    if desc.layout == SAG_LAYOUT_BSND:
+        return (desc.batch, s_max)
+    return (cu[desc.batch] if desc.batch >= 0 else 0,)
+
+
+def _derive(desc, dense=False):
+    """What calls with the descriptor go by: the tensors' shapes and type.  Strides come from the tensors, so the
+    descriptor serves dense tensors as it is only while its own are 0."""
+    if isinstance(desc, SrtDesc):
+        lead = _rows_of(desc, desc.cu_seqlens, desc.s_max)
+        desc._shapes = (lead + (desc.n1, desc.d), lead + (desc.n2, desc.d))
+    else:
+        desc._shapes = (_rows_of(desc, desc.cu_seqlens_q, desc.s1_max) + (desc.n1, desc.d),
+                        _rows_of(desc, desc.cu_seqlens_kv, desc.s2_max) + (desc.n2, desc.d))
+        for size in (cross_fwd_workspace_size, cross_grad_workspace_size):
+            desc.__dict__.pop(size, None)
+    desc._dtype = _torch_dtype(desc)
+    desc._dense = dense
+    desc._bytes = bytes(desc)
+    return desc
+
+
+def _given(desc):
+    """A kept descriptor, brought up to date if fields were set since."""
+    return desc if bytes(desc) == desc._bytes else _derive(desc)
+
+
 def _with(desc, **fields):
     """The descriptor, or a copy where a field differs (a kept one is never changed)."""
     if all(getattr(desc, k) == v for k, v in fields.items()):
@@ -664,18 +692,14 @@ class Rotary:
 
 def make_rotary_desc(rotary: Rotary, cu_seqlens, n1, n2, d, dtype=SAG_BF16, layout=SAG_LAYOUT_TND, s_max=0) -> SrtDesc:
     """Descriptor of a rotation (n2 = 0: no key); keeps the host arrays alive.
-    Its fields stay as they are once it is in use."""
+    The tensor calls take strides from the tensors, whatever the fields say."""
     cu = _i32(cu_seqlens)
     desc = SrtDesc(batch=len(cu) - 1, n1=n1, n2=n2, d=d, d_rot=rotary.d_rot, offset=rotary.offset, style=rotary.style,
                    dtype=dtype, layout=int(layout), s_max=int(s_max),
                    cu_seqlens=ctypes.cast(cu, ctypes.POINTER(ctypes.c_int32)),
                    inv_freq=ctypes.cast(rotary._freq, ctypes.POINTER(ctypes.c_double)), magnitude=rotary.magnitude)
     desc._keep = (cu, rotary._freq)
-    lead = (desc.batch, int(s_max)) if layout == SAG_LAYOUT_BSND else (cu[len(cu) - 1],)
-    desc._shapes = (lead + (n1, d), lead + (n2, d))
-    desc._dtype = _torch_dtype(desc)
-    desc._dense = True      # strides as made, 0
-    return desc
+    return _derive(desc, dense=True)
 
 
 def rotary_workspace_size(desc: SrtDesc) -> int:
@@ -693,6 +717,8 @@ def _rotary(entry, q, k, rotary, cu_seqlens, positions, out, workspace, stream, 
         bsnd = q.dim() == 4
         desc = make_rotary_desc(rotary, cu_seqlens, n1, n2, d, _sag_dtype(q), SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND,
                                 shape[1] if bsnd else 0)
+    else:
+        desc = _given(desc)
     qs, ks = desc._shapes
     dtype, device = desc._dtype, q.get_device()
     if q.dtype is not dtype or shape != qs:
@@ -754,8 +780,8 @@ def rotary_backward(dq, dk, rotary, cu_seqlens=None, positions=None, out=None, w
 
 def make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, dtype=SAG_BF16, layout=SAG_LAYOUT_TND, s1_max=0,
                     s2_max=0) -> ScaDesc:
-    """Descriptor of a cross attention; keeps the host arrays alive.  Its fields
-    stay as they are once it is in use."""
+    """Descriptor of a cross attention; keeps the host arrays alive.  The tensor
+    calls take strides from the tensors, whatever the fields say."""
     cq, ck = _i32(cu_seqlens_q), _i32(cu_seqlens_kv)
     if len(cq) != len(ck):
         raise ValueError("cu_seqlens_q and cu_seqlens_kv are of different batches")
@@ -763,12 +789,7 @@ def make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, dtype=SAG_BF1
                    cu_seqlens_q=ctypes.cast(cq, ctypes.POINTER(ctypes.c_int32)),
                    cu_seqlens_kv=ctypes.cast(ck, ctypes.POINTER(ctypes.c_int32)), s1_max=int(s1_max), s2_max=int(s2_max))
     desc._keep = (cq, ck)
-    bsnd = layout == SAG_LAYOUT_BSND
-    desc._shapes = (((desc.batch, int(s1_max)) if bsnd else (cq[len(cq) - 1],)) + (n1, d),
-                    ((desc.batch, int(s2_max)) if bsnd else (ck[len(ck) - 1],)) + (n2, d))
-    desc._dtype = _torch_dtype(desc)
-    desc._dense = True      # strides as made, 0
-    return desc
+    return _derive(desc, dense=True)
 
 
 def cross_fwd_workspace_size(desc: ScaDesc) -> int:
@@ -801,6 +822,8 @@ def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, w
         desc = make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, _sag_dtype(q),
                                SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND, q_shape[1] if bsnd else 0,
                                k_shape[1] if bsnd else 0)
+    else:
+        desc = _given(desc)
     dtype, device = desc._dtype, q.get_device()
     qs, ks = desc._shapes
     if q.dtype is not dtype or q_shape != qs:

@@ -147,3 +147,29 @@ def test_refusals_of_tensors():
         with pytest.raises(sab.SagError) as e:
             sab.cross_forward(q, k, k, desc=d, workspace=ws)
         assert e.value.status == sab.SAG_ERR_CUDA
+
+
+def test_descriptors_that_were_changed():
+    q = torch.randn(8, 4, 64, device="cuda").to(torch.bfloat16)
+    k = torch.randn(8, 2, 64, device="cuda").to(torch.bfloat16)
+    cu, rot = [0, 8], sab.Rotary(64)
+    # strides: the tensors' own
+    d = sab.make_rotary_desc(rot, cu, 4, 2, 64)
+    d.q_stride, d.q_out_stride, d.k_stride = 4096, 512, 256
+    for x, y in zip(sab.rotary_forward(q, k, rot, desc=d), sab.rotary_forward(q, k, rot, cu)):
+        assert torch.equal(x, y)
+    d = sab.make_cross_desc(cu, cu, 4, 2, 64, 0.1)
+    d.q_stride, d.k_stride, d.v_stride = 4096, 4096, 8192
+    for x, y in zip(sab.cross_forward(q, k, k, desc=d), sab.cross_forward(q, k, k, cu, cu, 0.1)):
+        assert torch.equal(x, y)
+    # another scale is taken, another size refused
+    d.scale = 0.2
+    for x, y in zip(sab.cross_forward(q, k, k, desc=d), sab.cross_forward(q, k, k, cu, cu, 0.2)):
+        assert torch.equal(x, y)
+    d.n1 = 8
+    with pytest.raises(ValueError):
+        sab.cross_forward(q, k, k, desc=d)
+    d = sab.make_rotary_desc(rot, cu, 4, 2, 64)
+    d.d = 128
+    with pytest.raises(ValueError):
+        sab.rotary_forward(q, k, rot, desc=d)

@@ -237,3 +237,24 @@ def test_rows_of_an_output_over_its_input_lie_where_the_inputs_do(lib, entry, wh
     assert call(out_stride=width + 8) == call(stride=width + 8) == call(stride=width + 8, out_stride=width + 16) == SHAPE
     for legal in (dict(), dict(out_stride=width), dict(stride=width + 8, out_stride=width + 8)):
         assert call(**legal) == sab.SAG_ERR_CUDA
+
+
+def test_descriptors_that_were_changed_are_brought_up_to_date():
+    """What the tensor calls check tensors against follows fields that were set after a descriptor was made."""
+    for field, value in (("n1", 4), ("d", 64), ("dtype", sab.SAG_FP16), ("batch", 1), ("scale", 0.5), ("q_stride", 1024), ("v_stride", 512)):
+        kept, made = _cross(), _cross(**({field: value} if field in ("n1", "d", "dtype", "scale") else {}))
+        size = sab.cross_fwd_workspace_size
+        kept.__dict__[size] = 1 << 40
+        assert sab._given(kept) is kept and size in kept.__dict__ and kept._dense
+        setattr(kept, field, value)
+        assert sab._given(kept) is kept and not kept._dense and size not in kept.__dict__
+        want = (((3, 8, 128), (7, 2, 128)) if field == "batch" else made._shapes)
+        assert kept._shapes == want and kept._dtype == made._dtype
+    kept = _rot(layout=1, s_max=7)
+    assert kept._shapes == ((3, 7, 4, 128), (3, 7, 2, 128))
+    kept.s_max, kept.n2 = 9, 1
+    assert sab._given(kept)._shapes == ((3, 9, 4, 128), (3, 9, 1, 128))
+    kept.layout = kept.s_max = 0
+    assert sab._given(kept)._shapes == ((10, 4, 128), (10, 1, 128))
+    kept.batch = -1
+    assert sab._given(kept)._shapes[0][0] == 0
