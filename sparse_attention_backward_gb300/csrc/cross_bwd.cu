@@ -33,10 +33,10 @@
 // there cost 2269 us against 2271 without and 2100 with pieces for the gradient
 // below: a cluster's CTAs cannot take unit after unit.)
 //
-// Measured on one GB300, 2 x 8192 x 4096 tokens, 32 heads of 128 (bf16): k_xpre 51
-// us (5.3 TB/s), k_xdq 905 us (the tensor pipe 75 % active), k_xdkv 1117 us (80 %):
-// 1860 TFLOP/s of products, 0.98 of the measured bf16 rate; call after call, at the
-// power limit, 2.1 to 2.25 ms.
+// Measured on one GB300, 2 x 8192 x 4096 tokens, 32 heads of 128 (bf16): k_xpre 50
+// us (5.3 TB/s), k_xdq 906 us (the tensor pipe 75 % active), k_xdkv 1130 us (80 %):
+// 1840 TFLOP/s of products, 0.92 of the measured bf16 rate (2000); call after call,
+// at the power limit, 2.2 to 2.3 ms.
 // 64-wide heads: 1530 us for the same tokens; a thread's chain of a tile bounds it
 // (16 softmax warps of 32 columns instead of 8 of 64: 1620 us, 136 -> 150 us for
 // 4 x 1000 x 1290 masked tokens).

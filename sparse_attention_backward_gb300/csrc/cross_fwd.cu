@@ -12,11 +12,11 @@
 // that read the keys together was slower at every size: its softmax warps all
 // wait for one MMA warp (131072 keys: 242 us against 199; 8192 x 4096: 722, 682).
 //
-// Measured on one GB300: 2 x 8192 x 4096 tokens, 32 heads of 128 (bf16) 682 to 714
-// us, 1540 to 1610 TFLOP/s, the tensor pipe 65 % active; what bounds it is the chain from
+// Measured on one GB300: 2 x 8192 x 4096 tokens, 32 heads of 128 (bf16) 682 to 734
+// us, 1500 to 1610 TFLOP/s, the tensor pipe 65 % active; what bounds it is the chain from
 // scores to scores of a CTA (softmax 1500 cycles, its products 1024, hand-offs),
 // of which two run at a time.  One token of 64 sequences against 2048 to 4096
-// states: 68 us, 6.0 TB/s of 6.8.  64-wide heads: 510 us for 2 x 8192 x 4096
+// states: 68 us, 5.9 TB/s of 6.7.  64-wide heads: 510 us for 2 x 8192 x 4096
 // tokens, issue slots 57 % used, the tensor pipe 41 %.
 //
 // The running maximum is lazy: O and the sum are rescaled only when a row's

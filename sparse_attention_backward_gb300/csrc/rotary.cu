@@ -14,7 +14,7 @@
 // its tokens are computed once, into shared memory, while the first loads are on
 // their way.  A thread that kept its columns and walked over heads instead had
 // its sines in registers, but spread each access over several tokens' rows:
-// 106 us against 90 for 32768 tokens of 68 heads of 64 (84 at the measured copy
+// 106 us against 90 for 32768 tokens of 68 heads of 64 (85 at the measured copy
 // rate; 6.3 TB/s).  64 tokens: 3 us, a launch.
 #include <math.h>
 
