@@ -594,6 +594,166 @@ sag_status cross_attn_grad(const sca_desc *desc, const sca_io *io, void *workspa
 sag_status cross_attn_query_error(const void *workspace, void *stream);
 
 /*
+ * Windowed attention: the same as cross attention, for queries that stand at a
+ * position among the keys.  Query i of a sequence of qlen queries and klen keys
+ * is at key position p = i + klen - qlen (the last query at the last key), and
+ * attends to the keys j that are there with p - left <= j <= p + right:
+ * causal attention with left = -1 and right = 0, the local branch of a layer
+ * with left = window - 1 and right = 0.  A query with no such key (klen < qlen,
+ * masked keys) has O = 0 and lse = -inf and gives and takes no gradient.
+ *
+ *   attn          as for the cross attention: the two lengths of a sequence may differ
+ *   left, right   keys before and behind the query's own position, >= 0; -1 (any negative number): no limit
+ *
+ * The tensors are a sca_io.  What masked, padding and foreign rows hold never
+ * counts; the rows of a sequence's own keys have to be finite, whether or not a
+ * query's window holds them (a NaN may reach the queries of its tile).
+ */
+typedef struct swa_desc {
+    sca_desc attn;
+    int32_t left, right;
+} swa_desc;
+
+/* Phase 1, phase 2 and device status as for the cross attention; SAG_ERR_UNSUPPORTED also when a gradient's or a forward's
+ * head dim is not 64 or 128. */
+sag_status window_attn_fwd_workspace_size(const swa_desc *desc, size_t *workspace_bytes);
+sag_status window_attn_grad_workspace_size(const swa_desc *desc, size_t *workspace_bytes);
+sag_status window_attn_fwd(const swa_desc *desc, const sca_io *io, void *workspace, size_t workspace_bytes, void *stream);
+sag_status window_attn_grad(const swa_desc *desc, const sca_io *io, void *workspace, size_t workspace_bytes, void *stream);
+sag_status window_attn_query_error(const void *workspace, void *stream);
+
+/*
+ * Paged cache: keys and values of running sequences lie in pages of page_size
+ * rows, [pages, page_size, n2, d], and position j of sequence b is row j %
+ * page_size of page page_table[b][j / page_size].  A step brings qlen new
+ * tokens a sequence, the last of its kv_lens[b] positions:
+ *   paged_append    writes their keys and values into their places;
+ *   paged_attn_fwd  is the windowed attention of their queries to the cache,
+ *                   the new tokens' own positions included.
+ * The page table and the lengths are device memory, read when the kernels run:
+ * a captured step may be replayed while sequences grow.
+ *
+ *   batch, layout, cu_seqlens_q, s1_max: the new tokens, as in sag_desc (batch <= 65536, up to 2M rows in all)
+ *   n1, n2, d, dtype, scale, left, right: as for the windowed attention
+ *   page_size     a multiple of 16, <= 65536
+ *   pages         pages of the cache, >= 1
+ *   width         pages that a row of the table has room for, >= 1; width * page_size <= 2^28
+ *   kv_expected   length that the split of the work is planned for; 0: width * page_size.  Any length within the table
+ *                 is right whatever it says.
+ *   q_stride, k_stride, v_stride: elements from one new token to the next of query, key and value (0: dense), as in sca_desc
+ *   k_row, k_page, v_row, v_page: elements from one row of a page, and from one page, to the next in the caches, multiples
+ *                 of 8 (0: dense); a row's heads and columns are dense
+ */
+typedef struct spa_desc {
+    int32_t batch;
+    int32_t n1, n2;
+    int32_t d;
+    int32_t dtype;
+    int32_t layout;
+    double scale;
+    const int32_t *cu_seqlens_q;
+    int32_t s1_max;
+    int32_t left, right;
+    int32_t page_size, pages, width;
+    int32_t kv_expected;
+    int32_t reserved_;   /* must be 0 */
+    int64_t q_stride, k_stride, v_stride;
+    int64_t k_row, k_page, v_row, v_page;
+} spa_desc;
+
+/*
+ * Tensors (device pointers, 16-byte aligned; page_table and kv_lens 4-byte aligned; R1 rows as in sag_io):
+ *   query                   [R1, n1, d]                 dtype (attention)
+ *   key, value              [R1, n2, d]                 dtype (append)
+ *   key_cache, value_cache  [pages, page_size, n2, d]   dtype; the append writes them, the attention reads them
+ *   page_table              [batch, width]              int32; entries that no needed position lies in are not looked at
+ *   kv_lens                 [batch]                     int32: positions of the sequence, the new tokens included
+ *   attention_out           [R1, n1, d]                 dtype, written (attention)
+ *   softmax_lse             [R1, n1]                    fp32, written (attention)
+ * A length outside [0, width * page_size] is taken as the nearest one in it, a page outside [0, pages) as page 0 (its
+ * tokens are not written); both are reported (SAG_ERR_INDEX), and outputs are then not meaningful.  New tokens at
+ * positions before 0 (kv_lens[b] < qlen) attend to nothing and are not written.  Rows of the cache behind a sequence's
+ * length, and those before every window, may hold anything.  BSND: padding rows get zeros in attention_out and
+ * softmax_lse, and are not appended.  TND: rows behind the last sequence are left as they were.
+ */
+typedef struct spa_io {
+    const void *query, *key, *value;
+    void *key_cache, *value_cache;
+    const int32_t *page_table, *kv_lens;
+    void *attention_out;
+    float *softmax_lse;
+} spa_io;
+
+/* Phase 1 (host only).  SAG_ERR_UNSUPPORTED for d other than 64 or 128 (the append takes any d that is a multiple of 8, up
+ * to 512) or a page size that is not a multiple of 16. */
+sag_status paged_attn_fwd_workspace_size(const spa_desc *desc, size_t *workspace_bytes);
+sag_status paged_append_workspace_size(const spa_desc *desc, size_t *workspace_bytes);
+
+/* Phase 2: as for the cross attention, bit-identical run to run, capturable.  Two new tokens that a page table sends to the
+ * same place leave one or the other there. */
+sag_status paged_attn_fwd(const spa_desc *desc, const spa_io *io, void *workspace, size_t workspace_bytes, void *stream);
+sag_status paged_append(const spa_desc *desc, const spa_io *io, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Waits for `stream` and returns the status the device recorded in `workspace` during the last paged_attn_fwd or
+ * paged_append on it: SAG_OK, SAG_ERR_INDEX, SAG_ERR_TIMEOUT, or SAG_ERR_CUDA. */
+sag_status paged_query_error(const void *workspace, void *stream);
+
+/*
+ * Norms of queries and keys for each head with the rotation in the same pass,
+ * and the gradient.  A head x of d columns, its weight w = weight_offset +
+ * weight, and the rotation R of the row's position (srt_desc):
+ *     r = 1 / sqrt(mean(x^2) + eps),   y = R (x r w)
+ *     g = w R^T dy,   dx = r (g - x r^2 mean(g x)),   dweight = sum over rows and heads of (R^T dy) x r
+ * in fp32, with one rounding to the dtype; sums of dweight are taken in a fixed
+ * order, so every output is bit-identical run to run.
+ *
+ *   rotary        rows, heads, head dim, columns that turn, frequencies, strides: as for the rotary positions (q_out_stride
+ *                 and k_out_stride are those of query_out and key_out, or of query_grad and key_grad)
+ *   eps           finite, > 0
+ *   weight_offset finite: added to the weights (1 for weights that are held as differences from 1)
+ *   weight_fp32   0: weights are of the dtype; 1: fp32
+ *   q_grad_stride, k_grad_stride: row strides of query_out_grad and key_out_grad (0: dense); the forward ignores them
+ */
+typedef struct snr_desc {
+    srt_desc rotary;
+    double eps;
+    double weight_offset;
+    int32_t weight_fp32;
+    int32_t reserved_;   /* must be 0 */
+    int64_t q_grad_stride, k_grad_stride;
+} snr_desc;
+
+/*
+ * Tensors (device pointers, 16-byte aligned, positions 4-byte aligned; R rows as in srt_io):
+ *   query, key              [R, n1, d], [R, n2, d]   dtype, read (key NULL when n2 = 0; so are its others)
+ *   query_weight, key_weight [d]                     weights; NULL: the norm has none (weight 1, whatever weight_offset says)
+ *   positions               [R] int32, or NULL
+ *   query_out, key_out      forward: written; each may be its input itself
+ *   query_out_grad, key_out_grad   gradient: read
+ *   query_grad, key_grad    gradient: written, like query and key; each may be its input or its out_grad itself (same
+ *                           pointer and stride), but outputs must not overlap inputs otherwise
+ *   query_weight_grad, key_weight_grad [d] fp32: written; NULL where the weight is NULL, or to leave it out
+ * BSND: padding rows are not read and get zeros.  TND: rows behind the last sequence are left as they were.
+ */
+typedef struct snr_io {
+    const void *query, *key;
+    const void *query_weight, *key_weight;
+    const int32_t *positions;
+    void *query_out, *key_out;
+    const void *query_out_grad, *key_out_grad;
+    void *query_grad, *key_grad;
+    float *query_weight_grad, *key_weight_grad;
+} snr_io;
+
+/* Phase 1 (host only): validation and workspace size (the forward's is 0 for batches of up to 64 sequences). */
+sag_status norm_rotary_fwd_workspace_size(const snr_desc *desc, size_t *workspace_bytes);
+sag_status norm_rotary_grad_workspace_size(const snr_desc *desc, size_t *workspace_bytes);
+
+/* Phase 2: ownership and errors as for the rotary positions. */
+sag_status norm_rotary_fwd(const snr_desc *desc, const snr_io *io, void *workspace, size_t workspace_bytes, void *stream);
+sag_status norm_rotary_grad(const snr_desc *desc, const snr_io *io, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Self-test of the device failure path (not part of the operator; the pages
  * have no counterpart).  Enqueues one small kernel that runs the library's
  * bounded mbarrier wait on a barrier nothing ever arrives on: after limit_ns

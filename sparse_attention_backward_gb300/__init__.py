@@ -18,7 +18,10 @@ the gradients come back as (dq, dk, dv, dq_rope, dk_rope).
 Next to it, in the same layouts: ``forward`` and ``indexer_backward``; rotary
 positions (``Rotary``, ``rotary_forward`` / ``rotary_backward``, or ``rotary=``
 of forward and backward); cross attention to an encoder's states
-(``cross_forward`` / ``cross_backward``).
+(``cross_forward`` / ``cross_backward``); norms of queries and keys with the
+rotation in the same pass (``norm_rotary_forward`` / ``norm_rotary_backward``);
+causal and windowed attention (``window_forward`` / ``window_backward``); and,
+for new tokens over a paged cache, ``paged_append`` and ``paged_forward``.
 """
 from __future__ import annotations
 
@@ -458,6 +461,10 @@ def indexer_backward(q, k, weights, dy, indices, cu_seqlens_q, cu_seqlens_kv, de
 EXPORTED_NEIGHBOURS = ("rotary_frequencies", "rotary_workspace_size", "rotary_fwd", "rotary_grad",
                        "cross_attn_fwd_workspace_size", "cross_attn_fwd", "cross_attn_grad_workspace_size",
                        "cross_attn_grad", "cross_attn_query_error")
+EXPORTED_LAYER = ("norm_rotary_fwd_workspace_size", "norm_rotary_grad_workspace_size", "norm_rotary_fwd", "norm_rotary_grad",
+                  "window_attn_fwd_workspace_size", "window_attn_grad_workspace_size", "window_attn_fwd",
+                  "window_attn_grad", "window_attn_query_error", "paged_attn_fwd_workspace_size",
+                  "paged_append_workspace_size", "paged_attn_fwd", "paged_append", "paged_query_error")
 SRT_HALF, SRT_INTERLEAVED = 0, 1
 _ROTARY_STYLES = {"half": SRT_HALF, "interleaved": SRT_INTERLEAVED}
 _ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
@@ -492,6 +499,47 @@ class ScaDesc(ctypes.Structure):
     ]
 
 
+class SwaDesc(ctypes.Structure):
+    """Mirror of ``swa_desc`` in include/selattn.h (the cross attention's fields by their own names)."""
+    _anonymous_ = ("attn",)
+    _fields_ = [("attn", ScaDesc), ("left", ctypes.c_int32), ("right", ctypes.c_int32)]
+
+
+class SnrDesc(ctypes.Structure):
+    """Mirror of ``snr_desc`` in include/selattn.h (the rotary positions' fields by their own names)."""
+    _anonymous_ = ("rotary",)
+    _fields_ = [("rotary", SrtDesc), ("eps", ctypes.c_double), ("weight_offset", ctypes.c_double),
+                ("weight_fp32", ctypes.c_int32), ("reserved_", ctypes.c_int32),
+                ("q_grad_stride", ctypes.c_int64), ("k_grad_stride", ctypes.c_int64)]
+
+
+class SnrIo(ctypes.Structure):
+    """Mirror of ``snr_io`` in include/selattn.h (device pointers as ints)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "query", "key", "query_weight", "key_weight", "positions", "query_out", "key_out", "query_out_grad", "key_out_grad",
+        "query_grad", "key_grad", "query_weight_grad", "key_weight_grad")]
+
+
+class SpaDesc(ctypes.Structure):
+    """Mirror of ``spa_desc`` in include/selattn.h."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("n1", ctypes.c_int32), ("n2", ctypes.c_int32), ("d", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32), ("scale", ctypes.c_double),
+        ("cu_seqlens_q", ctypes.POINTER(ctypes.c_int32)), ("s1_max", ctypes.c_int32),
+        ("left", ctypes.c_int32), ("right", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("pages", ctypes.c_int32), ("width", ctypes.c_int32),
+        ("kv_expected", ctypes.c_int32), ("reserved_", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("k_row", ctypes.c_int64), ("k_page", ctypes.c_int64), ("v_row", ctypes.c_int64), ("v_page", ctypes.c_int64),
+    ]
+
+
+class SpaIo(ctypes.Structure):
+    """Mirror of ``spa_io`` in include/selattn.h (device pointers as ints)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "query", "key", "value", "key_cache", "value_cache", "page_table", "kv_lens", "attention_out", "softmax_lse")]
+
+
 class ScaIo(ctypes.Structure):
     """Mirror of ``sca_io`` in include/selattn.h (device pointers as ints)."""
     _fields_ = [(n, ctypes.c_void_p) for n in (
@@ -514,13 +562,19 @@ def _lib_neighbours():
     lib.rotary_frequencies.argtypes = [ctypes.c_int32, dbl, ctypes.c_int32] + [dbl] * 6 + [ctypes.POINTER(dbl)] * 2
     lib.cross_attn_query_error.argtypes = [vp, vp]
     for prefix, desc, io, names in (("rotary", SrtDesc, SrtIo, ("fwd", "grad")),
-                                    ("cross_attn", ScaDesc, ScaIo, ("fwd", "grad"))):
+                                    ("cross_attn", ScaDesc, ScaIo, ("fwd", "grad")),
+                                    ("window_attn", SwaDesc, ScaIo, ("fwd", "grad")),
+                                    ("norm_rotary", SnrDesc, SnrIo, ("fwd", "grad")),
+                                    ("paged", SpaDesc, SpaIo, ("attn_fwd", "append"))):
         for n in names:
             getattr(lib, f"{prefix}_{n}").argtypes = [ctypes.POINTER(desc), ctypes.POINTER(io), vp, sz, vp]
+            if prefix not in ("rotary", "cross_attn"):
+                getattr(lib, f"{prefix}_{n}_workspace_size").argtypes = [ctypes.POINTER(desc), psz]
+    lib.window_attn_query_error.argtypes = lib.paged_query_error.argtypes = [vp, vp]
     lib.rotary_workspace_size.argtypes = [ctypes.POINTER(SrtDesc), psz]
     lib.cross_attn_fwd_workspace_size.argtypes = [ctypes.POINTER(ScaDesc), psz]
     lib.cross_attn_grad_workspace_size.argtypes = [ctypes.POINTER(ScaDesc), psz]
-    for n in EXPORTED_NEIGHBOURS:
+    for n in EXPORTED_NEIGHBOURS + EXPORTED_LAYER:
         getattr(lib, n).restype = ctypes.c_int
     _neighbours = lib
     return lib
@@ -612,18 +666,37 @@ def _rows_of(desc, cu, s_max):
 def _derive(desc, dense=False):
     """What calls with the descriptor go by: the tensors' shapes and type.  Strides come from the tensors, so the
     descriptor serves dense tensors as it is only while its own are 0."""
-    if isinstance(desc, SrtDesc):
+    if isinstance(desc, (SrtDesc, SnrDesc)):
         lead = _rows_of(desc, desc.cu_seqlens, desc.s_max)
         desc._shapes = (lead + (desc.n1, desc.d), lead + (desc.n2, desc.d))
+    elif isinstance(desc, SpaDesc):
+        lead = _rows_of(desc, desc.cu_seqlens_q, desc.s1_max)
+        desc._shapes = (lead + (desc.n1, desc.d), lead + (desc.n2, desc.d),
+                        (desc.pages, desc.page_size, desc.n2, desc.d), (desc.batch, desc.width))
     else:
         desc._shapes = (_rows_of(desc, desc.cu_seqlens_q, desc.s1_max) + (desc.n1, desc.d),
                         _rows_of(desc, desc.cu_seqlens_kv, desc.s2_max) + (desc.n2, desc.d))
-        for size in (cross_fwd_workspace_size, cross_grad_workspace_size):
-            desc.__dict__.pop(size, None)
+    for size in _SIZES:
+        desc.__dict__.pop(size, None)
     desc._dtype = _torch_dtype(desc)
     desc._dense = dense
     desc._bytes = bytes(desc)
     return desc
+
+
+def _size_of(desc, size):
+    """Phase 1 of a kept descriptor, once."""
+    need = desc.__dict__.get(size)
+    if need is None:
+        need = desc.__dict__[size] = size(desc)
+    return need
+
+
+def _scratch(workspace, need, device):
+    """The caller's workspace where it is large enough, or a new one."""
+    if workspace is None or workspace.numel() < need:
+        return _torch.empty(need, dtype=_torch.uint8, device=device)
+    return workspace
 
 
 def _given(desc):
@@ -807,9 +880,11 @@ def cross_query_error(workspace, stream) -> int:
     return _lib_neighbours().cross_attn_query_error(workspace, stream)
 
 
-def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, workspace, stream, check, desc, tensors):
-    """Shared by the two directions: ``tensors(io, device, dtype)`` fills in
-    the remaining sca_io pointers and gives the outputs."""
+def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, workspace, stream, check, desc, tensors,
+           make=None):
+    """Shared by the two directions of cross and windowed attention:
+    ``tensors(io, device, dtype)`` fills in the remaining sca_io pointers and
+    gives the outputs; ``make`` is what builds the descriptor."""
     if not q.is_cuda:
         raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
     q_shape, k_shape = q.shape, k.shape
@@ -819,9 +894,9 @@ def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, w
         bsnd = q.dim() == 4
         if bsnd and k.dim() != 4:
             raise ValueError("BSND needs 4-D query and key tensors")
-        desc = make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, _sag_dtype(q),
-                               SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND, q_shape[1] if bsnd else 0,
-                               k_shape[1] if bsnd else 0)
+        desc = (make or make_cross_desc)(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, dtype=_sag_dtype(q),
+                                         layout=SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND,
+                                         s1_max=q_shape[1] if bsnd else 0, s2_max=k_shape[1] if bsnd else 0)
     else:
         desc = _given(desc)
     dtype, device = desc._dtype, q.get_device()
@@ -845,12 +920,8 @@ def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, w
 
     def call(handle):
         outs = tensors(io, device, dtype)
-        need = desc.__dict__.get(size)
-        if need is None:
-            need = desc.__dict__[size] = size(desc)
-        ws = workspace
-        if ws is None or ws.numel() < need:
-            ws = _torch.empty(need, dtype=_torch.uint8, device=q.device)
+        need = _size_of(desc, size)
+        ws = _scratch(workspace, need, q.device)
         st = entry(use, io, ws.data_ptr(), need, handle)
         if st == SAG_OK and check:
             st = cross_query_error(ws.data_ptr(), handle)
@@ -861,17 +932,8 @@ def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, w
     return _launch(device, stream, call)
 
 
-def cross_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, key_mask=None, out=None, workspace=None,
-                  stream=None, check=False, desc=None):
-    """Cross attention of q [.., n1, d] to the encoder states k, v [.., n2, d] of
-    the same sequences, TND or 4-D BSND: returns (attention_out [.., n1, d],
-    softmax_lse [.., n1] in fp32).
-
-    ``key_mask`` (bool or uint8, the shape of k without heads and columns):
-    states where it is 0 are not there.  q, k and v may be strided by rows.
-    ``desc`` (make_cross_desc) replaces cu_seqlens_* and scale; ``check`` reads
-    the device status back (this synchronizes the stream).
-    """
+def _attention_out(q, out):
+    """The forward's outputs as _cross wants them."""
     def tensors(io, device, dtype):
         if out is None:
             o, lse = _new(q), _torch.empty(q.shape[:-1], dtype=_torch.float32, device=q.device)
@@ -881,15 +943,11 @@ def cross_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, ke
             io.attention_out = _dense("attention_out", o, device, q.shape, dtype)
             io.softmax_lse = _dense("softmax_lse", lse, device, q.shape[:-1], _torch.float32)
         return o, lse
-
-    return _cross(_lib_neighbours().cross_attn_fwd, cross_fwd_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,
-                  workspace, stream, check, desc, tensors)
+    return tensors
 
 
-def cross_backward(q, k, v, o, dy, lse, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, key_mask=None, out=None,
-                   workspace=None, stream=None, check=False, desc=None):
-    """Gradient of ``cross_forward``: returns (dq, dk, dv), from the forward's o
-    and lse and the gradient dy of o; the other arguments as there."""
+def _attention_grads(q, k, v, o, dy, lse, out):
+    """The gradient's remaining inputs and its outputs as _cross wants them."""
     def tensors(io, device, dtype):
         io.attention_out = _dense("o", o, device, q.shape, dtype)
         io.attention_out_grad = _dense("dy", dy, device, q.shape, dtype)
@@ -903,6 +961,356 @@ def cross_backward(q, k, v, o, dy, lse, cu_seqlens_q=None, cu_seqlens_kv=None, s
             io.dk = _dense("dk", dk, device, k.shape, dtype)
             io.dv = _dense("dv", dv, device, k.shape, dtype)
         return outs
+    return tensors
 
+
+def cross_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, key_mask=None, out=None, workspace=None,
+                  stream=None, check=False, desc=None):
+    """Cross attention of q [.., n1, d] to the encoder states k, v [.., n2, d] of
+    the same sequences, TND or 4-D BSND: returns (attention_out [.., n1, d],
+    softmax_lse [.., n1] in fp32).
+
+    ``key_mask`` (bool or uint8, the shape of k without heads and columns):
+    states where it is 0 are not there.  q, k and v may be strided by rows.
+    ``desc`` (make_cross_desc) replaces cu_seqlens_* and scale; ``check`` reads
+    the device status back (this synchronizes the stream).
+    """
+    return _cross(_lib_neighbours().cross_attn_fwd, cross_fwd_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,
+                  workspace, stream, check, desc, _attention_out(q, out))
+
+
+def cross_backward(q, k, v, o, dy, lse, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, key_mask=None, out=None,
+                   workspace=None, stream=None, check=False, desc=None):
+    """Gradient of ``cross_forward``: returns (dq, dk, dv), from the forward's o
+    and lse and the gradient dy of o; the other arguments as there."""
     return _cross(_lib_neighbours().cross_attn_grad, cross_grad_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,
-                  workspace, stream, check, desc, tensors)
+                  workspace, stream, check, desc, _attention_grads(q, k, v, o, dy, lse, out))
+
+
+# ------------------------------------------------------- windowed attention
+def make_window_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, left=-1, right=0, dtype=SAG_BF16, layout=SAG_LAYOUT_TND,
+                     s1_max=0, s2_max=0) -> SwaDesc:
+    """Descriptor of a windowed attention; ``left`` and ``right`` are the keys
+    before and behind a query's position that it attends to (-1: all of them).
+    Keeps the host arrays alive; the tensor calls take strides from the tensors."""
+    base = make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, dtype, layout, s1_max, s2_max)
+    desc = SwaDesc(attn=base, left=int(left), right=int(right))
+    desc._keep = base._keep
+    return _derive(desc, dense=True)
+
+
+def window_fwd_workspace_size(desc: SwaDesc) -> int:
+    """Phase 1 of the forward: validate and return the workspace size in bytes."""
+    return _phase1("window_attn_fwd_workspace_size", desc)
+
+
+def window_grad_workspace_size(desc: SwaDesc) -> int:
+    """Phase 1 of the gradient: validate and return the workspace size in bytes."""
+    return _phase1("window_attn_grad_workspace_size", desc)
+
+
+def window_query_error(workspace, stream) -> int:
+    """Wait for the stream; return the status the device recorded."""
+    return _lib_neighbours().window_attn_query_error(workspace, stream)
+
+
+def _make_window(left, right):
+    return lambda *args, **kw: make_window_desc(*args, left=left, right=right, **kw)
+
+
+def window_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, left=-1, right=0, key_mask=None, out=None,
+                   workspace=None, stream=None, check=False, desc=None):
+    """Attention of q [.., n1, d] to the keys k, v [.., n2, d] of the same
+    sequences from ``left`` before to ``right`` behind each query's position
+    (-1: all; the last query stands at the last key), TND or 4-D BSND: returns
+    (attention_out [.., n1, d], softmax_lse [.., n1] in fp32).
+
+    Causal by default; the other arguments as in ``cross_forward``, with
+    ``desc`` from make_window_desc (it replaces left and right too)."""
+    return _cross(_lib_neighbours().window_attn_fwd, window_fwd_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale,
+                  key_mask, workspace, stream, check, desc, _attention_out(q, out), _make_window(left, right))
+
+
+def window_backward(q, k, v, o, dy, lse, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, left=-1, right=0, key_mask=None,
+                    out=None, workspace=None, stream=None, check=False, desc=None):
+    """Gradient of ``window_forward``: returns (dq, dk, dv), from the forward's
+    o and lse and the gradient dy of o; the probabilities are formed again."""
+    return _cross(_lib_neighbours().window_attn_grad, window_grad_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale,
+                  key_mask, workspace, stream, check, desc, _attention_grads(q, k, v, o, dy, lse, out),
+                  _make_window(left, right))
+
+
+# ------------------------------------------------------------- paged cache
+def make_paged_desc(cu_seqlens_q, n1, n2, d, scale, pages, page_size, width, left=-1, right=0, dtype=SAG_BF16,
+                    layout=SAG_LAYOUT_TND, s1_max=0, kv_expected=0) -> SpaDesc:
+    """Descriptor of new tokens over a paged cache of ``pages`` pages of
+    ``page_size`` rows, ``width`` of them a sequence at most; serves
+    ``paged_append`` and ``paged_forward``.  Keeps the host array alive; the
+    tensor calls take strides from the tensors."""
+    cq = _i32(cu_seqlens_q)
+    desc = SpaDesc(batch=len(cq) - 1, n1=n1, n2=n2, d=d, dtype=dtype, layout=int(layout), scale=float(scale),
+                   cu_seqlens_q=ctypes.cast(cq, ctypes.POINTER(ctypes.c_int32)), s1_max=int(s1_max), left=int(left),
+                   right=int(right), page_size=int(page_size), pages=int(pages), width=int(width),
+                   kv_expected=int(kv_expected), reserved_=0)
+    desc._keep = (cq,)
+    return _derive(desc, dense=True)
+
+
+def paged_fwd_workspace_size(desc: SpaDesc) -> int:
+    """Phase 1 of the attention: validate and return the workspace size in bytes."""
+    return _phase1("paged_attn_fwd_workspace_size", desc)
+
+
+def paged_append_workspace_size(desc: SpaDesc) -> int:
+    """Phase 1 of the append: validate and return the workspace size in bytes."""
+    return _phase1("paged_append_workspace_size", desc)
+
+
+def paged_query_error(workspace, stream) -> int:
+    """Wait for the stream; return the status the device recorded."""
+    return _lib_neighbours().paged_query_error(workspace, stream)
+
+
+def _cache_strides(name, t, shape, dtype, device):
+    """(row, page) strides of a cache tensor; 0 for a dense one."""
+    _check(name, t, device, shape, dtype)
+    if t.is_contiguous():
+        return 0, 0
+    pages, page, heads, d = shape
+    if (d > 1 and t.stride(3) != 1) or (heads > 1 and t.stride(2) != d):
+        raise ValueError(f"{name}: the heads and columns of a row must be dense")
+    row = t.stride(1) if page > 1 else heads * d
+    return row, t.stride(0) if pages > 1 else row * page
+
+
+def _paged(entry, size, x, desc, k_cache, v_cache, page_table, kv_lens, workspace, stream, check, fill):
+    """Shared by the append and the attention: ``x`` is a tensor of new tokens,
+    ``fill(io, device, dtype)`` sets the other pointers and gives the outputs
+    and the strides that differ from 0."""
+    desc = _given(desc)
+    dtype, device = desc._dtype, x.get_device()
+    cache, table = desc._shapes[2:]
+    io = SpaIo()
+    io.key_cache, io.value_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    k_row, k_page = _cache_strides("k_cache", k_cache, cache, dtype, device)
+    v_row, v_page = _cache_strides("v_cache", v_cache, cache, dtype, device)
+    io.page_table = _dense("page_table", page_table, device, table, _torch.int32)
+    io.kv_lens = _dense("kv_lens", kv_lens, device, table[:1], _torch.int32)
+
+    def call(handle):
+        outs, strides = fill(io, device, dtype)
+        use = desc
+        if not desc._dense or strides or k_row or v_row or k_page or v_page:
+            use = _with(desc, **dict(dict(q_stride=0, k_stride=0, v_stride=0), **strides), k_row=k_row, k_page=k_page, v_row=v_row,
+                        v_page=v_page)
+        need = _size_of(desc, size)
+        ws = _scratch(workspace, need, x.device)
+        st = entry(use, io, ws.data_ptr(), need, handle)
+        if st == SAG_OK and check:
+            st = paged_query_error(ws.data_ptr(), handle)
+        if st != SAG_OK:
+            raise SagError(st, entry.__name__)
+        return outs
+
+    return _launch(device, stream, call)
+
+
+def _paged_layout(x):
+    bsnd = x.dim() == 4
+    return dict(dtype=_sag_dtype(x), layout=SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND, s1_max=x.shape[1] if bsnd else 0)
+
+
+def paged_append(k, v, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q=None, workspace=None, stream=None, check=False,
+                 desc=None):
+    """Writes the new tokens' k, v [.., n2, d] (TND or 4-D BSND) into the caches
+    [pages, page_size, n2, d]: token i of a sequence with q new ones goes to
+    position kv_lens - q + i, in page page_table[sequence, position //
+    page_size].  page_table [batch, width] and kv_lens [batch] are int32 tensors
+    on the device (the lengths include the new tokens).  Returns the caches.
+
+    ``desc`` (make_paged_desc) replaces cu_seqlens_q; ``check`` reads the device
+    status back (a page or length out of range)."""
+    lib = _lib_neighbours()
+    if not k.is_cuda:
+        raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
+    if desc is None:
+        desc = make_paged_desc(cu_seqlens_q, k.shape[-2], k.shape[-2], k.shape[-1], 1.0, k_cache.shape[0], k_cache.shape[1],
+                               page_table.shape[1], **_paged_layout(k))
+
+    def fill(io, device, dtype):
+        shape = desc._shapes[1]
+        _check_rows("k", k, shape, dtype)
+        _check("v", v, device, k.shape, dtype)
+        io.key, io.value = k.data_ptr(), v.data_ptr()
+        strides = {}
+        if not (k.is_contiguous() and v.is_contiguous()):
+            strides = dict(k_stride=_row_stride("k", k, *shape[-2:]), v_stride=_row_stride("v", v, *shape[-2:]))
+        return (k_cache, v_cache), strides
+
+    return _paged(lib.paged_append, paged_append_workspace_size, k, desc, k_cache, v_cache, page_table, kv_lens, workspace, stream,
+                  check, fill)
+
+
+def paged_forward(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q=None, scale=None, left=-1, right=0, out=None,
+                  workspace=None, stream=None, check=False, desc=None):
+    """Attention of the new tokens' q [.., n1, d] (TND or 4-D BSND) to a paged
+    cache (see ``paged_append``), which holds their own keys and values already:
+    returns (attention_out [.., n1, d], softmax_lse [.., n1] in fp32).
+
+    Causal by default, or within a window as in ``window_forward``; ``desc``
+    (make_paged_desc) replaces cu_seqlens_q, scale, left and right.  The page
+    table and the lengths are read on the device, so a captured call may be
+    replayed as sequences grow."""
+    lib = _lib_neighbours()
+    if not q.is_cuda:
+        raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
+    if desc is None:
+        desc = make_paged_desc(cu_seqlens_q, q.shape[-2], k_cache.shape[-2], q.shape[-1], scale, k_cache.shape[0],
+                               k_cache.shape[1], page_table.shape[1], left, right, **_paged_layout(q))
+
+    def fill(io, device, dtype):
+        shape = desc._shapes[0]
+        if q.dtype is not dtype or q.shape != shape:
+            _check_rows("q", q, shape, dtype)
+        io.query = q.data_ptr()
+        outs = _attention_out(q, out)(io, device, dtype)
+        return outs, {} if q.is_contiguous() else dict(q_stride=_row_stride("q", q, *shape[-2:]))
+
+    return _paged(lib.paged_attn_fwd, paged_fwd_workspace_size, q, desc, k_cache, v_cache, page_table, kv_lens, workspace, stream,
+                  check, fill)
+
+
+# ---------------------------------------- norms of queries and keys, rotated
+def make_norm_rotary_desc(rotary: Rotary, cu_seqlens, n1, n2, d, eps=1e-6, weight_offset=0.0, dtype=SAG_BF16,
+                          layout=SAG_LAYOUT_TND, s_max=0) -> SnrDesc:
+    """Descriptor of norms with rotation (n2 = 0: no key); keeps the host arrays
+    alive.  The tensor calls take strides and the weights' type from the tensors."""
+    base = make_rotary_desc(rotary, cu_seqlens, n1, n2, d, dtype, layout, s_max)
+    desc = SnrDesc(rotary=base, eps=float(eps), weight_offset=float(weight_offset), weight_fp32=0, reserved_=0)
+    desc._keep = base._keep
+    return _derive(desc, dense=True)
+
+
+def norm_rotary_fwd_workspace_size(desc: SnrDesc) -> int:
+    """Phase 1 of the forward: validate and return the workspace size in bytes (0 for small batches)."""
+    return _phase1("norm_rotary_fwd_workspace_size", desc)
+
+
+def norm_rotary_grad_workspace_size(desc: SnrDesc) -> int:
+    """Phase 1 of the gradient: validate and return the workspace size in bytes."""
+    return _phase1("norm_rotary_grad_workspace_size", desc)
+
+
+def _norm_rotary(entry, size, q, k, dq, dk, rotary, q_weight, k_weight, eps, weight_offset, cu_seqlens, positions, out, workspace,
+                 stream, desc):
+    """Both directions: with dq (and dk) the gradient."""
+    if not q.is_cuda:
+        raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
+    shape = q.shape
+    n1, d = shape[-2:]
+    n2 = k.shape[-2] if k is not None else 0
+    if desc is None:
+        bsnd = q.dim() == 4
+        desc = make_norm_rotary_desc(rotary, cu_seqlens, n1, n2, d, eps, weight_offset, _sag_dtype(q),
+                                     SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND, shape[1] if bsnd else 0)
+    else:
+        desc = _given(desc)
+    qs, ks = desc._shapes
+    dtype, device, grad = desc._dtype, q.get_device(), dq is not None
+    if q.dtype is not dtype or shape != qs:
+        _check_rows("q", q, qs, dtype)
+    lead = shape[:-2]
+    if k is not None:
+        _check("k", k, device, lead + ks[-2:], dtype)
+    elif ks[-2]:
+        raise ValueError("the descriptor has a key")
+    io = SnrIo(query=q.data_ptr(), key=k.data_ptr() if n2 else None)
+    wtype = None
+    for name, w, side in (("q_weight", q_weight, "query_weight"), ("k_weight", k_weight if n2 else None, "key_weight")):
+        if w is None:
+            continue
+        if wtype not in (None, w.dtype):
+            raise ValueError("q_weight and k_weight are of different types")
+        wtype = w.dtype
+        setattr(io, side, _dense(name, w, device, (d,), dtype if wtype is not _torch.float32 else wtype))
+    if positions is not None:
+        io.positions = _dense("positions", positions, device, lead, _torch.int32)
+    tensors = [q] if k is None else [q, k]
+    if grad:
+        _check("dq", dq, device, shape, dtype)
+        io.query_out_grad = dq.data_ptr()
+        if n2:
+            _check("dk", dk, device, k.shape, dtype)
+            io.key_out_grad = dk.data_ptr()
+        tensors += [dq] if k is None else [dq, dk]
+
+    def call(handle):
+        wq = wk = None
+        if out is None:
+            qo, ko = _new(q), _new(k) if k is not None else None
+            if grad:
+                wq = _torch.empty(d, dtype=_torch.float32, device=q.device) if q_weight is not None else None
+                wk = _torch.empty(d, dtype=_torch.float32, device=q.device) if k_weight is not None and n2 else None
+        else:
+            given = tuple(out) if isinstance(out, (tuple, list)) else (out,)
+            given += (None,) * ((4 if grad else 2) - len(given))
+            qo, ko = given[:2]
+            _check("out", qo, device, shape, dtype)
+            if k is not None:
+                _check("out", ko, device, k.shape, dtype)
+            if grad:
+                wq, wk = given[2:]
+        use, fp32 = desc, int(wtype is _torch.float32)
+        if not (desc._dense and out is None and all(t.is_contiguous() for t in tensors)) or fp32 != desc.weight_fp32:
+            use = _with(desc, weight_fp32=fp32, q_stride=_row_stride("q", q, n1, d), q_out_stride=_row_stride("out", qo, n1, d),
+                        k_stride=_row_stride("k", k, n2, d) if n2 else 0,
+                        k_out_stride=_row_stride("out", ko, n2, d) if n2 else 0,
+                        q_grad_stride=_row_stride("dq", dq, n1, d) if grad else 0,
+                        k_grad_stride=_row_stride("dk", dk, n2, d) if grad and n2 else 0)
+        if grad:
+            io.query_grad, io.key_grad = qo.data_ptr(), ko.data_ptr() if n2 else None
+            io.query_weight_grad = _dense("dq_weight", wq, device, (d,), _torch.float32) if wq is not None else None
+            io.key_weight_grad = _dense("dk_weight", wk, device, (d,), _torch.float32) if wk is not None else None
+        else:
+            io.query_out, io.key_out = qo.data_ptr(), ko.data_ptr() if n2 else None
+        need = 0
+        if grad or desc.batch > 64:
+            need = _size_of(desc, size)
+        ws = _scratch(workspace, need, q.device) if need else None
+        st = entry(use, io, ws.data_ptr() if need else None, need, handle)
+        if st != SAG_OK:
+            raise SagError(st, entry.__name__)
+        if grad:
+            return (qo, ko, wq, wk) if k is not None else (qo, wq)
+        return (qo, ko) if k is not None else qo
+
+    return _launch(device, stream, call)
+
+
+def norm_rotary_forward(q, k, rotary, q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, cu_seqlens=None, positions=None,
+                        out=None, workspace=None, stream=None, desc=None):
+    """Each head of q [.., n1, d] and k [.., n2, d] (or None) over its root mean
+    square, times ``q_weight`` / ``k_weight`` [d] (fp32 or the tensors' type, plus
+    ``weight_offset``; None: no weight), then rotated: returns (q, k), or q alone.
+
+    The other arguments as in ``rotary_forward``; ``desc``
+    (make_norm_rotary_desc) replaces rotary, cu_seqlens, eps and weight_offset."""
+    return _norm_rotary(_lib_neighbours().norm_rotary_fwd, norm_rotary_fwd_workspace_size, q, k, None, None, rotary, q_weight,
+                        k_weight, eps, weight_offset, cu_seqlens, positions, out, workspace, stream, desc)
+
+
+def norm_rotary_backward(q, k, dq, dk, rotary, q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, cu_seqlens=None,
+                         positions=None, out=None, workspace=None, stream=None, desc=None):
+    """Gradient of ``norm_rotary_forward`` from its inputs q, k and the gradients
+    dq, dk of its outputs: returns (q's, k's, q_weight's, k_weight's), the
+    weights' in fp32 (None without a weight); without k (q's, q_weight's).
+    ``out`` takes the same tuple; a weight's gradient left out of it is not computed."""
+    if dq is None or (dk is None) != (k is None):
+        raise ValueError("dq and, with k, dk are needed")
+    return _norm_rotary(_lib_neighbours().norm_rotary_grad, norm_rotary_grad_workspace_size, q, k, dq, dk, rotary, q_weight, k_weight,
+                        eps, weight_offset, cu_seqlens, positions, out, workspace, stream, desc)
+
+
+# phase 1 of calls that keep its result with their descriptor
+_SIZES = (cross_fwd_workspace_size, cross_grad_workspace_size, window_fwd_workspace_size, window_grad_workspace_size,
+          paged_fwd_workspace_size, paged_append_workspace_size, norm_rotary_fwd_workspace_size, norm_rotary_grad_workspace_size)

@@ -1,5 +1,6 @@
-// Pieces shared by the cross-attention kernels: arguments, tile geometry, the
-// TMEM and cluster instructions they add, and the masks of a key tile.
+// Pieces shared by the kernels of cross, windowed and paged attention: arguments,
+// tile geometry, the TMEM and cluster instructions they add, and the masks of a
+// key tile.
 //
 // A tile has 128 rows.  A query tile packs 128 / G tokens with the G heads that
 // share a key/value head (row = token * G + head), so keys are read once for the
@@ -19,6 +20,10 @@ constexpr int kXThreads = 320;          // warps 0-7 softmax and epilogue, 8 TMA
 constexpr uint64_t kXWaitNs = 2000000000ull;
 // A half keeps 11 bits down to 2^-14 only, and a probability of a long sequence lies below that.  Both passes shift
 // fp16 probabilities up by a power of two that cannot overflow 65504, and undo it in fp32.
+constexpr int32_t kNoLimit = 1 << 29;   // `left` or `right` without a limit
+constexpr int32_t kMaxPos = 1 << 28;    // key positions of a sequence: sums of two or three such numbers fit 32 bits
+// Which keys a query row may attend to: all of its sequence; those within a window of its position; the same, in pages.
+enum XMode { kAll = 0, kBand = 1, kPaged = 2 };
 constexpr float kFwdShiftF16 = 7.f;     // forward: exp2(x - max) <= 2^8 (lazy maximum), so <= 2^15
 constexpr float kGradShiftF16 = 15.f;   // gradient: P <= 1 (up to rounding), so <= 2^15
 
@@ -32,7 +37,8 @@ struct XArgs {
     int32_t ctas;                       // of the launch: units * nsplit, or fewer that take unit after unit
     // gradient kernels: work items are `full` whole units, then pieces of the others, `pieces` each
     int32_t items, full, pieces;
-    float *parts;                       // partial sums of the pieces
+    float *parts;                       // partial sums of the pieces; forward: [unit][piece][128][D] O
+    float2 *part_ml;                    // forward: [unit][piece][128] maximum and sum
     unsigned *arrived;                  // pieces of a unit whose sums are there, for each softmax warp
     int32_t n_arrived;                  // such counters of the call
     unsigned *ticket;                   // next items of the two gradient kernels; zeroed by k_xpre, like the counters
@@ -48,12 +54,22 @@ struct XArgs {
     int32_t q_tiles, k_tiles;
     int32_t *count, *status;            // device status: number of words, one word for each CTA
     int32_t n_status;                   // value for *count
+    // windowed and paged attention
+    int32_t left, right;                // keys before and behind a query's position (kNoLimit: all)
+    const int32_t *table, *klens;       // pages [batch][width], key lengths [batch]
+    int32_t width, page, pages;         // pages of a sequence at most, rows of a page, pages of the cache
+    int32_t box;                        // rows of a load: what a page and a key tile have in common
 };
 
 cudaError_t launch_xfwd(const XArgs &a, const sca_io &io, const sca_desc &d, bool long_loops, cudaStream_t s);
+// windowed: a.pieces CTAs without a cluster share a unit if it is more than 1, and k_xjoin adds them up
+cudaError_t launch_wfwd(const XArgs &a, const sca_io &io, const sca_desc &d, bool long_loops, cudaStream_t s);
+cudaError_t launch_pfwd(const XArgs &a, const spa_io &io, const spa_desc &d, bool long_loops, cudaStream_t s);
 cudaError_t launch_xpre(const XArgs &a, bool fp16, int d, cudaStream_t s);
 cudaError_t launch_xdq(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s);
 cudaError_t launch_xdkv(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s);
+cudaError_t launch_wdq(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s);
+cudaError_t launch_wdkv(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s);
 
 namespace {
 
@@ -225,20 +241,28 @@ __device__ __forceinline__ uint32_t xpack(float a, float b) {
 // Unit -> sequence, key/value head, tile within the sequence.  Units of a
 // sequence are consecutive, and within it those of a head, so that CTAs that
 // run at the same time read the same keys (or queries) from L2.
+// kAcross: heads fastest, then tiles (from the last one with kDown: the longest
+// loops of causal attention first, so that short ones fill the end).
+enum XOrder { kByHead = 0, kAcross = 1, kDown = 2 };
 struct XUnit {
     SeqRow seq;
     int b, head, tile;
     int64_t tile_id;                    // (tiles of the sequences before + tile) * n2 + head
 };
-template <int32_t SeqRow::*field>
+template <int32_t SeqRow::*field, int kOrder = kByHead>
 __device__ __forceinline__ XUnit x_decode(const XArgs &A, int unit) {
     XUnit x;
     x.b = seq_find<field>(A.seq, unit / A.n2);
     x.seq = seq_row(A.seq, x.b);
     const int first = x.seq.*field, nt = seq_get<field>(A.seq, x.b + 1) - first;
     const int local = unit - first * A.n2;
-    x.head = local / nt;
-    x.tile = local % nt;
+    if (kOrder == kByHead) {
+        x.head = local / nt;
+        x.tile = local % nt;
+    } else {
+        x.head = local % A.n2;
+        x.tile = kOrder == kDown ? nt - 1 - local / A.n2 : local / A.n2;
+    }
     x.tile_id = (int64_t)(first + x.tile) * A.n2 + x.head;
     return x;
 }
@@ -272,6 +296,14 @@ struct KeyBits {
             w[j] = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
         }
     }
+    // none but those from a on, before b
+    __device__ __forceinline__ void clip(int a, int b) {
+        KeyBits from, to;
+        from.set_first(a);
+        to.set_first(b);
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) w[j] &= to.w[j] & ~from.w[j];
+    }
 };
 // In two steps, so that a tile's mask bytes are on their way while the tile before is worked on.
 template <int kWords>
@@ -296,6 +328,25 @@ struct KeyLoad {
 #pragma unroll
         for (int j = 0; j < kWords; ++j) k.w[j] = __ballot_sync(0xffffffffu, byte[j] != 0);
         return k;
+    }
+};
+
+// Keys that the rows of a query tile may attend to, when query i of a sequence stands at key position i + klen - qlen and
+// sees the keys from `left` before it to `right` behind it.  The loop's tiles start at `base` (paged: a multiple of the
+// tile, so that loads do not cross pages); those in [f0, f1) are seen whole by every row.
+struct BandKeys {
+    int lo, hi, base, tiles, f0, f1;
+    template <int kKeys, bool kAligned>
+    __device__ __forceinline__ static BandKeys of(const XArgs &A, const SeqRow &s, int tok0) {
+        BandKeys w;
+        const int p0 = tok0 + s.klen - s.qlen, p1 = min(tok0 + A.tpt, s.qlen) - 1 + s.klen - s.qlen;
+        w.lo = max(0, p0 - A.left);
+        w.hi = min(s.klen, p1 + A.right + 1);
+        w.base = kAligned ? w.lo / kKeys * kKeys : w.lo;
+        w.tiles = tok0 < s.qlen && w.hi > w.lo ? (w.hi - w.base + kKeys - 1) / kKeys : 0;
+        w.f0 = (max(p1 - A.left - w.base, 0) + kKeys - 1) / kKeys;
+        w.f1 = max(min(s.klen, p0 + A.right + 1) - w.base, 0) / kKeys;
+        return w;
     }
 };
 

@@ -21,14 +21,39 @@
 #include <type_traits>
 
 #include "kernels.cuh"
-#include "seqtab.cuh"
+#include "rotary.cuh"
 
 namespace sag {
+
+sag_status check_rotary(const srt_desc *d) {
+    if (!d || !d->cu_seqlens || !d->inv_freq) return SAG_ERR_NULL;
+    if (d->dtype != SAG_BF16 && d->dtype != SAG_FP16) return SAG_ERR_DTYPE;
+    if (d->style != SRT_HALF && d->style != SRT_INTERLEAVED) return SAG_ERR_SHAPE;
+    if (d->n1 < 1 || d->n1 > 128 || d->n2 < 0 || d->n2 > 128 || d->d < 1 || d->d > 512) return SAG_ERR_SHAPE;
+    if (d->d_rot < 2 || d->d_rot > kMaxRot || d->d_rot % 2 || d->offset < 0 || d->offset + d->d_rot > d->d)
+        return SAG_ERR_SHAPE;
+    if (!isfinite(d->magnitude)) return SAG_ERR_SHAPE;
+    for (int i = 0; i < d->d_rot / 2; ++i)
+        if (!isfinite(d->inv_freq[i])) return SAG_ERR_SHAPE;
+    const int64_t st[] = {d->q_stride, d->q_out_stride, d->k_stride, d->k_out_stride};
+    for (int i = 0; i < 4; ++i)
+        if (st[i] != 0 && (st[i] < (int64_t)(i < 2 ? d->n1 : d->n2) * d->d || st[i] > (1LL << 40))) return SAG_ERR_SHAPE;
+    return check_seqs(d->batch, d->layout, d->cu_seqlens, d->s_max);
+}
+
+void rotary_turns(const srt_desc *d, bool grad, uint64_t *turns) {
+    for (int i = 0; i < d->d_rot / 2; ++i) {
+        // fraction of a turn per position, then 64 bits of it
+        double t = d->inv_freq[i] / (2.0 * M_PI);
+        t -= floor(t);
+        uint64_t q = t >= 1.0 ? 0 : (uint64_t)ldexp(t, 64);
+        turns[i] = grad ? (uint64_t)0 - q : q;
+    }
+}
 
 namespace {
 
 constexpr int kRotThreads = 256;
-constexpr int kMaxRot = 256;
 constexpr int kInFlight = 4;
 constexpr int kMaxTokens = 256, kMaxSines = 2048;   // of a block
 
@@ -61,22 +86,6 @@ union Pack {
     uint32_t w[(V + 1) / 2];
 };
 
-template <bool kFp16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-    if constexpr (kFp16) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-    else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-template <bool kFp16>
-__device__ __forceinline__ uint32_t round2(float a, float b) {
-    if constexpr (kFp16) {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-}
-
 // kHalf: the vector at column c and its partner at c + d_rot / 2; otherwise V / 2 interleaved pairs in one vector.
 template <bool kFp16, bool kHalf, int V>
 __global__ void __launch_bounds__(kRotThreads, 4) k_rotary(const __grid_constant__ RotArgs A) {
@@ -93,17 +102,7 @@ __global__ void __launch_bounds__(kRotThreads, 4) k_rotary(const __grid_constant
     const int lo = blockIdx.y * A.chunk, hi = min(lo + A.chunk, n_tok * A.items);
     const int words = kWords * A.rot_units;              // of a token in the table
 
-    // the row's sequence and place in it; false for padding
-    auto locate = [&](int row, int *place) -> bool {
-        *place = 0;
-        if (A.s_max) {
-            const int b = row / A.s_max;
-            *place = row - b * A.s_max;
-            return *place < seq_get<&SeqRow::qlen>(A.seq, b);
-        }
-        if (!A.positions) *place = row - seq_get<&SeqRow::q0>(A.seq, seq_find<&SeqRow::q0>(A.seq, row));
-        return true;
-    };
+    auto locate = [&](int row, int *place) { return locate_row(A.seq, A.s_max, A.positions, row, place); };
     for (int i = threadIdx.x; i < A.d_rot / 2; i += kRotThreads) turns[i] = A.turns[i];
     if (threadIdx.x < n_tok) {
         int place;
@@ -201,22 +200,6 @@ cudaError_t launch_vec(const RotArgs &a, int vec, dim3 grid, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-sag_status check_rotary(const srt_desc *d) {
-    if (!d || !d->cu_seqlens || !d->inv_freq) return SAG_ERR_NULL;
-    if (d->dtype != SAG_BF16 && d->dtype != SAG_FP16) return SAG_ERR_DTYPE;
-    if (d->style != SRT_HALF && d->style != SRT_INTERLEAVED) return SAG_ERR_SHAPE;
-    if (d->n1 < 1 || d->n1 > 128 || d->n2 < 0 || d->n2 > 128 || d->d < 1 || d->d > 512) return SAG_ERR_SHAPE;
-    if (d->d_rot < 2 || d->d_rot > kMaxRot || d->d_rot % 2 || d->offset < 0 || d->offset + d->d_rot > d->d)
-        return SAG_ERR_SHAPE;
-    if (!isfinite(d->magnitude)) return SAG_ERR_SHAPE;
-    for (int i = 0; i < d->d_rot / 2; ++i)
-        if (!isfinite(d->inv_freq[i])) return SAG_ERR_SHAPE;
-    const int64_t st[] = {d->q_stride, d->q_out_stride, d->k_stride, d->k_out_stride};
-    for (int i = 0; i < 4; ++i)
-        if (st[i] != 0 && (st[i] < (int64_t)(i < 2 ? d->n1 : d->n2) * d->d || st[i] > (1LL << 40))) return SAG_ERR_SHAPE;
-    return check_seqs(d->batch, d->layout, d->cu_seqlens, d->s_max);
-}
-
 sag_status run_rotary(const srt_desc *d, const srt_io *io, void *workspace, size_t workspace_bytes, void *stream,
                       bool grad) {
     sag_status st = check_rotary(d);
@@ -259,13 +242,7 @@ sag_status run_rotary(const srt_desc *d, const srt_io *io, void *workspace, size
     a.in[1] = static_cast<const uint16_t *>(io->key);
     a.out[0] = static_cast<uint16_t *>(io->query_out);
     a.out[1] = static_cast<uint16_t *>(io->key_out);
-    for (int i = 0; i < d->d_rot / 2; ++i) {
-        // fraction of a turn per position, then 64 bits of it
-        double t = d->inv_freq[i] / (2.0 * M_PI);
-        t -= floor(t);
-        uint64_t q = t >= 1.0 ? 0 : (uint64_t)ldexp(t, 64);
-        a.turns[i] = grad ? (uint64_t)0 - q : q;
-    }
+    rotary_turns(d, grad, a.turns);
     // widest vector that every address, stride and part boundary allows
     const bool half = d->style == SRT_HALF;
     int64_t all = (int64_t)d->d | d->offset | (half ? d->d_rot / 2 : d->d_rot) | a.in_stride[0] | a.out_stride[0];
