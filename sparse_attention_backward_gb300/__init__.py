@@ -646,6 +646,8 @@ def _check(name, t, device, shape, dtype):
 
 
 def _dense(name, t, device, shape, dtype):
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
     _check(name, t, device, shape, dtype)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -654,6 +656,8 @@ def _dense(name, t, device, shape, dtype):
 
 def _new(like):
     """A dense tensor of the same shape, type and device."""
+    if like.is_contiguous():
+        return _torch.empty_like(like)
     return _torch.empty_like(like, memory_format=_torch.contiguous_format)
 
 
@@ -905,7 +909,8 @@ def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, w
         _check_rows("q", q, qs, dtype)
     if k.dtype is not dtype or k_shape != ks:
         _check_rows("k", k, ks, dtype)
-    _check("v", v, device, k_shape, dtype)
+    if v.dtype is not dtype or v.shape != k_shape or v.get_device() != device:
+        _check("v", v, device, k_shape, dtype)
     if k.get_device() != device:
         raise ValueError(f"k: on {k.device}, not on {q.device}")
     use = desc
@@ -1219,69 +1224,80 @@ def _norm_rotary(entry, size, q, k, dq, dk, rotary, q_weight, k_weight, eps, wei
     dtype, device, grad = desc._dtype, q.get_device(), dq is not None
     if q.dtype is not dtype or shape != qs:
         _check_rows("q", q, qs, dtype)
-    lead = shape[:-2]
+        lead = shape[:-2]
+        ks = lead + ks[-2:]
+    else:
+        lead = qs[:-2]
+    dense = desc._dense and q.is_contiguous()
     if k is not None:
-        _check("k", k, device, lead + ks[-2:], dtype)
+        if k.dtype is not dtype or k.shape != ks or k.get_device() != device:
+            _check("k", k, device, ks, dtype)
+        dense = dense and k.is_contiguous()
     elif ks[-2]:
         raise ValueError("the descriptor has a key")
-    io = SnrIo(query=q.data_ptr(), key=k.data_ptr() if n2 else None)
-    wtype = None
-    for name, w, side in (("q_weight", q_weight, "query_weight"), ("k_weight", k_weight if n2 else None, "key_weight")):
-        if w is None:
-            continue
-        if wtype not in (None, w.dtype):
-            raise ValueError("q_weight and k_weight are of different types")
-        wtype = w.dtype
-        setattr(io, side, _dense(name, w, device, (d,), dtype if wtype is not _torch.float32 else wtype))
+    if not n2:
+        k_weight = None
+    w = q_weight if q_weight is not None else k_weight
+    wtype, fp32 = dtype, 0
+    if w is not None and w.dtype is _torch.float32:
+        wtype, fp32 = w.dtype, 1
+    wq = wk = pos = None
+    if q_weight is not None:
+        wq = _dense("q_weight", q_weight, device, (d,), wtype)
+    if k_weight is not None:
+        wk = _dense("k_weight", k_weight, device, (d,), wtype)
     if positions is not None:
-        io.positions = _dense("positions", positions, device, lead, _torch.int32)
-    tensors = [q] if k is None else [q, k]
+        pos = _dense("positions", positions, device, lead, _torch.int32)
     if grad:
         _check("dq", dq, device, shape, dtype)
-        io.query_out_grad = dq.data_ptr()
+        dense = dense and dq.is_contiguous()
         if n2:
-            _check("dk", dk, device, k.shape, dtype)
-            io.key_out_grad = dk.data_ptr()
-        tensors += [dq] if k is None else [dq, dk]
+            _check("dk", dk, device, ks, dtype)
+            dense = dense and dk.is_contiguous()
 
     def call(handle):
-        wq = wk = None
+        gq = gk = None
         if out is None:
             qo, ko = _new(q), _new(k) if k is not None else None
             if grad:
-                wq = _torch.empty(d, dtype=_torch.float32, device=q.device) if q_weight is not None else None
-                wk = _torch.empty(d, dtype=_torch.float32, device=q.device) if k_weight is not None and n2 else None
+                gq = _torch.empty(d, dtype=_torch.float32, device=q.device) if wq else None
+                gk = _torch.empty(d, dtype=_torch.float32, device=q.device) if wk else None
         else:
             given = tuple(out) if isinstance(out, (tuple, list)) else (out,)
+            if grad and k is None:
+                given = given[:1] + (None,) + given[1:]
             given += (None,) * ((4 if grad else 2) - len(given))
             qo, ko = given[:2]
             _check("out", qo, device, shape, dtype)
             if k is not None:
-                _check("out", ko, device, k.shape, dtype)
+                _check("out", ko, device, ks, dtype)
             if grad:
-                wq, wk = given[2:]
-        use, fp32 = desc, int(wtype is _torch.float32)
-        if not (desc._dense and out is None and all(t.is_contiguous() for t in tensors)) or fp32 != desc.weight_fp32:
+                gq, gk = given[2:]
+        use = desc
+        if not dense or out is not None:
             use = _with(desc, weight_fp32=fp32, q_stride=_row_stride("q", q, n1, d), q_out_stride=_row_stride("out", qo, n1, d),
                         k_stride=_row_stride("k", k, n2, d) if n2 else 0,
                         k_out_stride=_row_stride("out", ko, n2, d) if n2 else 0,
                         q_grad_stride=_row_stride("dq", dq, n1, d) if grad else 0,
                         k_grad_stride=_row_stride("dk", dk, n2, d) if grad and n2 else 0)
+        elif fp32 != desc.weight_fp32:
+            use = _with(desc, weight_fp32=fp32)
+        kp, kop = (k.data_ptr(), ko.data_ptr()) if n2 else (None, None)
         if grad:
-            io.query_grad, io.key_grad = qo.data_ptr(), ko.data_ptr() if n2 else None
-            io.query_weight_grad = _dense("dq_weight", wq, device, (d,), _torch.float32) if wq is not None else None
-            io.key_weight_grad = _dense("dk_weight", wk, device, (d,), _torch.float32) if wk is not None else None
+            io = SnrIo(q.data_ptr(), kp, wq, wk, pos, None, None, dq.data_ptr(), dk.data_ptr() if n2 else None, qo.data_ptr(), kop,
+                       _dense("dq_weight", gq, device, (d,), _torch.float32) if gq is not None else None,
+                       _dense("dk_weight", gk, device, (d,), _torch.float32) if gk is not None else None)
         else:
-            io.query_out, io.key_out = qo.data_ptr(), ko.data_ptr() if n2 else None
-        need = 0
+            io = SnrIo(q.data_ptr(), kp, wq, wk, pos, qo.data_ptr(), kop)
+        ws, need = None, 0
         if grad or desc.batch > 64:
             need = _size_of(desc, size)
-        ws = _scratch(workspace, need, q.device) if need else None
+            ws = _scratch(workspace, need, q.device)
         st = entry(use, io, ws.data_ptr() if need else None, need, handle)
         if st != SAG_OK:
             raise SagError(st, entry.__name__)
         if grad:
-            return (qo, ko, wq, wk) if k is not None else (qo, wq)
+            return (qo, ko, gq, gk) if k is not None else (qo, gq)
         return (qo, ko) if k is not None else qo
 
     return _launch(device, stream, call)
