@@ -59,6 +59,7 @@ struct XArgs {
     int32_t left, right;                // keys before and behind a query's position (kNoLimit: all)
     const int32_t *table, *klens;       // pages [batch][width], key lengths [batch]
     int32_t width, page, pages;         // pages of a sequence at most, rows of a page, pages of the cache
+    int32_t join_rows;                  // rows of a tile that may hold tokens, for k_xjoin
     int32_t box;                        // rows of a load: what a page and a key tile have in common
 };
 

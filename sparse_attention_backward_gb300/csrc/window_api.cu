@@ -105,12 +105,25 @@ sag_status p_plan(const spa_desc *d, PPlan *p) {
     return SAG_OK;
 }
 
-void use_parts(XArgs *a, const Parts &p, char *ws) {
+// longest: most rows of a sequence that the outputs have (padding included)
+void use_parts(XArgs *a, const Parts &p, char *ws, int longest) {
+    a->join_rows = (longest < a->tpt ? longest : a->tpt) * a->group;
     a->nsplit = p.split.nsplit;
     a->pieces = p.split.pieces;
     a->parts = reinterpret_cast<float *>(ws + p.o_parts);
     a->part_ml = reinterpret_cast<float2 *>(ws + p.o_ml);
     a->n_status = a->ctas = a->units * a->nsplit * a->pieces;
+}
+
+template <class Desc>
+int longest_of(const Desc &d) {
+    if (d.layout == SAG_LAYOUT_BSND) return d.s1_max;
+    int most = 0;
+    for (int b = 0; b < d.batch; ++b) {
+        const int n = d.cu_seqlens_q[b + 1] - d.cu_seqlens_q[b];
+        most = n > most ? n : most;
+    }
+    return most;
 }
 
 // 128-key tiles: full query tiles, and at least 2048 keys a CTA (xfwd.cuh has the times)
@@ -160,7 +173,7 @@ extern "C" sag_status window_attn_fwd(const swa_desc *desc, const sca_io *io, vo
     a.right = limit_of(desc->right);
     if (x_table(&a, d, p, ws, s) != cudaSuccess) return SAG_ERR_CUDA;
     a.units = (int)(p.q_tiles * d->n2);
-    use_parts(&a, parts, ws);
+    use_parts(&a, parts, ws, longest_of(*d));
     const int64_t keys = reach(desc->left, desc->right, p.tpt, (int64_t)p.max_k * kXRows);
     return launch_wfwd(a, *io, *d, long_loops(p.max_q, keys, a), s) == cudaSuccess ? SAG_OK : SAG_ERR_CUDA;
 }
@@ -282,7 +295,7 @@ extern "C" sag_status paged_attn_fwd(const spa_desc *desc, const spa_io *io, voi
         }) != cudaSuccess)
         return SAG_ERR_CUDA;
     a.units = (int)(p.q_tiles * desc->n2);
-    use_parts(&a, p.parts, ws);
+    use_parts(&a, p.parts, ws, longest_of(*desc));
     return launch_pfwd(a, *io, *desc, long_loops(p.max_q, p.keys, a), s) == cudaSuccess ? SAG_OK : SAG_ERR_CUDA;
 }
 

@@ -23,7 +23,7 @@ cudaError_t launch(const XArgs &a, const CUtensorMap &mq, const CUtensorMap &mk,
     cudaError_t e = x_launch(k_xfwd<kFp16, D, kKeys, kMode>, a.ctas, kFwdThreads, a.nsplit, FwdShape<D, kKeys>::TOTAL, false, s,
                              mq, mk, mv, a);
     if (e != cudaSuccess || a.pieces == 1) return e;
-    return x_launch(k_xjoin<kFp16, D>, a.units * a.tpt * a.group, kJoinWarps * 32, 1, 0, true, s, a);
+    return x_launch(k_xjoin<kFp16, D>, a.units * a.join_rows, kJoinWarps * 32, 1, 0, true, s, a);
 }
 
 template <int kMode>

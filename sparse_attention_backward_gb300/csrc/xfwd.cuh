@@ -71,25 +71,48 @@ struct FwdShape {
 // XF_S: scores of an even / odd tile formed, and P V of the tile two before complete; XF_P: P written
 enum { XF_Q = 0, XF_S = 1, XF_P = 3, XF_DRAIN = 5, XF_FULL = 6 };
 
-// A sequence's pages as the loop comes to them, 64 at hand: lane l has those `base` + l and `base` + 32 + l on.
-struct PageIds {
-    const int32_t *row;
-    int base, cur, nxt;
-    __device__ __forceinline__ int load(const XArgs &A, int p) const { return p < A.width ? __ldg(row + p) : -1; }
-    __device__ __forceinline__ PageIds(const XArgs &A, int b, int first, int lane)
-        : row(A.table + (int64_t)b * A.width), base(first) {
+// Pages of a loop's tiles, for the lane whose load takes `shift` keys from a tile's first one on.  Lane l holds the table's
+// entries `base` + l, and those 32 on, which are on their way since the last refill.
+struct PageWalk {
+    const int32_t *table;
+    int base, cur, nxt;                 // the first entry at hand is the tile's first page
+    int first, first_row;               // the tile's first page and row in it
+    int page, row;                      // of this lane
+    int by_page, by_row;
+    __device__ __forceinline__ int load(const XArgs &A, int p) const { return p < A.width ? __ldg(table + p) : -1; }
+    __device__ __forceinline__ static void on(const XArgs &A, int pages, int rows, int *page, int *row) {
+        *page += pages;
+        *row += rows;
+        if (*row >= A.page) {
+            *row -= A.page;
+            ++*page;
+        }
+    }
+    __device__ __forceinline__ PageWalk(const XArgs &A, int b, int key, int keys, int shift, int lane)
+        : table(A.table + (int64_t)b * A.width), by_page(keys / A.page), by_row(keys % A.page) {
+        first = key / A.page;
+        first_row = key - first * A.page;
+        page = (key + shift) / A.page;
+        row = key + shift - page * A.page;
+        base = first;
         cur = load(A, base + lane);
         nxt = load(A, base + 32 + lane);
     }
-    // page p of a tile whose first one is `first` (the same for the warp); they do not go back
-    __device__ __forceinline__ int get(const XArgs &A, int first, int p, int lane) {
-        while (first >= base + 32) {
+    __device__ __forceinline__ int id(const XArgs &A, int lane) {
+        const int i = page - base;
+        const int c = __shfl_sync(0xffffffffu, cur, i & 31);
+        if (__all_sync(0xffffffffu, i < 32)) return c;
+        const int n = __shfl_sync(0xffffffffu, nxt, i & 31);
+        return i < 32 ? c : n;
+    }
+    __device__ __forceinline__ void next(const XArgs &A, int lane) {
+        on(A, by_page, by_row, &first, &first_row);
+        on(A, by_page, by_row, &page, &row);
+        if (first >= base + 32) {
             base += 32;
             cur = nxt;
             nxt = load(A, base + 32 + lane);
         }
-        const int i = p - base, c = __shfl_sync(0xffffffffu, cur, i & 31), n = __shfl_sync(0xffffffffu, nxt, i & 31);
-        return i < 32 ? c : n;
     }
 };
 
@@ -159,23 +182,24 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                 bool ok = true;
                 int loads = 0;
                 const int per = kKeys / A.box, box = lane % per, chunk = lane / per;
-                PageIds ids_k(A, u.b, first_key(0) / A.page, lane), ids_v = ids_k;
-                auto stage = [&](const CUtensorMap *map, PageIds &ids, int key) {
+                PageWalk walk_k(A, u.b, first_key(0), kKeys, box * A.box, lane), walk_v = walk_k;
+                auto stage = [&](const CUtensorMap *map, PageWalk &walk, int key) {
                     const int s = loads % ST, use = loads / ST;
-                    if (use > 0 && !warp_wait(abort_flag, Phase{&empty[s], (uint32_t)(use - 1) & 1u})) return false;
-                    const int k = key + box * A.box, p = k / A.page;
-                    int id = ids.get(A, key / A.page, p, lane);
+                    int id = walk.id(A, lane);
+                    const int k = key + box * A.box, in_page = walk.row;
                     const bool on = chunk < L::KC && k < band.hi && k + A.box > band.lo;
                     if (on && (unsigned)id >= (unsigned)A.pages) {
                         *bad_index = 1;
                         id = 0;
                     }
                     const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, on)) * A.box * 128;
+                    if (use > 0 && !warp_wait(abort_flag, Phase{&empty[s], (uint32_t)(use - 1) & 1u})) return false;
                     if (lane == 0) tc::mbar_arrive_expect_tx(&full[s], bytes);
                     __syncwarp();
                     if (on)
                         tc::tma_load_4d(smem + L::OFF_RING + s * L::TILE + (chunk * kKeys + box * A.box) * 128, map, chunk * 64,
-                                        u.head, k - p * A.page, id, &full[s]);
+                                        u.head, in_page, id, &full[s]);
+                    walk.next(A, lane);
                     ++loads;
                     return true;
                 };
@@ -186,8 +210,8 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                 }
                 __syncwarp();
                 for (int i = -NB; i < n && ok; ++i) {    // the order of the MMA warp, as below
-                    if (i >= 0) ok = stage(&map_v, ids_v, first_key(i));
-                    if (ok && i + NB < n) ok = stage(&map_k, ids_k, first_key(i + NB));
+                    if (i >= 0) ok = stage(&map_v, walk_v, first_key(i));
+                    if (ok && i + NB < n) ok = stage(&map_k, walk_k, first_key(i + NB));
                 }
                 if (!ok) fail();
                 if (lane == 0) {
@@ -478,50 +502,86 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                 }
             }
             cluster_sync();
-            constexpr int E = D / 64;                    // float2 a lane and row
-            for (int k = rank + ns * warp; k < A.tpt * G; k += ns * 4) {
-                const int tok = tok0 + k / G;
-                if (tok >= cover) break;
-                const int64_t row = (int64_t)(u.seq.q0 + tok) * A.n1 + u.head * G + k % G;
-                const bool pad = tok >= u.seq.qlen;
-                // lane p holds rank p's maximum and sum; a rank that saw nothing has (-inf, 0) and no O
-                float2 v = make_float2(-INFINITY, 0.f);
-                if (!pad && lane < ns) v = peer_ld2(peer_addr(tc::smem_u32(ml + k), lane));
-                float2 y[kMaxSplit][E], acc[E] = {};
+            const int mine = min(A.tpt * G, (cover - tok0) * G);
+            auto join = [&](auto np) {
+                // A remote read takes 600 cycles, so a warp has eight (row, rank) pairs' reads in flight while it adds the
+                // eight before up, and what a row needs besides is formed for all rows of a round at once, by lanes NP i + p
+                // for row i and rank p.  (A row after the other, a full tile took 14000 cycles.)  A rank that saw nothing has
+                // (-inf, 0) and no O.
+                constexpr int NP = decltype(np)::value;  // ranks, up to a power of two
+                constexpr int RG = 32 / NP, RS = 8 / NP; // rows of a round of the warp, and of eight reads
+                constexpr int E = D / 64;                // float2 a lane and row
+                uint32_t at[NP];
 #pragma unroll
-                for (int p = 0; p < kMaxSplit; ++p)
-                    if (p < ns) {
-                        const uint32_t a = peer_addr(tc::smem_u32(xo + k * L::XROW + lane * 2), p);
+                for (int p = 0; p < NP; ++p) at[p] = peer_addr(tc::smem_u32(xo + lane * 2), p < ns ? p : 0);
+                for (int first = rank + ns * warp; first < mine; first += ns * 4 * RG) {
+                    auto row_of = [&](int i) { return first + i * ns * 4; };
+                    float2 y[2][RS][NP][E];
+                    auto read = [&](int sub) {
 #pragma unroll
-                        for (int e = 0; e < E; ++e) y[p][e] = peer_ld2(a + e * 256);
+                        for (int a = 0; a < RS; ++a) {
+                            const uint32_t off = min(row_of(sub * RS + a), mine - 1) * (L::XROW * 4);
+#pragma unroll
+                            for (int p = 0; p < NP; ++p)
+                                if (p < ns)
+#pragma unroll
+                                    for (int e = 0; e < E; ++e) y[sub & 1][a][p][e] = peer_ld2(at[p] + off + e * 256);
+                        }
+                    };
+                    const int k = row_of(lane / NP), p_lane = lane % NP, base = lane & ~(NP - 1), tok = tok0 + k / G;
+                    const bool pad = tok >= u.seq.qlen;
+                    float2 v = make_float2(-INFINITY, 0.f);
+                    if (p_lane < ns && k < mine && !pad) v = peer_ld2(peer_addr(tc::smem_u32(ml + k), p_lane));
+                    read(0);
+                    // place of the row; negative: none
+                    const int row = k < mine ? (u.seq.q0 + tok) * A.n1 + u.head * G + k % G : -1;
+                    float top = v.x;
+#pragma unroll
+                    for (int o = NP / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    // A rank that saw something counts even where its weight underflows: 0 times its NaN is NaN, as in an
+                    // undivided loop.  (A rank of NaN scores alone has -inf and NaN.)
+                    const float w = v.y == 0.f ? -1.f : xex2(v.x - top);           // -1: saw nothing
+                    float sum = 0.f;
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) {
+                        const float wp = __shfl_sync(0xffffffffu, w, base + p), lp = __shfl_sync(0xffffffffu, v.y, base + p);
+                        if (wp != -1.f) sum += lp * wp;
                     }
-                float top = v.x;
+                    const bool some = sum > 0.f || sum != sum;
+                    const float inv = some ? 1.f / sum : 0.f;
+                    if (p_lane == 0 && row >= 0) A.lse[row] = pad ? 0.f : some ? (top - kShift) * kLn2 + logf(sum) : -INFINITY;
 #pragma unroll
-                for (int o = kMaxSplit / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                top = __shfl_sync(0xffffffffu, top, 0);
-                // A rank that saw something counts even where its weight underflows: 0 times its NaN is NaN, as in an undivided
-                // loop.  (A rank of NaN scores alone has -inf and NaN.)
-                const float w = v.y == 0.f ? 0.f : xex2(v.x - top);
-                float sum = 0.f;
+                    for (int sub = 0; sub < 4; ++sub) {
+                        if (row_of(sub * RS) >= mine) break;             // the same for the warp
+                        if (sub < 3) read(sub + 1);
 #pragma unroll
-                for (int p = 0; p < kMaxSplit; ++p) {
-                    const float wp = __shfl_sync(0xffffffffu, w, p), lp = __shfl_sync(0xffffffffu, v.y, p);
-                    if (lp == 0.f) continue;
-                    sum += lp * wp;
+                        for (int a = 0; a < RS; ++a) {
+                            const int from = (sub * RS + a) * NP;
+                            float2 acc[E] = {};
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        acc[e].x += y[p][e].x * wp;
-                        acc[e].y += y[p][e].y * wp;
+                            for (int p = 0; p < NP; ++p) {
+                                const float wp = __shfl_sync(0xffffffffu, w, from + p);
+                                if (p >= ns || wp == -1.f) continue;
+#pragma unroll
+                                for (int e = 0; e < E; ++e) {
+                                    acc[e].x += y[sub & 1][a][p][e].x * wp;
+                                    acc[e].y += y[sub & 1][a][p][e].y * wp;
+                                }
+                            }
+                            const int to = __shfl_sync(0xffffffffu, row, from);
+                            const float f = __shfl_sync(0xffffffffu, inv, from);
+                            if (to < 0) continue;
+#pragma unroll
+                            for (int e = 0; e < E; ++e)          // (f = 0 where no rank saw anything, and so is the sum)
+                                *reinterpret_cast<uint32_t *>(A.o + (int64_t)to * D + e * 64 + lane * 2) =
+                                    xpack<kFp16>(acc[e].x * f, acc[e].y * f);
+                        }
                     }
                 }
-                const bool some = sum > 0.f || sum != sum;
-                const float inv = some ? 1.f / sum : 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    *reinterpret_cast<uint32_t *>(A.o + row * D + e * 64 + lane * 2) =
-                        some ? xpack<kFp16>(acc[e].x * inv, acc[e].y * inv) : 0u;
-                if (lane == 0) A.lse[row] = pad ? 0.f : some ? (top - kShift) * kLn2 + logf(sum) : -INFINITY;
-            }
+            };
+            if (ns == 2) join(std::integral_constant<int, 2>{});
+            else if (ns <= 4) join(std::integral_constant<int, 4>{});
+            else join(std::integral_constant<int, 8>{});
             cluster_sync();                              // peers are done with this CTA's shared memory
         }
     }
@@ -537,52 +597,78 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
     }
 }
 
-// Joins the pieces of units: a block a row, its warps take every eighth piece and are added up in their order.
-constexpr int kJoinWarps = 8;
+// Joins the pieces of units: a block a row; its warps take every eighth piece and are added up in their order.  All
+// maxima and sums are read at once, then eight pieces' rows at a time.
+constexpr int kJoinWarps = 8, kMaxJoin = 512;            // pieces of a unit at most
 template <bool kFp16, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_xjoin(const __grid_constant__ XArgs A) {
     constexpr float kShift = kFp16 ? kFwdShiftF16 : 0.f;
     constexpr int E = D / 32;
-    __shared__ float acc_of[kJoinWarps][D];
-    __shared__ float2 ml_of[kJoinWarps];
-    const int per = A.tpt * A.group, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int unit = blockIdx.x / per, k = blockIdx.x % per;
+    __shared__ float acc_of[kJoinWarps][D], weight_of[kMaxJoin], red[2][kJoinWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int unit = blockIdx.x / A.join_rows, k = blockIdx.x % A.join_rows;
     const XUnit u = x_decode<&SeqRow::qtile0, kDown>(A, unit);
     const int tok = u.tile * A.tpt + k / A.group;
     const int64_t row = (int64_t)(u.seq.q0 + tok) * A.n1 + u.head * A.group + k % A.group;
     grid_wait();                                         // the pieces
     if (tok >= (A.s1_pad ? A.s1_pad : u.seq.qlen)) return;
+    const bool pad = tok >= u.seq.qlen;
+    const int pieces = pad ? 0 : A.pieces;
+    const float2 *ml = A.part_ml + ((int64_t)unit * A.pieces * kXRows + k);
+    const float *part = A.parts + ((int64_t)unit * A.pieces * kXRows + k) * D + lane * E;
+    float2 v[2];
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int p = threadIdx.x + i * kJoinWarps * 32;
+        v[i] = p < pieces ? ml[(int64_t)p * kXRows] : make_float2(-INFINITY, 0.f);
+        top = fmaxf(top, v[i].x);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) red[0][warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, red[0][i]);
+    // a piece that saw nothing does not count (its O was not written); one whose weight underflows does: 0 times NaN is NaN
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool saw = v[i].y != 0.f;
+        const float w = saw ? xex2(v[i].x - top) : 0.f;
+        if (saw) sum += v[i].y * w;
+        weight_of[threadIdx.x + i * kJoinWarps * 32] = saw ? w : -1.f;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) red[1][warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) sum += red[1][i];
     float acc[E] = {};
-    float m = -INFINITY, l = 0.f;
-    if (tok < u.seq.qlen) {
-        const float2 *ml = A.part_ml + ((int64_t)unit * A.pieces * kXRows + k);
-        const float *part = A.parts + ((int64_t)unit * A.pieces * kXRows + k) * D + lane * E;
-        float top = -INFINITY;
-        for (int p = lane; p < A.pieces; p += 32) top = fmaxf(top, ml[(int64_t)p * kXRows].x);
+    for (int p0 = warp; p0 < pieces; p0 += 8 * kJoinWarps) {
+        float y[8][E], w[8];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        m = top;
-#pragma unroll 4
-        for (int p = warp; p < A.pieces; p += kJoinWarps) {
-            const float2 v = ml[(int64_t)p * kXRows];
-            if (v.y == 0.f) continue;                    // a piece that saw nothing; one whose weight underflows counts (NaN)
-            const float w = xex2(v.x - top);
-            l += v.y * w;
-            float y[E];
-            if constexpr (E == 4) *reinterpret_cast<float4 *>(y) = *reinterpret_cast<const float4 *>(part + (int64_t)p * kXRows * D);
-            else *reinterpret_cast<float2 *>(y) = *reinterpret_cast<const float2 *>(part + (int64_t)p * kXRows * D);
+        for (int i = 0; i < 8; ++i) {
+            const int p = p0 + i * kJoinWarps;
+            w[i] = p < pieces ? weight_of[p] : -1.f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += y[e] * w;
+            for (int e = 0; e < E; ++e) y[i][e] = 0.f;
+            if (w[i] == -1.f) continue;
+            const float *at = part + (int64_t)p * kXRows * D;
+            if constexpr (E == 4) *reinterpret_cast<float4 *>(y[i]) = *reinterpret_cast<const float4 *>(at);
+            else *reinterpret_cast<float2 *>(y[i]) = *reinterpret_cast<const float2 *>(at);
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += y[i][e] * w[i];
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) acc_of[warp][lane * E + e] = acc[e];
-    if (lane == 0) ml_of[warp] = make_float2(m, l);
     __syncthreads();
-    float sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) sum += ml_of[w].y;
-    const bool pad = tok >= u.seq.qlen, some = sum > 0.f || sum != sum;
+    const bool some = sum > 0.f || sum != sum;
     const float inv = some ? 1.f / sum : 0.f;
     for (int c = threadIdx.x; c < D; c += kJoinWarps * 32) {
         float y = 0.f;
@@ -590,7 +676,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_xjoin(const __grid_constant
         for (int w = 0; w < kJoinWarps; ++w) y += acc_of[w][c];
         A.o[row * D + c] = some ? f_to_u16<kFp16>(y * inv) : (uint16_t)0;
     }
-    if (threadIdx.x == 0) A.lse[row] = pad ? 0.f : some ? (m - kShift) * 0.6931471805599453f + logf(sum) : -INFINITY;
+    if (threadIdx.x == 0) A.lse[row] = pad ? 0.f : some ? (top - kShift) * 0.6931471805599453f + logf(sum) : -INFINITY;
 }
 
 }  // namespace

@@ -117,7 +117,7 @@ struct XSplit {
 };
 inline XSplit fwd_split(int64_t units, int tiles, int per_sm) {
     const int64_t room = 152 * per_sm;
-    XSplit x{split_of(units, tiles, per_sm, 152), 1};
+    XSplit x{tiles < 8 ? 1 : split_of(units, tiles / 2, per_sm, 152), 1};
     int64_t pieces = units ? room / units : 1;
     if (pieces > tiles / 4) pieces = tiles / 4;
     if (pieces > kMaxFwdPieces) pieces = kMaxFwdPieces;
