@@ -19,7 +19,11 @@ bool cache_map(CUtensorMap *m, const void *base, const spa_desc &d, int64_t row,
 }
 
 template <bool kFp16, int D, int kKeys, int kMode>
-cudaError_t launch(const XArgs &a, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
+cudaError_t launch(const XArgs &a_in, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
+    // CTAs that run at once take unit after unit
+    const int room = 152 * FwdShape<D, kKeys>::CTAS;
+    XArgs a = a_in;
+    if (x_walks(kMode, D, kKeys) && a.nsplit * a.pieces == 1 && a.ctas > room) a.ctas = a.n_status = room;
     cudaError_t e = x_launch(k_xfwd<kFp16, D, kKeys, kMode>, a.ctas, kFwdThreads, a.nsplit, FwdShape<D, kKeys>::TOTAL, false, s,
                              mq, mk, mv, a);
     if (e != cudaSuccess || a.pieces == 1) return e;

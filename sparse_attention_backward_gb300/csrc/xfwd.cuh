@@ -68,8 +68,36 @@ struct FwdShape {
     static_assert(OFF_ML + kXRows * 8 <= OFF_BAR, "the exchange overlays Q and the ring");
     static_assert(CTAS * (TOTAL + 1024) <= 228 * 1024, "shared memory of an SM");
 };
-// XF_S: scores of an even / odd tile formed, and P V of the tile two before complete; XF_P: P written
-enum { XF_Q = 0, XF_S = 1, XF_P = 3, XF_DRAIN = 5, XF_FULL = 6 };
+// XF_S: scores of an even / odd tile formed, and P V of the tile two before complete; XF_P: P written; XF_QE: Q has been read
+enum { XF_Q = 0, XF_S = 1, XF_P = 3, XF_DRAIN = 5, XF_QE = 6, XF_FULL = 7 };
+
+// Whether CTAs take unit after unit: with short loops, which 128-key tiles are not for, and registers for it (64-wide heads,
+// four CTAs an SM, have none to spare).
+__host__ __device__ constexpr bool x_walks(int mode, int d, int keys) { return mode != kAll && d == 128 && keys == 64; }
+
+// What a CTA does for a query tile and key/value head.
+struct XJob {
+    XUnit u;
+    BandKeys band;
+    int tok0, cover;                    // first token, tokens that the outputs have
+    int t0, n;                          // first tile of this CTA's share of the keys, and their number
+    int whole, partial;                 // tiles of the share from `whole` on, before `partial`, lack no key
+};
+template <int kKeys, int kMode>
+__device__ __forceinline__ XJob x_job(const XArgs &A, int unit, int rank, int ways) {
+    XJob w;
+    w.u = x_decode<&SeqRow::qtile0, kMode == kAll ? kByHead : kDown>(A, unit);
+    if (kMode == kPaged) w.u.seq.klen = min(max(__ldg(A.klens + w.u.b), 0), A.width * A.page);
+    w.tok0 = w.u.tile * A.tpt;
+    w.cover = A.s1_pad ? A.s1_pad : w.u.seq.qlen;
+    if constexpr (kMode != kAll) w.band = BandKeys::of<kKeys, kMode == kPaged>(A, w.u.seq, w.tok0);
+    else w.band = BandKeys{};
+    const int nkt = kMode != kAll ? w.band.tiles : w.tok0 < w.u.seq.qlen ? (w.u.seq.klen + kKeys - 1) / kKeys : 0;
+    x_share(nkt, rank, ways, &w.t0, &w.n);
+    w.whole = kMode == kAll ? 0 : w.band.f0 - w.t0;
+    w.partial = A.mask ? 0 : (kMode == kAll ? w.u.seq.klen / kKeys : w.band.f1) - w.t0;
+    return w;
+}
 
 // Pages of a loop's tiles, for the lane whose load takes `shift` keys from a tile's first one on.  Lane l holds the table's
 // entries `base` + l, and those 32 on, which are on their way since the last refill.
@@ -116,6 +144,12 @@ struct PageWalk {
     }
 };
 
+// Parities by which the barriers of NB score buffers move on over n tiles, a bit a buffer.
+template <int NB>
+__device__ __forceinline__ uint32_t x_parity(int n) {
+    return NB == 1 ? (uint32_t)n & 1u : (uint32_t)(((n + 1) / 2) & 1) | (uint32_t)((n / 2) & 1) << 1;
+}
+
 template <bool kFp16, int D, int kKeys, int kMode>
 __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
     k_xfwd(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -150,27 +184,19 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
     const int ns = A.nsplit;
     const int ways = kMode == kAll ? ns : ns * A.pieces; // CTAs of the unit: a cluster's, or pieces
     const int rank = blockIdx.x % ways;
-    XUnit u = x_decode<&SeqRow::qtile0, kMode == kAll ? kByHead : kDown>(A, blockIdx.x / ways);
-    const int given = kMode == kPaged ? __ldg(A.klens + u.b) : 0;
-    if (kMode == kPaged) u.seq.klen = min(max(given, 0), A.width * A.page);
+    // windowed: CTAs that share no unit take one after the other, so that the next one's loads and first scores run beside
+    // the last one's end (their loops are short: with a unit a CTA, 32768 tokens and a window of 512 took FIGURE us)
+    const int unit0 = blockIdx.x / ways;
+    auto next_unit = [&](int unit) { return x_walks(kMode, D, kKeys) && ways == 1 ? unit + (int)gridDim.x : 1 << 30; };
+    XJob w = x_job<kKeys, kMode>(A, unit0, rank, ways);
     if (kMode != kAll && A.pieces > 1) grid_next();
     tc::tc_fence_before();
     __syncthreads();
-    if (kMode == kPaged && threadIdx.x == 0 && given != u.seq.klen) *bad_index = 1;
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t sbase = tc::smem_u32(smem);
-    const int G = A.group, tok0 = u.tile * A.tpt;
-    const int cover = A.s1_pad ? A.s1_pad : u.seq.qlen;
-    BandKeys band{};
-    if constexpr (kMode != kAll) band = BandKeys::of<kKeys, kMode == kPaged>(A, u.seq, tok0);
-    const int nkt = kMode != kAll ? band.tiles : tok0 < u.seq.qlen ? (u.seq.klen + kKeys - 1) / kKeys : 0;
-    int t0, n;
-    x_share(nkt, rank, ways, &t0, &n);
-    // tiles of this share from `whole` on, before `partial`, lack no key
-    const int whole = kMode == kAll ? 0 : band.f0 - t0;
-    const int partial = A.mask ? 0 : (kMode == kAll ? u.seq.klen / kKeys : band.f1) - t0;
-    auto first_key = [&](int i) { return band.base + (t0 + i) * kKeys; };
+    const int G = A.group;
+    auto first_key = [&](int i) { return w.band.base + (w.t0 + i) * kKeys; };
     auto fail = [&]() { *abort_flag = 1; };
 
     if (warp >= kFwdTma) {
@@ -180,70 +206,91 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                 // The whole warp: a lane issues one load, of `box` rows within a page.  A tile's rows outside the window are
                 // not loaded: what the buffer held is masked out of the scores, and zeroed before P V.
                 bool ok = true;
-                int loads = 0;
+                int loads = 0, nonempty = 0;
                 const int per = kKeys / A.box, box = lane % per, chunk = lane / per;
-                PageWalk walk_k(A, u.b, first_key(0), kKeys, box * A.box, lane), walk_v = walk_k;
-                auto stage = [&](const CUtensorMap *map, PageWalk &walk, int key) {
-                    const int s = loads % ST, use = loads / ST;
-                    int id = walk.id(A, lane);
-                    const int k = key + box * A.box, in_page = walk.row;
-                    const bool on = chunk < L::KC && k < band.hi && k + A.box > band.lo;
-                    if (on && (unsigned)id >= (unsigned)A.pages) {
-                        *bad_index = 1;
-                        id = 0;
+                for (int unit = unit0;;) {
+                    if (const int given = __ldg(A.klens + w.u.b); given != w.u.seq.klen) *bad_index = 1;
+                    PageWalk walk_k(A, w.u.b, first_key(0), kKeys, box * A.box, lane), walk_v = walk_k;
+                    auto stage = [&](const CUtensorMap *map, PageWalk &walk, int key) {
+                        const int s = loads % ST, use = loads / ST;
+                        int id = walk.id(A, lane);
+                        const int k = key + box * A.box, in_page = walk.row;
+                        const bool on = chunk < L::KC && k < w.band.hi && k + A.box > w.band.lo;
+                        if (on && (unsigned)id >= (unsigned)A.pages) {
+                            *bad_index = 1;
+                            id = 0;
+                        }
+                        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, on)) * A.box * 128;
+                        if (use > 0 && !warp_wait(abort_flag, Phase{&empty[s], (uint32_t)(use - 1) & 1u})) return false;
+                        if (lane == 0) tc::mbar_arrive_expect_tx(&full[s], bytes);
+                        __syncwarp();
+                        if (on)
+                            tc::tma_load_4d(smem + L::OFF_RING + s * L::TILE + (chunk * kKeys + box * A.box) * 128, map, chunk * 64,
+                                            w.u.head, in_page, id, &full[s]);
+                        walk.next(A, lane);
+                        ++loads;
+                        return true;
+                    };
+                    if (w.n > 0) {
+                        if (nonempty > 0) ok = warp_wait(abort_flag, Phase{&bars[XF_QE], (uint32_t)(nonempty - 1) & 1u});
+                        if (!ok) break;
+                        if (lane == 0) {
+                            tc::mbar_arrive_expect_tx(&bars[XF_Q], (uint32_t)L::KC * A.tpt * G * 128);
+                            for (int c = 0; c < L::KC; ++c)
+                                tc::tma_load_3d(smem + c * 16384, &map_q, c * 64, w.u.head * G, w.u.seq.q0 + w.tok0, &bars[XF_Q]);
+                        }
+                        __syncwarp();
+                        ++nonempty;
                     }
-                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, on)) * A.box * 128;
-                    if (use > 0 && !warp_wait(abort_flag, Phase{&empty[s], (uint32_t)(use - 1) & 1u})) return false;
-                    if (lane == 0) tc::mbar_arrive_expect_tx(&full[s], bytes);
-                    __syncwarp();
-                    if (on)
-                        tc::tma_load_4d(smem + L::OFF_RING + s * L::TILE + (chunk * kKeys + box * A.box) * 128, map, chunk * 64,
-                                        u.head, in_page, id, &full[s]);
-                    walk.next(A, lane);
-                    ++loads;
-                    return true;
-                };
-                if (lane == 0 && n > 0) {
-                    tc::mbar_arrive_expect_tx(&bars[XF_Q], (uint32_t)L::KC * A.tpt * G * 128);
-                    for (int c = 0; c < L::KC; ++c)
-                        tc::tma_load_3d(smem + c * 16384, &map_q, c * 64, u.head * G, u.seq.q0 + tok0, &bars[XF_Q]);
-                }
-                __syncwarp();
-                for (int i = -NB; i < n && ok; ++i) {    // the order of the MMA warp, as below
-                    if (i >= 0) ok = stage(&map_v, walk_v, first_key(i));
-                    if (ok && i + NB < n) ok = stage(&map_k, walk_k, first_key(i + NB));
+                    for (int i = -NB; i < w.n && ok; ++i) {      // the order of the MMA warp, as below
+                        if (i >= 0) ok = stage(&map_v, walk_v, first_key(i));
+                        if (ok && i + NB < w.n) ok = stage(&map_k, walk_k, first_key(i + NB));
+                    }
+                    unit = next_unit(unit);
+                    if (!ok || !x_walks(kMode, D, kKeys) || unit >= A.units) break;
+                    w = x_job<kKeys, kMode>(A, unit, rank, ways);
                 }
                 if (!ok) fail();
                 if (lane == 0) {
-                    bool drained = tc::drain_armed(&bars[XF_Q], n > 0, kXWaitNs);
+                    bool drained = tc::drain_armed(&bars[XF_Q], nonempty, kXWaitNs);
                     for (int s = 0; s < ST; ++s)
                         drained = tc::drain_armed(&full[s], loads > s ? (loads - s - 1) / ST + 1 : 0, kXWaitNs) && drained;
                     if (!drained) fail();
                 }
-            } else if (lane == 0 && n > 0) {
+            } else if (lane == 0) {
                 bool ok = true;
-                int loads = 0;
+                int loads = 0, nonempty = 0;
                 auto stage = [&](const CUtensorMap *map, int key) {
                     const int s = loads % ST, use = loads / ST;
                     if (use > 0 && !tc::mbar_wait(&empty[s], (use - 1) & 1, abort_flag, kXWaitNs)) return false;
                     tc::mbar_arrive_expect_tx(&full[s], L::TILE);
                     for (int c = 0; c < L::KC; ++c)
-                        tc::tma_load_3d(smem + L::OFF_RING + s * L::TILE + c * kKeys * 128, map, c * 64, u.head,
-                                        u.seq.k0 + key, &full[s]);
+                        tc::tma_load_3d(smem + L::OFF_RING + s * L::TILE + c * kKeys * 128, map, c * 64, w.u.head,
+                                        w.u.seq.k0 + key, &full[s]);
                     ++loads;
                     return true;
                 };
-                tc::mbar_arrive_expect_tx(&bars[XF_Q], (uint32_t)L::KC * A.tpt * G * 128);
-                for (int c = 0; c < L::KC; ++c)
-                    tc::tma_load_3d(smem + c * 16384, &map_q, c * 64, u.head * G, u.seq.q0 + tok0, &bars[XF_Q]);
-                // in the order the MMA warp takes them: the first K, then V i and K i + NB
-                for (int i = -NB; i < n && ok; ++i) {
-                    if (i >= 0) ok = stage(&map_v, first_key(i));
-                    if (ok && i + NB < n) ok = stage(&map_k, first_key(i + NB));
+                for (int unit = unit0;;) {
+                    if (w.n > 0) {
+                        if (nonempty > 0) ok = tc::mbar_wait(&bars[XF_QE], (nonempty - 1) & 1, abort_flag, kXWaitNs);
+                        if (!ok) break;
+                        tc::mbar_arrive_expect_tx(&bars[XF_Q], (uint32_t)L::KC * A.tpt * G * 128);
+                        for (int c = 0; c < L::KC; ++c)
+                            tc::tma_load_3d(smem + c * 16384, &map_q, c * 64, w.u.head * G, w.u.seq.q0 + w.tok0, &bars[XF_Q]);
+                        ++nonempty;
+                    }
+                    // in the order the MMA warp takes them: the first K, then V i and K i + NB
+                    for (int i = -NB; i < w.n && ok; ++i) {
+                        if (i >= 0) ok = stage(&map_v, first_key(i));
+                        if (ok && i + NB < w.n) ok = stage(&map_k, first_key(i + NB));
+                    }
+                    unit = next_unit(unit);
+                    if (!ok || !x_walks(kMode, D, kKeys) || unit >= A.units) break;
+                    w = x_job<kKeys, kMode>(A, unit, rank, ways);
                 }
                 if (!ok) fail();
                 // every load issued must have landed before the CTA exits
-                bool drained = tc::drain_armed(&bars[XF_Q], 1, kXWaitNs);
+                bool drained = tc::drain_armed(&bars[XF_Q], nonempty, kXWaitNs);
                 for (int s = 0; s < ST; ++s)
                     drained = tc::drain_armed(&full[s], loads > s ? (loads - s - 1) / ST + 1 : 0, kXWaitNs) && drained;
                 if (!drained) fail();
@@ -256,42 +303,55 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
             constexpr uint32_t id_s = tc::idesc_f16(kXRows, kKeys, !kFp16, false, false);
             constexpr uint32_t id_o = tc::idesc_f16(kXRows, D, !kFp16, false, true);
             const uint32_t ring = sbase + L::OFF_RING;
-            // load j of the ring: the first K tiles, then V i (behind min(i + NB, n) tiles of K) and K i + NB
-            auto landed = [&](int j) { return Phase{&full[j % ST], (uint32_t)(j / ST) & 1u}; };
-            auto issue_s = [&](int i, int j) {
-                mma_abt<D, kKeys>(tmem + i % NB * kKeys, sbase, ring + j % ST * L::TILE, id_s);
-                tc::mma_commit_warp(&bars[XF_S + i % NB]);
-                tc::mma_commit_warp(&empty[j % ST]);
-            };
             bool ok = true;
-            for (int i = 0; i < NB && i < n && ok; ++i) {
-                ok = warp_wait(abort_flag, Phase{&bars[XF_Q], 0}, landed(i));
-                tc::tc_fence_after();
-                if (ok) issue_s(i, i);
-            }
-            for (int i = 0; i < n && ok; ++i) {
-                const bool more = i + NB < n;
-                const int jv = i + (more ? i + NB : n);
-                const uint32_t vt = ring + jv % ST * L::TILE, acc = tmem + L::COL_O, pt = tmem + i % NB * kKeys + L::P_AT;
-                // P (its first half), V, and with the last half the K tile of the scores that follow
-                auto written = [&](int h) {
-                    return L::HALVES == 2 ? Phase{&bars[XF_P + h], (uint32_t)i & 1u}
-                                          : Phase{&bars[XF_P + i % NB], (uint32_t)(i / NB) & 1u};
+            int base = 0, nonempty = 0;                  // loads and units before this unit
+            uint32_t written_by = 0;                     // parities of XF_P before this unit, a bit a barrier
+            for (int unit = unit0;;) {
+                const int n = w.n;
+                // load j of the unit: the first K tiles, then V i (behind min(i + NB, n) tiles of K) and K i + NB
+                auto landed = [&](int j) { return Phase{&full[(base + j) % ST], (uint32_t)((base + j) / ST) & 1u}; };
+                auto issue_s = [&](int i, int j) {
+                    mma_abt<D, kKeys>(tmem + i % NB * kKeys, sbase, ring + (base + j) % ST * L::TILE, id_s);
+                    tc::mma_commit_warp(&bars[XF_S + i % NB]);
+                    tc::mma_commit_warp(&empty[(base + j) % ST]);
+                    if (x_walks(kMode, D, kKeys) && i + 1 == n) tc::mma_commit_warp(&bars[XF_QE]);
                 };
-                ok = L::HALVES == 1 && more ? warp_wait(abort_flag, written(0), landed(jv), landed(jv + 1))
-                                            : warp_wait(abort_flag, written(0), landed(jv));
-                if (!ok) break;
-                tc::tc_fence_after();
-                mma_ab<kKeys, 32, 0, 4>(acc, pt, vt, id_o, i > 0);
-                if (L::HALVES == 2) {
-                    ok = more ? warp_wait(abort_flag, written(1), landed(jv + 1)) : warp_wait(abort_flag, written(1));
+                for (int i = 0; i < NB && i < n && ok; ++i) {
+                    ok = warp_wait(abort_flag, Phase{&bars[XF_Q], (uint32_t)nonempty & 1u}, landed(i));
+                    tc::tc_fence_after();
+                    if (ok) issue_s(i, i);
+                }
+                for (int i = 0; i < n && ok; ++i) {
+                    const bool more = i + NB < n;
+                    const int jv = i + (more ? i + NB : n);
+                    const uint32_t vt = ring + (base + jv) % ST * L::TILE, acc = tmem + L::COL_O, pt = tmem + i % NB * kKeys + L::P_AT;
+                    // P (its first half), V, and with the last half the K tile of the scores that follow
+                    auto written = [&](int h) {
+                        const int b = L::HALVES == 2 ? h : i % NB;
+                        return Phase{&bars[XF_P + b], ((written_by >> b) ^ (uint32_t)(i / NB)) & 1u};
+                    };
+                    ok = L::HALVES == 1 && more ? warp_wait(abort_flag, written(0), landed(jv), landed(jv + 1))
+                                                : warp_wait(abort_flag, written(0), landed(jv));
                     if (!ok) break;
                     tc::tc_fence_after();
-                    mma_ab<kKeys, 32, 4, kKeys / 16>(acc, pt, vt, id_o, true);
+                    mma_ab<kKeys, 32, 0, 4>(acc, pt, vt, id_o, i > 0);
+                    if (L::HALVES == 2) {
+                        ok = more ? warp_wait(abort_flag, written(1), landed(jv + 1)) : warp_wait(abort_flag, written(1));
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        mma_ab<kKeys, 32, 4, kKeys / 16>(acc, pt, vt, id_o, true);
+                    }
+                    tc::mma_commit_warp(&empty[(base + jv) % ST]);
+                    if (more) issue_s(i + NB, jv + 1);
+                    else tc::mma_commit_warp(&bars[XF_S + i % NB]);
                 }
-                tc::mma_commit_warp(&empty[jv % ST]);
-                if (more) issue_s(i + NB, jv + 1);
-                else tc::mma_commit_warp(&bars[XF_S + i % NB]);
+                unit = next_unit(unit);
+                if (!ok || !x_walks(kMode, D, kKeys) || unit >= A.units) break;
+                base += 2 * n;
+                nonempty += n > 0;
+                if (L::HALVES == 2) written_by ^= n & 1 ? 3u : 0u;
+                else written_by ^= x_parity<NB>(n);
+                w = x_job<kKeys, kMode>(A, unit, rank, ways);
             }
             if (!ok && lane == 0) fail();
             // every MMA issued must be complete before TMEM is freed
@@ -308,6 +368,13 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
         const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
         const uint32_t to = trow + L::COL_O;
         float m = -INFINITY, l = 0.f;                    // reference maximum (log2 units), sum
+        const float kLn2 = 0.6931471805599453f;
+        int base = 0;                                    // loads before this unit
+        uint32_t formed_by = 0;                          // parities of XF_S before this unit, a bit a barrier
+        for (int unit = unit0;;) {
+        const int n = w.n, next = next_unit(unit);
+        bool ok = true;
+        XJob ahead;
         if (n > 0) {
             // -------------------------------------------------- softmax
             const float c = A.scale_log2;
@@ -315,31 +382,31 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                 return warp_wait(abort_flag, Phase{&bars[b], parity});
             };
             // tile i's scores (or, behind the last two tiles, just the products before) are complete
-            auto formed = [&](int i) { return wait(XF_S + i % NB, (uint32_t)(i / NB) & 1u); };
+            auto formed = [&](int i) { return wait(XF_S + i % NB, ((formed_by >> (i % NB)) ^ (uint32_t)(i / NB)) & 1u); };
             // One tile; a copy of its own for tiles with absent keys, whose
             // selects otherwise run for every tile.  Paired fp32 operations
             // (f32x2): half the instructions where issue slots are short,
             // 540 -> 507 us for 8192 x 4096 tokens of 64-wide heads.
             KeyLoad<kKeys / 32> keys{};                  // of the next tile that may lack keys
             // the row's keys, from the first tile's first one on
-            const int row_p = tok0 + r / G + u.seq.klen - u.seq.qlen - first_key(0);
+            const int row_p = w.tok0 + r / G + w.u.seq.klen - w.u.seq.qlen - first_key(0);
             const int row_a = row_p - A.left, row_b = row_p + A.right + 1;
             auto tile = [&](auto masked, int i) -> bool {
                 const uint32_t ts = trow + i % NB * kKeys;
                 KeyBits<kKeys / 32> kb{};
                 if constexpr (decltype(masked)::value) {
                     if (kMode == kAll || A.mask) {
-                        if (!L::MASK_AHEAD) keys.start(A.mask, u.seq, first_key(i), lane);
+                        if (!L::MASK_AHEAD) keys.start(A.mask, w.u.seq, first_key(i), lane);
                         kb = keys.finish();
-                        if (L::MASK_AHEAD && i + 1 < n) keys.start(A.mask, u.seq, first_key(i + 1), lane);
+                        if (L::MASK_AHEAD && i + 1 < n) keys.start(A.mask, w.u.seq, first_key(i + 1), lane);
                     } else {
                         kb.set_first(kKeys);
                     }
-                    if constexpr (kMode != kAll) kb.clip(band.lo - first_key(i), band.hi - first_key(i));
+                    if constexpr (kMode != kAll) kb.clip(w.band.lo - first_key(i), w.band.hi - first_key(i));
                     if (!kb.all()) {
                         const int jv = i + (i + NB < n ? i + NB : n);   // V's place in the ring, as in the MMA warp
-                        if (!warp_wait(abort_flag, Phase{&full[jv % ST], (uint32_t)(jv / ST) & 1u})) return false;
-                        zero_rows<L::KC, kKeys / 32, 128>(smem + L::OFF_RING + jv % ST * L::TILE, kb, r);
+                        if (!warp_wait(abort_flag, Phase{&full[(base + jv) % ST], (uint32_t)((base + jv) / ST) & 1u})) return false;
+                        zero_rows<L::KC, kKeys / 32, 128>(smem + L::OFF_RING + (base + jv) % ST * L::TILE, kb, r);
                     }
                     if constexpr (kMode != kAll) kb.clip(row_a - i * kKeys, row_b - i * kKeys);
                 }
@@ -387,8 +454,8 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                         }
                     }
                 }
-                const float base = m == -INFINITY ? 0.f : m - kShift;
-                const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+                const float from = m == -INFINITY ? 0.f : m - kShift;
+                const float2 c2 = make_float2(c, c), b2 = make_float2(-from, -from);
                 float2 sum[2] = {};
                 // two rounded probabilities
                 auto pair = [&](int j) {
@@ -427,46 +494,28 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                 l += both.x + both.y;
                 return true;
             };
-            if (L::MASK_AHEAD && partial < n && (kMode == kAll || A.mask))
-                keys.start(A.mask, u.seq, first_key(partial > 0 ? partial : 0), lane);
-            bool ok = true;
+            if (L::MASK_AHEAD && w.partial < n && (kMode == kAll || A.mask))
+                keys.start(A.mask, w.u.seq, first_key(w.partial > 0 ? w.partial : 0), lane);
             for (int i = 0; i < n && ok; ++i) {
                 ok = formed(i);
                 if (!ok) break;
                 tc::tc_fence_after();
-                ok = i >= whole && i < partial ? tile(std::false_type{}, i) : tile(std::true_type{}, i);
+                ok = i >= w.whole && i < w.partial ? tile(std::false_type{}, i) : tile(std::true_type{}, i);
             }
+            if (x_walks(kMode, D, kKeys) && next < A.units) ahead = x_job<kKeys, kMode>(A, next, rank, ways);   // beside the last product
             if (ok) ok = formed(n - 1 + NB);
+            // (so that no wait of the next unit can take this phase for its own)
+            if (x_walks(kMode, D, kKeys) && NB == 2 && n > 1 && ok) ok = formed(n - 2 + NB);
             if (!ok && lane == 0) fail();
             tc::tc_fence_after();
         }
 
-        // ------------------------------------------------------ epilogue
-        const float kLn2 = 0.6931471805599453f;
-        if (kMode != kAll && A.pieces > 1) {
-            // a piece's rows as they are, for k_xjoin
-            if (r < A.tpt * G && tok0 + r / G < u.seq.qlen) {
-                A.part_ml[(int64_t)blockIdx.x * kXRows + r] = make_float2(m, l);
-            }
-            if (n > 0) {
-#pragma unroll 1
-                for (int j = 0; j < D; j += 32) {
-                    float y[32];
-                    tmem_ld32(to + j, reinterpret_cast<uint32_t *>(y));
-                    tc::tmem_wait_ld();
-                    if (r < A.tpt * G && tok0 + r / G < u.seq.qlen) {
-                        float *at = A.parts + ((int64_t)blockIdx.x * kXRows + r) * D + j;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(at + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-                    }
-                }
-            }
-        } else if (ns == 1) {
-            const int tok = tok0 + r / G;
-            const bool mine = r < A.tpt * G && tok < cover;
-            const bool pad = tok >= u.seq.qlen;
-            const int64_t row = (int64_t)(u.seq.q0 + tok) * A.n1 + u.head * G + r % G;
+            if (ways > 1 || !ok) break;                  // stored below
+            // -------------------------------------------------- epilogue
+            const int tok = w.tok0 + r / G;
+            const bool mine = r < A.tpt * G && tok < w.cover;
+            const bool pad = tok >= w.u.seq.qlen;
+            const int64_t row = (int64_t)(w.u.seq.q0 + tok) * A.n1 + w.u.head * G + r % G;
             const bool some = l > 0.f || l != l;         // l is NaN when a score was
             const float inv = some ? 1.f / l : 0.f;
             RowStore<kFp16> rows;
@@ -483,7 +532,37 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                 rows.store(A.o, y, j, lane);
             }
             if (mine) A.lse[row] = pad ? 0.f : some ? (m - kShift) * kLn2 + logf(l) : -INFINITY;
-        } else {
+            if (!x_walks(kMode, D, kKeys) || next >= A.units) break;
+            if (n == 0) ahead = x_job<kKeys, kMode>(A, next, rank, ways);
+            tc::tc_fence_before();                       // O has been read before the next unit's products may follow
+            unit = next;
+            base += 2 * n;
+            formed_by ^= x_parity<NB>(n) ^ (NB == 1 ? n > 0 : (uint32_t)(n > 0) | (uint32_t)(n > 1) << 1);
+            m = -INFINITY;
+            l = 0.f;
+            w = ahead;
+        }
+        const int n = w.n;
+        if (kMode != kAll && A.pieces > 1) {
+            // a piece's rows as they are, for k_xjoin
+            if (r < A.tpt * G && w.tok0 + r / G < w.u.seq.qlen) {
+                A.part_ml[(int64_t)blockIdx.x * kXRows + r] = make_float2(m, l);
+            }
+            if (n > 0) {
+#pragma unroll 1
+                for (int j = 0; j < D; j += 32) {
+                    float y[32];
+                    tmem_ld32(to + j, reinterpret_cast<uint32_t *>(y));
+                    tc::tmem_wait_ld();
+                    if (r < A.tpt * G && w.tok0 + r / G < w.u.seq.qlen) {
+                        float *at = A.parts + ((int64_t)blockIdx.x * kXRows + r) * D + j;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(at + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                    }
+                }
+            }
+        } else if (ns > 1) {
             // partial O, maximum and sum of every rank into its shared memory, then each rank joins its share of the rows
             float2 *ml = reinterpret_cast<float2 *>(smem + L::OFF_ML);
             float *xo = reinterpret_cast<float *>(smem);
@@ -502,7 +581,7 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                 }
             }
             cluster_sync();
-            const int mine = min(A.tpt * G, (cover - tok0) * G);
+            const int mine = min(A.tpt * G, (w.cover - w.tok0) * G);
             auto join = [&](auto np) {
                 // A remote read takes 600 cycles, so a warp has eight (row, rank) pairs' reads in flight while it adds the
                 // eight before up, and what a row needs besides is formed for all rows of a round at once, by lanes NP i + p
@@ -528,23 +607,23 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                                     for (int e = 0; e < E; ++e) y[sub & 1][a][p][e] = peer_ld2(at[p] + off + e * 256);
                         }
                     };
-                    const int k = row_of(lane / NP), p_lane = lane % NP, base = lane & ~(NP - 1), tok = tok0 + k / G;
-                    const bool pad = tok >= u.seq.qlen;
+                    const int k = row_of(lane / NP), p_lane = lane % NP, group = lane & ~(NP - 1), tok = w.tok0 + k / G;
+                    const bool pad = tok >= w.u.seq.qlen;
                     float2 v = make_float2(-INFINITY, 0.f);
                     if (p_lane < ns && k < mine && !pad) v = peer_ld2(peer_addr(tc::smem_u32(ml + k), p_lane));
                     read(0);
                     // place of the row; negative: none
-                    const int row = k < mine ? (u.seq.q0 + tok) * A.n1 + u.head * G + k % G : -1;
+                    const int row = k < mine ? (w.u.seq.q0 + tok) * A.n1 + w.u.head * G + k % G : -1;
                     float top = v.x;
 #pragma unroll
                     for (int o = NP / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                     // A rank that saw something counts even where its weight underflows: 0 times its NaN is NaN, as in an
                     // undivided loop.  (A rank of NaN scores alone has -inf and NaN.)
-                    const float w = v.y == 0.f ? -1.f : xex2(v.x - top);           // -1: saw nothing
+                    const float weight = v.y == 0.f ? -1.f : xex2(v.x - top);           // -1: saw nothing
                     float sum = 0.f;
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
-                        const float wp = __shfl_sync(0xffffffffu, w, base + p), lp = __shfl_sync(0xffffffffu, v.y, base + p);
+                        const float wp = __shfl_sync(0xffffffffu, weight, group + p), lp = __shfl_sync(0xffffffffu, v.y, group + p);
                         if (wp != -1.f) sum += lp * wp;
                     }
                     const bool some = sum > 0.f || sum != sum;
@@ -560,7 +639,7 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                             float2 acc[E] = {};
 #pragma unroll
                             for (int p = 0; p < NP; ++p) {
-                                const float wp = __shfl_sync(0xffffffffu, w, from + p);
+                                const float wp = __shfl_sync(0xffffffffu, weight, from + p);
                                 if (p >= ns || wp == -1.f) continue;
 #pragma unroll
                                 for (int e = 0; e < E; ++e) {
