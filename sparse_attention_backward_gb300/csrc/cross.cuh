@@ -56,6 +56,7 @@ struct XArgs {
     int32_t *count, *status;            // device status: number of words, one word for each CTA
     int32_t n_status;                   // value for *count
     // windowed and paged attention
+    int32_t late;                       // k_xdq: launched behind k_xdkv, whose results it does not need
     int32_t left, right;                // keys before and behind a query's position (kNoLimit: all)
     const int32_t *table, *klens;       // pages [batch][width], key lengths [batch]
     int32_t width, page, pages;         // pages of a sequence at most, rows of a page, pages of the cache

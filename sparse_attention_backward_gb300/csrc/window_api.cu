@@ -209,19 +209,22 @@ extern "C" sag_status window_attn_grad(const swa_desc *desc, const sca_io *io, v
     if (launch_xpre(a, p.fp16, d->d, s) != cudaSuccess) return SAG_ERR_CUDA;
     // k_xpre zeroes the tickets; without query rows there is none
     if (!q_units && cudaMemsetAsync(a.ticket, 0, 2 * sizeof(unsigned), s) != cudaSuccess) return SAG_ERR_CUDA;
-    int before = 0;
+    // k_xdkv first; k_xdq starts as its CTAs leave (window_bwd.cu).  Status words: k_xdq's, then k_xdkv's
+    XArgs q = a;
     if (q_units) {
         use(q_units, (reach(desc->left, desc->right, p.tpt, (int64_t)p.max_k * kXRows) + kXRows - 1) / kXRows);
-        if (launch_wdq(a, *io, *d, s) != cudaSuccess) return SAG_ERR_CUDA;
-        before = a.ctas;
+        q = a;
+        q.late = k_units > 0;
     }
     if (k_units) {
+        const int before = q_units ? q.ctas : 0;
         a.status += before;
         a.ticket += 1;
         use(k_units, (reach(desc->left, desc->right, kXRows, (int64_t)p.max_q * p.tpt) + p.tpt - 1) / p.tpt);
         a.n_status = before + a.ctas;
         if (launch_wdkv(a, *io, *d, s) != cudaSuccess) return SAG_ERR_CUDA;
     }
+    if (q_units && launch_wdq(q, *io, *d, s) != cudaSuccess) return SAG_ERR_CUDA;
     return SAG_OK;
 }
 

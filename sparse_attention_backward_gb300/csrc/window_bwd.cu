@@ -1,4 +1,9 @@
-// Windowed attention, gradient: launches of k_xdq and k_xdkv (xbwd.cuh) over the tiles that a window reaches.
+// Windowed attention, gradient: launches of k_xdkv and k_xdq (xbwd.cuh) over the tiles that a window reaches.
+//
+// k_xdkv goes first, since its units are longer, and k_xdq does not wait for it:
+// both need only k_xpre, which is complete once k_xdkv lets the next kernel's
+// CTAs in.  They start as k_xdkv's leave, and take units by ticket, so the one's
+// last, unfilled round is filled by the other.
 #include "xbwd.cuh"
 
 namespace sag {

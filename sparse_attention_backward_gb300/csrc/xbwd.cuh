@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot, sbase = tc::smem_u32(smem);
-    grid_wait();                                         // statistics and tickets of the kernel before
+    if (!kBand || !A.late) grid_wait();                  // statistics and tickets of the kernel before
     const int ns = A.nsplit, rank = blockIdx.x % ns;
     const int G = A.group;
     grid_next();
@@ -711,6 +711,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         tc::tmem_dealloc(tmem, 512);
     }
     if (threadIdx.x == 0) A.status[blockIdx.x] = *abort_flag ? SAG_ERR_TIMEOUT : SAG_OK;
+    if (kBand && A.late) grid_wait();                    // what follows the call follows k_xdkv too
 }
 
 // ------------------------------------------------------------------ k_xdkv
@@ -760,6 +761,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot, sbase = tc::smem_u32(smem);
     grid_wait();                                         // statistics and tickets of the kernel before
+    if (kBand) grid_next();
     const int ns = A.nsplit, rank = blockIdx.x % ns;
     const int G = A.group;
     auto fail = [&]() { *abort_flag = 1; };

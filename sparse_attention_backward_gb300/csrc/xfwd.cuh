@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
     const int ways = kMode == kAll ? ns : ns * A.pieces; // CTAs of the unit: a cluster's, or pieces
     const int rank = blockIdx.x % ways;
     // windowed: CTAs that share no unit take one after the other, so that the next one's loads and first scores run beside
-    // the last one's end (their loops are short: with a unit a CTA, 32768 tokens and a window of 512 took FIGURE us)
+    // the last one's end (a window of 128 over 32768 tokens, 64 heads of 128: 376 us with a unit a CTA, 342 with this)
     const int unit0 = blockIdx.x / ways;
     auto next_unit = [&](int unit) { return x_walks(kMode, D, kKeys) && ways == 1 ? unit + (int)gridDim.x : 1 << 30; };
     XJob w = x_job<kKeys, kMode>(A, unit0, rank, ways);
@@ -392,9 +392,10 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
             const int row_p = w.tok0 + r / G + w.u.seq.klen - w.u.seq.qlen - first_key(0);
             const int row_a = row_p - A.left, row_b = row_p + A.right + 1;
             auto tile = [&](auto masked, int i) -> bool {
+                const bool lacking = masked;
                 const uint32_t ts = trow + i % NB * kKeys;
                 KeyBits<kKeys / 32> kb{};
-                if constexpr (decltype(masked)::value) {
+                if (lacking) {
                     if (kMode == kAll || A.mask) {
                         if (!L::MASK_AHEAD) keys.start(A.mask, w.u.seq, first_key(i), lane);
                         kb = keys.finish();
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
 #pragma unroll
                     for (int j = 0; j < kHeld; j += 32) tmem_ld32(ts + from + j, reinterpret_cast<uint32_t *>(x) + j);
                     tc::tmem_wait_ld();
-                    if constexpr (decltype(masked)::value) {
+                    if (lacking) {
 #pragma unroll
                         for (int j = 0; j < kHeld; ++j)
                             if (!((kb.w[(from + j) >> 5] >> (j & 31)) & 1u)) x[j] = -INFINITY;
@@ -500,7 +501,12 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                 ok = formed(i);
                 if (!ok) break;
                 tc::tc_fence_after();
-                ok = i >= w.whole && i < w.partial ? tile(std::false_type{}, i) : tile(std::true_type{}, i);
+                // Short loops alternate between the two: with a copy of the code for each, more instructions are fetched than
+                // found (a window of 128 over 32768 tokens: 342 us, with one copy 329).  Long ones hardly do (2 x 8192 causal
+                // tokens: 781 us, with one copy 821).
+                const bool lacking = i < w.whole || i >= w.partial;
+                if constexpr (kMode != kAll && kKeys == 64) ok = tile(lacking, i);
+                else ok = lacking ? tile(std::true_type{}, i) : tile(std::false_type{}, i);
             }
             if (x_walks(kMode, D, kKeys) && next < A.units) ahead = x_job<kKeys, kMode>(A, next, rank, ways);   // beside the last product
             if (ok) ok = formed(n - 1 + NB);
