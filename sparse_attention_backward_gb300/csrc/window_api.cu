@@ -199,11 +199,12 @@ extern "C" sag_status window_attn_grad(const swa_desc *desc, const sca_io *io, v
     const int sms = current_device_sms();
     if (p.fp16 && cudaMemsetAsync(a.norms, 0, sizeof(unsigned) * 2 * (size_t)d->batch * d->n2, s) != cudaSuccess)
         return SAG_ERR_CUDA;
-    // one CTA an SM: a cluster for each unit, or CTAs that take unit after unit
+    // one CTA an SM: CTAs that take unit after unit, or a cluster for each unit where loops are long enough for its join to pay
+    // (8 heads of 128, 1000 x 1000 tokens, 8 tiles: 24 us, split 35; 1 x 4000 tokens, 32 tiles: 49 us, split 27)
     auto use = [&](int units, int64_t tiles) {
         a.units = a.full = a.items = units;
         a.pieces = 1;
-        a.nsplit = split_of(units, (int)tiles, 1, 152);
+        a.nsplit = tiles < 12 ? 1 : split_of(units, (int)tiles / 2, 1, 152);
         a.ctas = a.nsplit > 1 ? units * a.nsplit : units < sms ? units : sms;
     };
     if (launch_xpre(a, p.fp16, d->d, s) != cudaSuccess) return SAG_ERR_CUDA;
