@@ -937,6 +937,34 @@ def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, w
     return _launch(device, stream, call)
 
 
+def _usual_forward(entry, size, q, k, v, key_mask, workspace, desc):
+    """The forward of a kept descriptor with dense tensors of just its shapes on the current device, which is what calls of a
+    few microseconds are: the checks of ``_cross`` in one condition.  None: not such a call."""
+    if bytes(desc) != desc._bytes or not desc._dense:
+        return None
+    qs, ks = desc._shapes
+    dtype, device = desc._dtype, q.get_device()
+    if not (q.dtype is dtype and k.dtype is dtype and v.dtype is dtype and q.shape == qs and k.shape == ks and v.shape == ks
+            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and device >= 0 and k.get_device() == device
+            and v.get_device() == device and _torch._C._cuda_getDevice() == device):
+        return None
+    mask = None
+    if key_mask is not None:
+        if key_mask.dtype is not _torch.bool or key_mask.shape != ks[:-2] or not key_mask.is_contiguous() \
+                or key_mask.get_device() != device:
+            return None
+        mask = key_mask.data_ptr()
+    where = q.device
+    o, lse = _torch.empty_like(q), _torch.empty(qs[:-1], dtype=_torch.float32, device=where)
+    need = _size_of(desc, size)
+    ws = _scratch(workspace, need, where)
+    io = ScaIo(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), None, lse.data_ptr(), mask)
+    st = entry(desc, io, ws.data_ptr(), need, _torch._C._cuda_getCurrentRawStream(device))
+    if st != SAG_OK:
+        raise SagError(st, entry.__name__)
+    return o, lse
+
+
 def _attention_out(q, out):
     """The forward's outputs as _cross wants them."""
     def tensors(io, device, dtype):
@@ -980,7 +1008,12 @@ def cross_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, ke
     ``desc`` (make_cross_desc) replaces cu_seqlens_* and scale; ``check`` reads
     the device status back (this synchronizes the stream).
     """
-    return _cross(_lib_neighbours().cross_attn_fwd, cross_fwd_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,
+    entry = _lib_neighbours().cross_attn_fwd
+    if desc is not None and out is None and stream is None and not check:
+        done = _usual_forward(entry, cross_fwd_workspace_size, q, k, v, key_mask, workspace, desc)
+        if done is not None:
+            return done
+    return _cross(entry, cross_fwd_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask,
                   workspace, stream, check, desc, _attention_out(q, out))
 
 
@@ -1032,7 +1065,12 @@ def window_forward(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, scale=None, l
 
     Causal by default; the other arguments as in ``cross_forward``, with
     ``desc`` from make_window_desc (it replaces left and right too)."""
-    return _cross(_lib_neighbours().window_attn_fwd, window_fwd_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale,
+    entry = _lib_neighbours().window_attn_fwd
+    if desc is not None and out is None and stream is None and not check:
+        done = _usual_forward(entry, window_fwd_workspace_size, q, k, v, key_mask, workspace, desc)
+        if done is not None:
+            return done
+    return _cross(entry, window_fwd_workspace_size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale,
                   key_mask, workspace, stream, check, desc, _attention_out(q, out), _make_window(left, right))
 
 
@@ -1120,6 +1158,31 @@ def _paged(entry, size, x, desc, k_cache, v_cache, page_table, kv_lens, workspac
     return _launch(device, stream, call)
 
 
+def _usual_paged(entry, q, k_cache, v_cache, page_table, kv_lens, workspace, desc):
+    """As ``_usual_forward``, over pages."""
+    if bytes(desc) != desc._bytes or not desc._dense:
+        return None
+    qs, _, cache, table = desc._shapes
+    dtype, device, i32 = desc._dtype, q.get_device(), _torch.int32
+    if not (q.dtype is dtype and k_cache.dtype is dtype and v_cache.dtype is dtype and page_table.dtype is i32
+            and kv_lens.dtype is i32 and q.shape == qs and k_cache.shape == cache and v_cache.shape == cache
+            and page_table.shape == table and kv_lens.shape == table[:1] and q.is_contiguous() and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and page_table.is_contiguous() and kv_lens.is_contiguous() and device >= 0
+            and k_cache.get_device() == device and v_cache.get_device() == device and page_table.get_device() == device
+            and kv_lens.get_device() == device and _torch._C._cuda_getDevice() == device):
+        return None
+    where = q.device
+    o, lse = _torch.empty_like(q), _torch.empty(qs[:-1], dtype=_torch.float32, device=where)
+    need = _size_of(desc, paged_fwd_workspace_size)
+    ws = _scratch(workspace, need, where)
+    io = SpaIo(q.data_ptr(), None, None, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(),
+               o.data_ptr(), lse.data_ptr())
+    st = entry(desc, io, ws.data_ptr(), need, _torch._C._cuda_getCurrentRawStream(device))
+    if st != SAG_OK:
+        raise SagError(st, entry.__name__)
+    return o, lse
+
+
 def _paged_layout(x):
     bsnd = x.dim() == 4
     return dict(dtype=_sag_dtype(x), layout=SAG_LAYOUT_BSND if bsnd else SAG_LAYOUT_TND, s1_max=x.shape[1] if bsnd else 0)
@@ -1167,6 +1230,10 @@ def paged_forward(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q=None, s
     table and the lengths are read on the device, so a captured call may be
     replayed as sequences grow."""
     lib = _lib_neighbours()
+    if desc is not None and out is None and stream is None and not check:
+        done = _usual_paged(lib.paged_attn_fwd, q, k_cache, v_cache, page_table, kv_lens, workspace, desc)
+        if done is not None:
+            return done
     if not q.is_cuda:
         raise ValueError("inputs must be CUDA tensors (there is no CPU path)")
     if desc is None:
@@ -1303,6 +1370,32 @@ def _norm_rotary(entry, size, q, k, dq, dk, rotary, q_weight, k_weight, eps, wei
     return _launch(device, stream, call)
 
 
+def _usual_norm(entry, q, k, q_weight, k_weight, positions, desc):
+    """As ``_usual_forward``: queries and keys, each with a weight of its type, and few sequences."""
+    if bytes(desc) != desc._bytes or not desc._dense or desc.batch > 64 or desc.weight_fp32:
+        return None
+    qs, ks = desc._shapes
+    dtype, device, d = desc._dtype, q.get_device(), ks[-1:]
+    if not (q.dtype is dtype and k.dtype is dtype and q_weight.dtype is dtype and k_weight.dtype is dtype and q.shape == qs
+            and k.shape == ks and q_weight.shape == d and k_weight.shape == d and q.is_contiguous() and k.is_contiguous()
+            and q_weight.is_contiguous() and k_weight.is_contiguous() and device >= 0 and k.get_device() == device
+            and q_weight.get_device() == device and k_weight.get_device() == device
+            and _torch._C._cuda_getDevice() == device):
+        return None
+    pos = None
+    if positions is not None:
+        if positions.dtype is not _torch.int32 or positions.shape != qs[:-2] or not positions.is_contiguous() \
+                or positions.get_device() != device:
+            return None
+        pos = positions.data_ptr()
+    qo, ko = _torch.empty_like(q), _torch.empty_like(k)
+    io = SnrIo(q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), pos, qo.data_ptr(), ko.data_ptr())
+    st = entry(desc, io, None, 0, _torch._C._cuda_getCurrentRawStream(device))
+    if st != SAG_OK:
+        raise SagError(st, entry.__name__)
+    return qo, ko
+
+
 def norm_rotary_forward(q, k, rotary, q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, cu_seqlens=None, positions=None,
                         out=None, workspace=None, stream=None, desc=None):
     """Each head of q [.., n1, d] and k [.., n2, d] (or None) over its root mean
@@ -1311,7 +1404,12 @@ def norm_rotary_forward(q, k, rotary, q_weight=None, k_weight=None, eps=1e-6, we
 
     The other arguments as in ``rotary_forward``; ``desc``
     (make_norm_rotary_desc) replaces rotary, cu_seqlens, eps and weight_offset."""
-    return _norm_rotary(_lib_neighbours().norm_rotary_fwd, norm_rotary_fwd_workspace_size, q, k, None, None, rotary, q_weight,
+    entry = _lib_neighbours().norm_rotary_fwd
+    if desc is not None and out is None and stream is None and k is not None and q_weight is not None and k_weight is not None:
+        done = _usual_norm(entry, q, k, q_weight, k_weight, positions, desc)
+        if done is not None:
+            return done
+    return _norm_rotary(entry, norm_rotary_fwd_workspace_size, q, k, None, None, rotary, q_weight,
                         k_weight, eps, weight_offset, cu_seqlens, positions, out, workspace, stream, desc)
 
 
