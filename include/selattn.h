@@ -606,8 +606,9 @@ sag_status cross_attn_query_error(const void *workspace, void *stream);
  *   left, right   keys before and behind the query's own position, >= 0; -1 (any negative number): no limit
  *
  * The tensors are a sca_io.  What masked, padding and foreign rows hold never
- * counts; the rows of a sequence's own keys have to be finite, whether or not a
- * query's window holds them (a NaN may reach the queries of its tile).
+ * counts.  A sequence's own rows have to be finite, whether or not a window joins
+ * them: a NaN or an infinity in one may reach the results of up to 128 rows
+ * around it whose windows do not hold it (a probability of 0 does not cancel it).
  */
 typedef struct swa_desc {
     sca_desc attn;
@@ -673,7 +674,7 @@ typedef struct spa_desc {
  * A length outside [0, width * page_size] is taken as the nearest one in it, a page outside [0, pages) as page 0 (its
  * tokens are not written); both are reported (SAG_ERR_INDEX), and outputs are then not meaningful.  New tokens at
  * positions before 0 (kv_lens[b] < qlen) attend to nothing and are not written.  Rows of the cache behind a sequence's
- * length, and those before every window, may hold anything.  BSND: padding rows get zeros in attention_out and
+ * length, and those before every window, may hold anything (others: as for the windowed attention).  BSND: padding rows get zeros in attention_out and
  * softmax_lse, and are not appended.  TND: rows behind the last sequence are left as they were.
  */
 typedef struct spa_io {
@@ -724,7 +725,7 @@ typedef struct snr_desc {
 } snr_desc;
 
 /*
- * Tensors (device pointers, 16-byte aligned, positions 4-byte aligned; R rows as in srt_io):
+ * Tensors (device pointers; those of R rows, as in srt_io, 16-byte aligned, the others aligned to their elements):
  *   query, key              [R, n1, d], [R, n2, d]   dtype, read (key NULL when n2 = 0; so are its others)
  *   query_weight, key_weight [d]                     weights; NULL: the norm has none (weight 1, whatever weight_offset says)
  *   positions               [R] int32, or NULL

@@ -209,7 +209,7 @@ sag_status run_norm(const snr_desc *desc, const snr_io *io, void *workspace, siz
     for (int i = 0; i < sides; ++i) {
         if (rows && (!ins[i] || !outs[i] || (grad && !dys[i]))) return SAG_ERR_NULL;
         if (rows && (off(ins[i], 15) || off(outs[i], 15) || (grad && off(dys[i], 15)))) return SAG_ERR_ALIGN;
-        if (off(weights[i], 15) || (grad && off(dws[i], 15))) return SAG_ERR_ALIGN;
+        if (off(weights[i], desc->weight_fp32 ? 3 : 1) || (grad && off(dws[i], 3))) return SAG_ERR_ALIGN;
     }
     if (off(io->positions, 3)) return SAG_ERR_ALIGN;
     NormArgs a{};

@@ -206,10 +206,10 @@ def test_norm_phase2(lib):
             setattr(io, name, keep)
     for name in ("query_weight", "key_weight", "positions"):
         keep = getattr(io, name)
-        setattr(io, name, 4098)
+        setattr(io, name, 4099)
         assert call(io) == ALIGN, name
         setattr(io, name, keep)
-    io.query_weight_grad = 4104
+    io.query_weight_grad = 4098
     assert grad(io) == ALIGN
     # an output over its input with another stride
     io.query_out = io.query

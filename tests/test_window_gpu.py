@@ -208,6 +208,15 @@ def test_pieces_of_padded_batches():
     run(Case([1, 3], [6000, 5000], 2, 1, 128, BF, -1, 0, padded=True, mask=0.2, seed=6))
 
 
+@pytest.mark.parametrize("l1,l2", [([0], [200]), ([200], [0]), ([0, 0], [0, 0]), ([0, 7], [300, 0])])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_sides_without_rows(l1, l2, dtype):
+    c = Case(l1, l2, 4, 2, 64, dtype, 30, 0, seed=17)
+    o, lse, dq, dk, dv = run(c)
+    assert dq.shape == c.q.shape and bool((dk == 0).all()) and bool((dv == 0).all())
+    assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+
+
 def test_many_sequences():
     l = [(b * 7) % 40 + 1 for b in range(300)]
     run(Case(l, l, 2, 1, 64, BF, 11, 0, seed=9))
@@ -392,6 +401,24 @@ def test_paged_is_the_windowed_attention():
     c = Case([100, 64], [500, 640], 8, 2, 128, BF, -1, 0, seed=4)
     check_forward(c, *Pages(c, 64).forward(c))
     check_forward(c, *sab.window_forward(c.q, c.k, c.v, **c.args()))
+
+
+def test_no_new_tokens():
+    c = Case([0, 0], [30, 40], 4, 2, 64, BF, -1, 0, seed=18)
+    p = Pages(c, 16)
+    before = p.k.clone()
+    o, lse = p.forward(c)
+    assert o.shape == c.q.shape
+    sab.paged_append(c.q[:, :2], c.q[:, :2], p.k, p.v, p.table, p.lens, c.cu1, check=True)
+    assert torch.equal(p.k.nan_to_num(0.0), before.nan_to_num(0.0))
+
+
+def test_expected_length_only_splits_the_work():
+    c = Case([1, 3], [6000, 4000], 4, 2, 128, BF, -1, 0, seed=19)
+    p = Pages(c, 64)
+    for expected in (0, 64, 1000, 6000, 2 ** 31 - 1):
+        desc = sab.make_paged_desc(c.cu1, 4, 2, 128, c.scale, p.k.shape[0], 64, p.width, kv_expected=expected)
+        check_forward(c, *sab.paged_forward(c.q, p.k, p.v, p.table, p.lens, desc=desc, check=True))
 
 
 def test_many_paged_sequences():
