@@ -22,16 +22,13 @@ __global__ void __launch_bounds__(kNormThreads, V == 1 ? 1 : S == 3 ? 2 : 4) k_n
     constexpr int P = I::P, kGroups = kNormThreads / kGroup;
     extern __shared__ __align__(16) float smem[];        // sines, [query, key] weights
     __shared__ uint64_t turns[kMaxRot / 2];
-    __shared__ int8_t is_live[kMaxNormTokens];
+    __shared__ TileRows rows;
     const int n1 = A.heads[0], heads = n1 + A.heads[1], half = A.d_rot / 2;
     const int tile = blockIdx.x / A.parts, row0 = tile * A.tokens, n_tok = min(A.tokens, A.rows - row0);
     const int lo = (blockIdx.x - tile * A.parts) * A.chunk, hi = min(lo + A.chunk, n_tok * heads);
     const int group = threadIdx.x / kGroup, lane = threadIdx.x % kGroup, wsize = 2 * A.units * P;
     const bool padded = A.s_max != 0;
-    if (threadIdx.x < n_tok) {
-        int place;
-        is_live[threadIdx.x] = locate_row(A.seq, A.s_max, A.positions, row0 + threadIdx.x, &place);
-    }
+    rows.fill(A, row0, n_tok);
     if (padded) __syncthreads();                         // only padded batches have rows that are not loaded
     Place<kPair, V> at[S];
 #pragma unroll
@@ -46,7 +43,7 @@ __global__ void __launch_bounds__(kNormThreads, V == 1 ? 1 : S == 3 ? 2 : 4) k_n
     auto load = [&](Ahead &a) {
         a.tok = tok;
         a.head = head;
-        if (left > 0 && (!padded || is_live[tok])) {
+        if (left > 0 && (!padded || rows.live[tok])) {
             const int w = head >= n1;
             const uint16_t *p = A.in[w] + ((int64_t)(row0 + tok) * A.in_stride[w] + (head - (w ? n1 : 0)) * A.d);
 #pragma unroll
@@ -70,7 +67,7 @@ __global__ void __launch_bounds__(kNormThreads, V == 1 ? 1 : S == 3 ? 2 : 4) k_n
     fill_weights<kFp16, kPair, V>(A, 0, weights);
     if (A.heads[1]) fill_weights<kFp16, kPair, V>(A, 1, weights + wsize);
     __syncthreads();
-    fill_sines<P>(A, turns, smem, row0, n_tok);
+    fill_sines<P>(A, turns, smem, rows, n_tok);
     __syncthreads();
     int todo = hi - lo;
     auto work = [&](Ahead &a) {
@@ -85,7 +82,7 @@ __global__ void __launch_bounds__(kNormThreads, V == 1 ? 1 : S == 3 ? 2 : 4) k_n
             });
         }
         const int t = a.tok, h = a.head;
-        const bool mine = todo > group, live = !padded || (mine && is_live[t]);
+        const bool mine = todo > group, live = !padded || (mine && rows.live[t]);
         load(a);                                         // two rounds on
         const float r = norm_rsqrt(group_sum<kGroup>(sq.x + sq.y) * A.inv_d + A.eps);
         todo -= kGroups;

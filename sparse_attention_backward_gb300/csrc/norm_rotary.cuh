@@ -28,7 +28,7 @@
 namespace sag {
 
 constexpr int kNormThreads = 256;
-constexpr int kMaxNormTokens = 64, kMaxSines = 1024;     // of a block: tokens, pairs of all of them
+constexpr int kMaxNormTokens = 64, kMaxSines = 2048;     // of a block: tokens, pairs of all of them
 constexpr int kGradBlocks = 304;                         // of a gradient launch: partial sums of the weights' gradients
 
 struct NormArgs {
@@ -229,27 +229,37 @@ __device__ __forceinline__ void run_read(const float *base, int it, int items, f
 // Sines of a block: [tokens][cos, sin][P of each turning item], in floats.
 __host__ __device__ inline int norm_sines(int tokens, int d_rot) { return (tokens * d_rot + 3) & ~3; }
 
-// Sine and cosine of a row's pair of columns; false for padding.
-__device__ __forceinline__ bool sine_of(const NormArgs &A, const uint64_t *turns, int row, int pair, float *sn, float *cs) {
-    int place;
-    if (!locate_row(A.seq, A.s_max, A.positions, row, &place)) return false;
-    const int64_t p = A.positions ? (int64_t)__ldg(A.positions + row) : (int64_t)place;
-    const int32_t t = (int32_t)(((uint64_t)p * turns[pair]) >> 32);
-    sincospif((float)t * 0x1p-31f, sn, cs);
-    *cs *= A.magnitude;
-    *sn *= A.magnitude;
-    return true;
-}
+// A tile's rows: whether each is there, and its position.
+struct TileRows {
+    int32_t position[kMaxNormTokens];
+    int8_t live[kMaxNormTokens];
+    __device__ __forceinline__ void fill(const NormArgs &A, int row0, int n_tok) {
+        if (threadIdx.x >= n_tok) return;
+        const int row = row0 + threadIdx.x;
+        int place;
+        live[threadIdx.x] = locate_row(A.seq, A.s_max, A.positions, row, &place);
+        position[threadIdx.x] = A.positions && live[threadIdx.x] ? __ldg(A.positions + row) : place;
+    }
+};
+
+// The sines of a tile's tokens (of padding rows too: any position's).
 template <int P>
-__device__ __forceinline__ void fill_sines(const NormArgs &A, const uint64_t *turns, float *sines, int row0, int n_tok) {
-    const int half = A.d_rot / 2;
-    for (int j = threadIdx.x; j < n_tok * half; j += kNormThreads) {
-        const int tok = j / half, pair = j - tok * half;
+__device__ __forceinline__ void fill_sines(const NormArgs &A, const uint64_t *turns, float *sines, const TileRows &rows, int n_tok) {
+    const int half = A.d_rot / 2, by_tok = kNormThreads / half, by_pair = kNormThreads - by_tok * half;
+    int tok = threadIdx.x / half, pair = threadIdx.x - tok * half;
+    while (tok < n_tok) {
+        const int32_t t = (int32_t)(((uint64_t)(int64_t)rows.position[tok] * turns[pair]) >> 32);
         float sn, cs;
-        if (!sine_of(A, turns, row0 + tok, pair, &sn, &cs)) continue;
+        sincospif((float)t * 0x1p-31f, &sn, &cs);
         float *at = sines + tok * A.d_rot + run_at<P>(pair / P, pair % P, A.rot_units);
-        at[0] = cs;
-        at[half] = sn;
+        at[0] = cs * A.magnitude;
+        at[half] = sn * A.magnitude;
+        tok += by_tok;
+        pair += by_pair;
+        if (pair >= half) {
+            pair -= half;
+            ++tok;
+        }
     }
 }
 

@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(kNormThreads, V == 1 ? 1 : 2) k_norm_grad(cons
     constexpr bool kHeld = kSums <= 16 && V > 1;         // weights in registers
     extern __shared__ __align__(16) float smem[];        // two tiles' sines, weights, the other side's sums of each thread
     __shared__ uint64_t turns[kMaxRot / 2];
-    __shared__ int8_t is_live[4][kMaxNormTokens];        // of this block's tiles, by their number, two ahead
+    __shared__ TileRows rows[4];                         // of this block's tiles, by their number, two ahead
     const int tokens = A.tokens, half = A.d_rot / 2, sines_size = norm_sines(tokens, A.d_rot), wsize = 2 * A.units * P;
     const int sides = A.heads[1] ? 2 : 1;
     float *weights = smem + 2 * sines_size, *others = weights + sides * wsize + threadIdx.x;
@@ -52,15 +52,14 @@ __global__ void __launch_bounds__(kNormThreads, V == 1 ? 1 : 2) k_norm_grad(cons
     }
     const int tiles = (A.rows + tokens - 1) / tokens;
     auto tile_tokens = [&](int tile) { return min(tokens, A.rows - tile * tokens); };
-    auto liveness = [&](int number) {
+    auto place_rows = [&](int number) {
         const int tile = blockIdx.x + number * gridDim.x;
-        if (tile >= tiles || threadIdx.x >= tile_tokens(tile)) return;
-        int place;
-        is_live[number & 3][threadIdx.x] = locate_row(A.seq, A.s_max, A.positions, tile * tokens + threadIdx.x, &place);
+        if (tile < tiles) rows[number & 3].fill(A, tile * tokens, tile_tokens(tile));
     };
     auto angles = [&](int number) {
         const int tile = blockIdx.x + number * gridDim.x;
-        if (tile < tiles) fill_sines<P>(A, turns, smem + (number & 1) * sines_size, tile * tokens, tile_tokens(tile));
+        if (tile < tiles)
+            fill_sines<P>(A, turns, smem + (number & 1) * sines_size, rows[number & 3], tile_tokens(tile));
     };
     // a group's heads of a tile and side, one every kGroups
     struct Steps {
@@ -89,7 +88,7 @@ __global__ void __launch_bounds__(kNormThreads, V == 1 ? 1 : 2) k_norm_grad(cons
         l_left = l_tile < tiles ? tile_tokens(l_tile) * l.heads : 0;
     };
     auto load = [&]() {
-        if (l_left > group && (!padded || is_live[l_number & 3][l.tok])) {
+        if (l_left > group && (!padded || rows[l_number & 3].live[l.tok])) {
             const int64_t row = (int64_t)l_tile * tokens + l.tok;
             const uint16_t *px = A.in[l_side] + (row * A.in_stride[l_side] + l.head * A.d);
             const uint16_t *py = A.dy[l_side] + (row * A.dy_stride[l_side] + l.head * A.d);
@@ -110,8 +109,8 @@ __global__ void __launch_bounds__(kNormThreads, V == 1 ? 1 : 2) k_norm_grad(cons
             begin();
         }
     };
-    liveness(0);
-    liveness(1);
+    place_rows(0);
+    place_rows(1);
     __syncthreads();                                     // frequencies, rows, weights
     begin();
     load();
@@ -121,7 +120,7 @@ __global__ void __launch_bounds__(kNormThreads, V == 1 ? 1 : 2) k_norm_grad(cons
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++number) {
         __syncthreads();                                 // this tile's sines are there, and the other buffer is free
         angles(number + 1);
-        liveness(number + 2);
+        place_rows(number + 2);
         const float *sines = smem + (number & 1) * sines_size;
         for (int w = 0; w < sides; ++w) {
             Steps c;
@@ -141,7 +140,7 @@ __global__ void __launch_bounds__(kNormThreads, V == 1 ? 1 : 2) k_norm_grad(cons
                 }
             };
             for (int left = tile_tokens(tile) * c.heads; left > 0; left -= kGroups, c.next()) {
-                const bool mine = left > group, live = mine && (!padded || is_live[number & 3][c.tok]);
+                const bool mine = left > group, live = mine && (!padded || rows[number & 3].live[c.tok]);
                 float2 sq = make_float2(0.f, 0.f), dot = sq;
                 float ga[S][P], gb[S][P];
                 I x[S];
