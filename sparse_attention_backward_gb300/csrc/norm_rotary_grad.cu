@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(kNormThreads, V == 1 ? 1 : 2) k_norm_grad(cons
     extern __shared__ __align__(16) float smem[];        // two tiles' sines, weights, the other side's sums of each thread
     __shared__ uint64_t turns[kMaxRot / 2];
     __shared__ TileRows rows[4];                         // of this block's tiles, by their number, two ahead
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tokens = A.tokens, half = A.d_rot / 2, sines_size = norm_sines(tokens, A.d_rot), wsize = 2 * A.units * P;
     const int sides = A.heads[1] ? 2 : 1;
     float *weights = smem + 2 * sines_size, *others = weights + sides * wsize + threadIdx.x;
@@ -247,25 +248,30 @@ __global__ void __launch_bounds__(kNormThreads, V == 1 ? 1 : 2) k_norm_grad(cons
     }
 }
 
-// Adds the blocks' sums up: a block takes 32 columns of one tensor, its warps every eighth of the blocks.
-__global__ void __launch_bounds__(kNormThreads) k_norm_dw(const float *part, int d, int blocks, float *dwq, float *dwk) {
-    __shared__ float sums[kNormThreads / 32][32];
+// Adds the blocks' sums up: a block takes 32 columns of one tensor, its warps every 32nd of the blocks.  It is placed while
+// k_norm_grad runs.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(kSumWarps * 32) k_norm_dw(const float *part, int d, int blocks, float *dwq, float *dwk) {
+    __shared__ float sums[kSumWarps][33];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
     float *dw = blockIdx.y ? dwk : dwq;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!dw) return;
     float u = 0.f;
     if (c < d) {
-#pragma unroll 8
-        for (int k = warp; k < blocks; k += kNormThreads / 32) u += part[((int64_t)k * 2 + blockIdx.y) * d + c];
+#pragma unroll
+        for (int i = 0; i < (kGradBlocks + kSumWarps - 1) / kSumWarps; ++i) {
+            const int k = warp + i * kSumWarps;
+            if (k < blocks) u += part[((int64_t)k * 2 + blockIdx.y) * d + c];
+        }
     }
     sums[warp][lane] = u;
     __syncthreads();
-    if (warp == 0 && c < d) {
-        float t = 0.f;
+    // warp w adds the sums of column w of the 32 up, in the warps' order
+    float t = sums[lane][warp];
 #pragma unroll
-        for (int k = 0; k < kNormThreads / 32; ++k) t += sums[k][lane];
-        dw[c] = t;
-    }
+    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0 && blockIdx.x * 32 + warp < d) dw[blockIdx.x * 32 + warp] = t;
 }
 
 }  // namespace
@@ -283,8 +289,17 @@ cudaError_t launch_norm_grad(const NormArgs &a, bool fp16, const NormShape &p, i
         return cudaGetLastError();
     });
     if (e != cudaSuccess || !(a.dw[0] || a.dw[1])) return e;
-    k_norm_dw<<<dim3((unsigned)(a.d + 31) / 32, a.heads[1] ? 2 : 1), kNormThreads, 0, s>>>(a.part, a.d, blocks, a.dw[0], a.dw[1]);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.d + 31) / 32, a.heads[1] ? 2 : 1);
+    cfg.blockDim = dim3(kSumWarps * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const float *part = a.part;
+    return cudaLaunchKernelEx(&cfg, k_norm_dw, part, (int)a.d, blocks, a.dw[0], a.dw[1]);
 }
 
 }  // namespace sag
