@@ -29,9 +29,100 @@ Parts parts_of(int64_t units, int64_t keys, int d, size_t at) {
     return p;
 }
 
-sag_status w_plan(const swa_desc *d, bool grad, XPlan *p, Parts *parts) {
+// How a gradient kernel's units are shared: a cluster for each; or CTAs (one an SM) that take units, or `pieces` of each, as they
+// come to them, from the longest on.
+struct Share {
+    int units, nsplit, pieces;
+    int64_t items() const { return (int64_t)units * pieces; }
+    size_t part_bytes(int cols) const { return pieces > 1 ? (size_t)items() * 256 * cols * sizeof(float) : 0; }
+};
+// One way to share them: the longest item and all of them together, in tiles of the loop.  A piece takes about fourteen tiles
+// more (its start, its sums' way through the workspace) and one for each piece added up, a cluster's join four.
+struct Way {
+    Share share;
+    int64_t one, all;
+};
+int ways_of(int64_t units, int64_t longest, int64_t total, Way *to) {
+    int n = 0;
+    to[n++] = {{(int)units, 1, 1}, longest, total};
+    if (units == 0 || units > kMaxPieces || longest < 12) return n;
+    const int ns = split_of(units, (int)(longest / 2), 1, 152);
+    if (ns > 1) {
+        const int64_t one = (longest + ns - 1) / ns + 4;
+        to[n++] = {{(int)units, ns, 1}, one, one * units * ns};
+    }
+    for (int s = 2; s <= kMaxSplit && s * 2 <= longest && units * s <= kMaxPieces; ++s)
+        to[n++] = {{(int)units, 1, s}, (longest + s - 1) / s + 14 + s, total + 14 * units * s};
+    return n;
+}
+// Both kernels run side by side on 152 SMs; a tile of k_xdkv takes five units of time, one of k_xdq four.  Causal units differ: 64
+// key tiles of 2 heads have loops of 4 to 256 query tiles of 32 tokens, and the longest would hold up the rest (8192 tokens, 8 / 2
+// heads of 128: 381 us, the units of k_xdkv in two pieces each 286).  From the descriptor alone, so that a call's sums have the
+// same order on every GB300.
+void share_both(int64_t q_units, int64_t q_most, int64_t q_all, int64_t k_units, int64_t k_most, int64_t k_all, Share *q, Share *k) {
+    Way qs[kMaxSplit + 2], ks[kMaxSplit + 2];
+    const int nq = ways_of(q_units, q_most, q_all, qs), nk = ways_of(k_units, k_most, k_all, ks);
+    int64_t best = INT64_MAX;
+    for (int i = 0; i < nq; ++i)
+        for (int j = 0; j < nk; ++j) {
+            int64_t t = (4 * qs[i].all + 5 * ks[j].all) / 152;
+            t = 4 * qs[i].one > t ? 4 * qs[i].one : t;
+            t = 5 * ks[j].one > t ? 5 * ks[j].one : t;
+            if (t >= best) continue;
+            best = t;
+            *q = qs[i].share;
+            *k = ks[j].share;
+        }
+}
+
+struct GradPlan {
+    Share q, k;
+    size_t o_parts_q, o_parts_k, o_arrived, total;
+};
+GradPlan grad_plan(const swa_desc *desc, const XPlan &p) {
+    const sca_desc *d = &desc->attn;
+    GradPlan g{};
+    const int64_t left = limit_of(desc->left), right = limit_of(desc->right);
+    const int64_t q_units = p.q_tiles * d->n2, k_units = p.k_tiles * d->n2;
+    int64_t q_most = 0, q_all = 0, k_most = 0, k_all = 0;
+    for (int b = 0; b < d->batch && (q_units <= kMaxPieces || k_units <= kMaxPieces); ++b) {
+        const int64_t ql = d->cu_seqlens_q[b + 1] - d->cu_seqlens_q[b], kl = d->cu_seqlens_kv[b + 1] - d->cu_seqlens_kv[b];
+        const int64_t off = kl - ql;
+        auto count = [](int64_t lo, int64_t hi, int64_t step) { return hi > lo ? (hi - lo + step - 1) / step : 0; };
+        if (q_units <= kMaxPieces)
+            for (int64_t t = 0; t < ql; t += p.tpt) {
+                const int64_t last = (t + p.tpt < ql ? t + p.tpt : ql) - 1, lo = t + off - left, hi = last + off + right + 1;
+                const int64_t n = count(lo > 0 ? lo : 0, hi < kl ? hi : kl, kXRows);
+                q_most = n > q_most ? n : q_most;
+                q_all += n * d->n2;
+            }
+        if (k_units <= kMaxPieces)
+            for (int64_t k = 0; k < kl; k += kXRows) {
+                const int64_t last = (k + kXRows < kl ? k + kXRows : kl) - 1, lo = k - off - right, hi = last - off + left + 1;
+                const int64_t from = lo > 0 ? lo / p.tpt * p.tpt : 0, n = count(from, hi < ql ? hi : ql, p.tpt);
+                k_most = n > k_most ? n : k_most;
+                k_all += n * d->n2;
+            }
+    }
+    // pairs of tiles are about as many on either side
+    if (q_units > kMaxPieces) q_all = k_all;
+    if (k_units > kMaxPieces) k_all = q_all;
+    share_both(q_units, q_most, q_all, k_units, k_most, k_all, &g.q, &g.k);
+    g.o_parts_q = p.o_parts;                // (x_plan's own are the last)
+    g.o_parts_k = up256(g.o_parts_q + g.q.part_bytes(d->d / 2));
+    g.o_arrived = up256(g.o_parts_k + g.k.part_bytes(d->d));
+    g.total = up256(g.o_arrived + sizeof(unsigned) * 8 * (size_t)((g.q.pieces > 1 ? g.q.units : 0) + (g.k.pieces > 1 ? g.k.units : 0)));
+    return g;
+}
+
+sag_status w_plan(const swa_desc *d, bool grad, XPlan *p, Parts *parts, GradPlan *g) {
     const sag_status st = x_plan(d ? &d->attn : nullptr, grad, p);
-    if (st != SAG_OK || grad) return st;
+    if (st != SAG_OK) return st;
+    if (grad) {
+        *g = grad_plan(d, *p);
+        p->total = g->total;
+        return SAG_OK;
+    }
     int64_t most = 0;
     for (int b = 0; b < d->attn.batch; ++b) {
         const int64_t k = d->attn.cu_seqlens_kv[b + 1] - d->attn.cu_seqlens_kv[b];
@@ -140,7 +231,7 @@ extern "C" sag_status window_attn_fwd_workspace_size(const swa_desc *desc, size_
     if (!workspace_bytes) return SAG_ERR_NULL;
     XPlan p;
     Parts parts;
-    const sag_status st = w_plan(desc, false, &p, &parts);
+    const sag_status st = w_plan(desc, false, &p, &parts, nullptr);
     if (st == SAG_OK) *workspace_bytes = p.total;
     return st;
 }
@@ -148,7 +239,8 @@ extern "C" sag_status window_attn_fwd_workspace_size(const swa_desc *desc, size_
 extern "C" sag_status window_attn_grad_workspace_size(const swa_desc *desc, size_t *workspace_bytes) {
     if (!workspace_bytes) return SAG_ERR_NULL;
     XPlan p;
-    const sag_status st = w_plan(desc, true, &p, nullptr);
+    GradPlan g;
+    const sag_status st = w_plan(desc, true, &p, nullptr, &g);
     if (st == SAG_OK) *workspace_bytes = p.total;
     return st;
 }
@@ -157,7 +249,7 @@ extern "C" sag_status window_attn_fwd(const swa_desc *desc, const sca_io *io, vo
                                       void *stream) {
     XPlan p;
     Parts parts;
-    sag_status st = w_plan(desc, false, &p, &parts);
+    sag_status st = w_plan(desc, false, &p, &parts, nullptr);
     if (st != SAG_OK) return st;
     const sca_desc *d = &desc->attn;
     st = x_check(d, io, p, false, workspace, workspace_bytes);
@@ -181,7 +273,8 @@ extern "C" sag_status window_attn_fwd(const swa_desc *desc, const sca_io *io, vo
 extern "C" sag_status window_attn_grad(const swa_desc *desc, const sca_io *io, void *workspace, size_t workspace_bytes,
                                        void *stream) {
     XPlan p;
-    sag_status st = w_plan(desc, true, &p, nullptr);
+    GradPlan g;
+    sag_status st = w_plan(desc, true, &p, nullptr, &g);
     if (st != SAG_OK) return st;
     const sca_desc *d = &desc->attn;
     st = x_check(d, io, p, true, workspace, workspace_bytes);
@@ -199,29 +292,34 @@ extern "C" sag_status window_attn_grad(const swa_desc *desc, const sca_io *io, v
     const int sms = current_device_sms();
     if (p.fp16 && cudaMemsetAsync(a.norms, 0, sizeof(unsigned) * 2 * (size_t)d->batch * d->n2, s) != cudaSuccess)
         return SAG_ERR_CUDA;
-    // one CTA an SM: CTAs that take unit after unit, or a cluster for each unit where loops are long enough for its join to pay
-    // (8 heads of 128, 1000 x 1000 tokens, 8 tiles: 24 us, split 35; 1 x 4000 tokens, 32 tiles: 49 us, split 27)
-    auto use = [&](int units, int64_t tiles) {
-        a.units = a.full = a.items = units;
-        a.pieces = 1;
-        a.nsplit = tiles < 12 ? 1 : split_of(units, (int)tiles / 2, 1, 152);
-        a.ctas = a.nsplit > 1 ? units * a.nsplit : units < sms ? units : sms;
+    auto use = [&](XArgs *x, const Share &h, size_t parts) {
+        x->units = h.units;
+        x->full = h.pieces > 1 ? 0 : h.units;
+        x->pieces = h.pieces;
+        x->nsplit = h.nsplit;
+        x->items = (int)h.items();
+        x->ctas = h.nsplit > 1 ? h.units * h.nsplit : x->items < sms ? x->items : sms;
+        x->parts = reinterpret_cast<float *>(ws + parts);
     };
+    unsigned *arrived = reinterpret_cast<unsigned *>(ws + g.o_arrived);
+    const int q_counts = g.q.pieces > 1 ? 8 * g.q.units : 0;
+    a.arrived = arrived;
+    a.n_arrived = q_counts + (g.k.pieces > 1 ? 8 * g.k.units : 0);
     if (launch_xpre(a, p.fp16, d->d, s) != cudaSuccess) return SAG_ERR_CUDA;
-    // k_xpre zeroes the tickets; without query rows there is none
+    // k_xpre zeroes the tickets and counters; without query rows there may be none (and no pieces)
     if (!q_units && cudaMemsetAsync(a.ticket, 0, 2 * sizeof(unsigned), s) != cudaSuccess) return SAG_ERR_CUDA;
     // k_xdkv first; k_xdq starts as its CTAs leave (window_bwd.cu).  Status words: k_xdq's, then k_xdkv's
     XArgs q = a;
     if (q_units) {
-        use(q_units, (reach(desc->left, desc->right, p.tpt, (int64_t)p.max_k * kXRows) + kXRows - 1) / kXRows);
-        q = a;
+        use(&q, g.q, g.o_parts_q);
         q.late = k_units > 0;
     }
     if (k_units) {
         const int before = q_units ? q.ctas : 0;
         a.status += before;
         a.ticket += 1;
-        use(k_units, (reach(desc->left, desc->right, kXRows, (int64_t)p.max_q * p.tpt) + p.tpt - 1) / p.tpt);
+        a.arrived = arrived + q_counts;
+        use(&a, g.k, g.o_parts_k);
         a.n_status = before + a.ctas;
         if (launch_wdkv(a, *io, *d, s) != cudaSuccess) return SAG_ERR_CUDA;
     }

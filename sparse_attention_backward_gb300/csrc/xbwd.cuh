@@ -211,7 +211,8 @@ struct Item {
             ranks = A.pieces;
         }
     }
-    // of a loop of `tiles`; a piece always has some (only units of long, alike loops are cut)
+    // of a loop of `tiles`; a piece always has some (only units of long, alike loops are cut), but for windowed attention,
+    // whose units differ
     __device__ __forceinline__ void share(int tiles, Work *w) const {
         x_share(tiles, rank, ranks, &w->t0, &w->n);
         w->piece = piece;
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             // beside the last product: the places of this unit's rows, and the next unit (they took 600 of a unit's 5400 cycles
             // after it, with one tile a unit)
             const int piece = w.piece;
-            const bool pad = n == 0 || w.first + my_tok >= w.seq.qlen;
+            const bool pad = (n == 0 && (!kBand || piece < 0)) || w.first + my_tok >= w.seq.qlen;   // (others have a piece's sums)
             RowStore<kFp16> rows;
             if (ns == 1 && ok) {
                 rows.rows(place(my_tok, my_head), lane);

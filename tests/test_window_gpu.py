@@ -204,6 +204,26 @@ def test_few_queries_of_long_contexts(d, dtype, n1, n2, l1, l2, left):
     run(Case(l1, l2, n1, n2, d, dtype, left, 0, seed=5))
 
 
+# units of few heads and long loops are cut into pieces, some of which have nothing to do, or shared by clusters: the first, of
+# the units of dK and dV; the next two of both kernels', or with a cluster for the others; then a cluster for dQ alone
+@pytest.mark.parametrize("dtype,drop", [(BF, None), (HF, 0.3)])
+@pytest.mark.parametrize("l1,l2,n1,n2,d,left,right", [
+    ([1195], [1195], 32, 8, 128, 2000, 0), ([697, 5290], [348, 10580], 1, 1, 64, 1000, -1), ([5327, 2511], [5327, 1255], 1, 1, 128, -1, 0),
+    ([705], [1410], 1, 1, 128, -1, 0), ([3000], [3000], 2, 1, 128, -1, 0), ([2500, 300, 0], [2500, 700, 60], 8, 2, 64, -1, 0), ([4100], [4100], 4, 4, 64, 2600, 0),
+    ([2000], [2900], 6, 2, 128, -1, 300), ([3500], [1700], 2, 2, 64, -1, 0), ([1800], [1800], 16, 1, 128, 1700, -1)])
+def test_gradient_in_pieces(l1, l2, n1, n2, d, dtype, drop, left, right):
+    run(Case(l1, l2, n1, n2, d, dtype, left, right, mask=drop, seed=l1[0]))
+
+
+def test_pieces_are_added_up_in_their_order():
+    c = Case([3000], [3000], 8, 2, 128, BF, -1, 0, seed=23)
+    o, lse = sab.window_forward(c.q, c.k, c.v, **c.args())
+    want = sab.window_backward(c.q, c.k, c.v, o, c.dy, lse, check=True, **c.args())
+    for _ in range(20):
+        for x, y in zip(want, sab.window_backward(c.q, c.k, c.v, o, c.dy, lse, **c.args())):
+            assert torch.equal(x, y)
+
+
 def test_pieces_of_padded_batches():
     run(Case([1, 3], [6000, 5000], 2, 1, 128, BF, -1, 0, padded=True, mask=0.2, seed=6))
 
