@@ -68,8 +68,10 @@ struct FwdShape {
     static_assert(OFF_ML + kXRows * 8 <= OFF_BAR, "the exchange overlays Q and the ring");
     static_assert(CTAS * (TOTAL + 1024) <= 228 * 1024, "shared memory of an SM");
 };
-// XF_S: scores of an even / odd tile formed, and P V of the tile two before complete; XF_P: P written; XF_QE: Q has been read
-enum { XF_Q = 0, XF_S = 1, XF_P = 3, XF_DRAIN = 5, XF_QE = 6, XF_FULL = 7 };
+// XF_S: scores of an even / odd tile formed, and P V of the tile two before complete; XF_P: P written.  Where CTAs take unit
+// after unit, also XF_QE: Q has been read, and XF_O: the unit's last P V complete.  It is no phase of XF_S there: the next
+// unit's scores may complete before a softmax warp looks, which would wait for a phase that is two behind (modelled in the tests).
+enum { XF_Q = 0, XF_S = 1, XF_P = 3, XF_DRAIN = 5, XF_QE = 6, XF_O = 7, XF_FULL = 8 };
 
 // Whether CTAs take unit after unit: with short loops, which 128-key tiles are not for, and registers for it (64-wide heads,
 // four CTAs an SM, have none to spare).
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                     }
                     tc::mma_commit_warp(&empty[(base + jv) % ST]);
                     if (more) issue_s(i + NB, jv + 1);
-                    else tc::mma_commit_warp(&bars[XF_S + i % NB]);
+                    else tc::mma_commit_warp(&bars[x_walks(kMode, D, kKeys) && i + 1 == n ? XF_O : XF_S + i % NB]);
                 }
                 unit = next_unit(unit);
                 if (!ok || !x_walks(kMode, D, kKeys) || unit >= A.units) break;
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
         float m = -INFINITY, l = 0.f;                    // reference maximum (log2 units), sum
         const float kLn2 = 0.6931471805599453f;
         int base = 0;                                    // loads before this unit
-        uint32_t formed_by = 0;                          // parities of XF_S before this unit, a bit a barrier
+        uint32_t formed_by = 0, ended = 0;               // parities of XF_S (a bit a barrier) and of XF_O before this unit
         for (int unit = unit0;;) {
         const int n = w.n, next = next_unit(unit);
         bool ok = true;
@@ -465,6 +467,9 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                     sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], e);
                     return xpack<kFp16>(e.x, e.y);
                 };
+                // the product two tiles before is complete, whether or not that was waited for: so no wait of the next unit finds
+                // its barrier a phase behind
+                if (x_walks(kMode, D, kKeys) && NB == 2 && n > 1 && i + 1 == n && !formed(n)) return false;
                 auto written = [&](int which) {
                     tmem_wait_st();
                     tc::tc_fence_before();
@@ -509,9 +514,8 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                 else ok = lacking ? tile(std::true_type{}, i) : tile(std::false_type{}, i);
             }
             if (x_walks(kMode, D, kKeys) && next < A.units) ahead = x_job<kKeys, kMode>(A, next, rank, ways);   // beside the last product
-            if (ok) ok = formed(n - 1 + NB);
-            // (so that no wait of the next unit can take this phase for its own)
-            if (x_walks(kMode, D, kKeys) && NB == 2 && n > 1 && ok) ok = formed(n - 2 + NB);
+            if (ok) ok = x_walks(kMode, D, kKeys) ? wait(XF_O, ended) : formed(n - 1 + NB);
+            ended ^= 1;
             if (!ok && lane == 0) fail();
             tc::tc_fence_after();
         }
@@ -543,7 +547,7 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
             tc::tc_fence_before();                       // O has been read before the next unit's products may follow
             unit = next;
             base += 2 * n;
-            formed_by ^= x_parity<NB>(n) ^ (NB == 1 ? n > 0 : (uint32_t)(n > 0) | (uint32_t)(n > 1) << 1);
+            formed_by ^= x_parity<NB>(n) ^ (NB == 2 && n > 1 ? 1u << (n % NB) : 0u);
             m = -INFINITY;
             l = 0.f;
             w = ahead;
