@@ -1026,13 +1026,18 @@ def cross_backward(q, k, v, o, dy, lse, cu_seqlens_q=None, cu_seqlens_kv=None, s
 
 
 # ------------------------------------------------------- windowed attention
+def _reach(keys):
+    """A window's side as the descriptors hold it: beyond 32 bits it has no limit that shows."""
+    return max(-1, min(int(keys), 2 ** 31 - 1))
+
+
 def make_window_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, left=-1, right=0, dtype=SAG_BF16, layout=SAG_LAYOUT_TND,
                      s1_max=0, s2_max=0) -> SwaDesc:
     """Descriptor of a windowed attention; ``left`` and ``right`` are the keys
     before and behind a query's position that it attends to (-1: all of them).
     Keeps the host arrays alive; the tensor calls take strides from the tensors."""
     base = make_cross_desc(cu_seqlens_q, cu_seqlens_kv, n1, n2, d, scale, dtype, layout, s1_max, s2_max)
-    desc = SwaDesc(attn=base, left=int(left), right=int(right))
+    desc = SwaDesc(attn=base, left=_reach(left), right=_reach(right))
     desc._keep = base._keep
     return _derive(desc, dense=True)
 
@@ -1092,8 +1097,8 @@ def make_paged_desc(cu_seqlens_q, n1, n2, d, scale, pages, page_size, width, lef
     tensor calls take strides from the tensors."""
     cq = _i32(cu_seqlens_q)
     desc = SpaDesc(batch=len(cq) - 1, n1=n1, n2=n2, d=d, dtype=dtype, layout=int(layout), scale=float(scale),
-                   cu_seqlens_q=ctypes.cast(cq, ctypes.POINTER(ctypes.c_int32)), s1_max=int(s1_max), left=int(left),
-                   right=int(right), page_size=int(page_size), pages=int(pages), width=int(width),
+                   cu_seqlens_q=ctypes.cast(cq, ctypes.POINTER(ctypes.c_int32)), s1_max=int(s1_max), left=_reach(left),
+                   right=_reach(right), page_size=int(page_size), pages=int(pages), width=int(width),
                    kv_expected=int(kv_expected), reserved_=0)
     desc._keep = (cq,)
     return _derive(desc, dense=True)
@@ -1123,7 +1128,10 @@ def _cache_strides(name, t, shape, dtype, device):
     if (d > 1 and t.stride(3) != 1) or (heads > 1 and t.stride(2) != d):
         raise ValueError(f"{name}: the heads and columns of a row must be dense")
     row = t.stride(1) if page > 1 else heads * d
-    return row, t.stride(0) if pages > 1 else row * page
+    between = t.stride(0) if pages > 1 else row * page
+    if row < heads * d or between < row * (page - 1) + heads * d:
+        raise ValueError(f"{name}: rows and pages must not overlap or interleave")
+    return row, between
 
 
 def _paged(entry, size, x, desc, k_cache, v_cache, page_table, kv_lens, workspace, stream, check, fill):

@@ -1,5 +1,8 @@
-// Cross attention, forward: O = softmax(scale Q K^T) V over the key rows of
-// each query row's sequence, one pass with a running maximum and sum.
+// Attention, forward: O = softmax(scale Q K^T) V over the key rows of each query
+// row's sequence that a mode lets it see, one pass with a running maximum and sum.
+//   kAll    cross attention: all of them
+//   kBand   a window of positions around the row's own (cross.cuh)
+//   kPaged  the same over a cache in pages, whose lengths the device holds
 //
 // A CTA takes a tile of 128 query rows of one key/value head and walks over
 // key tiles of 64 (or 128): S = Q K^T and O += P V on the tensor cores

@@ -96,6 +96,26 @@ def test_window_phase2(lib):
     assert lib.window_attn_query_error(None, None) == NULL
 
 
+@pytest.mark.parametrize("given,held", [(0, 0), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1),
+                                        (2 ** 63, 2 ** 31 - 1), (-1, -1), (-2 ** 32, -1), (-2 ** 31 - 5, -1)])
+def test_sides_beyond_32_bits(given, held):
+    w = sab.make_window_desc([0, 3], [0, 5], 2, 2, 64, 0.1, left=given, right=given)
+    p = sab.make_paged_desc([0, 3], 2, 2, 64, 0.1, 8, 16, 4, left=given, right=given)
+    assert (w.left, w.right, p.left, p.right) == (held,) * 4
+
+
+@pytest.mark.parametrize("step,ok", [((64, 0), False), ((0, 128), False), ((128 * 15, 128), False), ((128 * 16, 64), False),
+                                     ((128 * 16, 127), False), ((256, 128), False), ((128 * 17, 128), True), ((256 * 16, 256), True)])
+def test_caches_whose_rows_overlap_are_refused(step, ok):
+    """Strides of 0 mean dense ones to the library, which would look beyond an expanded tensor."""
+    t = torch.empty(64 * 1024, dtype=torch.bfloat16).as_strided((4, 16, 2, 64), step + (64, 1))
+    if ok:
+        assert sab._cache_strides("k_cache", t, t.shape, t.dtype, t.get_device()) == (step[1], step[0])
+        return
+    with pytest.raises(ValueError, match="overlap"):
+        sab._cache_strides("k_cache", t, t.shape, t.dtype, t.get_device())
+
+
 def test_window_arguments():
     z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
     with pytest.raises(ValueError):
