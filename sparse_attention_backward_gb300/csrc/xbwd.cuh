@@ -59,6 +59,7 @@ template <bool kFp16, int D>
 __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
     constexpr int LPR = D / 8;                           // lanes a row, 16 bytes each
     constexpr int RPW = 32 / LPR;
+    constexpr int STEP = 8 * RPW, AHEAD = 4;             // rows of a step of the block, steps whose loads are in flight
     __shared__ float red[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = lane % LPR;
@@ -74,65 +75,95 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
         const XUnit u = x_decode<&SeqRow::qtile0>(A, blockIdx.x);
         slot = ((int64_t)u.b * A.n2 + u.head) * 2;
         float *st = A.stats + u.tile_id * 256;
-#pragma unroll 4
-        for (int r = warp * RPW + lane / LPR; r < kXRows; r += 8 * RPW) {
-            const int tok = u.tile * A.tpt + r / A.group;
-            const bool live = r < A.tpt * A.group && tok < u.seq.qlen;
-            const int64_t row = (int64_t)(u.seq.q0 + tok) * A.n1 + u.head * A.group + r % A.group;
-            float dot = 0.f, nrm = 0.f, lse = -INFINITY;
-            if (live) {
-                uint4 a = *reinterpret_cast<const uint4 *>(A.o_in + row * D + part * 8);
-                uint4 b = *reinterpret_cast<const uint4 *>(A.dy + row * D + part * 8);
-                lse = A.lse[row];
-                const uint32_t *pa = &a.x, *pb = &b.x;
+        int r = warp * RPW + lane / LPR, tok = r / A.group, h = r - tok * A.group;
+        const int step_tok = STEP / A.group, step_h = STEP - step_tok * A.group;
+        const int row0 = u.seq.q0 + u.tile * A.tpt, most = min(A.tpt, u.seq.qlen - u.tile * A.tpt);
+#pragma unroll
+        for (int done = 0; done < kXRows / STEP; done += AHEAD) {
+            uint4 a[AHEAD], b[AHEAD];
+            float lses[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                a[k] = b[k] = make_uint4(0, 0, 0, 0);
+                lses[k] = -INFINITY;
+                if (tok < most) {
+                    const int64_t row = (int64_t)(row0 + tok) * A.n1 + u.head * A.group + h;
+                    a[k] = *reinterpret_cast<const uint4 *>(A.o_in + row * D + part * 8);
+                    b[k] = *reinterpret_cast<const uint4 *>(A.dy + row * D + part * 8);
+                    lses[k] = A.lse[row];
+                }
+                tok += step_tok;
+                h += step_h;
+                if (h >= A.group) {
+                    h -= A.group;
+                    ++tok;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const uint32_t *pa = &a[k].x, *pb = &b[k].x;
+                float dot = 0.f, nrm = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float y0 = u16_to_f<kFp16>((uint16_t)pb[i]), y1 = u16_to_f<kFp16>((uint16_t)(pb[i] >> 16));
                     dot += u16_to_f<kFp16>((uint16_t)pa[i]) * y0 + u16_to_f<kFp16>((uint16_t)(pa[i] >> 16)) * y1;
                     nrm += y0 * y0 + y1 * y1;
                 }
-            }
 #pragma unroll
-            for (int o = LPR / 2; o; o >>= 1) {
-                dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                nrm += __shfl_xor_sync(0xffffffffu, nrm, o);
+                for (int o = LPR / 2; o; o >>= 1) {
+                    dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                    if constexpr (kFp16) nrm += __shfl_xor_sync(0xffffffffu, nrm, o);
+                }
+                if (part == 0) {
+                    const bool some = lses[k] != -INFINITY;
+                    st[r] = some ? -lses[k] * kLog2e : -INFINITY;   // makes P = 0 where there is nothing
+                    st[128 + r] = some ? -dot : 0.f;
+                    if constexpr (kFp16) A.row_norms[u.tile_id * kXRows + r] = nrm;
+                }
+                if (nrm < INFINITY) top = fmaxf(top, nrm);
+                r += STEP;
             }
-            if (part == 0) {
-                const bool some = live && lse != -INFINITY;
-                st[r] = some ? -lse * kLog2e : -INFINITY;   // makes P = 0 where there is nothing
-                st[128 + r] = some ? -dot : 0.f;
-                if constexpr (kFp16) A.row_norms[u.tile_id * kXRows + r] = nrm;
-            }
-            if (nrm < INFINITY) top = fmaxf(top, nrm);
         }
     } else {
         // zeros for the gradients of absent states; fp16: row norms of V
         const XUnit u = x_decode<&SeqRow::ktile0>(A, blockIdx.x - q_units);
         slot = ((int64_t)u.b * A.n2 + u.head) * 2 + 1;
         const int cover = A.s2_pad ? A.s2_pad : u.seq.klen;
-#pragma unroll 4
-        for (int r = warp * RPW + lane / LPR; r < kXRows; r += 8 * RPW) {
-            const int key = u.tile * kXRows + r;
-            const int64_t row = (int64_t)u.seq.k0 + key;
-            const bool there = key < u.seq.klen && (!A.mask || A.mask[row]);
-            if (!there && key < cover) {
-                const int64_t at = (row * A.n2 + u.head) * D + part * 8;
-                *reinterpret_cast<uint4 *>(A.dk + at) = *reinterpret_cast<uint4 *>(A.dv + at) = make_uint4(0, 0, 0, 0);
-            }
+#pragma unroll
+        for (int done = 0; done < kXRows / STEP; done += AHEAD) {
+            uint4 a[AHEAD];
+            bool there[AHEAD];
+            const int key0 = u.tile * kXRows + done * STEP + warp * RPW + lane / LPR;
+            const int64_t row0 = (int64_t)u.seq.k0 + key0;
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                there[k] = key0 + k * STEP < u.seq.klen && (!A.mask || A.mask[row0 + k * STEP]);
             if constexpr (kFp16) {
-                float nrm = 0.f;
-                if (there) {
-                    uint4 a = *reinterpret_cast<const uint4 *>(A.v_in + row * A.v_stride + u.head * D + part * 8);
-                    const uint32_t *pa = &a.x;
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) {
+                    a[k] = make_uint4(0, 0, 0, 0);
+                    if (there[k])
+                        a[k] = *reinterpret_cast<const uint4 *>(A.v_in + (row0 + k * STEP) * A.v_stride + u.head * D + part * 8);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                if (!there[k] && key0 + k * STEP < cover) {
+                    const int64_t at = ((row0 + k * STEP) * A.n2 + u.head) * D + part * 8;
+                    *reinterpret_cast<uint4 *>(A.dk + at) = *reinterpret_cast<uint4 *>(A.dv + at) = make_uint4(0, 0, 0, 0);
+                }
+                if constexpr (kFp16) {
+                    float nrm = 0.f;
+                    const uint32_t *pa = &a[k].x;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float y0 = u16_to_f<kFp16>((uint16_t)pa[i]), y1 = u16_to_f<kFp16>((uint16_t)(pa[i] >> 16));
                         nrm += y0 * y0 + y1 * y1;
                     }
-                }
 #pragma unroll
-                for (int o = LPR / 2; o; o >>= 1) nrm += __shfl_xor_sync(0xffffffffu, nrm, o);
-                if (nrm < INFINITY) top = fmaxf(top, nrm);
+                    for (int o = LPR / 2; o; o >>= 1) nrm += __shfl_xor_sync(0xffffffffu, nrm, o);
+                    if (nrm < INFINITY) top = fmaxf(top, nrm);
+                }
             }
         }
     }

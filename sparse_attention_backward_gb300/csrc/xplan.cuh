@@ -112,7 +112,7 @@ inline int split_of(int64_t units, int tiles, int per_sm, int sms) {
 // Windowed and paged forward: CTAs of a cluster, with two key tiles each at least, where loops are long enough for the join to
 // pay (8 heads of 64, 500 x 500 tokens, 8 tiles: 10.7 us, split 8.8; 191 keys, 3 tiles: 4.7 us, split 10), or pieces of a unit
 // joined by k_xjoin, where eight CTAs a unit would leave much of the GPU idle: decoding few sequences with long caches.  A piece
-// has four tiles at least (one token over 131072 states, 4 heads of 128: 8 CTAs a head 270 us, 76 pieces 50).  From the descriptor
+// has four tiles at least (one token over 131072 states, 4 heads of 128: 8 CTAs a head 293 us, 76 pieces 50).  From the descriptor
 // alone, for 152 SMs, so that phase 1 knows the workspace and a call's sums have the same order on every GB300.
 struct XSplit {
     int nsplit, pieces;
