@@ -386,11 +386,15 @@ struct RowStore {
         trade(a.w, b.w, upper, with);
     }
     __device__ __forceinline__ void store(uint16_t *base, const float *y, int col, int lane) const {
+        uint32_t p[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) p[k] = xpack<kFp16>(y[2 * k], y[2 * k + 1]);
+        store_packed(base, p, col, lane);
+    }
+    __device__ __forceinline__ void store_packed(uint16_t *base, const uint32_t *p, int col, int lane) const {
         uint4 c[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            c[k] = make_uint4(xpack<kFp16>(y[8 * k], y[8 * k + 1]), xpack<kFp16>(y[8 * k + 2], y[8 * k + 3]),
-                              xpack<kFp16>(y[8 * k + 4], y[8 * k + 5]), xpack<kFp16>(y[8 * k + 6], y[8 * k + 7]));
+        for (int k = 0; k < 4; ++k) c[k] = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
         const bool odd = lane & 1, high = lane & 2;
 #pragma unroll
         for (int k = 0; k < 4; k += 2) trade(c[k], c[k + 1], odd, 1);

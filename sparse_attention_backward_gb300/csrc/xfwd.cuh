@@ -88,11 +88,9 @@ struct XJob {
     int t0, n;                          // first tile of this CTA's share of the keys, and their number
     int whole, partial;                 // tiles of the share from `whole` on, before `partial`, lack no key
 };
+// The keys of a unit whose sequence, head and tile are known.
 template <int kKeys, int kMode>
-__device__ __forceinline__ XJob x_job(const XArgs &A, int unit, int rank, int ways) {
-    XJob w;
-    w.u = x_decode<&SeqRow::qtile0, kMode == kAll ? kByHead : kDown>(A, unit);
-    if (kMode == kPaged) w.u.seq.klen = min(max(__ldg(A.klens + w.u.b), 0), A.width * A.page);
+__device__ __forceinline__ void x_keys(const XArgs &A, int rank, int ways, XJob &w) {
     w.tok0 = w.u.tile * A.tpt;
     w.cover = A.s1_pad ? A.s1_pad : w.u.seq.qlen;
     if constexpr (kMode != kAll) w.band = BandKeys::of<kKeys, kMode == kPaged>(A, w.u.seq, w.tok0);
@@ -101,6 +99,33 @@ __device__ __forceinline__ XJob x_job(const XArgs &A, int unit, int rank, int wa
     x_share(nkt, rank, ways, &w.t0, &w.n);
     w.whole = kMode == kAll ? 0 : w.band.f0 - w.t0;
     w.partial = A.mask ? 0 : (kMode == kAll ? w.u.seq.klen / kKeys : w.band.f1) - w.t0;
+}
+template <int kKeys, int kMode>
+__device__ __forceinline__ XJob x_job(const XArgs &A, int unit, int rank, int ways) {
+    XJob w;
+    w.u = x_decode<&SeqRow::qtile0, kMode == kAll ? kByHead : kDown>(A, unit);
+    if (kMode == kPaged) w.u.seq.klen = min(max(__ldg(A.klens + w.u.b), 0), A.width * A.page);
+    x_keys<kKeys, kMode>(A, rank, ways, w);
+    return w;
+}
+
+// The next unit of a CTA that walks, as many tiles and heads on as the grid has CTAs: without divisions or loads, unless it
+// is another sequence's.
+struct XStep {
+    int tiles, heads;
+    __device__ __forceinline__ explicit XStep(const XArgs &A) : tiles(gridDim.x / A.n2), heads(gridDim.x - tiles * A.n2) {}
+};
+template <int kKeys, int kMode>
+__device__ __forceinline__ XJob x_job_after(const XArgs &A, XJob w, const XStep &step, int unit, int rank, int ways) {
+    int head = w.u.head + step.heads, tile = w.u.tile - step.tiles;
+    if (head >= A.n2) {
+        head -= A.n2;
+        --tile;
+    }
+    if (tile < 0) return x_job<kKeys, kMode>(A, unit, rank, ways);
+    w.u.head = head;
+    w.u.tile = tile;
+    x_keys<kKeys, kMode>(A, rank, ways, w);
     return w;
 }
 
@@ -190,10 +215,12 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
     const int ways = kMode == kAll ? ns : ns * A.pieces; // CTAs of the unit: a cluster's, or pieces
     const int rank = blockIdx.x % ways;
     // windowed: CTAs that share no unit take one after the other, so that the next one's loads and first scores run beside
-    // the last one's end (a window of 128 over 32768 tokens, 64 heads of 128: 376 us with a unit a CTA, 342 with this)
+    // the last one's end (a window of 128 over 32768 tokens, 64 heads of 128: 376 us with a unit a CTA, 342 with this; 266
+    // with the next unit stepped to instead of looked up, its divisions and loads gone, and a shorter end)
     const int unit0 = blockIdx.x / ways;
     auto next_unit = [&](int unit) { return x_walks(kMode, D, kKeys) && ways == 1 ? unit + (int)gridDim.x : 1 << 30; };
     XJob w = x_job<kKeys, kMode>(A, unit0, rank, ways);
+    const XStep step(A);
     if (kMode != kAll && A.pieces > 1) grid_next();
     tc::tc_fence_before();
     __syncthreads();
@@ -253,7 +280,7 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                     }
                     unit = next_unit(unit);
                     if (!ok || !x_walks(kMode, D, kKeys) || unit >= A.units) break;
-                    w = x_job<kKeys, kMode>(A, unit, rank, ways);
+                    w = x_job_after<kKeys, kMode>(A, w, step, unit, rank, ways);
                 }
                 if (!ok) fail();
                 if (lane == 0) {
@@ -291,7 +318,7 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                     }
                     unit = next_unit(unit);
                     if (!ok || !x_walks(kMode, D, kKeys) || unit >= A.units) break;
-                    w = x_job<kKeys, kMode>(A, unit, rank, ways);
+                    w = x_job_after<kKeys, kMode>(A, w, step, unit, rank, ways);
                 }
                 if (!ok) fail();
                 // every load issued must have landed before the CTA exits
@@ -356,7 +383,7 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                 nonempty += n > 0;
                 if (L::HALVES == 2) written_by ^= n & 1 ? 3u : 0u;
                 else written_by ^= x_parity<NB>(n);
-                w = x_job<kKeys, kMode>(A, unit, rank, ways);
+                w = x_job_after<kKeys, kMode>(A, w, step, unit, rank, ways);
             }
             if (!ok && lane == 0) fail();
             // every MMA issued must be complete before TMEM is freed
@@ -370,6 +397,7 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
         }
     } else {
         const int r = warp * 32 + lane;                  // query row = TMEM lane
+        const int r_tok = r / G, r_head = r - r_tok * G;
         const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
         const uint32_t to = trow + L::COL_O;
         float m = -INFINITY, l = 0.f;                    // reference maximum (log2 units), sum
@@ -379,22 +407,19 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
         for (int unit = unit0;;) {
         const int n = w.n, next = next_unit(unit);
         bool ok = true;
-        XJob ahead;
+        auto wait = [&](int b, uint32_t parity) { return warp_wait(abort_flag, Phase{&bars[b], parity}); };
+        // tile i's scores (or, behind the last two tiles, just the products before) are complete
+        auto formed = [&](int i) { return wait(XF_S + i % NB, ((formed_by >> (i % NB)) ^ (uint32_t)(i / NB)) & 1u); };
         if (n > 0) {
             // -------------------------------------------------- softmax
             const float c = A.scale_log2;
-            auto wait = [&](int b, uint32_t parity) {
-                return warp_wait(abort_flag, Phase{&bars[b], parity});
-            };
-            // tile i's scores (or, behind the last two tiles, just the products before) are complete
-            auto formed = [&](int i) { return wait(XF_S + i % NB, ((formed_by >> (i % NB)) ^ (uint32_t)(i / NB)) & 1u); };
             // One tile; a copy of its own for tiles with absent keys, whose
             // selects otherwise run for every tile.  Paired fp32 operations
             // (f32x2): half the instructions where issue slots are short,
             // 540 -> 507 us for 8192 x 4096 tokens of 64-wide heads.
             KeyLoad<kKeys / 32> keys{};                  // of the next tile that may lack keys
             // the row's keys, from the first tile's first one on
-            const int row_p = w.tok0 + r / G + w.u.seq.klen - w.u.seq.qlen - first_key(0);
+            const int row_p = w.tok0 + r_tok + w.u.seq.klen - w.u.seq.qlen - first_key(0);
             const int row_a = row_p - A.left, row_b = row_p + A.right + 1;
             auto tile = [&](auto masked, int i) -> bool {
                 const bool lacking = masked;
@@ -408,7 +433,9 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                     } else {
                         kb.set_first(kKeys);
                     }
-                    if constexpr (kMode != kAll) kb.clip(w.band.lo - first_key(i), w.band.hi - first_key(i));
+                    // rows that are not the sequence's may hold anything; paged: rows that no window holds were not loaded
+                    if constexpr (kMode == kBand) kb.clip(0, w.u.seq.klen - first_key(i));
+                    if constexpr (kMode == kPaged) kb.clip(w.band.lo - first_key(i), w.band.hi - first_key(i));
                     if (!kb.all()) {
                         const int jv = i + (i + NB < n ? i + NB : n);   // V's place in the ring, as in the MMA warp
                         if (!warp_wait(abort_flag, Phase{&full[(base + jv) % ST], (uint32_t)((base + jv) / ST) & 1u})) return false;
@@ -510,13 +537,19 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                 if (!ok) break;
                 tc::tc_fence_after();
                 // Short loops alternate between the two: with a copy of the code for each, more instructions are fetched than
-                // found (a window of 128 over 32768 tokens: 342 us, with one copy 329).  Long ones hardly do (2 x 8192 causal
+                // found (a window of 128 over 32768 tokens, then: 342 us, with one copy 329).  Long ones hardly do (2 x 8192 causal
                 // tokens: 781 us, with one copy 821).
                 const bool lacking = i < w.whole || i >= w.partial;
                 if constexpr (kMode != kAll && kKeys == 64) ok = tile(lacking, i);
                 else ok = lacking ? tile(std::true_type{}, i) : tile(std::false_type{}, i);
             }
-            if (x_walks(kMode, D, kKeys) && next < A.units) ahead = x_job<kKeys, kMode>(A, next, rank, ways);   // beside the last product
+        }
+        const int tok = w.tok0 + r_tok;
+        const bool mine = r < A.tpt * G && tok < w.cover, pad = tok >= w.u.seq.qlen;
+        const int64_t row = (int64_t)(w.u.seq.q0 + tok) * A.n1 + w.u.head * G + r_head;
+        const bool more = x_walks(kMode, D, kKeys) && next < A.units;
+        if (more) w = x_job_after<kKeys, kMode>(A, w, step, next, rank, ways);   // beside the last product
+        if (n > 0) {
             if (ok) ok = x_walks(kMode, D, kKeys) ? wait(XF_O, ended) : formed(n - 1 + NB);
             ended ^= 1;
             if (!ok && lane == 0) fail();
@@ -525,35 +558,34 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
 
             if (ways > 1 || !ok) break;                  // stored below
             // -------------------------------------------------- epilogue
-            const int tok = w.tok0 + r / G;
-            const bool mine = r < A.tpt * G && tok < w.cover;
-            const bool pad = tok >= w.u.seq.qlen;
-            const int64_t row = (int64_t)(w.u.seq.q0 + tok) * A.n1 + w.u.head * G + r % G;
             const bool some = l > 0.f || l != l;         // l is NaN when a score was
             const float inv = some ? 1.f / l : 0.f;
             RowStore<kFp16> rows;
             rows.rows(mine ? row * D : -1, lane);
+            const uint32_t keep = n > 0 && some && !pad ? 0xffffffffu : 0u;
 #pragma unroll
-            for (int j = 0; j < D; j += 32) {
+            for (int j = 0; j < D; j += 32) {            // (the next columns' loads ahead of these: spilled registers, 507 -> 580 us)
                 float y[32];
                 if (n > 0) {
                     tmem_ld32(to + j, reinterpret_cast<uint32_t *>(y));
                     tc::tmem_wait_ld();
                 }
+                uint32_t p[16];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = some && !pad ? y[e] * inv : 0.f;
-                rows.store(A.o, y, j, lane);
+                for (int e = 0; e < 16; ++e) {
+                    const float2 v = mul2(make_float2(y[2 * e], y[2 * e + 1]), make_float2(inv, inv));
+                    p[e] = xpack<kFp16>(v.x, v.y) & keep;
+                }
+                rows.store_packed(A.o, p, j, lane);
             }
             if (mine) A.lse[row] = pad ? 0.f : some ? (m - kShift) * kLn2 + logf(l) : -INFINITY;
-            if (!x_walks(kMode, D, kKeys) || next >= A.units) break;
-            if (n == 0) ahead = x_job<kKeys, kMode>(A, next, rank, ways);
+            if (!more) break;
             tc::tc_fence_before();                       // O has been read before the next unit's products may follow
             unit = next;
             base += 2 * n;
             formed_by ^= x_parity<NB>(n) ^ (NB == 2 && n > 1 ? 1u << (n % NB) : 0u);
             m = -INFINITY;
             l = 0.f;
-            w = ahead;
         }
         const int n = w.n;
         if (kMode != kAll && A.pieces > 1) {
