@@ -364,26 +364,22 @@ __device__ __forceinline__ void mma_ab(uint32_t acc, uint32_t a, uint32_t b, uin
 }
 
 // Stores of accumulator rows.  A lane holds 32 columns of its own row; written as they stand, each instruction of a warp
-// would touch 32 lines for 16 bytes each.  Groups of four lanes swap their 16-byte pieces first (two steps of a 4 x 4
-// transposition), so that an instruction writes 64 consecutive bytes of eight rows.  Collective over a warp.
+// would touch 32 lines for 16 bytes each (a window of 128 over 32768 tokens: 311 us).  The lanes of a pair swap 16-byte
+// pieces first, so that an instruction writes 32 consecutive bytes, a memory sector, of 16 rows (267 us; 64 bytes of eight
+// rows by a second swap take no less, and 64-wide heads more: a window of 512 over 32768 tokens 417 us against 406).
+// Collective over a warp.
 template <bool kFp16>
 struct RowStore {
-    int64_t off[4];                     // elements from `base` to the rows of this lane's group; negative: not stored
+    int64_t off[2];                     // elements from `base` to the rows of this lane's pair; negative: not stored
     __device__ __forceinline__ void rows(int64_t mine, int lane) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) off[i] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + i);
+        for (int i = 0; i < 2; ++i) off[i] = __shfl_sync(0xffffffffu, mine, (lane & ~1) + i);
     }
     // the lower lane of a pair gives b for the other's a
-    __device__ __forceinline__ static void trade(uint32_t &a, uint32_t &b, bool upper, int with) {
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? a : b, with);
+    __device__ __forceinline__ static void trade(uint32_t &a, uint32_t &b, bool upper) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? a : b, 1);
         a = upper ? got : a;
         b = upper ? b : got;
-    }
-    __device__ __forceinline__ static void trade(uint4 &a, uint4 &b, bool upper, int with) {
-        trade(a.x, b.x, upper, with);
-        trade(a.y, b.y, upper, with);
-        trade(a.z, b.z, upper, with);
-        trade(a.w, b.w, upper, with);
     }
     __device__ __forceinline__ void store(uint16_t *base, const float *y, int col, int lane) const {
         uint32_t p[16];
@@ -391,18 +387,18 @@ struct RowStore {
         for (int k = 0; k < 16; ++k) p[k] = xpack<kFp16>(y[2 * k], y[2 * k + 1]);
         store_packed(base, p, col, lane);
     }
-    __device__ __forceinline__ void store_packed(uint16_t *base, const uint32_t *p, int col, int lane) const {
-        uint4 c[4];
+    __device__ __forceinline__ void store_packed(uint16_t *base, uint32_t *p, int col, int lane) const {
+        const int odd = lane & 1;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) c[k] = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
-        const bool odd = lane & 1, high = lane & 2;
+        for (int k = 0; k < 16; k += 8) {
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) trade(c[k], c[k + 1], odd, 1);
+            for (int e = 0; e < 4; ++e) trade(p[k + e], p[k + 4 + e], odd);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) trade(c[k], c[k + 2], high, 2);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (off[i] >= 0) *reinterpret_cast<uint4 *>(base + off[i] + col + 8 * (lane & 3)) = c[i];
+            for (int i = 0; i < 2; ++i)
+                if (off[i] >= 0)
+                    *reinterpret_cast<uint4 *>(base + off[i] + col + 2 * k + 8 * odd) =
+                        make_uint4(p[k + 4 * i], p[k + 4 * i + 1], p[k + 4 * i + 2], p[k + 4 * i + 3]);
+        }
     }
 };
 
