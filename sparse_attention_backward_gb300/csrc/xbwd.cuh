@@ -584,9 +584,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 const int partial = A.mask ? 0 : kBand ? w.f1 : w.seq.klen / kXRows - w.t0;
                 KeyLoad<4> keys{};                       // of the next tile that may lack keys
                 if (partial < n && (!kBand || A.mask)) keys.start(A.mask, w.seq, first_key(w, partial > 0 ? partial : 0), lane);
-                // the row's keys, and those of the whole tile, from the first tile's first one on
+                // the row's keys, from the first tile's first one on
                 const int row_p = w.first + my_tok + w.seq.klen - w.seq.qlen - w.base;
-                const int p_end = min(w.first + A.tpt, w.seq.qlen) - 1 + w.seq.klen - w.seq.qlen - w.base;
                 // dS over the scores; a copy of its own for tiles with absent keys
                 auto tile = [&](auto masked, int i) -> bool {
                     const uint32_t ts = trow + (g & 1) * 128 + h * 64;
@@ -609,8 +608,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
                         } else {
                             kb.set_first(kXRows);
                         }
-                        if constexpr (kBand) kb.clip(0, min(w.seq.klen - w.base, p_end + A.right + 1) - i * kXRows);
-                        // the scores have read this tile's keys, so its dead rows may go before dS K
+                        if constexpr (kBand) kb.clip(0, w.seq.klen - w.base - i * kXRows);
+                        // the scores have read this tile's keys, so the rows in it that are not the sequence's, which may hold
+                        // anything, may go before dS K
                         if (!kb.all()) zero_rows<L::KC, 4, 256>(smem + L::OFF_A + g % L::RA * L::TILE, kb, threadIdx.x);
                         if constexpr (kBand) kb.clip(row_p - A.left - i * kXRows, row_p + A.right + 1 - i * kXRows);
                         bits[0] = h ? kb.w[2] : kb.w[0];
