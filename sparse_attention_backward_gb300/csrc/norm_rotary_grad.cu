@@ -10,8 +10,8 @@
 // thread keeps the sums of its columns over all heads that its group takes (the
 // other side's in shared memory meanwhile); a block adds its groups up in their
 // order, and k_norm_dw the blocks in theirs, so the result does not depend on
-// timing.  4 x 4095 padded tokens of 32 heads of 192, 64 of them turning: 107
-// us, 5.2 TB/s; 32768 tokens of 40 heads of 128: 188 us.  (Blocks of queries
+// timing.  4 x 4095 padded tokens of 32 heads of 192, 64 of them turning: 103
+// us, 5.4 TB/s; 32768 tokens of 40 heads of 128: 182 us.  (Blocks of queries
 // and of keys apart, each with sines of its own: 120 and 226 us.)
 #include <type_traits>
 

@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 rows.store(A.dq, y, h * (D / 2) + j, lane);
             };
             if (piece < 0) {
-#pragma unroll
+#pragma unroll 1
                 for (int j = 0; j < D / 2; j += 32) {
                     float y[32];
                     sums(j, y);

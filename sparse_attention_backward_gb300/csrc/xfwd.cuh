@@ -563,8 +563,10 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
             RowStore<kFp16> rows;
             rows.rows(mine ? row * D : -1, lane);
             const uint32_t keep = n > 0 && some && !pad ? 0xffffffffu : 0u;
-#pragma unroll
-            for (int j = 0; j < D; j += 32) {            // (the next columns' loads ahead of these: spilled registers, 507 -> 580 us)
+            // in a loop: instructions that run once a unit are fetched each time (a window of 128 over 32768 tokens: 270 us
+            // unrolled, 263 so; 64 wide 404, 412).  The next columns' loads ahead of these spill registers (window 512: 507, 580).
+#pragma unroll(L::NARROW ? 2 : 1)
+            for (int j = 0; j < D; j += 32) {
                 float y[32];
                 if (n > 0) {
                     tmem_ld32(to + j, reinterpret_cast<uint32_t *>(y));
