@@ -225,6 +225,26 @@ def test_bitwise_and_captured_on_another_stream():
             assert torch.equal(a, b)
 
 
+def test_offsets_beyond_32_bits():
+    """A sequence behind one of so many tokens that elements and bytes before it pass 32 bits; those are zeros, which give
+    zeros and add nothing to the weights' gradients."""
+    c, rows = Case([300], 16, 16, 128, sab.Rotary(128), BF, seed=60), 2 ** 20 + 70000
+    assert rows * 16 * 128 > 2 ** 31
+    c.cu = [0, rows - 300, rows]
+
+    def behind(x):
+        big = torch.zeros(rows, 16, 128, dtype=BF, device="cuda")
+        big[-300:] = x.cuda()
+        return big
+
+    x, dy, w = [behind(t) for t in c.x], [behind(t) for t in c.dy], [t.cuda() for t in c.w]
+    got = sab.norm_rotary_forward(*x, c.rot, *w, **c.kw())
+    grads = sab.norm_rotary_backward(*x, *dy, c.rot, *w, **c.kw())
+    for t in got + grads[:2]:
+        assert bool((t[:-300:4099] == 0).all())
+    c.check([t[-300:] for t in got], [t[-300:] for t in grads[:2]] + list(grads[2:]))
+
+
 def test_rotation_alone_agrees():
     # a head of unit mean square and no weight is rotated as rotary_forward does, but for roundings of the norm
     rot = sab.Rotary(64, offset=32)

@@ -351,6 +351,28 @@ def test_gradient_against_differences(d, dtype, left, right):
         assert abs(float((got[at] * e).sum()) - diff) <= allowed + 1e-4 * abs(diff), name
 
 
+def test_offsets_beyond_32_bits():
+    """A sequence behind one of so many tokens that elements and bytes before it pass 32 bits."""
+    c, rows = Case([300], [300], 16, 16, 128, BF, 63, 0, seed=40), 2 ** 20 + 70000
+    assert rows * 16 * 128 > 2 ** 31
+    cu = [0, rows - 300, rows]
+
+    def behind(x):
+        big = torch.zeros(rows, 16, 128, dtype=BF, device="cuda")
+        big[-300:] = x
+        return big
+
+    q, k, v, dy = (behind(x) for x in (c.q, c.k, c.v, c.dy))
+    o, lse = sab.window_forward(q, k, v, cu, cu, c.scale, left=63, check=True)
+    check_forward(c, o[-300:], lse[-300:])
+    assert bool((o[:-300:4099] == 0).all())
+    grads = sab.window_backward(q, k, v, o, dy, lse, cu, cu, c.scale, left=63, check=True)
+    want, tol = c.backward(o[-300:], lse[-300:])
+    for name, x, w, t in zip(("dq", "dk", "dv"), grads, want, tol):
+        _within(name, x[-300:], w, t, BF)
+        assert bool((x[:-300:4099] == 0).all())
+
+
 # ------------------------------------------------------------------- pages
 class Pages:
     """A case's keys and values in shuffled pages of a cache that holds NaN elsewhere, and a table with junk where nothing
@@ -522,6 +544,25 @@ def test_append(dtype, page, n2, d, padded, strided):
     with pytest.raises(sab.SagError) as e:      # its tokens are not written
         sab.paged_append(k, v, kc, vc, bad.cuda(), lens, cu, check=True)
     assert e.value.status == sab.SAG_ERR_INDEX and torch.equal(kc, before)
+
+
+def test_pages_beyond_32_bits():
+    """Pages whose elements and bytes pass 32 bits, written by the append and read by the attention."""
+    c, pages = Case([5, 130], [400, 900], 8, 2, 128, HF, -1, 0, seed=41), 600000
+    p = Pages(c, 16)
+    big = [torch.empty(pages, 16, 2, 128, dtype=HF, device="cuda") for _ in range(2)]
+    assert big[0].numel() > 2 ** 31
+    table = torch.where(p.table >= 0, p.table, 0)           # (entries that nothing looks at hold any number)
+    for b, n in enumerate(c.l2):
+        used = p.table[b, :-(-n // 16)].long()
+        far = pages - 1 - used * 1000                       # over all of the cache
+        big[0][far], big[1][far] = p.k[used], p.v[used]
+        table[b, :len(far)] = far.int()
+        for at in range(n - c.l1[b], n):
+            big[0][far[at // 16], at % 16] = big[1][far[at // 16], at % 16] = NAN
+    new = torch.cat([torch.arange(c.cu2[b + 1] - c.l1[b], c.cu2[b + 1]) for b in range(2)]).cuda()
+    sab.paged_append(c.k[new], c.v[new], *big, table, p.lens, c.cu1, check=True)
+    check_forward(c, *sab.paged_forward(c.q, *big, table, p.lens, c.cu1, c.scale, check=True))
 
 
 def test_append_of_many_sequences_then_attention():
