@@ -17,6 +17,7 @@ namespace sag {
 constexpr int kXRows = 128;             // rows of a query tile, keys of a key tile
 constexpr int kMaxSplit = 8;            // CTAs of a cluster, pieces of a unit
 constexpr int kMaxPieces = 304;         // pieces of a launch: each has its partial sums in the workspace
+constexpr int kMaxFwdPieces = 152;      // pieces of a unit of a forward
 constexpr int kXThreads = 320;          // warps 0-7 softmax and epilogue, 8 TMA, 9 MMA
 constexpr uint64_t kXWaitNs = 2000000000ull;
 // A half keeps 11 bits down to 2^-14 only, and a probability of a long sequence lies below that.  Both passes shift

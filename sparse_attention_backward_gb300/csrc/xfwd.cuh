@@ -723,9 +723,10 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
     }
 }
 
-// Joins the pieces of units: a block a row; its warps take every eighth piece and are added up in their order.  All
-// maxima and sums are read at once, then eight pieces' rows at a time.
-constexpr int kJoinWarps = 8, kMaxJoin = 512;            // pieces of a unit at most
+// Joins the pieces of units: a block a row; its warps take every sixteenth piece and are added up in their order.  All
+// maxima and sums are read at once, and a warp's first eight pieces' rows beside them (one token over 131072 states: 48.4 us;
+// eight warps, and rows after sums: 50.3).
+constexpr int kJoinWarps = 16, kMaxJoin = 512;           // pieces of a unit at most
 template <bool kFp16, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_xjoin(const __grid_constant__ XArgs A) {
     constexpr float kShift = kFp16 ? kFwdShiftF16 : 0.f;
@@ -742,14 +743,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_xjoin(const __grid_constant
     const int pieces = pad ? 0 : A.pieces;
     const float2 *ml = A.part_ml + ((int64_t)unit * A.pieces * kXRows + k);
     const float *part = A.parts + ((int64_t)unit * A.pieces * kXRows + k) * D + lane * E;
-    float2 v[2];
-    float top = -INFINITY;
+    static_assert(kMaxFwdPieces <= kMaxJoin && kMaxJoin == kJoinWarps * 32, "a thread a piece");
+    const float2 v = (int)threadIdx.x < pieces ? ml[(int64_t)threadIdx.x * kXRows] : make_float2(-INFINITY, 0.f);
+    float y[8][E];
+    auto read = [&](int p0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int p = threadIdx.x + i * kJoinWarps * 32;
-        v[i] = p < pieces ? ml[(int64_t)p * kXRows] : make_float2(-INFINITY, 0.f);
-        top = fmaxf(top, v[i].x);
-    }
+        for (int i = 0; i < 8; ++i) {
+            const int p = p0 + i * kJoinWarps;
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[i][e] = 0.f;
+            if (p >= pieces) continue;
+            const float *at = part + (int64_t)p * kXRows * D;
+            if constexpr (E == 4) *reinterpret_cast<float4 *>(y[i]) = *reinterpret_cast<const float4 *>(at);
+            else *reinterpret_cast<float2 *>(y[i]) = *reinterpret_cast<const float2 *>(at);
+        }
+    };
+    read(warp);
+    float top = v.x;
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) red[0][warp] = top;
@@ -757,14 +767,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_xjoin(const __grid_constant
 #pragma unroll
     for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, red[0][i]);
     // a piece that saw nothing does not count (its O was not written); one whose weight underflows does: 0 times NaN is NaN
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const bool saw = v[i].y != 0.f;
-        const float w = saw ? xex2(v[i].x - top) : 0.f;
-        if (saw) sum += v[i].y * w;
-        weight_of[threadIdx.x + i * kJoinWarps * 32] = saw ? w : -1.f;
-    }
+    const bool saw = v.y != 0.f;
+    const float weight = saw ? xex2(v.x - top) : 0.f;
+    float sum = saw ? v.y * weight : 0.f;
+    weight_of[threadIdx.x] = saw ? weight : -1.f;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) red[1][warp] = sum;
@@ -774,33 +780,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_xjoin(const __grid_constant
     for (int i = 0; i < kJoinWarps; ++i) sum += red[1][i];
     float acc[E] = {};
     for (int p0 = warp; p0 < pieces; p0 += 8 * kJoinWarps) {
-        float y[8][E], w[8];
+        if (p0 != warp) read(p0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int p = p0 + i * kJoinWarps;
-            w[i] = p < pieces ? weight_of[p] : -1.f;
+            const float w = p < pieces ? weight_of[p] : -1.f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) y[i][e] = 0.f;
-            if (w[i] == -1.f) continue;
-            const float *at = part + (int64_t)p * kXRows * D;
-            if constexpr (E == 4) *reinterpret_cast<float4 *>(y[i]) = *reinterpret_cast<const float4 *>(at);
-            else *reinterpret_cast<float2 *>(y[i]) = *reinterpret_cast<const float2 *>(at);
+            for (int e = 0; e < E; ++e)
+                if (w != -1.f) acc[e] += y[i][e] * w;    // (else what was read is no sum)
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += y[i][e] * w[i];
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) acc_of[warp][lane * E + e] = acc[e];
     __syncthreads();
     const bool some = sum > 0.f || sum != sum;
     const float inv = some ? 1.f / sum : 0.f;
-    for (int c = threadIdx.x; c < D; c += kJoinWarps * 32) {
-        float y = 0.f;
+    if (threadIdx.x < D) {
+        float sums = 0.f;
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) y += acc_of[w][c];
-        A.o[row * D + c] = some ? f_to_u16<kFp16>(y * inv) : (uint16_t)0;
+        for (int w = 0; w < kJoinWarps; ++w) sums += acc_of[w][threadIdx.x];
+        A.o[row * D + threadIdx.x] = some ? f_to_u16<kFp16>(sums * inv) : (uint16_t)0;
     }
     if (threadIdx.x == 0) A.lse[row] = pad ? 0.f : some ? (top - kShift) * 0.6931471805599453f + logf(sum) : -INFINITY;
 }

@@ -20,7 +20,6 @@ constexpr size_t kStatusAt = 256;           // status words, behind the workspac
 inline size_t up256(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 // most CTAs of a launch whose units are split, for the status words
 constexpr int64_t kSplitCtas = 1024;
-constexpr int kMaxFwdPieces = 152;
 
 struct XPlan {
     bool fp16, bsnd;
