@@ -1006,11 +1006,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 if (!((seen.w[(j + e) >> 5] >> ((j + e) & 31)) & 1u)) p[j + e] = 0.f;
-                        } else {
-                            if (kMasked && !live) p[j] = p[j + 1] = p[j + 2] = p[j + 3] = 0.f;
                         }
                         q[j / 2] = xpack<kFp16>(p[j], p[j + 1]);
                         q[j / 2 + 1] = xpack<kFp16>(p[j + 2], p[j + 3]);
+                        if (kMasked && !kBand && !live) q[j / 2] = q[j / 2 + 1] = 0u;
                     }
                     tmem_st32(trow + h * 64, q);
                     tmem_wait_st();
@@ -1036,9 +1035,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
                             }
                             e = mul2(e, make_float2(pp[0], pp[1]));
                             o = mul2(o, make_float2(pp[2], pp[3]));
-                            if (kMasked && !live) e.x = e.y = o.x = o.y = 0.f;
                             q[(f * 32 + j) / 2] = xpack<kFp16>(e.x, e.y);
                             q[(f * 32 + j) / 2 + 1] = xpack<kFp16>(o.x, o.y);
+                            if (kMasked && !live) q[(f * 32 + j) / 2] = q[(f * 32 + j) / 2 + 1] = 0u;
                         }
                     }
                     tmem_st32(trow + 128 + h * 64, q);
