@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
                 tc::tc_fence_after();
                 // Short loops alternate between the two: with a copy of the code for each, more instructions are fetched than
                 // found (a window of 128 over 32768 tokens, then: 342 us, with one copy 329).  Long ones hardly do (2 x 8192 causal
-                // tokens: 781 us, with one copy 821).
+                // tokens, then: 781 us, with one copy 821).
                 const bool lacking = i < w.whole || i >= w.partial;
                 if constexpr (kMode != kAll && kKeys == 64) ok = tile(lacking, i);
                 else ok = lacking ? tile(std::true_type{}, i) : tile(std::false_type{}, i);
@@ -564,8 +564,9 @@ __global__ void __launch_bounds__(kFwdThreads, FwdShape<D, kKeys>::CTAS)
             rows.rows(mine ? row * D : -1, lane);
             const uint32_t keep = n > 0 && some && !pad ? 0xffffffffu : 0u;
             // in a loop: instructions that run once a unit are fetched each time (a window of 128 over 32768 tokens: 270 us
-            // unrolled, 263 so; 64 wide 404, 412).  The next columns' loads ahead of these spill registers (window 512: 507, 580).
-#pragma unroll(L::NARROW ? 2 : 1)
+            // unrolled, 263 so; 64 wide 404, 412; cross attention of 2 x 8192 x 4096 tokens 691, 694).  The next columns' loads
+            // ahead of these spill registers (window 512: 507, 580).
+#pragma unroll(L::NARROW || kMode == kAll ? 4 : 1)
             for (int j = 0; j < D; j += 32) {
                 float y[32];
                 if (n > 0) {
