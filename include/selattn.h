@@ -674,8 +674,9 @@ typedef struct spa_desc {
  * A length outside [0, width * page_size] is taken as the nearest one in it, a page outside [0, pages) as page 0 (its
  * tokens are not written); both are reported (SAG_ERR_INDEX), and outputs are then not meaningful.  New tokens at
  * positions before 0 (kv_lens[b] < qlen) attend to nothing and are not written.  Rows of the cache behind a sequence's
- * length, and those before every window, may hold anything (others: as for the windowed attention).  BSND: padding rows get zeros in attention_out and
- * softmax_lse, and are not appended.  TND: rows behind the last sequence are left as they were.
+ * length, and those before every window, may hold anything (others: as for the windowed attention).  BSND: padding rows
+ * get zeros in attention_out and softmax_lse, and are not appended.  TND: rows behind the last sequence are left as they
+ * were.
  */
 typedef struct spa_io {
     const void *query, *key, *value;
