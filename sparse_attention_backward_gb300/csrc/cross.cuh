@@ -53,6 +53,11 @@ struct XArgs {
     float *stats;                       // [query tile][n2][256]: lse * log2(e), then Delta, of the tile's 128 rows
     unsigned *norms;                    // fp16: [batch][n2][2] largest squared row norms of dY and of V, as float bits
     float *row_norms;                   // fp16: [query tile][n2][128] squared norms of the rows of dY
+    // fp16, windowed: [key tile][n2][128] squared norms of the rows of V; the largest of each query tile's squared norms and
+    // |Delta|, and of each key tile's squared norms; the exponents of dS of the query rows, and of the keys
+    float *key_norms;
+    float2 *q_tops, *k_tops;
+    float *q_up, *k_up;
     int32_t q_tiles, k_tiles;
     int32_t *count, *status;            // device status: number of words, one word for each CTA
     int32_t n_status;                   // value for *count
@@ -72,6 +77,8 @@ cudaError_t launch_pfwd(const XArgs &a, const spa_io &io, const spa_desc &d, boo
 cudaError_t launch_xpre(const XArgs &a, bool fp16, int d, cudaStream_t s);
 cudaError_t launch_xdq(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s);
 cudaError_t launch_xdkv(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s);
+// windowed, fp16: exponents from what k_xpre has left
+cudaError_t launch_wscale(const XArgs &a, cudaStream_t s);
 cudaError_t launch_wdq(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s);
 cudaError_t launch_wdkv(const XArgs &a, const sca_io &io, const sca_desc &d, cudaStream_t s);
 

@@ -7,11 +7,13 @@ cudaError_t launch_xpre(const XArgs &a, bool fp16, int d, cudaStream_t s) {
     const int64_t ctas = (int64_t)a.q_tiles * a.n2 + (fp16 || a.mask || a.s2_pad ? (int64_t)a.k_tiles * a.n2 : 0);
     if (ctas == 0) return cudaSuccess;
     if (d == 128) {
-        if (fp16) k_xpre<true, 128><<<(unsigned)ctas, 256, 0, s>>>(a);
-        else k_xpre<false, 128><<<(unsigned)ctas, 256, 0, s>>>(a);
+        if (fp16 && a.key_norms) k_xpre<true, 128, true><<<(unsigned)ctas, 256, 0, s>>>(a);
+        else if (fp16) k_xpre<true, 128, false><<<(unsigned)ctas, 256, 0, s>>>(a);
+        else k_xpre<false, 128, false><<<(unsigned)ctas, 256, 0, s>>>(a);
     } else {
-        if (fp16) k_xpre<true, 64><<<(unsigned)ctas, 256, 0, s>>>(a);
-        else k_xpre<false, 64><<<(unsigned)ctas, 256, 0, s>>>(a);
+        if (fp16 && a.key_norms) k_xpre<true, 64, true><<<(unsigned)ctas, 256, 0, s>>>(a);
+        else if (fp16) k_xpre<true, 64, false><<<(unsigned)ctas, 256, 0, s>>>(a);
+        else k_xpre<false, 64, false><<<(unsigned)ctas, 256, 0, s>>>(a);
     }
     return cudaGetLastError();
 }

@@ -77,7 +77,7 @@ void share_both(int64_t q_units, int64_t q_most, int64_t q_all, int64_t k_units,
 
 struct GradPlan {
     Share q, k;
-    size_t o_parts_q, o_parts_k, o_arrived, total;
+    size_t o_parts_q, o_parts_k, o_arrived, o_key_norms, o_tops, o_up, total;
 };
 GradPlan grad_plan(const swa_desc *desc, const XPlan &p) {
     const sca_desc *d = &desc->attn;
@@ -111,7 +111,13 @@ GradPlan grad_plan(const swa_desc *desc, const XPlan &p) {
     g.o_parts_q = p.o_parts;                // (x_plan's own are the last)
     g.o_parts_k = up256(g.o_parts_q + g.q.part_bytes(d->d / 2));
     g.o_arrived = up256(g.o_parts_k + g.k.part_bytes(d->d));
-    g.total = up256(g.o_arrived + sizeof(unsigned) * 8 * (size_t)((g.q.pieces > 1 ? g.q.units : 0) + (g.k.pieces > 1 ? g.k.units : 0)));
+    g.o_key_norms =
+        up256(g.o_arrived + sizeof(unsigned) * 8 * (size_t)((g.q.pieces > 1 ? g.q.units : 0) + (g.k.pieces > 1 ? g.k.units : 0)));
+    // fp16: of each key, and of query and key tiles, and of query rows and keys (k_wscale)
+    const size_t scaled = p.fp16 ? (size_t)(q_units + k_units) : 0;
+    g.o_tops = up256(g.o_key_norms + (p.fp16 ? sizeof(float) * kXRows * (size_t)k_units : 0));
+    g.o_up = up256(g.o_tops + sizeof(float2) * scaled);
+    g.total = up256(g.o_up + sizeof(float) * kXRows * scaled);
     return g;
 }
 
@@ -290,8 +296,13 @@ extern "C" sag_status window_attn_grad(const swa_desc *desc, const sca_io *io, v
     a.right = limit_of(desc->right);
     if (x_table(&a, d, p, ws, s) != cudaSuccess) return SAG_ERR_CUDA;
     const int sms = current_device_sms();
-    if (p.fp16 && cudaMemsetAsync(a.norms, 0, sizeof(unsigned) * 2 * (size_t)d->batch * d->n2, s) != cudaSuccess)
-        return SAG_ERR_CUDA;
+    if (p.fp16) {
+        a.key_norms = reinterpret_cast<float *>(ws + g.o_key_norms);
+        a.q_tops = reinterpret_cast<float2 *>(ws + g.o_tops);
+        a.k_tops = a.q_tops + q_units;
+        a.q_up = reinterpret_cast<float *>(ws + g.o_up);
+        a.k_up = a.q_up + (size_t)q_units * kXRows;
+    }
     auto use = [&](XArgs *x, const Share &h, size_t parts) {
         x->units = h.units;
         x->full = h.pieces > 1 ? 0 : h.units;
@@ -306,6 +317,7 @@ extern "C" sag_status window_attn_grad(const swa_desc *desc, const sca_io *io, v
     a.arrived = arrived;
     a.n_arrived = q_counts + (g.k.pieces > 1 ? 8 * g.k.units : 0);
     if (launch_xpre(a, p.fp16, d->d, s) != cudaSuccess) return SAG_ERR_CUDA;
+    if (p.fp16 && launch_wscale(a, s) != cudaSuccess) return SAG_ERR_CUDA;
     // k_xpre zeroes the tickets and counters; without query rows there may be none (and no pieces)
     if (!q_units && cudaMemsetAsync(a.ticket, 0, 2 * sizeof(unsigned), s) != cudaSuccess) return SAG_ERR_CUDA;
     // k_xdkv first; k_xdq starts as its CTAs leave (window_bwd.cu).  Status words: k_xdq's, then k_xdkv's

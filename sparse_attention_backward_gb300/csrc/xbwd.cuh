@@ -23,7 +23,9 @@
 // of small dY lost their bits to subnormals (30000 states, dY 2^-18 of the
 // largest: dQ off by 12 %, now by 0.03 %; 1500 states: 0.6 %).  k_xdkv sums over
 // the rows of a sequence, where the largest count most, and takes one exponent
-// from the largest |dY|.
+// from the largest |dY|.  In a window the largest row need not be in a key's sum,
+// nor the largest V in a row's: there each key and each query row has its own
+// exponent, from what its window joins (k_wscale).
 //
 // A CTA (one per SM) walks over units, so that the next unit's tiles land and
 // its first products run beside the last one's stores.  Few units: a cluster's
@@ -55,12 +57,13 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------ k_xpre
-template <bool kFp16, int D>
+// kScaled: fp16 of windows, whose norms k_wscale takes
+template <bool kFp16, int D, bool kScaled>
 __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
     constexpr int LPR = D / 8;                           // lanes a row, 16 bytes each
     constexpr int RPW = 32 / LPR;
     constexpr int STEP = 8 * RPW, AHEAD = 4;             // rows of a step of the block, steps whose loads are in flight
-    __shared__ float red[8];
+    __shared__ float2 red[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = lane % LPR;
     if (blockIdx.x == 0) {
@@ -69,11 +72,12 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
     }
     grid_next();
     const int q_units = A.q_tiles * A.n2;
-    float top = 0.f;
-    int64_t slot;
+    float top = 0.f, far = 0.f;                          // largest squared norm, and |Delta|
+    int64_t slot, tile_id;
     if ((int)blockIdx.x < q_units) {
         const XUnit u = x_decode<&SeqRow::qtile0>(A, blockIdx.x);
         slot = ((int64_t)u.b * A.n2 + u.head) * 2;
+        tile_id = u.tile_id;
         float *st = A.stats + u.tile_id * 256;
         int r = warp * RPW + lane / LPR, tok = r / A.group, h = r - tok * A.group;
         const int step_tok = STEP / A.group, step_h = STEP - step_tok * A.group;
@@ -121,6 +125,7 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
                     if constexpr (kFp16) A.row_norms[u.tile_id * kXRows + r] = nrm;
                 }
                 if (nrm < INFINITY) top = fmaxf(top, nrm);
+                if (kScaled && fabsf(dot) < INFINITY) far = fmaxf(far, fabsf(dot));
                 r += STEP;
             }
         }
@@ -128,6 +133,7 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
         // zeros for the gradients of absent states; fp16: row norms of V
         const XUnit u = x_decode<&SeqRow::ktile0>(A, blockIdx.x - q_units);
         slot = ((int64_t)u.b * A.n2 + u.head) * 2 + 1;
+        tile_id = u.tile_id;
         const int cover = A.s2_pad ? A.s2_pad : u.seq.klen;
 #pragma unroll
         for (int done = 0; done < kXRows / STEP; done += AHEAD) {
@@ -163,28 +169,38 @@ __global__ void __launch_bounds__(256) k_xpre(const __grid_constant__ XArgs A) {
 #pragma unroll
                     for (int o = LPR / 2; o; o >>= 1) nrm += __shfl_xor_sync(0xffffffffu, nrm, o);
                     if (nrm < INFINITY) top = fmaxf(top, nrm);
+                    if (kScaled && part == 0)
+                        A.key_norms[u.tile_id * kXRows + key0 - u.tile * kXRows + k * STEP] = nrm;
                 }
             }
         }
     }
     if constexpr (kFp16) {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (lane == 0) red[warp] = top;
+        for (int o = 16; o; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if constexpr (kScaled) far = fmaxf(far, __shfl_xor_sync(0xffffffffu, far, o));
+        }
+        if (lane == 0) red[warp] = make_float2(top, far);
         __syncthreads();
         if (threadIdx.x == 0) {
-            for (int i = 1; i < 8; ++i) top = fmaxf(top, red[i]);
-            atomicMax(A.norms + slot, __float_as_uint(top));   // a maximum does not depend on the order
+            for (int i = 1; i < 8; ++i) {
+                top = fmaxf(top, red[i].x);
+                far = fmaxf(far, red[i].y);
+            }
+            if constexpr (kScaled) ((int)blockIdx.x < q_units ? A.q_tops : A.k_tops)[tile_id] = make_float2(top, far);
+            else atomicMax(A.norms + slot, __float_as_uint(top));   // a maximum does not depend on the order
         }
     }
 }
 
-// fp16: exponent e such that 2^e |dS| <= 2^15 for every dS of rows of dY and V whose largest squared norms are given.
-__device__ __forceinline__ float ds_exponent(float dy, float v) {
-    const float bound = 2.f * sqrtf(dy) * sqrtf(v);
+// fp16: exponent e such that 2^e |dS| <= 2^15 for every |dS| <= bound, or for every dS of rows of dY and V whose largest
+// squared norms are given.
+__device__ __forceinline__ float ds_exponent(float bound) {
     if (!(bound > 0.f) || !(bound < INFINITY)) return 0.f;
     return fminf(fmaxf(14.f - (float)ilogbf(bound), -40.f), 40.f);
 }
+__device__ __forceinline__ float ds_exponent(float dy, float v) { return ds_exponent(2.f * sqrtf(dy) * sqrtf(v)); }
 __device__ __forceinline__ float2 ds_norms(const XArgs &A, int b, int head) {
     return *reinterpret_cast<const float2 *>(A.norms + ((int64_t)b * A.n2 + head) * 2);
 }
@@ -224,7 +240,7 @@ struct alignas(16) Work {
     int32_t b, head;
     int32_t first;                      // k_xdq: first token, k_xdkv: first key, within the sequence
     int32_t t0, n;                      // this rank's first tile of the loop and their number; n < 0: no more units
-    int32_t stat;                       // k_xdq: (query tile of all sequences) * n2 + head
+    int32_t stat;                       // (tile of all sequences) * n2 + head
     int32_t piece;                      // number of the piece; -1: a whole unit, or a cluster's
     // windowed: first key of the loop's first tile (k_xdq), and the tiles [f0, f1) of this share that no window's edge crosses
     int32_t base, f0, f1;
@@ -568,13 +584,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
             if (!ok || w.n < 0) return;
             st_nl = A.stats[(int64_t)w.stat * 256 + r];
             st_nd = A.stats[(int64_t)w.stat * 256 + 128 + r];
-            if constexpr (kFp16)
+            if constexpr (kFp16 && kBand) norms.x = A.q_up[(int64_t)w.stat * kXRows + r];
+            else if constexpr (kFp16)
                 norms = make_float2(A.row_norms[(int64_t)w.stat * kXRows + r], ds_norms(A, w.b, w.head).y);
         };
         begin(0);
         for (int k = 0; ok && w.n >= 0; ++k) {
             const int n = w.n;
-            if constexpr (kFp16) up = ds_exponent(norms.x, norms.y);
+            if constexpr (kFp16) up = kBand ? norms.x : ds_exponent(norms.x, norms.y);
             const float nl = st_nl + up, nd = st_nd;
             if (n > 0) {
                 // ---------------------------------------------- softmax
@@ -805,6 +822,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         w.b = u.b;
         w.head = u.head;
         w.first = u.tile * kXRows;
+        w.stat = (int32_t)u.tile_id;
         if constexpr (kBand) {
             // queries that see any of the tile's keys, and the tiles of queries that all see all of them
             const int off = u.seq.klen - u.seq.qlen, last = min(w.first + kXRows, u.seq.klen) - 1;
@@ -944,7 +962,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float fv = kFp16 ? exp2f(-kShift) : 1.f;
     Work w{};
-    float up = 0.f;                                      // exponent that dS is scaled by
+    float up = 0.f;                                      // exponent that dS is scaled by (windowed: of the thread's key)
     bool st_live = false;                                // the thread's key is there
     auto out = [&](int k) -> int64_t {                   // place of key row k in dK and dV; negative: none
         const int key = w.first + k;
@@ -960,12 +978,13 @@ __global__ void __launch_bounds__(kXThreads, 1)
             ok = units.read(k, abort_flag, lane, &w);
             if (!ok || w.n < 0) return;
             st_live = w.first + r < w.seq.klen && (!A.mask || A.mask[(int64_t)w.seq.k0 + w.first + r] != 0);
-            if constexpr (kFp16) norms = ds_norms(A, w.b, w.head);
+            if constexpr (kFp16 && kBand) norms.x = A.k_up[(int64_t)w.stat * kXRows + r];
+            else if constexpr (kFp16) norms = ds_norms(A, w.b, w.head);
         };
         begin(0);
         for (int turn = 0; ok && w.n >= 0; ++turn) {
             const int n = w.n;
-            if constexpr (kFp16) up = ds_exponent(norms.x, norms.y);
+            if constexpr (kFp16) up = kBand ? norms.x : ds_exponent(norms.x, norms.y);
             const bool live = st_live;
             if (n > 0) {
                 // ---------------------------------------------- softmax
@@ -1117,6 +1136,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         // the CTA's only unit: partial sums into shared memory, then each rank joins its share of the rows
         float *xo = reinterpret_cast<float *>(smem);
         __syncthreads();                                 // loads and products on this memory are complete
+        const float down = kFp16 && kBand && h ? exp2f(-up) : 1.f;   // of this key, undone before rows change threads
         if (warp < 8) {
 #pragma unroll
             for (int j = 0; j < D; j += 32) {
@@ -1124,6 +1144,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 if (w.n > 0) {
                     tmem_ld32(trow + 256 + h * 128 + j, reinterpret_cast<uint32_t *>(y));
                     tc::tmem_wait_ld();
+                    if constexpr (kFp16 && kBand) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) y[e] *= down;
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
@@ -1133,7 +1157,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         }
         cluster_sync();
         if (warp < 8) {
-            const float fk = A.scale * (kFp16 ? exp2f(-up) : 1.f);
+            const float fk = A.scale * (kFp16 && !kBand ? exp2f(-up) : 1.f);
             join_rows<kFp16, D>(xo, A.dv, ns, rank, warp, lane, out, fv);
             join_rows<kFp16, D>(xo + kXRows * L::XROW, A.dk, ns, rank, warp, lane, out, fk);
         }
