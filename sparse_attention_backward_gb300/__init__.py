@@ -661,6 +661,9 @@ def _new(like):
     return _torch.empty_like(like, memory_format=_torch.contiguous_format)
 
 
+_PREFIXES = ("cu_seqlens", "cu_seqlens_q", "cu_seqlens_kv")
+
+
 def _rows_of(desc, cu, s_max):
     if desc.layout == SAG_LAYOUT_BSND:
         return (desc.batch, s_max)
@@ -685,7 +688,21 @@ def _derive(desc, dense=False):
     desc._dtype = _torch_dtype(desc)
     desc._dense = dense
     desc._bytes = bytes(desc)
+    # the prefix sums, which the descriptor has by address only
+    views = [(ctypes.c_char * (4 * (desc.batch + 1))).from_address(ctypes.addressof(p.contents))
+             for p in (getattr(desc, name, None) for name in _PREFIXES) if p and desc.batch >= 0]
+    desc._lengths = [(v, v.raw) for v in views]
     return desc
+
+
+def _unchanged(desc):
+    """Whether a kept descriptor, and the lengths that it points to, are what _derive saw."""
+    if bytes(desc) != desc._bytes:
+        return False
+    for view, seen in desc._lengths:
+        if view.raw != seen:
+            return False
+    return True
 
 
 def _size_of(desc, size):
@@ -704,8 +721,8 @@ def _scratch(workspace, need, device):
 
 
 def _given(desc):
-    """A kept descriptor, brought up to date if fields were set since."""
-    return desc if bytes(desc) == desc._bytes else _derive(desc)
+    """A kept descriptor, brought up to date if fields or lengths were set since."""
+    return desc if _unchanged(desc) else _derive(desc)
 
 
 def _with(desc, **fields):
@@ -940,7 +957,7 @@ def _cross(entry, size, q, k, v, cu_seqlens_q, cu_seqlens_kv, scale, key_mask, w
 def _usual_forward(entry, size, q, k, v, key_mask, workspace, desc):
     """The forward of a kept descriptor with dense tensors of just its shapes on the current device, which is what calls of a
     few microseconds are: the checks of ``_cross`` in one condition.  None: not such a call."""
-    if bytes(desc) != desc._bytes or not desc._dense:
+    if not desc._dense or not _unchanged(desc):
         return None
     qs, ks = desc._shapes
     dtype, device = desc._dtype, q.get_device()
@@ -1168,7 +1185,7 @@ def _paged(entry, size, x, desc, k_cache, v_cache, page_table, kv_lens, workspac
 
 def _usual_paged(entry, q, k_cache, v_cache, page_table, kv_lens, workspace, desc):
     """As ``_usual_forward``, over pages."""
-    if bytes(desc) != desc._bytes or not desc._dense:
+    if not desc._dense or not _unchanged(desc):
         return None
     qs, _, cache, table = desc._shapes
     dtype, device, i32 = desc._dtype, q.get_device(), _torch.int32
@@ -1380,7 +1397,7 @@ def _norm_rotary(entry, size, q, k, dq, dk, rotary, q_weight, k_weight, eps, wei
 
 def _usual_norm(entry, q, k, q_weight, k_weight, positions, desc):
     """As ``_usual_forward``: queries and keys, each with a weight of its type, and few sequences."""
-    if bytes(desc) != desc._bytes or not desc._dense or desc.batch > 64 or desc.weight_fp32:
+    if not desc._dense or desc.batch > 64 or desc.weight_fp32 or not _unchanged(desc):
         return None
     qs, ks = desc._shapes
     dtype, device, d = desc._dtype, q.get_device(), ks[-1:]
