@@ -607,8 +607,11 @@ sag_status cross_attn_query_error(const void *workspace, void *stream);
  *
  * The tensors are a sca_io.  What masked, padding and foreign rows hold never
  * counts.  A sequence's own rows have to be finite, whether or not a window joins
- * them: a NaN or an infinity in one may reach the results of up to 128 rows
- * around it whose windows do not hold it (a probability of 0 does not cancel it).
+ * them.  Where one holds a NaN or an infinity, results up to 254 positions beyond
+ * those that a window joins it to may be NaN (a probability of 0 does not cancel
+ * it): of a row of value in attention_out, of key in dq, and of query,
+ * attention_out or attention_out_grad in dk and dv.  A gradient taken of an
+ * attention_out that this has reached carries it as far again.
  */
 typedef struct swa_desc {
     sca_desc attn;
