@@ -694,8 +694,8 @@ typedef struct spa_io {
 sag_status paged_attn_fwd_workspace_size(const spa_desc *desc, size_t *workspace_bytes);
 sag_status paged_append_workspace_size(const spa_desc *desc, size_t *workspace_bytes);
 
-/* Phase 2: as for the cross attention, bit-identical run to run, capturable.  Two new tokens that a page table sends to the
- * same place leave one or the other there. */
+/* Phase 2: as for the cross attention, bit-identical run to run, capturable.  Of two new tokens that a page table sends to the
+ * same place, each 16 bytes there are the one's or the other's, which may differ run to run. */
 sag_status paged_attn_fwd(const spa_desc *desc, const spa_io *io, void *workspace, size_t workspace_bytes, void *stream);
 sag_status paged_append(const spa_desc *desc, const spa_io *io, void *workspace, size_t workspace_bytes, void *stream);
 

@@ -1219,7 +1219,8 @@ def paged_append(k, v, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q=None,
     [pages, page_size, n2, d]: token i of a sequence with q new ones goes to
     position kv_lens - q + i, in page page_table[sequence, position //
     page_size].  page_table [batch, width] and kv_lens [batch] are int32 tensors
-    on the device (the lengths include the new tokens).  Returns the caches.
+    on the device (the lengths include the new tokens).  Returns the caches.  No
+    two tokens may go to the same place: it would hold parts of both.
 
     ``desc`` (make_paged_desc) replaces cu_seqlens_q; ``check`` reads the device
     status back (a page or length out of range)."""
