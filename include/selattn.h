@@ -714,7 +714,7 @@ sag_status paged_query_error(const void *workspace, void *stream);
  *
  *   rotary        rows, heads, head dim, columns that turn, frequencies, strides: as for the rotary positions (q_out_stride
  *                 and k_out_stride are those of query_out and key_out, or of query_grad and key_grad)
- *   eps           finite, > 0
+ *   eps           finite, >= 2^-126 as fp32 (a smaller one would be flushed to 0)
  *   weight_offset finite: added to the weights (1 for weights that are held as differences from 1)
  *   weight_fp32   0: weights are of the dtype; 1: fp32
  *   q_grad_stride, k_grad_stride: row strides of query_out_grad and key_out_grad (0: dense); the forward ignores them

@@ -1254,7 +1254,9 @@ def paged_forward(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens_q=None, s
     Causal by default, or within a window as in ``window_forward``; ``desc``
     (make_paged_desc) replaces cu_seqlens_q, scale, left and right.  The page
     table and the lengths are read on the device, so a captured call may be
-    replayed as sequences grow."""
+    replayed as sequences grow.  How few tokens' loops are split is planned for
+    the whole width of the table, or for a descriptor's ``kv_expected``, where
+    tables are much wider than sequences are long."""
     lib = _lib_neighbours()
     if desc is not None and out is None and stream is None and not check:
         done = _usual_paged(lib.paged_attn_fwd, q, k_cache, v_cache, page_table, kv_lens, workspace, desc)

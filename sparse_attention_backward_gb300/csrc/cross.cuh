@@ -20,12 +20,12 @@ constexpr int kMaxPieces = 304;         // pieces of a launch: each has its part
 constexpr int kMaxFwdPieces = 152;      // pieces of a unit of a forward
 constexpr int kXThreads = 320;          // warps 0-7 softmax and epilogue, 8 TMA, 9 MMA
 constexpr uint64_t kXWaitNs = 2000000000ull;
-// A half keeps 11 bits down to 2^-14 only, and a probability of a long sequence lies below that.  Both passes shift
-// fp16 probabilities up by a power of two that cannot overflow 65504, and undo it in fp32.
 constexpr int32_t kNoLimit = 1 << 29;   // `left` or `right` without a limit
 constexpr int32_t kMaxPos = 1 << 28;    // key positions of a sequence: sums of two or three such numbers fit 32 bits
 // Which keys a query row may attend to: all of its sequence; those within a window of its position; the same, in pages.
 enum XMode { kAll = 0, kBand = 1, kPaged = 2 };
+// A half keeps 11 bits down to 2^-14 only, and a probability of a long sequence lies below that.  Both passes shift
+// fp16 probabilities up by a power of two that cannot overflow 65504, and undo it in fp32.
 constexpr float kFwdShiftF16 = 7.f;     // forward: exp2(x - max) <= 2^8 (lazy maximum), so <= 2^15
 constexpr float kGradShiftF16 = 15.f;   // gradient: P <= 1 (up to rounding), so <= 2^15
 

@@ -1,4 +1,4 @@
-// Cross and windowed attention, gradient: three launches, no fp32 accumulators in memory (but
+// Cross and windowed attention, gradient: three launches (fp16 of windows: four, window_bwd.cu), no fp32 accumulators in memory (but
 // for the sums of a cut unit's pieces), no
 // atomics but a maximum, tickets and counters, so the same bits on every run.
 //

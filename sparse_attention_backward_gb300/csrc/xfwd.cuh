@@ -30,8 +30,11 @@
 //
 // Few query rows and many keys: the key tiles of a unit are split over the
 // CTAs of a cluster, whose partial O, maximum and sum are joined through
-// distributed shared memory in rank order: one launch, no workspace, the same
-// bits on every run.
+// distributed shared memory in rank order: one launch, no workspace.  Windowed and
+// paged ones with room for more than two such clusters a unit: up to 152 pieces
+// of a unit, whose fp32 O, maximum and sum go to the workspace, and a second
+// launch (k_xjoin) that adds them in their order.  Either way the same bits on
+// every run.
 #pragma once
 
 #include <type_traits>
