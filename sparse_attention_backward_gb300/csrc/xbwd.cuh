@@ -1,6 +1,7 @@
-// Cross and windowed attention, gradient: three launches (fp16 of windows: four, window_bwd.cu), no fp32 accumulators in memory (but
-// for the sums of a cut unit's pieces), no
-// atomics but a maximum, tickets and counters, so the same bits on every run.
+// Cross and windowed attention, gradient: three launches (four for windows in
+// fp16, window_bwd.cu), no fp32 accumulators in memory (but for the sums of a cut
+// unit's pieces), no atomics but a maximum, tickets and counters, so the same bits
+// on every run.
 //
 //   k_xpre  Delta = rowsum(dY * O) and lse in log2 units, packed by query tile; zeros for absent states
 //   k_xdq   per query tile:  S = Q K^T, dP = dY V^T, dS = P (dP - Delta),  dQ += dS K      (over key tiles)

@@ -14,7 +14,7 @@ import torch
 
 import sparse_attention_backward_gb300 as sab
 
-from .test_window_gpu import HF, Case, _within
+from .test_window_gpu import BF, HF, Case, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +87,29 @@ def test_rows_that_are_not_finite_do_not_scale_others(bad):
     for x, y in zip(clean, spoilt):
         assert torch.equal(x[300:], y[300:])
     assert not bool(torch.isfinite(spoilt[2][3]).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("l,n1,n2,left", [([700, 300], 8, 2, 100), ([3000], 2, 1, -1), ([120] * 40, 32, 8, 60)])
+def test_calls_of_other_inputs_in_one_workspace(dtype, l, n1, n2, left):
+    """Nothing of a call is left for the next: a captured forward and gradient, replayed with one input after the other."""
+    cases = [Case(l, l, n1, n2, 128, dtype, left, 0, seed=54 + i, dy_scale=4.0 ** -i) for i in range(3)]
+    want = []
+    for c in cases:
+        o, lse = sab.window_forward(c.q, c.k, c.v, **c.args())
+        want.append((o, lse) + sab.window_backward(c.q, c.k, c.v, o, c.dy, lse, **c.args()))
+    a = cases[0]
+    desc = sab.make_window_desc(a.cu1, a.cu2, n1, n2, 128, a.scale, left, 0, sab.SAG_FP16 if dtype is HF else sab.SAG_BF16)
+    ws = torch.empty(max(sab.window_fwd_workspace_size(desc), sab.window_grad_workspace_size(desc)), dtype=torch.uint8, device="cuda")
+    held = [torch.empty_like(x) for x in (a.q, a.k, a.v, a.dy)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = sab.window_forward(*held[:3], desc=desc, workspace=ws)
+        outs = (o, lse) + sab.window_backward(*held[:3], o, held[3], lse, desc=desc, workspace=ws)
+    for turn in range(30):
+        c = cases[turn * 2 % 3]
+        for x, y in zip(held, (c.q, c.k, c.v, c.dy)):
+            x.copy_(y)
+        g.replay()
+        for x, y in zip(outs, want[turn * 2 % 3]):
+            assert torch.equal(x, y)
