@@ -717,6 +717,8 @@ def _scratch(workspace, need, device):
     """The caller's workspace where it is large enough, or a new one."""
     if workspace is None or workspace.numel() < need:
         return _torch.empty(need, dtype=_torch.uint8, device=device)
+    if not workspace.is_contiguous():       # an expanded tensor has more elements than memory
+        raise ValueError("workspace must be contiguous")
     return workspace
 
 
@@ -841,11 +843,10 @@ def _rotary(entry, q, k, rotary, cu_seqlens, positions, out, workspace, stream, 
                         k_stride=_row_stride("k", k, n2, d) if n2 else 0,
                         k_out_stride=_row_stride("out", ko, n2, d) if n2 else 0)
         io = SrtIo(q.data_ptr(), k.data_ptr() if n2 else None, pos, qo.data_ptr(), ko.data_ptr() if n2 else None)
-        ws, need = workspace, 0
+        ws, need = None, 0
         if use.batch > 64:          # smaller tables travel with the launch
             need = rotary_workspace_size(use)
-            if ws is None or ws.numel() < need:
-                ws = _torch.empty(need, dtype=_torch.uint8, device=q.device)
+            ws = _scratch(workspace, need, q.device)
         st = entry(use, io, ws.data_ptr() if need else None, need, handle)
         if st != SAG_OK:
             raise SagError(st, entry.__name__)

@@ -1,9 +1,10 @@
-"""Kept descriptors whose lengths are edited in place: the arrays behind
+"""Kept descriptors whose lengths are edited in place (and workspaces): the arrays behind
 cu_seqlens are the caller's to reach (desc.cu_seqlens_q[1] = n), the library
 reads them anew at every call, and so must what the tensors are checked against
 and the workspace size kept with the descriptor: tensors of the old lengths under
 a plan for new ones would be written past their ends."""
 import pytest
+import torch
 
 import sparse_attention_backward_gb300 as sab
 from sparse_attention_backward_gb300 import build as libbuild
@@ -64,3 +65,13 @@ def test_a_descriptor_that_was_left_alone_keeps_its_sizes(which):
     assert sab._given(d) is d and all(sab._size_of(d, size) == 1 << 40 for size in sizes) and d._dense
     d.batch = -1
     assert sab._given(d)._shapes[0][0] == 0
+
+
+def test_workspaces_with_less_memory_than_elements_are_refused(lib):
+    sab._lib_neighbours()
+    small, large = torch.empty(16, dtype=torch.uint8), torch.empty(1000, dtype=torch.uint8)
+    assert sab._scratch(large, 1000, "cpu") is large and sab._scratch(large[100:], 900, "cpu").data_ptr() == large.data_ptr() + 100
+    assert sab._scratch(small, 17, "cpu").numel() == 17 and sab._scratch(None, 5, "cpu").numel() == 5
+    for bad in (small[:1].expand(1000), large[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            sab._scratch(bad, 500, "cpu")
