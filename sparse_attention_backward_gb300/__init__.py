@@ -688,9 +688,9 @@ def _derive(desc, dense=False):
     desc._dtype = _torch_dtype(desc)
     desc._dense = dense
     desc._bytes = bytes(desc)
-    # the prefix sums, which the descriptor has by address only
+    # the prefix sums, which the descriptor has by address only (of batches that the library takes)
     views = [(ctypes.c_char * (4 * (desc.batch + 1))).from_address(ctypes.addressof(p.contents))
-             for p in (getattr(desc, name, None) for name in _PREFIXES) if p and desc.batch >= 0]
+             for p in (getattr(desc, name, None) for name in _PREFIXES) if p and 0 <= desc.batch <= 65536]
     desc._lengths = [(v, v.raw) for v in views]
     return desc
 
